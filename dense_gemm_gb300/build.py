@@ -20,9 +20,10 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgemm_f16.so")
 DEBUG_LIB = os.path.join(HERE, "libgemm_f16_debug.so")
-SOURCES = [os.path.join(CSRC, "gemm_f16.cu")]
-DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_kernel.cuh", "gemm_pair.cuh", "ptx.cuh")] + \
-    [os.path.join(INCLUDE, "gemm_f16.h")]
+SOURCES = [os.path.join(CSRC, "library.cu")]
+DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_f16.cu", "ops.cu", "gemm_kernel.cuh", "gemm_pair.cuh",
+                                                     "ops_linear.cuh", "ops_norm.cuh", "ptx.cuh")] + \
+    [os.path.join(INCLUDE, f) for f in ("gemm_f16.h", "gemm_ops.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,0 +1,813 @@
+// Host side of the gemm_ops C ABI (declared in include/gemm_ops.h): argument
+// validation, the choice of kernel and launch shape, tensor maps and launches.
+// Compiled in one translation unit with gemm_f16.cu (library.cu), whose device
+// set-up, tensor-map, launch and status helpers it uses.
+#include "gemm_ops.h"
+#include "ops_linear.cuh"
+#include "ops_norm.cuh"
+
+namespace {
+
+bool is_c_type(int32_t t) { return t >= GEMM_TYPE_F32 && t <= GEMM_TYPE_BF16; }
+int type_bytes(int32_t t) { return t == GEMM_TYPE_F32 ? 4 : t == GEMM_TYPE_E4M3 ? 1 : 2; }
+bool present(const gemm_matrix_t *m) { return m != nullptr && m->data != nullptr; }
+bool element_aligned(const void *p, int32_t type) { return (reinterpret_cast<uintptr_t>(p) & uintptr_t(type_bytes(type) - 1)) == 0; }
+uint64_t round128(uint64_t x) { return (x + 127u) / 128u * 128u; }
+bool sizes_ok(int64_t a, int64_t b, int64_t c) { return a >= 0 && b >= 0 && c >= 0 && a <= kMaxDim && b <= kMaxDim && c <= kMaxDim; }
+
+// A row-major matrix a call reads or writes element by element: [rows, cols] of
+// `type`, unit column stride, rows that do not overlap.
+gemm_status_t check_rows(const gemm_matrix_t *m, int64_t rows, int64_t cols) {
+    if (m->stride_row < 1 || m->stride_col < 1) return GEMM_ERR_INVALID_ARG;
+    if (!element_aligned(m->data, m->type)) return GEMM_ERR_INVALID_ARG;
+    if (m->stride_col != 1 && cols > 1) return GEMM_ERR_UNSUPPORTED;
+    if (rows > 1 && m->stride_row < cols) return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+int device_state(DeviceState **ds) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || device_init(dev, ds) != cudaSuccess) return -1;
+    return dev;
+}
+
+// Dynamic shared memory limits of this file's kernels, set once per device.
+struct OpsState {
+    std::mutex mu;
+    std::atomic<bool> ready{false};
+};
+OpsState g_ops[kMaxDevices];
+
+template <typename K>
+cudaError_t allow_smem(K *kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+bool ops_init(int dev) {
+    OpsState &o = g_ops[dev];
+    if (o.ready.load(std::memory_order_acquire)) return true;
+    std::lock_guard<std::mutex> lock(o.mu);
+    if (o.ready.load(std::memory_order_relaxed)) return true;
+    cudaError_t e = allow_smem(linear_pair<false, 2>, lin::PAIR_SMEM);
+    if (e == cudaSuccess) e = allow_smem(linear_pair<false, 4>, lin::PAIR_SMEM);
+    if (e == cudaSuccess) e = allow_smem(linear_pair<true, 2>, lin::PAIR_SMEM);
+    if (e == cudaSuccess) e = allow_smem(linear_pair<true, 4>, lin::PAIR_SMEM);
+    if (e == cudaSuccess) e = allow_smem(linear_split<false>, 232448);
+    if (e == cudaSuccess) e = allow_smem(linear_split<true>, 232448);
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return false;
+    }
+    o.ready.store(true, std::memory_order_release);
+    return true;
+}
+
+// launch_overlapped with a 2-D grid and block, and a cluster along x where
+// `cluster` > 1.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_shape(void (*kernel)(KArgs...), dim3 grid, dim3 block, int smem, int cluster, cudaStream_t stream,
+                         Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+    if (e != cudaSuccess) (void)cudaGetLastError();
+    return e;
+}
+
+// ------------------------------------------------------------------ linear: operands
+// An operand of the product as rows of contiguous elements: K-major (rows along
+// M or N) or MN-major (rows along K).
+struct Operand {
+    const void *data;
+    int64_t rows, inner, ld;
+    int32_t type;
+    bool mn_major;
+    bool tma() const { return tma_ok(data, inner, ld, type_bytes(type)); }
+    int64_t copy_ld() const { return int64_t(round128(uint64_t(inner) * type_bytes(type))) / type_bytes(type); }
+    uint64_t copy_bytes() const { return uint64_t(rows) * uint64_t(copy_ld()) * type_bytes(type); }
+};
+
+// A [M,K] (`outer` = M, k along columns) or, with the strides exchanged, B^T [N,K].
+gemm_status_t classify(const void *data, int32_t type, int64_t outer, int64_t K, int64_t stride_outer, int64_t stride_k,
+                       Operand *op) {
+    if (stride_outer < 1 || stride_k < 1) return GEMM_ERR_INVALID_ARG;
+    if (!element_aligned(data, type)) return GEMM_ERR_INVALID_ARG;
+    // a dimension of one element has no stride of its own
+    if (stride_k == 1 || K == 1) {
+        *op = Operand{data, outer, K, stride_outer, type, false};
+    } else if (stride_outer == 1 || outer == 1) {
+        if (type == GEMM_TYPE_E4M3) return GEMM_ERR_UNSUPPORTED;
+        *op = Operand{data, K, outer, stride_k, type, true};
+    } else {
+        return GEMM_ERR_UNSUPPORTED;
+    }
+    if (K == 1 && stride_outer == 1 && type != GEMM_TYPE_E4M3) *op = Operand{data, 1, outer, stride_k, type, true};
+    if (op->rows == 1) op->ld = op->copy_ld();
+    return GEMM_OK;
+}
+
+// Copies up to two operands of one type onto 128-byte lines at dst_a / dst_b
+// (nullptr: that one stays) and points them at the copies.
+cudaError_t pack_operands(Operand *a, void *dst_a, Operand *b, void *dst_b, int num_sms, cudaStream_t stream) {
+    const int32_t type = a->type;
+    int64_t total = 0;
+    auto blocks_for = [&](int64_t n) { return int(std::min<int64_t>(cdiv(n, 256), 8 * int64_t(num_sms))); };
+    cudaError_t e = cudaSuccess;
+    if (type == GEMM_TYPE_E4M3) {
+        auto job = [](const Operand &o, void *dst) {
+            PackBytesJob j;
+            j.src = static_cast<const uint8_t *>(o.data);
+            j.dst = static_cast<uint8_t *>(dst);
+            j.rows = o.rows;
+            j.inner = o.inner;
+            j.ld_src = o.ld;
+            j.ld_dst = o.copy_ld();
+            j.gpr = (o.inner + 15) / 16;
+            j.granules = dst != nullptr ? o.rows * j.gpr : 0;
+            return j;
+        };
+        const PackBytesJob ja = job(*a, dst_a), jb = job(*b, dst_b);
+        total = ja.granules + jb.granules;
+        if (total > 0) e = launch_overlapped(pack_bytes_kernel, blocks_for(total), 256, 0, stream, ja, jb);
+    } else {
+        auto job = [](const Operand &o, void *dst) {
+            PackJob j;
+            j.src = static_cast<const uint16_t *>(o.data);
+            j.dst = static_cast<uint16_t *>(dst);
+            j.rows = o.rows;
+            j.inner = o.inner;
+            j.ld_src = o.ld;
+            j.ld_dst = o.copy_ld();
+            j.gpr = (o.inner + 7) / 8;
+            j.granules = dst != nullptr ? o.rows * j.gpr : 0;
+            return j;
+        };
+        const PackJob ja = job(*a, dst_a), jb = job(*b, dst_b);
+        total = ja.granules + jb.granules;
+        if (total > 0) e = launch_overlapped(pack_rows_kernel, blocks_for(total), 256, 0, stream, ja, jb);
+    }
+    for (Operand *o : {a, b}) {
+        void *dst = o == a ? dst_a : dst_b;
+        if (dst == nullptr) continue;
+        o->ld = o->copy_ld();
+        o->data = dst;
+    }
+    return e;
+}
+
+bool encode_operand(CUtensorMap *map, const Operand &o, int rows_per_copy) {
+    const int es = type_bytes(o.type);
+    const CUtensorMapDataType dt = o.type == GEMM_TYPE_E4M3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : o.type == GEMM_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return o.mn_major ? encode_2d(map, dt, o.data, uint64_t(o.inner), uint64_t(o.rows), uint64_t(o.ld) * es, MN_CHUNK, BK)
+                      : encode_2d(map, dt, o.data, uint64_t(o.inner), uint64_t(o.rows), uint64_t(o.ld) * es, 128 / es,
+                                  rows_per_copy);
+}
+
+// The same descriptor fields as make_idesc with the operands' format: fp16 0,
+// bf16 1 (kind::f16); e4m3 0 (kind::f8f6f4).
+uint32_t linear_idesc(int32_t type, bool a_mn, bool b_mn, uint32_t m, uint32_t n) {
+    const uint32_t f = type == GEMM_TYPE_BF16 ? 1u : 0u;
+    return make_idesc(a_mn, b_mn, m, n) | (f << 7) | (f << 10);
+}
+
+// ------------------------------------------------------------------ linear: which kernel
+struct LinearPlan {
+    bool pair;
+    int T, split, stages;
+};
+
+// linear_split's shape for M rows. T is the smallest row count that holds them
+// (an M-major A comes in chunks of 64 rows). Up to 64 rows a CTA's ring is
+// kept under half the SM's shared memory, so that two CTAs share an SM and one's
+// set-up and sum overlap the other's stream.
+LinearPlan plan_split(int64_t M, int64_t N, int64_t num_kb, bool a_mn, int num_sms) {
+    LinearPlan pl{false, 16, 1, 6};
+    while (pl.T < 256 && (pl.T < M || (a_mn && pl.T < 64))) pl.T *= 2;
+    const bool two = pl.T <= 64;
+    pl.stages = pl.T <= 16 ? 6 : pl.T <= 32 ? 5 : pl.T <= 64 ? 4 : pl.T <= 128 ? 6 : 4;
+    const int64_t tiles = cdiv(N, lin::SPLIT_ROWS) * cdiv(M, pl.T);
+    const int64_t slots = two ? 2 * int64_t(num_sms) : num_sms;
+    while (pl.split < lin::MAX_SPLIT && tiles * pl.split * 2 <= slots && pl.split * 2 * 4 <= num_kb) pl.split *= 2;
+    return pl;
+}
+
+LinearPlan plan_linear(int64_t M, int64_t N, int64_t num_kb, bool a_mn, uint32_t flags, const DeviceState &ds) {
+    LinearPlan pl = plan_split(M, N, num_kb, a_mn, ds.num_sms);
+    const int64_t pair_tiles = cdiv(M, pair::TILE_M) * cdiv(N, pair::TILE_N);
+    if (flags & GEMM_LINEAR_PAIR) pl.pair = true;
+    else if (flags & GEMM_LINEAR_SPLIT) pl.pair = false;
+    else pl.pair = M > 256 && pair_tiles * 4 >= 3 * int64_t(ds.max_pairs);
+    return pl;
+}
+
+bool c_map(CUtensorMap *map, const void *data, int32_t type, int64_t M, int64_t N, int64_t ld) {
+    const int es = type_bytes(type);
+    const CUtensorMapDataType dt = type == GEMM_TYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : type == GEMM_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return encode_2d(map, dt, data, uint64_t(N), uint64_t(M), uint64_t(ld) * es, 128 / es, 32);
+}
+
+bool quad_aligned(const void *p, int64_t ld, int es) {
+    return (reinterpret_cast<uintptr_t>(p) & uintptr_t(4 * es - 1)) == 0 && ld % 4 == 0;
+}
+
+// The product and its epilogue on operands that TMA can describe. K >= 1.
+gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t N, int64_t K, const EpilogueParams &e,
+                         uint32_t flags, DeviceState *ds, cudaStream_t stream) {
+    const bool f8 = A.type == GEMM_TYPE_E4M3;
+    const int es = e.type == 0 ? 4 : 2;
+    LinearParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.M = M;
+    p.N = N;
+    p.e = e;
+    p.num_kb = int32_t(cdiv(K, f8 ? 128 : 64));
+    p.a_mn = A.mn_major;
+    p.b_mn = B.mn_major;
+    p.wait.timeout_ns = g_timeout_ns.load();
+    p.wait.epoch = next_epoch();
+    const LinearPlan pl = plan_linear(M, N, p.num_kb, A.mn_major, flags, *ds);
+    CUtensorMap tmA, tmB, tmC, tmR, tmP;
+    cudaError_t err;
+    if (pl.pair) {
+        const int64_t nm = cdiv(M, pair::TILE_M), nn = cdiv(N, pair::TILE_N);
+        if (nm * nn > kMaxDim / 2) return GEMM_ERR_UNSUPPORTED;
+        std::memset(&tmC, 0, sizeof(tmC));
+        tmR = tmP = tmC;
+        if (!encode_operand(&tmA, A, pair::CTA_M) || !encode_operand(&tmB, B, pair::CTA_N)) return GEMM_ERR_CUDA;
+        // a clipped TMA store writes whole 16-byte granules: C's and pre's rows must end on one
+        const bool ends = (N * es) % 16 == 0;
+        p.e.c_tma = ends && tma_ok(e.c, N, e.ldc, es);
+        p.e.p_tma = e.pre != nullptr && ends && tma_ok(e.pre, N, e.ldp, es);
+        p.e.r_tma = e.r != nullptr && tma_ok(e.r, N, e.ldr, es);
+        if ((p.e.c_tma && !c_map(&tmC, e.c, int32_t(e.type), M, N, e.ldc)) ||
+            (p.e.p_tma && !c_map(&tmP, e.pre, int32_t(e.type), M, N, e.ldp)) ||
+            (p.e.r_tma && !c_map(&tmR, e.r, int32_t(e.type), M, N, e.ldr)))
+            return GEMM_ERR_CUDA;
+        p.sched.nm = int32_t(nm);
+        p.sched.nn = int32_t(nn);
+        p.sched.group_m = 8;
+        p.sched.grouped = 1;
+        p.num_tiles = int32_t(nm * nn);
+        p.idesc = linear_idesc(A.type, A.mn_major, B.mn_major, 2 * pair::CTA_M, pair::TILE_N);
+        p.bufs = e.r != nullptr || e.pre != nullptr ? 2 : 1;
+        p.stages = p.bufs == 2 ? 5 : 6;
+        const dim3 grid(unsigned(2 * std::min<int64_t>(p.num_tiles, ds->max_pairs)));
+        auto *kernel = f8 ? (es == 4 ? linear_pair<true, 4> : linear_pair<true, 2>)
+                          : (es == 4 ? linear_pair<false, 4> : linear_pair<false, 2>);
+        err = launch_shape(kernel, grid, dim3(lin::PAIR_THREADS), lin::PAIR_SMEM, 1, stream, tmA, tmB, tmC, tmR, tmP, p);
+    } else {
+        const int64_t nm = cdiv(M, pl.T), nn = cdiv(N, lin::SPLIT_ROWS);
+        if (nm * nn > kMaxDim / lin::MAX_SPLIT) return GEMM_ERR_UNSUPPORTED;
+        if (!encode_operand(&tmA, A, pl.T) || !encode_operand(&tmB, B, lin::SPLIT_ROWS)) return GEMM_ERR_CUDA;
+        p.sched.nm = int32_t(nm);
+        p.sched.nn = int32_t(nn);
+        p.num_tiles = int32_t(nm * nn);
+        p.T = pl.T;
+        p.tmem_cols = pl.T < 32 ? 32 : pl.T;
+        p.split = pl.split;
+        p.stages = pl.stages;
+        // transposed product: the weights are the 128-row operand
+        p.idesc = linear_idesc(A.type, B.mn_major, A.mn_major, lin::SPLIT_ROWS, uint32_t(pl.T));
+        p.e.vec4 = quad_aligned(e.c, e.ldc, es) && (e.pre == nullptr || quad_aligned(e.pre, e.ldp, es));
+        const dim3 grid(unsigned(int64_t(p.num_tiles) * pl.split));
+        err = launch_shape(f8 ? linear_split<true> : linear_split<false>, grid, dim3(lin::SPLIT_THREADS),
+                           lin::split_smem(pl.stages, pl.T), pl.split, stream, tmB, tmA, p);
+    }
+    if (log_enabled())
+        std::fprintf(stderr, "[gemm_linear] M=%lld N=%lld K=%lld kernel=%s T=%d split=%d stages=%d tiles=%d\n", (long long)M,
+                     (long long)N, (long long)K, pl.pair ? "pair" : "split", p.T, p.split, p.stages, p.num_tiles);
+    return err == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+// Workspace of two operands' copies: [A's][B's], each from a 256-byte boundary.
+void copies_needed(const Operand &A, const Operand &B, uint64_t *a_bytes, uint64_t *b_bytes) {
+    *a_bytes = A.tma() ? 0u : round256(A.copy_bytes());
+    *b_bytes = B.tma() ? 0u : round256(B.copy_bytes());
+}
+
+gemm_status_t check_operands(const gemm_matrix_t *A, const gemm_matrix_t *B, int64_t M, int64_t N, int64_t K, Operand *a,
+                             Operand *b) {
+    if (A == nullptr || B == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (A->type != B->type || A->type < GEMM_TYPE_F16 || A->type > GEMM_TYPE_E4M3) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = classify(A->data, A->type, M, K, A->stride_row, A->stride_col, a);
+    if (st == GEMM_OK) st = classify(B->data, B->type, N, K, B->stride_col, B->stride_row, b);
+    return st;
+}
+
+gemm_status_t check_workspace(const void *ws, uint64_t bytes, uint64_t need, uintptr_t align) {
+    if (need == 0) return GEMM_OK;
+    if (ws == nullptr || bytes < need || (reinterpret_cast<uintptr_t>(ws) & (align - 1))) return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_linear_workspace_size(const gemm_matrix_t *A, const gemm_matrix_t *B, int64_t M, int64_t N,
+                                         int64_t K, uint64_t *bytes) {
+    if (!sizes_ok(M, N, K)) return GEMM_ERR_INVALID_ARG;
+    Operand a, b;
+    const gemm_status_t st = check_operands(A, B, M, N, K, &a, &b);
+    if (st != GEMM_OK) return st;
+    uint64_t na = 0, nb = 0;
+    if (M > 0 && N > 0 && K > 0) copies_needed(a, b, &na, &nb);
+    if (bytes) *bytes = na + nb;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_linear(const gemm_matrix_t *A, const gemm_matrix_t *B, const gemm_matrix_t *C,
+                          const gemm_epilogue_t *ep, int64_t M, int64_t N, int64_t K, uint32_t flags, void *workspace,
+                          uint64_t workspace_bytes, gemm_stream_t stream_) {
+    // ---- validation (no GPU work before this point)
+    if (!sizes_ok(M, N, K) || C == nullptr) return GEMM_ERR_INVALID_ARG;
+    if ((flags & ~GEMM_LINEAR_ALL_FLAGS) || flags == GEMM_LINEAR_ALL_FLAGS) return GEMM_ERR_INVALID_ARG;
+    static const gemm_epilogue_t kPlain = {};
+    if (ep == nullptr) ep = &kPlain;
+    Operand a, b;
+    gemm_status_t st = check_operands(A, B, M, N, K, &a, &b);
+    if (st != GEMM_OK) return st;
+    if (!is_c_type(C->type)) return GEMM_ERR_INVALID_ARG;
+    if (ep->activation < GEMM_ACT_NONE || ep->activation > GEMM_ACT_SILU) return GEMM_ERR_INVALID_ARG;
+    if (ep->bias != nullptr && ((ep->bias_type != GEMM_TYPE_F32 && ep->bias_type != C->type) ||
+                                !element_aligned(ep->bias, ep->bias_type)))
+        return GEMM_ERR_INVALID_ARG;
+    const bool f8 = A->type == GEMM_TYPE_E4M3;
+    if ((ep->scale_a == nullptr) != (ep->scale_b == nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (f8 != (ep->scale_a != nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (((reinterpret_cast<uintptr_t>(ep->scale_a) | reinterpret_cast<uintptr_t>(ep->scale_b)) & 3u))
+        return GEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return GEMM_OK;
+    if (C->data == nullptr || (K > 0 && (A->data == nullptr || B->data == nullptr))) return GEMM_ERR_INVALID_ARG;
+    for (const gemm_matrix_t *m : {C, &ep->residual, &ep->pre}) {
+        if (m->data == nullptr) continue;
+        if (m->type != C->type) return GEMM_ERR_INVALID_ARG;
+        st = check_rows(m, M, N);
+        if (st != GEMM_OK) return st;
+    }
+    uint64_t na = 0, nb = 0;
+    if (K > 0) copies_needed(a, b, &na, &nb);
+    st = check_workspace(workspace, workspace_bytes, na + nb, 128);
+    if (st != GEMM_OK) return st;
+
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    DeviceState *ds = nullptr;
+    const int dev = device_state(&ds);
+    if (dev < 0 || !ops_init(dev)) return GEMM_ERR_CUDA;
+    EpilogueParams e;
+    std::memset(&e, 0, sizeof(e));
+    e.c = C->data;
+    e.ldc = C->stride_row;
+    e.r = ep->residual.data;
+    e.ldr = ep->residual.stride_row;
+    e.pre = ep->pre.data;
+    e.ldp = ep->pre.stride_row;
+    e.bias = ep->bias;
+    e.bias_type = uint32_t(ep->bias_type);
+    e.sa = ep->scale_a;
+    e.sb = ep->scale_b;
+    e.type = uint32_t(C->type);
+    e.act = uint32_t(ep->activation);
+    if (K == 0) {
+        LinearParams p;
+        std::memset(&p, 0, sizeof(p));
+        p.M = M;
+        p.N = N;
+        p.e = e;
+        const int blocks = int(std::min<int64_t>(cdiv(M * N, 256), 8 * int64_t(ds->num_sms)));
+        return launch_overlapped(linear_empty_kernel, blocks, 256, 0, stream, p) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    }
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    if (na + nb > 0 && pack_operands(&a, na ? ws : nullptr, &b, nb ? ws + na : nullptr, ds->num_sms, stream) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    return run_linear(a, b, M, N, K, e, flags, ds, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ linear, backward
+namespace {
+
+// Column sums of D: each block sums a strip of columns over up to this many
+// rows, in kGradGroups interleaved groups.
+struct GradPlan {
+    int64_t rows_per_block, parts;
+};
+GradPlan plan_grad(int64_t M) {
+    GradPlan g;
+    g.rows_per_block = 64;
+    if (cdiv(M, g.rows_per_block) > 512) g.rows_per_block = cdiv(cdiv(M, 512), 8) * 8;
+    g.parts = cdiv(M, g.rows_per_block);
+    return g;
+}
+
+struct BackwardSpace {
+    uint64_t d, partial, a, b, total;
+    int64_t ldd;
+    bool store_d;
+};
+
+// The gradient's matrix D = G act'(pre) is stored where it differs from G or G
+// cannot be read by TMA.
+gemm_status_t backward_space(const gemm_matrix_t *G, const Operand &a, const Operand &b, int32_t act, bool need_dbias,
+                             int64_t M, int64_t N, int64_t K, BackwardSpace *s) {
+    std::memset(s, 0, sizeof(*s));
+    if (M == 0 || N == 0) return GEMM_OK;
+    s->store_d = act != GEMM_ACT_NONE || !tma_ok(G->data, N, G->stride_row, 2);
+    s->ldd = (N + 63) / 64 * 64;
+    if (s->store_d && K > 0) s->d = round256(uint64_t(M) * uint64_t(s->ldd) * 2u);
+    if (need_dbias) {
+        const GradPlan g = plan_grad(M);
+        if (g.parts > 1) s->partial = round256(uint64_t(g.parts) * uint64_t(N) * 4u);
+    }
+    if (K > 0) copies_needed(a, b, &s->a, &s->b);
+    s->total = s->d + s->partial + s->a + s->b;
+    return GEMM_OK;
+}
+
+gemm_status_t check_backward(const gemm_matrix_t *G, const gemm_matrix_t *A, const gemm_matrix_t *B, int64_t M, int64_t N,
+                             int64_t K, Operand *a, Operand *b) {
+    if (!sizes_ok(M, N, K) || G == nullptr) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = check_operands(A, B, M, N, K, a, b);
+    if (st != GEMM_OK) return st;
+    if (A->type == GEMM_TYPE_E4M3) return GEMM_ERR_UNSUPPORTED;
+    if (G->type != A->type) return GEMM_ERR_INVALID_ARG;
+    return check_rows(G, M, N);
+}
+
+// A gradient is stored row by row or, like a weight kept as its transpose,
+// column by column (*turned).
+gemm_status_t check_gradient(const gemm_matrix_t *m, int64_t rows, int64_t cols, bool *turned) {
+    if (!is_c_type(m->type)) return GEMM_ERR_INVALID_ARG;
+    *turned = m->stride_col != 1 && m->stride_row == 1 && cols > 1;
+    if (!*turned) return check_rows(m, rows, cols);
+    const gemm_matrix_t t{m->data, m->stride_col, m->stride_row, m->type};
+    return check_rows(&t, cols, rows);
+}
+
+cudaError_t zero_matrix(const gemm_matrix_t *m, bool turned, int64_t rows, int64_t cols, int num_sms, cudaStream_t stream) {
+    if (rows == 0 || cols == 0) return cudaSuccess;
+    if (turned) std::swap(rows, cols);
+    const int blocks = int(std::min<int64_t>(cdiv(rows * cols, 256), 8 * int64_t(num_sms)));
+    zero_c_kernel<<<blocks, 256, 0, stream>>>(m->data, rows, cols, turned ? m->stride_col : m->stride_row, type_bytes(m->type));
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_grad(const GradParams &p, bool vec, int64_t parts, cudaStream_t stream) {
+    const int64_t strip = vec ? 256 : 32;
+    const dim3 grid(unsigned(cdiv(p.N, strip)), unsigned(parts)), block(32, kGradGroups);
+    return vec ? launch_shape(linear_grad_kernel<T, 8>, grid, block, 0, 1, stream, p)
+               : launch_shape(linear_grad_kernel<T, 1>, grid, block, 0, 1, stream, p);
+}
+
+bool vec16(const void *p, int64_t ld, int es) { return aligned16(p) && (ld * es) % 16 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_linear_backward_workspace_size(const gemm_matrix_t *G, const gemm_matrix_t *A,
+                                                  const gemm_matrix_t *B, int32_t activation, int32_t need_dbias,
+                                                  int64_t M, int64_t N, int64_t K, uint64_t *bytes) {
+    Operand a, b;
+    gemm_status_t st = check_backward(G, A, B, M, N, K, &a, &b);
+    if (st != GEMM_OK) return st;
+    if (activation < GEMM_ACT_NONE || activation > GEMM_ACT_SILU) return GEMM_ERR_INVALID_ARG;
+    BackwardSpace s;
+    st = backward_space(G, a, b, activation, need_dbias != 0, M, N, K, &s);
+    if (st == GEMM_OK && bytes) *bytes = s.total;
+    return st;
+}
+
+gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *A, const gemm_matrix_t *B,
+                                   const gemm_matrix_t *pre, int32_t activation, const gemm_matrix_t *dA,
+                                   const gemm_matrix_t *dB, float *dbias, int64_t M, int64_t N, int64_t K,
+                                   uint32_t flags, void *workspace, uint64_t workspace_bytes, gemm_stream_t stream_) {
+    // ---- validation (no GPU work before this point)
+    Operand a, b;
+    gemm_status_t st = check_backward(G, A, B, M, N, K, &a, &b);
+    if (st != GEMM_OK) return st;
+    if ((flags & ~GEMM_LINEAR_ALL_FLAGS) || flags == GEMM_LINEAR_ALL_FLAGS) return GEMM_ERR_INVALID_ARG;
+    if (activation < GEMM_ACT_NONE || activation > GEMM_ACT_SILU) return GEMM_ERR_INVALID_ARG;
+    const bool has_pre = activation != GEMM_ACT_NONE;
+    if (has_pre && M > 0 && N > 0) {
+        if (!present(pre) || pre->type != G->type) return GEMM_ERR_INVALID_ARG;
+        st = check_rows(pre, M, N);
+        if (st != GEMM_OK) return st;
+    }
+    bool dA_t = false, dB_t = false;
+    if (present(dA)) st = check_gradient(dA, M, K, &dA_t);
+    if (st == GEMM_OK && present(dB)) st = check_gradient(dB, K, N, &dB_t);
+    if (st != GEMM_OK) return st;
+    if (reinterpret_cast<uintptr_t>(dbias) & 3u) return GEMM_ERR_INVALID_ARG;
+    if (M > 0 && N > 0 && G->data == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (M > 0 && N > 0 && K > 0 && ((present(dA) && B->data == nullptr) || (present(dB) && A->data == nullptr)))
+        return GEMM_ERR_INVALID_ARG;
+    BackwardSpace s;
+    st = backward_space(G, a, b, activation, dbias != nullptr, M, N, K, &s);
+    if (st != GEMM_OK) return st;
+    st = check_workspace(workspace, workspace_bytes, s.total, 128);
+    if (st != GEMM_OK) return st;
+
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    DeviceState *ds = nullptr;
+    const int dev = device_state(&ds);
+    if (dev < 0 || !ops_init(dev)) return GEMM_ERR_CUDA;
+    if (M == 0 || N == 0) {  // empty sums
+        if (present(dA) && zero_matrix(dA, dA_t, M, K, ds->num_sms, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+        if (present(dB) && zero_matrix(dB, dB_t, K, N, ds->num_sms, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+        if (dbias != nullptr && N > 0 && cudaMemsetAsync(dbias, 0, size_t(N) * 4u, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+        return GEMM_OK;
+    }
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    void *ws_d = ws, *ws_a = ws + s.d + s.partial, *ws_b = ws + s.d + s.partial + s.a;
+    float *ws_part = reinterpret_cast<float *>(ws + s.d);
+    const bool products = K > 0 && (present(dA) || present(dB));
+
+    // ---- D and its column sums
+    Operand d_rows{G->data, M, N, G->stride_row, G->type, false};
+    if ((s.store_d && products) || dbias != nullptr) {
+        const GradPlan gp = plan_grad(M);
+        GradParams p;
+        std::memset(&p, 0, sizeof(p));
+        p.g = G->data;
+        p.ldg = G->stride_row;
+        p.pre = has_pre ? pre->data : nullptr;
+        p.ldp = has_pre ? pre->stride_row : 0;
+        p.d = s.store_d && products ? ws_d : nullptr;
+        p.ldd = s.ldd;
+        p.partial = dbias == nullptr ? nullptr : gp.parts > 1 ? ws_part : dbias;
+        p.M = M;
+        p.N = N;
+        p.rows_per_block = gp.rows_per_block;
+        p.act = uint32_t(activation);
+        const bool vec = N % 8 == 0 && vec16(p.g, p.ldg, 2) && (!has_pre || vec16(p.pre, p.ldp, 2));
+        cudaError_t e = G->type == GEMM_TYPE_F16 ? launch_grad<__half>(p, vec, gp.parts, stream)
+                                                 : launch_grad<__nv_bfloat16>(p, vec, gp.parts, stream);
+        if (e == cudaSuccess && dbias != nullptr && gp.parts > 1)
+            e = launch_shape(sum_partials_kernel, dim3(unsigned(cdiv(N, 32))), dim3(32, kPartGroups), 0, 1, stream,
+                             static_cast<const float *>(ws_part), dbias, gp.parts, N);
+        if (e != cudaSuccess) return GEMM_ERR_CUDA;
+        if (p.d != nullptr) {
+            d_rows.data = ws_d;
+            d_rows.ld = s.ldd;
+        }
+    }
+    if (!products) {
+        return GEMM_OK;
+    }
+    const bool pack_a = present(dB) && s.a > 0, pack_b = present(dA) && s.b > 0;
+    if ((pack_a || pack_b) &&
+        pack_operands(&a, pack_a ? ws_a : nullptr, &b, pack_b ? ws_b : nullptr, ds->num_sms, stream) != cudaSuccess)
+        return GEMM_ERR_CUDA;
+    auto out = [](const gemm_matrix_t *m, bool turned) {
+        EpilogueParams e;
+        std::memset(&e, 0, sizeof(e));
+        e.c = m->data;
+        e.ldc = turned ? m->stride_col : m->stride_row;
+        e.type = uint32_t(m->type);
+        return e;
+    };
+    // An operand whose rows run along the summed dimension is MN-major. The forward
+    // product summed over K; these sum over N (dA) and M (dB).
+    auto turned = [](Operand o) {
+        o.mn_major = !o.mn_major;
+        return o;
+    };
+    if (present(dA)) {  // dA = D B^T, or its transpose B D^T
+        const Operand w = turned(b);
+        st = dA_t ? run_linear(w, d_rows, K, M, N, out(dA, true), flags, ds, stream)
+                  : run_linear(d_rows, w, M, K, N, out(dA, false), flags, ds, stream);
+        if (st != GEMM_OK) return st;
+    }
+    if (present(dB)) {  // dB = A^T D, or its transpose D^T A
+        const Operand x = turned(a), d = turned(d_rows);
+        st = dB_t ? run_linear(d, x, N, K, M, out(dB, true), flags, ds, stream)
+                  : run_linear(x, d, K, N, M, out(dB, false), flags, ds, stream);
+    }
+    return st;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ RMS norm
+namespace {
+
+constexpr int64_t kNormParts = 608;  // blocks of the backward pass at most: 4 per SM
+
+struct RowShape {
+    bool vec;       // 16-byte vectors (8 elements), else single elements
+    int nv;         // loads per thread
+    int tpr, rpb;   // threads per row, rows per block
+    bool fits;      // the row fits its threads' registers
+};
+
+// Threads per row: enough for one load each where possible, at most 1024; short
+// rows share a block of 256 threads.
+RowShape row_shape(int64_t width, bool vec, const int *nvs, int count) {
+    RowShape s{vec, nvs[0], 32, 1, false};
+    const int64_t v = vec ? 8 : 1;
+    for (int i = 0; i < count; ++i) {
+        s.nv = nvs[i];
+        const int64_t t = cdiv(cdiv(width, v * s.nv), 32) * 32;
+        const int64_t most = i + 1 < count ? 512 : 1024;
+        if (t <= most) {
+            s.tpr = int(t);
+            s.fits = true;
+            break;
+        }
+    }
+    if (s.fits && s.tpr <= 128) s.rpb = 256 / s.tpr;
+    return s;
+}
+
+template <typename T>
+cudaError_t launch_norm(const NormParams &p, bool vec, bool quant, cudaStream_t stream) {
+    static const int kVecNv[] = {1, 2, 4}, kOneNv[] = {4, 16, 32};
+    const RowShape s = row_shape(p.width, vec, vec ? kVecNv : kOneNv, 3);
+    if (!s.fits) {
+        if (p.rows > kMaxDim) return cudaErrorInvalidValue;
+        return launch_shape(rms_norm_long_kernel<T>, dim3(unsigned(p.rows)), dim3(1024), 0, 1, stream, p, int32_t(quant));
+    }
+    using Kernel = void (*)(const NormParams);
+    Kernel k;
+    if (vec) {
+        k = s.nv == 1 ? (quant ? rms_norm_kernel<T, 8, 1, true> : rms_norm_kernel<T, 8, 1, false>)
+            : s.nv == 2 ? (quant ? rms_norm_kernel<T, 8, 2, true> : rms_norm_kernel<T, 8, 2, false>)
+                        : (quant ? rms_norm_kernel<T, 8, 4, true> : rms_norm_kernel<T, 8, 4, false>);
+    } else {
+        k = s.nv == 4 ? (quant ? rms_norm_kernel<T, 1, 4, true> : rms_norm_kernel<T, 1, 4, false>)
+            : s.nv == 16 ? (quant ? rms_norm_kernel<T, 1, 16, true> : rms_norm_kernel<T, 1, 16, false>)
+                         : (quant ? rms_norm_kernel<T, 1, 32, true> : rms_norm_kernel<T, 1, 32, false>);
+    }
+    return launch_shape(k, dim3(unsigned(cdiv(p.rows, s.rpb))), dim3(unsigned(s.tpr), unsigned(s.rpb)), 0, 1, stream, p);
+}
+
+template <typename T>
+cudaError_t launch_norm_backward(NormBackwardParams p, bool vec, float *dweight, float *partial, cudaStream_t stream) {
+    static const int kVecNv[] = {1, 2}, kOneNv[] = {4, 16};
+    const RowShape s = row_shape(p.width, vec, vec ? kVecNv : kOneNv, 2);
+    p.partial = dweight != nullptr ? partial : nullptr;
+    int64_t parts;
+    cudaError_t e;
+    if (s.fits) {
+        using Kernel = void (*)(const NormBackwardParams);
+        Kernel k = vec ? (s.nv == 1 ? rms_norm_backward_kernel<T, 8, 1> : rms_norm_backward_kernel<T, 8, 2>)
+                       : (s.nv == 4 ? rms_norm_backward_kernel<T, 1, 4> : rms_norm_backward_kernel<T, 1, 16>);
+        parts = std::min<int64_t>(cdiv(p.rows, s.rpb), kNormParts);
+        const int smem = s.rpb > 1 ? s.rpb * s.tpr * (vec ? 8 : 1) * s.nv * 4 : 0;
+        e = launch_shape(k, dim3(unsigned(parts)), dim3(unsigned(s.tpr), unsigned(s.rpb)), smem, 1, stream, p);
+    } else {
+        e = launch_shape(rms_norm_backward_long_kernel<T>, dim3(unsigned(p.rows)), dim3(1024), 0, 1, stream, p);
+        const int64_t rows_per_block = cdiv(p.rows, kNormParts);
+        parts = cdiv(p.rows, rows_per_block);
+        if (e == cudaSuccess && dweight != nullptr)
+            e = launch_shape(rms_norm_dweight_long_kernel<T>, dim3(unsigned(cdiv(p.width, 256)), unsigned(parts)), dim3(256),
+                             0, 1, stream, p, rows_per_block);
+    }
+    if (e == cudaSuccess && dweight != nullptr)
+        e = launch_shape(sum_partials_kernel, dim3(unsigned(cdiv(p.width, 32))), dim3(32, kPartGroups), 0, 1, stream,
+                         static_cast<const float *>(partial), dweight, parts, p.width);
+    return e;
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_rms_norm(const gemm_matrix_t *x, const gemm_matrix_t *residual, const void *weight,
+                            int32_t weight_type, const gemm_matrix_t *y, const gemm_matrix_t *h, float *scale,
+                            float *rstd, int64_t rows, int64_t width, float eps, gemm_stream_t stream_) {
+    // ---- validation (no GPU work before this point)
+    if (!sizes_ok(rows, width, 0) || x == nullptr || y == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (!is_c_type(x->type) || (y->type != x->type && y->type != GEMM_TYPE_E4M3)) return GEMM_ERR_INVALID_ARG;
+    if (weight_type != GEMM_TYPE_F32 && weight_type != x->type) return GEMM_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || !(eps <= 3.0e38f)) return GEMM_ERR_INVALID_ARG;
+    const bool quant = y->type == GEMM_TYPE_E4M3;
+    if (rows == 0 || width == 0) return GEMM_OK;
+    if (x->data == nullptr || y->data == nullptr || weight == nullptr || quant != (scale != nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (present(h) && !present(residual)) return GEMM_ERR_INVALID_ARG;
+    if (!element_aligned(weight, weight_type) ||
+        ((reinterpret_cast<uintptr_t>(scale) | reinterpret_cast<uintptr_t>(rstd)) & 3u))
+        return GEMM_ERR_INVALID_ARG;
+    for (const gemm_matrix_t *m : {x, residual, y, h}) {
+        if (!present(m)) continue;
+        if (m != y && m->type != x->type) return GEMM_ERR_INVALID_ARG;
+        const gemm_status_t st = check_rows(m, rows, width);
+        if (st != GEMM_OK) return st;
+    }
+    DeviceState *ds = nullptr;
+    if (device_state(&ds) < 0) return GEMM_ERR_CUDA;
+    NormParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.x = x->data;
+    p.ldx = x->stride_row;
+    p.r = present(residual) ? residual->data : nullptr;
+    p.ldr = present(residual) ? residual->stride_row : 0;
+    p.y = y->data;
+    p.ldy = y->stride_row;
+    p.h = present(h) ? h->data : nullptr;
+    p.ldh = present(h) ? h->stride_row : 0;
+    p.w = weight;
+    p.w_f32 = weight_type == GEMM_TYPE_F32;
+    p.scale = scale;
+    p.rstd = rstd;
+    p.rows = rows;
+    p.width = width;
+    p.eps = eps;
+    p.inv_width = 1.0f / float(width);
+    const int es = type_bytes(x->type);
+    bool vec = width % 8 == 0 && aligned16(weight) && vec16(p.x, p.ldx, es);
+    if (p.r != nullptr) vec = vec && vec16(p.r, p.ldr, es);
+    if (p.h != nullptr) vec = vec && vec16(p.h, p.ldh, es);
+    vec = vec && (quant ? (reinterpret_cast<uintptr_t>(p.y) & 7u) == 0 && p.ldy % 8 == 0 : vec16(p.y, p.ldy, es));
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const cudaError_t e = x->type == GEMM_TYPE_F32   ? launch_norm<float>(p, vec, quant, stream)
+                          : x->type == GEMM_TYPE_F16 ? launch_norm<__half>(p, vec, quant, stream)
+                                                     : launch_norm<__nv_bfloat16>(p, vec, quant, stream);
+    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+gemm_status_t gemm_rms_norm_backward_workspace_size(int64_t rows, int64_t width, uint64_t *bytes) {
+    if (!sizes_ok(rows, width, 0)) return GEMM_ERR_INVALID_ARG;
+    if (bytes) *bytes = uint64_t(std::min<int64_t>(rows, kNormParts)) * uint64_t(width) * 4u;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_rms_norm_backward(const gemm_matrix_t *grad, const gemm_matrix_t *h, const void *weight,
+                                     int32_t weight_type, const float *rstd, const gemm_matrix_t *grad_h,
+                                     const gemm_matrix_t *dx, float *dweight, int64_t rows, int64_t width,
+                                     void *workspace, uint64_t workspace_bytes, gemm_stream_t stream_) {
+    // ---- validation (no GPU work before this point)
+    if (!sizes_ok(rows, width, 0) || grad == nullptr || h == nullptr || dx == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (!is_c_type(grad->type)) return GEMM_ERR_INVALID_ARG;
+    if (weight_type != GEMM_TYPE_F32 && weight_type != grad->type) return GEMM_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(dweight) & 3u) return GEMM_ERR_INVALID_ARG;
+    if (width == 0) return GEMM_OK;
+    if (rows > 0) {
+        if (grad->data == nullptr || h->data == nullptr || dx->data == nullptr || weight == nullptr || rstd == nullptr)
+            return GEMM_ERR_INVALID_ARG;
+        if (!element_aligned(weight, weight_type) || (reinterpret_cast<uintptr_t>(rstd) & 3u)) return GEMM_ERR_INVALID_ARG;
+        for (const gemm_matrix_t *m : {grad, h, grad_h, dx}) {
+            if (!present(m)) continue;
+            if (m->type != grad->type) return GEMM_ERR_INVALID_ARG;
+            const gemm_status_t st = check_rows(m, rows, width);
+            if (st != GEMM_OK) return st;
+        }
+    }
+    uint64_t need = 0;
+    if (dweight != nullptr) (void)gemm_rms_norm_backward_workspace_size(rows, width, &need);
+    const gemm_status_t st = check_workspace(workspace, workspace_bytes, need, 16);
+    if (st != GEMM_OK) return st;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    DeviceState *ds = nullptr;
+    if (device_state(&ds) < 0) return GEMM_ERR_CUDA;
+    if (rows == 0) {
+        if (dweight != nullptr && cudaMemsetAsync(dweight, 0, size_t(width) * 4u, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+        return GEMM_OK;
+    }
+    NormBackwardParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.g = grad->data;
+    p.ldg = grad->stride_row;
+    p.h = h->data;
+    p.ldh = h->stride_row;
+    p.dh = present(grad_h) ? grad_h->data : nullptr;
+    p.lddh = present(grad_h) ? grad_h->stride_row : 0;
+    p.dx = dx->data;
+    p.lddx = dx->stride_row;
+    p.w = weight;
+    p.w_f32 = weight_type == GEMM_TYPE_F32;
+    p.rstd = rstd;
+    p.rows = rows;
+    p.width = width;
+    p.inv_width = 1.0f / float(width);
+    const int es = type_bytes(grad->type);
+    bool vec = width % 8 == 0 && aligned16(weight) && vec16(p.g, p.ldg, es) && vec16(p.h, p.ldh, es) &&
+               vec16(p.dx, p.lddx, es);
+    if (p.dh != nullptr) vec = vec && vec16(p.dh, p.lddh, es);
+    float *part = static_cast<float *>(workspace);
+    const cudaError_t e = grad->type == GEMM_TYPE_F32   ? launch_norm_backward<float>(p, vec, dweight, part, stream)
+                          : grad->type == GEMM_TYPE_F16 ? launch_norm_backward<__half>(p, vec, dweight, part, stream)
+                                                        : launch_norm_backward<__nv_bfloat16>(p, vec, dweight, part, stream);
+    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+}  // extern "C"

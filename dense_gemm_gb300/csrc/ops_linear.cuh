@@ -1,0 +1,1011 @@
+// A product with its epilogue (sm_103a): C = act(s_a s_b (A @ B) + bias) + R,
+// fp16 / bf16 / e4m3 operands, fp32 sums, and the elementwise part of its
+// backward pass (D = G act'(P) with the column sums of D).
+//
+// Two kernels:
+//   linear_pair   256 x 256 tiles on CTA pairs: the persistent tcgen05 kernel of
+//                 gemm_pair.cuh (same rings, roles and tile order; TMA loads,
+//                 static order) with an epilogue that works on the tile while it
+//                 is in registers. The residual's tile is fetched by TMA into the
+//                 buffers the output leaves through, during the main loop.
+//   linear_split  few rows or few tiles: 128 columns of C by T rows per CTA with
+//                 the product transposed (the weights are the 128-row operand, the
+//                 T tokens the N side), K split over a cluster and the partial
+//                 sums added through distributed shared memory.
+#pragma once
+#include "gemm_pair.cuh"
+#include "ops_norm.cuh"
+
+namespace g16 {
+
+// ------------------------------------------------------------------ 8-bit tensor-core products
+// kind::f8f6f4 with both operands e4m3: K = 32 per instruction, 32 bytes as
+// kind::f16's K = 16, so descriptors and steps are the same.
+__device__ __forceinline__ void mma_f8_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred pe, pa;\n\t"
+        "elect.sync _|pe, 0xffffffff;\n\t"
+        "setp.ne.b32 pa, %4, 0;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, pa;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_f8_pair_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                  uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred pe, pa;\n\t"
+        "elect.sync _|pe, 0xffffffff;\n\t"
+        "setp.ne.b32 pa, %4, 0;\n\t"
+        "@pe tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, pa;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// ------------------------------------------------------------------ activations
+// The library's exponential (__expf) is within 2 + |1.2 x| units in the last
+// place and the quotients within 2, far inside the 16-bit outputs' rounding
+// and about 1e-6 for fp32 ones; the erf is CUDA's erff.
+constexpr uint32_t kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4;  // GEMM_ACT_*
+constexpr float kSqrtHalf = 0.70710678118654752f;
+constexpr float kInvSqrt2Pi = 0.39894228040143268f;
+constexpr float kTwoSqrt2OverPi = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+
+template <uint32_t ACT>
+__device__ __forceinline__ float act_value(float x) {
+    if constexpr (ACT == kActRelu) return x < 0.0f ? 0.0f : x;
+    else if constexpr (ACT == kActSilu) return __fdividef(x, 1.0f + __expf(-x));
+    else if constexpr (ACT == kActGelu) return 0.5f * x * (1.0f + erff(x * kSqrtHalf));
+    else if constexpr (ACT == kActGeluTanh)
+        return __fdividef(x, 1.0f + __expf(-kTwoSqrt2OverPi * fmaf(0.044715f * x * x, x, x)));
+    else return x;
+}
+
+template <uint32_t ACT>
+__device__ __forceinline__ float act_slope(float x) {
+    if constexpr (ACT == kActRelu) return x > 0.0f ? 1.0f : 0.0f;
+    else if constexpr (ACT == kActSilu) {
+        const float s = __fdividef(1.0f, 1.0f + __expf(-x));
+        return s * fmaf(x, 1.0f - s, 1.0f);
+    } else if constexpr (ACT == kActGelu) {
+        return fmaf(x * kInvSqrt2Pi, __expf(-0.5f * x * x), 0.5f * (1.0f + erff(x * kSqrtHalf)));
+    } else if constexpr (ACT == kActGeluTanh) {
+        // x s(z) with z = c (x + 0.044715 x^3): s + x s (1 - s) z'
+        const float s = __fdividef(1.0f, 1.0f + __expf(-kTwoSqrt2OverPi * fmaf(0.044715f * x * x, x, x)));
+        const float dz = kTwoSqrt2OverPi * fmaf(0.134145f * x, x, 1.0f);
+        return fmaf(x * s * (1.0f - s), dz, s);
+    } else return 1.0f;
+}
+
+template <int N>
+__device__ __forceinline__ void apply_act(uint32_t act, float (&x)[N]) {
+    switch (act) {  // uniform
+        case kActRelu:
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = act_value<kActRelu>(x[i]);
+            break;
+        case kActGelu:
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = act_value<kActGelu>(x[i]);
+            break;
+        case kActGeluTanh:
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = act_value<kActGeluTanh>(x[i]);
+            break;
+        case kActSilu:
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = act_value<kActSilu>(x[i]);
+            break;
+        default: break;
+    }
+}
+
+// ------------------------------------------------------------------ elements by run-time type (0 fp32, 1 fp16, 2 bf16)
+__device__ __forceinline__ float load_elem(const void *p, uint32_t type, int64_t at) {
+    if (type == 0) return static_cast<const float *>(p)[at];
+    if (type == 1) return __half2float(static_cast<const __half *>(p)[at]);
+    return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[at]);
+}
+
+__device__ __forceinline__ void store_elem(void *p, uint32_t type, int64_t at, float v) {
+    if (type == 0) static_cast<float *>(p)[at] = v;
+    else if (type == 1) static_cast<__half *>(p)[at] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16 *>(p)[at] = __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ float2 unpack_16x2(uint32_t w, uint32_t type) {
+    if (type == 1) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
+}
+
+// ------------------------------------------------------------------ parameters
+struct EpilogueParams {
+    void *c;
+    const void *r;  // nullptr: no residual
+    void *pre;      // nullptr: not stored
+    const void *bias;
+    const float *sa, *sb;
+    int64_t ldc, ldr, ldp;
+    uint32_t type;       // of C, residual and pre
+    uint32_t bias_type;
+    uint32_t act;
+    uint32_t c_tma, r_tma, p_tma;  // described by a tensor map (linear_pair)
+    uint32_t vec4;                 // four consecutive columns of C, R and pre are aligned to their size together
+};
+
+struct LinearParams {
+    int64_t M, N;
+    Sched sched;
+    int32_t num_tiles, num_kb;
+    uint32_t a_mn, b_mn, idesc;
+    int32_t stages, bufs;     // linear_pair: ring depth, staging buffers per epilogue warp
+    int32_t T, tmem_cols;     // linear_split: rows of C per CTA, TMEM columns
+    int32_t split;            // linear_split: CTAs of a cluster along K
+    EpilogueParams e;
+    WaitCtl wait;
+};
+
+// ================================================================== linear_pair
+namespace lin {
+constexpr int PAIR_STAGES = 6;  // at most; 5 when two staging buffers per warp are needed
+constexpr int STAGE_BYTES = pair::A_STAGE_BYTES + pair::B_STAGE_BYTES;
+constexpr int PAIR_THREADS = (2 + EPI_WARPS) * 32;
+constexpr int BUF_BYTES = 4096;  // 32 rows of 128 bytes
+// full[6], empty[6], tfull[2], tempty[2], tdone[2], drain, residual[8 warps][2]
+constexpr int PAIR_BARS = 2 * PAIR_STAGES + 3 * NUM_ACC + 1 + 2 * EPI_WARPS;
+constexpr int ring_and_staging(int stages, int bufs) { return stages * STAGE_BYTES + bufs * EPI_WARPS * BUF_BYTES; }
+constexpr int PAIR_RING = ring_and_staging(6, 1);
+static_assert(ring_and_staging(5, 2) == PAIR_RING, "one shared-memory size for both shapes");
+constexpr int PAIR_OFF_BAR = PAIR_RING;
+constexpr int PAIR_OFF_SLOT = PAIR_OFF_BAR + PAIR_BARS * 8;
+constexpr int PAIR_SMEM = PAIR_OFF_SLOT + 16 + 1024;
+static_assert(PAIR_SMEM <= 232448, "exceeds the 227 KiB per-CTA shared memory limit");
+}  // namespace lin
+
+// The epilogue of one warp: 32 rows (TMEM lanes) by the 128 columns of its half.
+// OB: bytes per element of C. A chunk is 128 bytes of each row.
+template <bool kF8, int OB>
+struct PairEpilogue {
+    static constexpr int CHUNK = 128 / OB;       // columns: 64 or 32
+    static constexpr int PER_TILE = 128 / CHUNK;  // chunks of the warp's half: 2 or 4
+    const LinearParams &p;
+    const CUtensorMap *tmC, *tmR, *tmP;
+    uint32_t stg, rbar;  // this warp's staging buffers and residual barriers (2)
+    int lane;
+    uint32_t r_issued[2], r_used[2];
+
+    __device__ __forceinline__ uint32_t buf(int b) const { return stg + uint32_t(b) * lin::BUF_BYTES; }
+    __device__ __forceinline__ bool prefetches() const { return p.e.r != nullptr && p.e.r_tma && p.e.pre == nullptr; }
+
+    // Start fetching the residual's 32 rows x CHUNK columns into buffer b (whole warp).
+    __device__ __forceinline__ void fetch_residual(int b, int64_t row0, int64_t col0) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(rbar + 8u * b, lin::BUF_BYTES);
+            tma_load_2d(buf(b), tmR, int32_t(col0), int32_t(row0), rbar + 8u * b);
+        }
+        ++r_issued[b];
+    }
+
+    // Buffer b <- the residual's 32 rows x CHUNK columns, with plain loads.
+    __device__ __forceinline__ void load_residual(int b, int64_t row0, int64_t col0) {
+        const int64_t rows = p.M - row0;
+        constexpr int PER_LANE = CHUNK / 32;
+        const int64_t col = col0 + PER_LANE * lane;
+#pragma unroll 8
+        for (int r = 0; r < 32; ++r) {
+            uint32_t w = 0;
+            if (r < rows && col < p.N) {
+                if constexpr (OB == 4) {
+                    w = static_cast<const uint32_t *>(p.e.r)[(row0 + r) * p.e.ldr + col];
+                } else {
+                    const uint16_t *src = static_cast<const uint16_t *>(p.e.r) + (row0 + r) * p.e.ldr + col;
+                    w = src[0];
+                    if (col + 1 < p.N) w |= uint32_t(src[1]) << 16;
+                }
+            }
+            st_shared_s32(buf(b) + swz128(r, lane >> 2) + (lane & 3) * 4, int32_t(w));
+        }
+        __syncwarp();
+    }
+
+    // Buffer b -> 32 rows x CHUNK columns of `dst`, by TMA or plain stores.
+    __device__ __forceinline__ void store(int b, void *dst, int64_t ld, const CUtensorMap *map, bool tma, int64_t row0,
+                                          int64_t col0) {
+        if (tma) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (row0 < p.M && col0 < p.N)
+                    tma_store_2d_hint(map, buf(b), int32_t(col0), int32_t(row0), l2_policy_evict_normal());
+                bulk_commit_group();
+            }
+            return;
+        }
+        __syncwarp();
+        const int64_t rows = p.M - row0;
+        constexpr int PER_LANE = CHUNK / 32;
+        const int64_t col = col0 + PER_LANE * lane;
+        if (col < p.N) {
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r) {
+                const uint32_t w = ld_shared_b32(buf(b) + swz128(r, lane >> 2) + (lane & 3) * 4);
+                if (r >= rows || !G16_CHECK(row0 + r < p.M && col >= 0)) continue;
+                if constexpr (OB == 4) {
+                    static_cast<uint32_t *>(dst)[(row0 + r) * ld + col] = w;
+                } else {
+                    uint16_t *d = static_cast<uint16_t *>(dst) + (row0 + r) * ld + col;
+                    d[0] = uint16_t(w & 0xffffu);
+                    if (col + 1 < p.N) d[1] = uint16_t(w >> 16);
+                }
+            }
+        }
+        __syncwarp();  // every lane has read the buffer
+        fence_proxy_async_smem();  // before a TMA fetch writes it
+    }
+
+    // x -> units of this lane's row of buffer b; `half` of the chunk (16-bit: two halves of 32 columns)
+    __device__ __forceinline__ void put(int b, int half, const float (&x)[32]) {
+        if constexpr (OB == 4) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                st_shared_v4(buf(b) + swz128(lane, u), __float_as_uint(x[4 * u]), __float_as_uint(x[4 * u + 1]),
+                             __float_as_uint(x[4 * u + 2]), __float_as_uint(x[4 * u + 3]));
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                st_shared_v4(buf(b) + swz128(lane, 4 * half + u), pack_16x2(x[8 * u], x[8 * u + 1], p.e.type),
+                             pack_16x2(x[8 * u + 2], x[8 * u + 3], p.e.type),
+                             pack_16x2(x[8 * u + 4], x[8 * u + 5], p.e.type),
+                             pack_16x2(x[8 * u + 6], x[8 * u + 7], p.e.type));
+        }
+    }
+
+    __device__ __forceinline__ void add_residual(int b, int half, float (&x)[32]) {
+        if constexpr (OB == 4) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                uint32_t w[4];
+                ld_shared_v4(buf(b) + swz128(lane, u), w[0], w[1], w[2], w[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[4 * u + i] += __uint_as_float(w[i]);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                uint32_t w[4];
+                ld_shared_v4(buf(b) + swz128(lane, 4 * half + u), w[0], w[1], w[2], w[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack_16x2(w[i], p.e.type);
+                    x[8 * u + 2 * i] += f.x;
+                    x[8 * u + 2 * i + 1] += f.y;
+                }
+            }
+        }
+    }
+
+    // One tile: rows row0 .. row0 + 31, columns col0 .. col0 + 127. `next`: the
+    // same for this warp's next tile (next_row0 < 0: none). False if a wait ran out.
+    template <typename Drained>
+    __device__ __forceinline__ bool tile(uint32_t t_addr, int64_t row0, int64_t col0, int64_t next_row0,
+                                         int64_t next_col0, const float (&bias)[4], const float (&sb)[4], float sa,
+                                         Drained drained) {
+        const bool has_r = p.e.r != nullptr, has_p = p.e.pre != nullptr, pref = prefetches();
+        const bool two = p.bufs == 2;
+        bool ok = true;
+        uint32_t v[2][32];
+        tmem_ld_32x32b_x32(t_addr, v[0]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = j * 32 / CHUNK;
+            const int half = OB == 4 ? 0 : (j & 1);
+            const int b = has_p ? 1 : (two ? (c & 1) : 0);  // C's buffer; pre's is 0
+            tmem_ld_wait();
+            if (j < 3) tmem_ld_32x32b_x32(t_addr + (j + 1) * 32, v[(j + 1) & 1]);
+            else drained();
+            if (half == 0) {  // the buffers of a new chunk
+                if (pref) {  // two buffers, taken in turn
+                    if (!__all_sync(0xffffffffu, mbar_wait(rbar + 8u * (c & 1), r_used[c & 1] & 1u, p.wait))) ok = false;
+                    else ++r_used[c & 1];
+                } else {
+                    // the buffer's previous store has read it; with two buffers taken in turn,
+                    // only the store before the last must have (pre and C go out as two stores)
+                    if (lane == 0) {
+                        if (two && !has_p) bulk_wait_group_read<1>();
+                        else bulk_wait_group_read<0>();
+                    }
+                    __syncwarp();
+                    if (has_r) load_residual(b, row0, col0 + c * CHUNK);
+                }
+            }
+            float x[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[j & 1][i]);
+            if constexpr (kF8) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] *= sa * __shfl_sync(0xffffffffu, sb[j], i);
+            }
+            if (p.e.bias != nullptr) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] += __shfl_sync(0xffffffffu, bias[j], i);
+            }
+            if (has_p) put(0, half, x);
+            apply_act(p.e.act, x);
+            if (has_r) add_residual(b, half, x);
+            put(b, half, x);
+            if (half == (OB == 4 ? 0 : 1)) {
+                if (has_p) store(0, p.e.pre, p.e.ldp, tmP, p.e.p_tma != 0, row0, col0 + c * CHUNK);
+                store(b, p.e.c, p.e.ldc, tmC, p.e.c_tma != 0, row0, col0 + c * CHUNK);
+                if (pref) {  // refill this buffer for the chunk after the next, of this tile or the next one
+                    const int cn = c + 2;
+                    const bool here = cn < PER_TILE;
+                    if (here || next_row0 >= 0) {
+                        if (lane == 0) bulk_wait_group_read<0>();
+                        __syncwarp();
+                        fetch_residual(c & 1, here ? row0 : next_row0,
+                                       (here ? col0 : next_col0) + (here ? cn : cn - PER_TILE) * CHUNK);
+                    }
+                }
+            }
+        }
+        return ok;
+    }
+
+    // Before the first tile.
+    __device__ __forceinline__ void begin(int64_t row0, int64_t col0) {
+        r_issued[0] = r_issued[1] = r_used[0] = r_used[1] = 0;
+        if (!prefetches()) return;
+        fetch_residual(0, row0, col0);
+        fetch_residual(1, row0, col0 + CHUNK);
+    }
+
+    // After the last tile, or after a wait ran out: no copy may still be on its
+    // way into or out of this warp's buffers when the CTA ends.
+    __device__ __forceinline__ void end() {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+            while (r_used[b] < r_issued[b]) {
+                mbar_wait_slow(rbar + 8u * b, r_used[b] & 1u, cleanup_wait(p.wait), false);
+                ++r_used[b];
+            }
+        if (lane == 0) bulk_wait_group<0>();
+        __syncwarp();
+    }
+};
+
+template <bool kF8, int OB>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1)
+    linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmR,
+                const __grid_constant__ CUtensorMap tmP, const LinearParams p) {
+    constexpr int MAXST = lin::PAIR_STAGES;
+    constexpr int BKE = kF8 ? 128 : 64;  // K per stage, elements
+    constexpr int MMA_WARP = 1, EPI_WARP0 = 2;
+    const int NST = p.stages;
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;  // same offset in both CTAs
+    uint8_t *smem = smem_raw + (base - raw);
+    const uint32_t sA = base;
+    const uint32_t sB = base + uint32_t(NST) * pair::A_STAGE_BYTES;
+    const uint32_t sE = base + uint32_t(NST) * lin::STAGE_BYTES;
+    const uint32_t bar0 = base + lin::PAIR_OFF_BAR;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (MAXST + s); };
+    auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * MAXST + a); };
+    auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * MAXST + NUM_ACC + a); };
+    auto tdone_bar = [&](int a) { return bar0 + 8u * (2 * MAXST + 2 * NUM_ACC + a); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * MAXST + 3 * NUM_ACC);
+    const uint32_t res_bar0 = drain_bar + 8u;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + lin::PAIR_OFF_SLOT);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();  // 0: issues the MMAs
+    const int32_t pair_id = int32_t(blockIdx.x >> 1);
+    const int32_t num_pairs = int32_t(gridDim.x >> 1);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < MAXST; ++s) {
+            mbar_init(full_bar(s), 1);   // CTA 0's arrive.expect_tx, both CTAs' bytes
+            mbar_init(empty_bar(s), 1);  // CTA 0's MMA commit (multicast)
+        }
+        for (int a = 0; a < NUM_ACC; ++a) {
+            mbar_init(tfull_bar(a), 1);               // CTA 0's MMA commit (multicast)
+            mbar_init(tempty_bar(a), EPI_WARPS + 1);  // CTA 0's epilogue warps, CTA 1's relay
+            mbar_init(tdone_bar(a), EPI_WARPS);       // this CTA's epilogue warps
+        }
+        mbar_init(drain_bar, 1);
+        for (int i = 0; i < 2 * EPI_WARPS; ++i) mbar_init(res_bar0 + 8u * i, 1);
+        fence_mbar_init();
+    }
+    if (warp == MMA_WARP) {  // one warp in each CTA of the pair, collectively
+        tmem_alloc_pair(smem_addr(tmem_slot), TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+    }
+    if (warp == EPI_WARP0 && lane == 0) {
+        if (p.e.c_tma) prefetch_tensormap(&tmC);
+        if (p.e.r_tma) prefetch_tensormap(&tmR);
+        if (p.e.p_tma) prefetch_tensormap(&tmP);
+    }
+    tc_fence_before();
+    cluster_sync();  // barriers initialised and TMEM allocated in both CTAs
+    tc_fence_after();
+    // The set-up above may overlap the end of the previous kernel on the
+    // stream; nothing below touches global memory before that kernel is done.
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t tmem_base = *tmem_slot;
+    const int32_t num_kb = p.num_kb;
+
+    if (warp == 0) {
+        // ============================================================ producer (both CTAs)
+        uint32_t stage = 0, phase = 0, issued = 0;
+        bool ok = true;
+        const int na = p.a_mn ? pair::CTA_M / MN_CHUNK : 1;  // copies of A per stage
+        const int nb = p.b_mn ? pair::CTA_N / MN_CHUNK : 1;  // copies of B per stage
+        for (int32_t u = pair_id; ok && u < p.num_tiles; u += num_pairs) {
+            int32_t tm, tn;
+            tile_coords(u, p.sched, tm, tn);
+            const int32_t m0 = tm * pair::TILE_M + int32_t(rank) * pair::CTA_M;
+            const int32_t n0 = tn * pair::TILE_N + int32_t(rank) * pair::CTA_N;
+            for (int32_t kb = 0; kb < num_kb; ++kb) {
+                if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, p.wait))) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0 && rank == 0) mbar_arrive_expect_tx(full_bar(stage), pair::PAIR_TX_BYTES);
+                const uint32_t fb = mapa_shared(full_bar(stage), 0);
+                const int32_t k0 = kb * BKE;
+                if (lane < na + nb) {  // lane: copy `lane` of A, or copy `lane - na` of B
+                    const bool is_a = lane < na;
+                    const int c = is_a ? lane : lane - na;
+                    const uint32_t dst = (is_a ? sA + stage * pair::A_STAGE_BYTES : sB + stage * pair::B_STAGE_BYTES) +
+                                         uint32_t(c) * MN_CHUNK_BYTES;
+                    const bool mn_major = (is_a ? p.a_mn : p.b_mn) != 0;
+                    const int32_t mn = (is_a ? m0 : n0) + c * MN_CHUNK;
+                    tma_load_2d_pair(dst, is_a ? &tmA : &tmB, mn_major ? mn : k0, mn_major ? k0 : mn, fb);
+                }
+                ++issued;
+                if (++stage == uint32_t(NST)) { stage = 0; phase ^= 1u; }
+            }
+        }
+        if (!ok && lane == 0) {
+            if (rank == 0) {
+                // Let the copies counted on this CTA's barriers land before exiting.
+                const uint32_t n = issued < uint32_t(NST) ? issued : uint32_t(NST);
+                for (uint32_t q = issued - n; q < issued; ++q)
+                    mbar_wait_slow(full_bar(q % NST), (q / NST) & 1u, cleanup_wait(p.wait), false);
+            } else {
+                // The peer's copies count on CTA 0's barriers, which it cannot wait on; give
+                // copies already issued time to land (16 KiB reads, microseconds at most).
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 200000ull) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == MMA_WARP) {
+        if (rank == 1) {
+            // ======================================================== relay (CTA 1)
+            // One release at cluster scope per tile tells CTA 0 that all of this CTA's
+            // epilogue warps have drained the accumulator.
+            int32_t it = 0;
+            for (int32_t u = pair_id; u < p.num_tiles; u += num_pairs, ++it) {
+                const uint32_t acc = it & 1;
+                if (!__all_sync(0xffffffffu, mbar_wait(tdone_bar(acc), (uint32_t(it) >> 1) & 1u, p.wait))) break;
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
+                __syncwarp();
+            }
+        } else {
+            // ======================================================== MMA issuer (CTA 0)
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            int32_t it = 0;
+            const DescStep da = make_desc_step(sA, p.a_mn, pair::A_STAGE_BYTES);
+            const DescStep db = make_desc_step(sB, p.b_mn, pair::B_STAGE_BYTES);
+            const uint32_t idesc = p.idesc;
+            for (int32_t u = pair_id; ok && u < p.num_tiles; u += num_pairs, ++it) {
+                const uint32_t acc = it & 1, use = it >> 1;
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(tempty_bar(acc), (use & 1u) ^ 1u, p.wait))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + acc * pair::TILE_N;
+                for (int32_t kb = 0; kb < num_kb; ++kb) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, p.wait))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t a0 = da.base + stage * da.stage;
+                    const uint64_t b0 = db.base + stage * db.stage;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {  // 32 bytes of K each
+                        if constexpr (kF8)
+                            mma_f8_pair_elect(d_tmem, a0 + ks * da.k16, b0 + ks * db.k16, idesc, (kb | ks) != 0 ? 1u : 0u);
+                        else
+                            mma_f16_pair_elect(d_tmem, a0 + ks * da.k16, b0 + ks * db.k16, idesc, (kb | ks) != 0 ? 1u : 0u);
+                    }
+                    mma_commit_pair_mc_elect(empty_bar(stage), 0x3);  // both CTAs' slots reusable
+                    if (++stage == uint32_t(NST)) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                mma_commit_pair_mc_elect(tfull_bar(acc), 0x3);  // both halves of the tile complete
+            }
+            mma_commit_pair_elect(drain_bar);
+            __all_sync(0xffffffffu, mbar_wait_slow(drain_bar, 0, cleanup_wait(p.wait), false));
+        }
+    } else {
+        // ============================================================ epilogue (both CTAs)
+        const int q = warp & 3;  // TMEM lane quarter this warp may access
+        const int ew = warp - EPI_WARP0;
+        const int half = ew / 4;  // columns [128 half, 128 half + 128) of the tile
+        PairEpilogue<kF8, OB> ep{p, &tmC, &tmR, &tmP, sE + uint32_t(ew) * uint32_t(p.bufs) * lin::BUF_BYTES,
+                                 res_bar0 + 16u * ew, lane, {0, 0}, {0, 0}};
+        auto place = [&](int32_t u, int64_t &row0, int64_t &col0) {
+            int32_t tm, tn;
+            tile_coords(u, p.sched, tm, tn);
+            row0 = int64_t(tm) * pair::TILE_M + int64_t(rank) * pair::CTA_M + q * 32;
+            col0 = int64_t(tn) * pair::TILE_N + half * 128;
+        };
+        int64_t row0 = -1, col0 = 0;
+        if (pair_id < p.num_tiles) {
+            place(pair_id, row0, col0);
+            ep.begin(row0, col0);
+        }
+        int32_t it = 0;
+        for (int32_t u = pair_id; u < p.num_tiles; u += num_pairs, ++it) {
+            const uint32_t acc = it & 1, use = it >> 1;
+            int64_t nrow = -1, ncol = 0;
+            if (u + num_pairs < p.num_tiles) place(u + num_pairs, nrow, ncol);
+            // column factors and the row's, one column of each 32 per lane
+            float bias[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {1.f, 1.f, 1.f, 1.f}, sa = 1.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int64_t col = col0 + 32 * j + lane;
+                if (col < p.N) {
+                    if (p.e.bias != nullptr) bias[j] = load_elem(p.e.bias, p.e.bias_type, col);
+                    if (kF8) sb[j] = p.e.sb[col];
+                }
+            }
+            if (kF8 && row0 + lane < p.M) sa = p.e.sa[row0 + lane];
+            if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), use & 1u, p.wait))) break;
+            tc_fence_after();
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(tdone_bar(acc));
+                    if (rank == 0) mbar_arrive(tempty_bar(acc));  // the MMA warp is in this CTA
+                }
+            };
+            if (!ep.tile(tmem_base + (uint32_t(q * 32) << 16) + acc * pair::TILE_N + half * 128, row0, col0, nrow, ncol,
+                         bias, sb, sa, release))
+                break;
+            row0 = nrow;
+            col0 = ncol;
+        }
+        ep.end();
+    }
+
+    // ---------------------------------------------------------------- teardown
+    tc_fence_before();
+    cluster_sync();  // no CTA leaves while its peer may still use its smem or barriers
+    if (warp == MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+}
+
+// ================================================================== linear_split
+namespace lin {
+constexpr int SPLIT_THREADS = (2 + EPI_WARPS) * 32;
+constexpr int SPLIT_ROWS = 128;                     // columns of C per CTA (TMEM lanes)
+constexpr int W_STAGE_BYTES = SPLIT_ROWS * 128;     // 16 KiB
+constexpr int SPLIT_MAX_STAGES = 8;
+constexpr int MAX_SPLIT = 8;
+// full[S], empty[S], done
+constexpr int SPLIT_BARS = 2 * SPLIT_MAX_STAGES + 1;
+constexpr int split_ring(int stages, int T) { return stages * (W_STAGE_BYTES + T * 128); }
+constexpr int split_smem(int stages, int T) { return split_ring(stages, T) + SPLIT_BARS * 8 + 16 + 1024; }
+}  // namespace lin
+
+__device__ __forceinline__ float4 ld_dsmem_v4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
+}
+
+// The epilogue on one value of C.
+__device__ __forceinline__ float act_one(uint32_t act, float x) {
+    float v[1] = {x};
+    apply_act(act, v);
+    return v[0];
+}
+
+// Cluster of p.split CTAs (1..8) along x, all on the same tile; CTA r sums the
+// k-blocks [r num_kb / split, (r + 1) num_kb / split).
+template <bool kF8>
+__global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
+    linear_split(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const LinearParams p) {
+    constexpr int BKE = kF8 ? 128 : 64;
+    constexpr int MMA_WARP = 1, EPI_WARP0 = 2;
+    const int NST = p.stages, T = p.T;
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;  // same offset in every CTA of the cluster
+    uint8_t *smem = smem_raw + (base - raw);
+    const uint32_t x_stage = uint32_t(T) * 128u;
+    const uint32_t sW = base;
+    const uint32_t sX = base + uint32_t(NST) * lin::W_STAGE_BYTES;
+    const uint32_t ring = uint32_t(NST) * (lin::W_STAGE_BYTES + x_stage);
+    const uint32_t bar0 = base + ring;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (lin::SPLIT_MAX_STAGES + s); };
+    const uint32_t done_bar = bar0 + 8u * (2 * lin::SPLIT_MAX_STAGES);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + ring + lin::SPLIT_BARS * 8);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int S = p.split;
+    const uint32_t rank = S > 1 ? cluster_ctarank() : 0u;
+    // rows of C vary fastest, so that the CTAs sharing weights run together
+    const int32_t tile = int32_t(blockIdx.x) / S;
+    const int32_t tn = tile / p.sched.nm, tm = tile - tn * p.sched.nm;
+    const int32_t m0 = tm * T, n0 = tn * lin::SPLIT_ROWS;
+    const int32_t kb0 = int32_t(int64_t(p.num_kb) * rank / S), kb1 = int32_t(int64_t(p.num_kb) * (rank + 1) / S);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NST; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(done_bar, 1);
+        fence_mbar_init();
+    }
+    if (warp == MMA_WARP) {
+        tmem_alloc(smem_addr(tmem_slot), uint32_t(p.tmem_cols));
+        tmem_relinquish();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmX);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_wait();
+    griddep_launch_dependents();
+    const uint32_t tmem_base = *tmem_slot;
+    bool ready = false;  // epilogue warps: the accumulator is complete
+
+    if (warp == 0) {
+        // ============================================================ producer
+        uint32_t stage = 0, phase = 0, issued = 0;
+        bool ok = true;
+        const int nw = p.b_mn ? lin::SPLIT_ROWS / MN_CHUNK : 1;
+        const int nx = p.a_mn ? T / MN_CHUNK : 1;
+        for (int32_t kb = kb0; kb < kb1; ++kb) {
+            if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, p.wait))) {
+                ok = false;
+                break;
+            }
+            const uint32_t fb = full_bar(stage);
+            if (lane == 0) mbar_arrive_expect_tx(fb, lin::W_STAGE_BYTES + x_stage);
+            __syncwarp();
+            const int32_t k0 = kb * BKE;
+            if (lane < nw + nx) {  // lane: copy `lane` of the weights, or copy `lane - nw` of the tokens
+                const bool is_w = lane < nw;
+                const int c = is_w ? lane : lane - nw;
+                const uint32_t dst = (is_w ? sW + stage * lin::W_STAGE_BYTES : sX + stage * x_stage) + uint32_t(c) * MN_CHUNK_BYTES;
+                const bool mn_major = (is_w ? p.b_mn : p.a_mn) != 0;
+                const int32_t mn = (is_w ? n0 : m0) + c * MN_CHUNK;
+                tma_load_2d(dst, is_w ? &tmW : &tmX, mn_major ? mn : k0, mn_major ? k0 : mn, fb);
+            }
+            ++issued;
+            if (++stage == uint32_t(NST)) { stage = 0; phase ^= 1u; }
+        }
+        if (!ok && lane == 0) {  // let the copies this warp started land before the CTA exits
+            const uint32_t n = issued < uint32_t(NST) ? issued : uint32_t(NST);
+            for (uint32_t q = issued - n; q < issued; ++q)
+                mbar_wait_slow(full_bar(q % NST), (q / NST) & 1u, cleanup_wait(p.wait), false);
+        }
+        __syncwarp();
+    } else if (warp == MMA_WARP) {
+        // ============================================================ MMA issuer
+        uint32_t stage = 0, phase = 0;
+        const DescStep dw = make_desc_step(sW, p.b_mn, lin::W_STAGE_BYTES);
+        const DescStep dx = make_desc_step(sX, p.a_mn, x_stage);
+        const uint32_t idesc = p.idesc;
+        for (int32_t kb = kb0; kb < kb1; ++kb) {
+            if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, p.wait))) break;
+            tc_fence_after();
+            const uint64_t w0 = dw.base + stage * dw.stage;
+            const uint64_t x0 = dx.base + stage * dx.stage;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                const uint32_t accumulate = kb != kb0 || ks != 0 ? 1u : 0u;
+                if constexpr (kF8) mma_f8_elect(tmem_base, w0 + ks * dw.k16, x0 + ks * dx.k16, idesc, accumulate);
+                else mma_f16_elect(tmem_base, w0 + ks * dw.k16, x0 + ks * dx.k16, idesc, accumulate);
+            }
+            mma_commit_elect(empty_bar(stage));
+            if (++stage == uint32_t(NST)) { stage = 0; phase ^= 1u; }
+        }
+        // also what the epilogue waits for; after a wait that ran out, no MMA may
+        // still be writing TMEM when it is freed
+        mma_commit_elect(done_bar);
+        __all_sync(0xffffffffu, mbar_wait_slow(done_bar, 0, cleanup_wait(p.wait), false));
+    } else {
+        // ============================================================ epilogue
+        const int q = warp & 3;
+        const int ew = warp - EPI_WARP0;
+        const int half = ew / 4;
+        ready = __all_sync(0xffffffffu, mbar_wait(done_bar, 0, p.wait));
+        tc_fence_after();
+        if (ready) {
+            // two warps per TMEM lane quarter: rows [0, T/2) and [T/2, T) of the tile
+            const int t0 = half * (T / 2), t1 = t0 + T / 2;
+            const int col = q * 32 + lane;  // column of the tile
+            const int64_t n = int64_t(n0) + col;
+            const int valid = int(p.M - m0 < T ? p.M - m0 : T);
+            const bool col_ok = n < p.N;
+            const float bias = S == 1 && col_ok && p.e.bias != nullptr ? load_elem(p.e.bias, p.e.bias_type, n) : 0.0f;
+            const float sb = kF8 && S == 1 && col_ok ? p.e.sb[n] : 1.0f;
+            for (int t = t0; t < t1 && t < valid; t += 32) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tmem_base + (uint32_t(q * 32) << 16) + min(t, p.tmem_cols - 32), v);
+                tmem_ld_wait();
+                const int lead = t - min(t, p.tmem_cols - 32);  // T = 16: columns 8.. of the one 32-column load
+                const int cnt = min(32, min(t1, valid) - t);
+                if (S > 1) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i >= lead && i - lead < cnt)
+                            st_shared_s32(base + uint32_t((t - lead + i) * lin::SPLIT_ROWS + col) * 4u, int32_t(v[i]));
+                } else {
+                    float x[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        x[i] = __uint_as_float(v[i]);
+                        if (kF8) x[i] *= sb * (i >= lead && i - lead < cnt ? p.e.sa[m0 + t - lead + i] : 1.0f);
+                        x[i] += bias;
+                    }
+                    if (p.e.pre != nullptr) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (col_ok && i >= lead && i - lead < cnt)
+                                store_elem(p.e.pre, p.e.type, int64_t(m0 + t - lead + i) * p.e.ldp + n, x[i]);
+                    }
+                    apply_act(p.e.act, x);
+                    if (p.e.r != nullptr) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (col_ok && i >= lead && i - lead < cnt)
+                                x[i] += load_elem(p.e.r, p.e.type, int64_t(m0 + t - lead + i) * p.e.ldr + n);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (col_ok && i >= lead && i - lead < cnt && G16_CHECK(m0 + t - lead + i < p.M))
+                            store_elem(p.e.c, p.e.type, int64_t(m0 + t - lead + i) * p.e.ldc + n, x[i]);
+                }
+            }
+        }
+        tc_fence_before();
+    }
+
+    // ---------------------------------------------------------------- the cluster's sum
+    if (S > 1) {
+        __syncwarp();
+        cluster_sync();  // every CTA's partial tile is in its shared memory
+        if (ready) {
+            const int ew = warp - EPI_WARP0;
+            const int valid = int(p.M - m0 < T ? p.M - m0 : T);
+            const int64_t n = int64_t(n0) + lane * 4;
+            const int cols = n < p.N ? int(p.N - n < 4 ? p.N - n : 4) : 0;
+            const bool vec = p.e.vec4 && cols == 4;
+            float bias[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i < cols && p.e.bias != nullptr) bias[i] = load_elem(p.e.bias, p.e.bias_type, n + i);
+                if (kF8 && i < cols) sb[i] = p.e.sb[n + i];
+            }
+            // row t of the tile belongs to CTA t % S, and there to warp (t / S) % 8
+            for (int t = int(rank) + S * ew; t < valid; t += S * EPI_WARPS) {
+                const uint32_t at = base + uint32_t(t * lin::SPLIT_ROWS + lane * 4) * 4u;
+                float4 part[lin::MAX_SPLIT];
+#pragma unroll
+                for (int s = 0; s < lin::MAX_SPLIT; ++s)
+                    if (s < S) part[s] = ld_dsmem_v4(mapa_shared(at, uint32_t(s)));
+                float x[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
+#pragma unroll
+                for (int s = 1; s < lin::MAX_SPLIT; ++s)
+                    if (s < S) {
+                        x[0] += part[s].x;
+                        x[1] += part[s].y;
+                        x[2] += part[s].z;
+                        x[3] += part[s].w;
+                    }
+                const int64_t m = int64_t(m0) + t;
+                const float sa = kF8 ? p.e.sa[m] : 1.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = (kF8 ? x[i] * (sa * sb[i]) : x[i]) + bias[i];
+                auto put = [&](void *dst, int64_t ld) {
+                    if (vec && p.e.type == 0) {
+                        *reinterpret_cast<float4 *>(static_cast<float *>(dst) + m * ld + n) = make_float4(x[0], x[1], x[2], x[3]);
+                    } else if (vec) {
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst) + m * ld + n) =
+                            make_uint2(pack_16x2(x[0], x[1], p.e.type), pack_16x2(x[2], x[3], p.e.type));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (i < cols && G16_CHECK(m < p.M && n + i < p.N)) store_elem(dst, p.e.type, m * ld + n + i, x[i]);
+                    }
+                };
+                if (p.e.pre != nullptr) put(p.e.pre, p.e.ldp);
+                apply_act(p.e.act, x);
+                if (p.e.r != nullptr) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < cols) x[i] += load_elem(p.e.r, p.e.type, m * p.e.ldr + n + i);
+                }
+                put(p.e.c, p.e.ldc);
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while others read its shared memory
+    } else {
+        __syncwarp();
+        __syncthreads();
+    }
+    if (warp == MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, uint32_t(p.tmem_cols));
+    }
+}
+
+// ================================================================== K = 0
+// The sum is empty: C = act(bias) + R.
+__global__ void linear_empty_kernel(const LinearParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t total = p.M * p.N;
+    for (int64_t e = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; e < total; e += int64_t(gridDim.x) * blockDim.x) {
+        const int64_t i = e / p.N, j = e - i * p.N;
+        float x = p.e.bias != nullptr ? load_elem(p.e.bias, p.e.bias_type, j) : 0.0f;
+        if (p.e.pre != nullptr) store_elem(p.e.pre, p.e.type, i * p.e.ldp + j, x);
+        x = act_one(p.e.act, x);
+        if (p.e.r != nullptr) x += load_elem(p.e.r, p.e.type, i * p.e.ldr + j);
+        store_elem(p.e.c, p.e.type, i * p.e.ldc + j, x);
+    }
+}
+
+// ================================================================== 8-bit operand copies
+// Rows of `inner` bytes, any base and pitch -> rows on 128-byte lines (dst 128-byte
+// aligned, ld_dst a multiple of 128), zero past `inner`. One 16-byte granule of
+// the copy per thread and step, from the one or two aligned source granules that
+// hold its bytes (a granule is read only when it holds a byte of the row).
+struct PackBytesJob {
+    const uint8_t *src;
+    uint8_t *dst;
+    int64_t rows, inner, ld_src, ld_dst;
+    int64_t gpr, granules;  // granules per row; rows * gpr, or 0: not copied
+};
+
+__global__ void pack_bytes_kernel(PackBytesJob a, PackBytesJob b) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t total = a.granules + b.granules;
+    for (int64_t e = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; e < total; e += int64_t(gridDim.x) * blockDim.x) {
+        const bool second = e >= a.granules;
+        const PackBytesJob &J = second ? b : a;
+        const int64_t f = second ? e - a.granules : e;
+        const int64_t r = f / J.gpr, i0 = (f - r * J.gpr) * 16;
+        if (!G16_CHECK(r < J.rows && i0 < J.inner)) continue;
+        const int64_t left = J.inner - i0;
+        const uint32_t cnt = left < 16 ? uint32_t(left) : 16u;
+        const uintptr_t s = reinterpret_cast<uintptr_t>(J.src + r * J.ld_src + i0);
+        const uintptr_t g0 = s & ~uintptr_t(15);
+        const uint32_t m = uint32_t(s - g0);
+        uint32_t w[9];
+        const uint4 lo = *reinterpret_cast<const uint4 *>(g0);
+        w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
+        uint4 hi = make_uint4(0u, 0u, 0u, 0u);
+        if (m + cnt > 16) hi = *reinterpret_cast<const uint4 *>(g0 + 16);
+        w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w, w[8] = 0u;
+        uint32_t x[7], y[5], o[4];
+#pragma unroll
+        for (int t = 0; t < 7; ++t) x[t] = (m & 8u) ? w[t + 2] : w[t];
+#pragma unroll
+        for (int t = 0; t < 5; ++t) y[t] = (m & 4u) ? x[t + 1] : x[t];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            o[t] = __funnelshift_r(y[t], y[t + 1], (m & 3u) * 8u);
+            const int keep = int(cnt) - 4 * t;  // bytes of this word inside the row
+            if (keep <= 0) o[t] = 0u;
+            else if (keep < 4) o[t] &= (1u << (8 * keep)) - 1u;
+        }
+        *reinterpret_cast<uint4 *>(J.dst + r * J.ld_dst + i0) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+// ================================================================== backward, elementwise part
+// D = G act'(P) and the column sums of D over blocks of rows. A block is 32
+// lanes x 8 row groups on a strip of 256 columns (8 per lane); the sums use D
+// before its rounding.
+struct GradParams {
+    const void *g, *pre;  // pre == nullptr: D = G
+    void *d;              // nullptr: not stored
+    float *partial;       // [gridDim.y][N] or nullptr
+    int64_t M, N, ldg, ldp, ldd;
+    int64_t rows_per_block;
+    uint32_t act;
+};
+constexpr int kGradGroups = 8;
+
+template <uint32_t ACT, typename T, int VEC>
+__device__ __forceinline__ void grad_rows(const GradParams &p, int64_t col, int64_t r0, int64_t r1, float (&sum)[VEC]) {
+    const T *g = static_cast<const T *>(p.g), *pre = static_cast<const T *>(p.pre);
+    T *d = static_cast<T *>(p.d);
+#pragma unroll 4
+    for (int64_t r = r0 + threadIdx.y; r < r1; r += kGradGroups) {
+        const Raw<T, VEC> a = load_raw<T, VEC>(g + r * p.ldg + col);
+        float x[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) x[i] = to_f32<T>(a.v[i]);
+        if constexpr (ACT != kActNone) {
+            const Raw<T, VEC> b = load_raw<T, VEC>(pre + r * p.ldp + col);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) x[i] *= act_slope<ACT>(to_f32<T>(b.v[i]));
+        }
+        if (d != nullptr) store_f32<T, VEC>(d + r * p.ldd + col, x);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sum[i] += x[i];
+    }
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(32 * kGradGroups) linear_grad_kernel(const GradParams p) {
+    __shared__ float s[kGradGroups][32 * VEC + 1];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t col = (int64_t(blockIdx.x) * 32 + threadIdx.x) * VEC;
+    const int64_t r0 = int64_t(blockIdx.y) * p.rows_per_block;
+    const int64_t r1 = r0 + p.rows_per_block < p.M ? r0 + p.rows_per_block : p.M;
+    float sum[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) sum[i] = 0.0f;
+    if (col < p.N) {
+        switch (p.act) {
+            case kActRelu: grad_rows<kActRelu, T, VEC>(p, col, r0, r1, sum); break;
+            case kActGelu: grad_rows<kActGelu, T, VEC>(p, col, r0, r1, sum); break;
+            case kActGeluTanh: grad_rows<kActGeluTanh, T, VEC>(p, col, r0, r1, sum); break;
+            case kActSilu: grad_rows<kActSilu, T, VEC>(p, col, r0, r1, sum); break;
+            default: grad_rows<kActNone, T, VEC>(p, col, r0, r1, sum); break;
+        }
+    }
+    if (p.partial == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s[threadIdx.y][threadIdx.x * VEC + i] = sum[i];
+    __syncthreads();
+    for (int c = threadIdx.y * 32 + threadIdx.x; c < 32 * VEC; c += 32 * kGradGroups) {
+        const int64_t at = int64_t(blockIdx.x) * 32 * VEC + c;
+        if (at >= p.N) continue;
+        float v = s[0][c];
+        for (int y = 1; y < kGradGroups; ++y) v += s[y][c];
+        p.partial[int64_t(blockIdx.y) * p.N + at] = v;
+    }
+}
+
+}  // namespace g16
