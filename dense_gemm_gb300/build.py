@@ -7,12 +7,14 @@ bounds and alignment checks (GEMM_DEBUG) that report GEMM_ERR_CHECK instead of
 trapping. The binding loads it when GEMM_LIBRARY=debug.
 
 One translation unit, one -gencode, static CUDA runtime; no cmake. The same
-command works on x86-64 and aarch64 hosts.
+command works on x86-64 and aarch64 hosts. Beside it, the CPython extension
+_native.so (ops.py's argument marshalling) is built with the host compiler.
 """
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -24,6 +26,9 @@ SOURCES = [os.path.join(CSRC, "library.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_f16.cu", "ops.cu", "gemm_kernel.cuh", "gemm_pair.cuh",
                                                      "ops_linear.cuh", "ops_norm.cuh", "ptx.cuh")] + \
     [os.path.join(INCLUDE, f) for f in ("gemm_f16.h", "gemm_ops.h")]
+
+NATIVE = os.path.join(HERE, "_native.so")
+NATIVE_DEPENDS = [os.path.join(CSRC, "native.cpp")] + [os.path.join(INCLUDE, f) for f in ("gemm_f16.h", "gemm_ops.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -45,15 +50,26 @@ def command(out: str, verbose_ptxas: bool = False, debug: bool = False):
     return cmd
 
 
-def up_to_date(lib: str = LIB) -> bool:
+def up_to_date(lib: str = LIB, depends=None) -> bool:
     if not os.path.exists(lib):
         return False
     t = os.path.getmtime(lib)
-    return all(os.path.getmtime(d) <= t for d in DEPENDS)
+    return all(os.path.getmtime(d) <= t for d in (DEPENDS if depends is None else depends))
+
+
+def build_native(force: bool = False) -> str:
+    if not force and up_to_date(NATIVE, NATIVE_DEPENDS):
+        return NATIVE
+    tmp = NATIVE + f".tmp{os.getpid()}"
+    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
+                    "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-o", tmp, NATIVE_DEPENDS[0]], check=True)
+    os.replace(tmp, NATIVE)
+    return NATIVE
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
     lib = DEBUG_LIB if debug else LIB
+    build_native(force)
     if not force and up_to_date(lib):
         return lib
     tmp = lib + f".tmp{os.getpid()}"

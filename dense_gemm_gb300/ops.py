@@ -1,8 +1,10 @@
-"""ctypes binding of ``include/gemm_ops.h`` (argument marshalling only): the
-product with its epilogue, the root-mean-square norm, and their gradients.
+"""Python side of ``include/gemm_ops.h``: the product with its epilogue, the
+root-mean-square norm, and their gradients.
 
-Outputs and workspaces that are not given are allocated on the stream the
-kernels run on (``stream``, or the current one).
+The arguments are checked and marshalled by the extension ``_native`` (built
+with the library); the arithmetic runs in the library's CUDA kernels. Outputs
+and workspaces that are not given are allocated on the stream the kernels run
+on (``stream``, or the current one).
 """
 import contextlib
 import ctypes
@@ -10,147 +12,66 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .binding import GemmError, _check, load_library  # noqa: F401
+from .binding import GemmError, load_library
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 LINEAR_KERNELS = {"auto": 0, "pair": 1, "split": 2}
 
-_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3}
-_C_TYPES = (torch.float32, torch.float16, torch.bfloat16)
-_OPERANDS = (torch.float16, torch.bfloat16, torch.float8_e4m3fn)
+_ENTRIES = ("gemm_linear", "gemm_linear_workspace_size", "gemm_linear_backward", "gemm_linear_backward_workspace_size",
+            "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_rms_norm_backward_workspace_size")
+
+# the C-level forms of torch.cuda.current_device / current_stream, 0.1 us against 0.3 and 2
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+_module = None
 
 
-class _Matrix(ctypes.Structure):  # gemm_matrix_t
-    _fields_ = [("data", ctypes.c_void_p), ("stride_row", ctypes.c_int64), ("stride_col", ctypes.c_int64),
-                ("type", ctypes.c_int32)]
-
-
-class _Epilogue(ctypes.Structure):  # gemm_epilogue_t
-    _fields_ = [("bias", ctypes.c_void_p), ("bias_type", ctypes.c_int32), ("activation", ctypes.c_int32),
-                ("scale_a", ctypes.c_void_p), ("scale_b", ctypes.c_void_p), ("residual", _Matrix), ("pre", _Matrix)]
-
-
-_ready = None
-
-
-def _lib():
-    global _ready
-    if _ready is not None:
-        return _ready
-    lib = load_library()
-    m, e, vp = ctypes.POINTER(_Matrix), ctypes.POINTER(_Epilogue), ctypes.c_void_p
-    i64, i32, u32, u64, f32 = ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_float
-    pu64 = ctypes.POINTER(u64)
-    lib.gemm_linear.argtypes = [m, m, m, e, i64, i64, i64, u32, vp, u64, vp]
-    lib.gemm_linear_workspace_size.argtypes = [m, m, i64, i64, i64, pu64]
-    lib.gemm_linear_backward.argtypes = [m, m, m, m, i32, m, m, vp, i64, i64, i64, u32, vp, u64, vp]
-    lib.gemm_linear_backward_workspace_size.argtypes = [m, m, m, i32, i32, i64, i64, i64, pu64]
-    lib.gemm_rms_norm.argtypes = [m, m, vp, i32, m, m, vp, vp, i64, i64, f32, vp]
-    lib.gemm_rms_norm_backward.argtypes = [m, m, vp, i32, vp, m, m, vp, i64, i64, vp, u64, vp]
-    lib.gemm_rms_norm_backward_workspace_size.argtypes = [i64, i64, pu64]
-    for name in ("gemm_linear", "gemm_linear_workspace_size", "gemm_linear_backward",
-                 "gemm_linear_backward_workspace_size", "gemm_rms_norm", "gemm_rms_norm_backward",
-                 "gemm_rms_norm_backward_workspace_size"):
-        getattr(lib, name).restype = ctypes.c_int
-    _ready = lib
-    return lib
-
-
-def _matrix(t: Optional[torch.Tensor]) -> _Matrix:
-    """The tensor's gemm_matrix_t. torch gives dimensions of one element any
-    stride, also 0; a stride of 0 elsewhere (an expanded tensor) goes through
-    and is refused."""
-    if t is None:
-        return _Matrix(None, 1, 1, 0)
-    r, c = t.stride()
-    rows, cols = t.shape
-    return _Matrix(t.data_ptr(), r if r or rows > 1 else 1, c if c or cols > 1 else 1, _TYPES[t.dtype])
-
-
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
+def _native():
+    """The marshalling extension, set up for the loaded library (once)."""
+    global _module
+    if _module is None:
+        lib = load_library()
+        try:
+            from . import _native as module
+        except ImportError as e:
+            raise GemmError(3, f"dense_gemm_gb300/_native.so ({e}): build it with `python -m dense_gemm_gb300.build`") from e
+        module.setup({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ENTRIES},
+                     (torch.float32, torch.float16, torch.bfloat16, torch.float8_e4m3fn), torch.uint8, torch.empty, _raw_stream,
+                     GemmError)
+        _module = module
+    return _module
 
 
 @contextlib.contextmanager
-def _other_device(dev):
-    with torch.cuda.device(dev):
+def _current(index: int, stream):
+    """Makes a tensor's device and the call's stream current."""
+    if stream is not None and stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on device {index}")
+    with torch.cuda.device(index), torch.cuda.stream(stream):
         yield
 
 
-class _Here:
-    """Stands in for the device and stream contexts where nothing changes."""
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *a):
-        return False
-
-
-_HERE = _Here()
+def _call(name: str, first: torch.Tensor, stream, args):
+    fn = getattr(_module or _native(), name)
+    index = first.get_device() if isinstance(first, torch.Tensor) else -1
+    if index < 0 or (stream is None and index == _current_device()):
+        return fn(*args)  # a tensor that is not on a GPU is refused there
+    with _current(index, stream):
+        return fn(*args)
 
 
-def _on(dev: torch.device, stream):
-    """(contexts' handle, device context, allocation context): the C entry points
-    act on the current device, and new tensors belong to the stream they are
-    written on."""
-    device = _HERE if torch.cuda.current_device() == dev.index else _other_device(dev)
-    if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream, device, _HERE
-    if stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    return stream.cuda_stream, device, torch.cuda.stream(stream)
-
-
-def _one_device(first: torch.Tensor, *others) -> torch.device:
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError("the operators take CUDA tensors")
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on one CUDA device, got {dev} and {t.device}")
-    return dev
-
-
-def _matrix_like(t, shape, dtype, what):
-    if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
-        raise ValueError(f"{what} must be {dtype} of shape {list(shape)}, got {t.dtype} {list(t.shape)}")
-
-
-def _vector(t, n, dtypes, what):
-    if t is None:
-        return
-    if t.dtype not in dtypes:
-        raise TypeError(f"{what} must be one of {dtypes}, got {t.dtype}")
-    if tuple(t.shape) != (n,) or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{what} must be a contiguous vector of {n} elements, got shape {list(t.shape)}")
-
-
-def _workspace(given, need, dev, what):
-    """(tensor, bytes): the caller's workspace, or one of `need` bytes."""
-    if given is None:
-        given = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        return given, need
-    if given.device != dev:
-        raise ValueError(f"{what}: the workspace is on {given.device}, the tensors on {dev}")
-    return given, given.numel() * given.element_size()
-
-
-def _operands(A, B):
-    if A.dtype not in _OPERANDS or A.dtype != B.dtype:
-        raise TypeError(f"A and B must both be float16, bfloat16 or float8_e4m3fn, got {A.dtype} and {B.dtype}")
-    if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[0]:
-        raise ValueError(f"shapes {tuple(A.shape)} @ {tuple(B.shape)} do not chain")
+def _code(table: dict, key, what: str) -> int:
+    code = table.get(key)
+    if code is None:
+        raise ValueError(f"{what} must be one of {list(table)}, got {key!r}")
+    return code
 
 
 def linear_workspace_size(A: torch.Tensor, B: torch.Tensor) -> int:
     """Workspace bytes of ``linear`` for these operands: 0 where their bases and
     row strides are multiples of 16 bytes."""
-    _operands(A, B)
-    n = ctypes.c_uint64()
-    _check(_lib().gemm_linear_workspace_size(_matrix(A), _matrix(B), A.shape[0], B.shape[1], A.shape[1], n),
-           "gemm_linear_workspace_size")
-    return int(n.value)
+    return _native().linear_workspace_size(A, B)
 
 
 def linear(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor = None, *, activation: str = "none",
@@ -169,49 +90,8 @@ def linear(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor = None, *, activ
     (C, pre) is returned. ``kernel`` chooses between "pair" and "split" by hand
     (gemm_linear in include/gemm_ops.h).
     """
-    _operands(A, B)
-    (M, K), N = A.shape, B.shape[1]
-    eight = A.dtype == torch.float8_e4m3fn
-    if activation not in ACTIVATIONS:
-        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
-    if kernel not in LINEAR_KERNELS:
-        raise ValueError(f"kernel must be one of {list(LINEAR_KERNELS)}, got {kernel!r}")
-    if eight != (scale_a is not None) or eight != (scale_b is not None):
-        raise ValueError("scale_a and scale_b go with float8_e4m3fn operands, and only with them")
-    dtype = out.dtype if out is not None else out_dtype if out_dtype is not None else residual.dtype \
-        if residual is not None else torch.bfloat16 if eight else A.dtype
-    if dtype not in _C_TYPES:
-        raise TypeError(f"C must be float32, float16 or bfloat16, got {dtype}")
-    dev = _one_device(A, B, bias, residual, scale_a, scale_b, out, pre)
-    _matrix_like(out, (M, N), dtype, "out")
-    _matrix_like(residual, (M, N), dtype, "residual")
-    _matrix_like(pre, (M, N), dtype, "pre")
-    _vector(bias, N, (torch.float32, dtype), "bias")
-    _vector(scale_a, M, (torch.float32,), "scale_a")
-    _vector(scale_b, N, (torch.float32,), "scale_b")
-    lib = _lib()
-    handle, device, alloc = _on(dev, stream)
-    a, b = _matrix(A), _matrix(B)
-    need = ctypes.c_uint64()
-    _check(lib.gemm_linear_workspace_size(a, b, M, N, K, need), "gemm_linear")
-    with device, alloc:
-        if out is None:
-            out = torch.empty((M, N), dtype=dtype, device=dev)
-        if pre is None and return_pre:
-            pre = torch.empty((M, N), dtype=dtype, device=dev)
-        ws, ws_bytes = _workspace(workspace, need.value, dev, "linear")
-        ep = _Epilogue(_ptr(bias), _TYPES[bias.dtype] if bias is not None else 0, ACTIVATIONS[activation], _ptr(scale_a),
-                       _ptr(scale_b), _matrix(residual), _matrix(pre))
-        _check(lib.gemm_linear(a, b, _matrix(out), ep, M, N, K, LINEAR_KERNELS[kernel], _ptr(ws), ws_bytes, handle),
-               "gemm_linear")
-    return (out, pre) if pre is not None else out
-
-
-def _empty_like_order(t, dtype):
-    """A new matrix of t's shape, stored by columns where t is (a weight kept as [N, K])."""
-    (r, c), by_columns = t.shape, t.stride(0) == 1 and t.stride(1) != 1
-    return torch.empty((c, r), dtype=dtype, device=t.device).t() if by_columns else \
-        torch.empty((r, c), dtype=dtype, device=t.device)
+    return _call("linear", A, stream, (A, B, bias, _code(ACTIVATIONS, activation, "activation"), residual, scale_a, scale_b, out,
+                                       out_dtype, pre, bool(return_pre), _code(LINEAR_KERNELS, kernel, "kernel"), workspace))
 
 
 def linear_backward(grad: torch.Tensor, A: torch.Tensor, B: torch.Tensor, *, pre: torch.Tensor = None,
@@ -225,38 +105,9 @@ def linear_backward(grad: torch.Tensor, A: torch.Tensor, B: torch.Tensor, *, pre
     and the memory order of A and B; dbias [N] is float32. The residual's
     gradient is ``grad`` itself.
     """
-    _operands(A, B)
-    if A.dtype == torch.float8_e4m3fn:
-        raise TypeError("linear_backward takes float16 or bfloat16 operands")
-    (M, K), N = A.shape, B.shape[1]
-    if activation not in ACTIVATIONS:
-        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
-    if kernel not in LINEAR_KERNELS:
-        raise ValueError(f"kernel must be one of {list(LINEAR_KERNELS)}, got {kernel!r}")
-    if activation != "none" and pre is None:
-        raise ValueError("with an activation, linear_backward needs pre (linear(..., return_pre=True))")
-    if activation == "none":
-        pre = None
-    dtype = A.dtype if grad_dtype is None else grad_dtype
-    if dtype not in _C_TYPES:
-        raise TypeError(f"gradients are float32, float16 or bfloat16, got {dtype}")
-    dev = _one_device(grad, A, B, pre)
-    _matrix_like(grad, (M, N), A.dtype, "grad")
-    _matrix_like(pre, (M, N), A.dtype, "pre")
-    lib = _lib()
-    handle, device, alloc = _on(dev, stream)
-    g, a, b = _matrix(grad), _matrix(A), _matrix(B)
-    act = ACTIVATIONS[activation]
-    need = ctypes.c_uint64()
-    _check(lib.gemm_linear_backward_workspace_size(g, a, b, act, int(need_bias), M, N, K, need), "gemm_linear_backward")
-    with device, alloc:
-        dA = _empty_like_order(A, dtype) if need_a else None
-        dB = _empty_like_order(B, dtype) if need_b else None
-        dbias = torch.empty(N, dtype=torch.float32, device=dev) if need_bias else None
-        ws, ws_bytes = _workspace(workspace, need.value, dev, "linear_backward")
-        _check(lib.gemm_linear_backward(g, a, b, _matrix(pre), act, _matrix(dA), _matrix(dB), _ptr(dbias), M, N, K,
-                                        LINEAR_KERNELS[kernel], _ptr(ws), ws_bytes, handle), "gemm_linear_backward")
-    return dA, dB, dbias
+    return _call("linear_backward", grad, stream, (grad, A, B, pre, _code(ACTIVATIONS, activation, "activation"), bool(need_a),
+                                                   bool(need_b), bool(need_bias), grad_dtype,
+                                                   _code(LINEAR_KERNELS, kernel, "kernel"), workspace))
 
 
 class RmsNormResult(NamedTuple):
@@ -279,30 +130,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor = 
     residual is given; ``h_out`` may be x or residual itself. ``return_rstd``
     keeps 1 / sqrt(mean(h^2) + eps) for ``rms_norm_backward``.
     """
-    if x.dim() != 2 or x.dtype not in _C_TYPES:
-        raise TypeError(f"x must be a float32, float16 or bfloat16 matrix, got {x.dtype} {list(x.shape)}")
-    rows, width = x.shape
-    dtype = out.dtype if out is not None else x.dtype if out_dtype is None else out_dtype
-    if dtype not in (x.dtype, torch.float8_e4m3fn):
-        raise TypeError(f"y has x's type or float8_e4m3fn, got {dtype}")
-    dev = _one_device(x, weight, residual, out, h_out)
-    _vector(weight, width, (torch.float32, x.dtype), "weight")
-    _matrix_like(residual, (rows, width), x.dtype, "residual")
-    _matrix_like(out, (rows, width), dtype, "out")
-    _matrix_like(h_out, (rows, width), x.dtype, "h_out")
-    if h_out is not None and residual is None:
-        raise ValueError("h_out goes with a residual: without one h is x")
-    lib = _lib()
-    handle, device, alloc = _on(dev, stream)
-    with device, alloc:
-        y = out if out is not None else torch.empty((rows, width), dtype=dtype, device=dev)
-        h = None if residual is None else h_out if h_out is not None else \
-            torch.empty((rows, width), dtype=x.dtype, device=dev)
-        scale = torch.empty(rows, dtype=torch.float32, device=dev) if dtype == torch.float8_e4m3fn else None
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev) if return_rstd else None
-        _check(lib.gemm_rms_norm(_matrix(x), _matrix(residual), weight.data_ptr(), _TYPES[weight.dtype], _matrix(y),
-                                 _matrix(h), _ptr(scale), _ptr(rstd), rows, width, eps, handle), "gemm_rms_norm")
-    return RmsNormResult(y, h, scale, rstd)
+    return RmsNormResult._make(_call("rms_norm", x, stream, (x, weight, residual, eps, out_dtype, bool(return_rstd), out, h_out)))
 
 
 def rms_norm_backward(grad: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, *,
@@ -316,25 +144,4 @@ def rms_norm_backward(grad: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     ``out`` may be grad or grad_h itself. dweight is float32 [width], None
     unless ``need_weight``.
     """
-    if h.dim() != 2 or h.dtype not in _C_TYPES:
-        raise TypeError(f"h must be a float32, float16 or bfloat16 matrix, got {h.dtype} {list(h.shape)}")
-    rows, width = h.shape
-    dev = _one_device(h, grad, weight, rstd, grad_h, out)
-    _matrix_like(grad, (rows, width), h.dtype, "grad")
-    _matrix_like(grad_h, (rows, width), h.dtype, "grad_h")
-    _matrix_like(out, (rows, width), h.dtype, "out")
-    _vector(weight, width, (torch.float32, h.dtype), "weight")
-    _vector(rstd, rows, (torch.float32,), "rstd")
-    lib = _lib()
-    handle, device, alloc = _on(dev, stream)
-    need = ctypes.c_uint64()
-    if need_weight:
-        _check(lib.gemm_rms_norm_backward_workspace_size(rows, width, need), "gemm_rms_norm_backward")
-    with device, alloc:
-        dx = out if out is not None else torch.empty((rows, width), dtype=h.dtype, device=dev)
-        dweight = torch.empty(width, dtype=torch.float32, device=dev) if need_weight else None
-        ws, ws_bytes = _workspace(workspace, need.value, dev, "rms_norm_backward")
-        _check(lib.gemm_rms_norm_backward(_matrix(grad), _matrix(h), weight.data_ptr(), _TYPES[weight.dtype], _ptr(rstd),
-                                          _matrix(grad_h), _matrix(dx), _ptr(dweight), rows, width, _ptr(ws), ws_bytes,
-                                          handle), "gemm_rms_norm_backward")
-    return dx, dweight
+    return _call("rms_norm_backward", grad, stream, (grad, h, weight, rstd, grad_h, bool(need_weight), out, workspace))

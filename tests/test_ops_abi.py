@@ -12,21 +12,39 @@ HEADER = os.path.join(ROOT, "include", "gemm_ops.h")
 F32, F16, BF16, E4M3 = 0, 1, 2, 3
 
 
+class _Matrix(C.Structure):  # gemm_matrix_t
+    _fields_ = [("data", C.c_void_p), ("stride_row", C.c_int64), ("stride_col", C.c_int64), ("type", C.c_int32)]
+
+
+class _Epilogue(C.Structure):  # gemm_epilogue_t
+    _fields_ = [("bias", C.c_void_p), ("bias_type", C.c_int32), ("activation", C.c_int32), ("scale_a", C.c_void_p),
+                ("scale_b", C.c_void_p), ("residual", _Matrix), ("pre", _Matrix)]
+
+
 @pytest.fixture(scope="module")
 def lib():
     from dense_gemm_gb300 import build as b
     b.build()
-    from dense_gemm_gb300 import ops
-    return ops._lib()
+    from dense_gemm_gb300 import binding
+    lib = binding.load_library()
+    m, e, vp = C.POINTER(_Matrix), C.POINTER(_Epilogue), C.c_void_p
+    i64, i32, u32, u64, f32 = C.c_int64, C.c_int32, C.c_uint32, C.c_uint64, C.c_float
+    pu64 = C.POINTER(u64)
+    lib.gemm_linear.argtypes = [m, m, m, e, i64, i64, i64, u32, vp, u64, vp]
+    lib.gemm_linear_workspace_size.argtypes = [m, m, i64, i64, i64, pu64]
+    lib.gemm_linear_backward.argtypes = [m, m, m, m, i32, m, m, vp, i64, i64, i64, u32, vp, u64, vp]
+    lib.gemm_linear_backward_workspace_size.argtypes = [m, m, m, i32, i32, i64, i64, i64, pu64]
+    lib.gemm_rms_norm.argtypes = [m, m, vp, i32, m, m, vp, vp, i64, i64, f32, vp]
+    lib.gemm_rms_norm_backward.argtypes = [m, m, vp, i32, vp, m, m, vp, i64, i64, vp, u64, vp]
+    lib.gemm_rms_norm_backward_workspace_size.argtypes = [i64, i64, pu64]
+    return lib
 
 
 def mat(data=256, r=8, c=1, t=F16):
-    from dense_gemm_gb300.ops import _Matrix
     return _Matrix(data, r, c, t)
 
 
 def epilogue(**kw):
-    from dense_gemm_gb300.ops import _Epilogue
     e = _Epilogue(None, 0, 0, None, None, mat(None), mat(None))
     for k, v in kw.items():
         setattr(e, k, v)
@@ -129,13 +147,28 @@ def test_rms_norm_refusals(lib):
     assert lib.gemm_rms_norm_backward_workspace_size(-1, 8, n) == 1
 
 
-def test_binding_passes_strides_as_they_are():
-    """Dimensions of one element may have any stride in torch; elsewhere a stride
-    of 0 (an expanded tensor) reaches the library, which refuses it."""
+def test_binding_checks_before_the_library():
+    """The Python entry points name what is wrong with host tensors, types, shapes
+    and keywords without a GPU."""
     import torch
-    from dense_gemm_gb300.ops import _matrix
-    t = torch.empty(1, 8, dtype=torch.float16)
-    assert (_matrix(t).stride_row, _matrix(t).stride_col) == (8, 1)
-    e = t.expand(4, 8)
-    assert _matrix(e).stride_row == 0
-    assert _matrix(t.as_strided((1, 8), (0, 1))).stride_row == 1
+    from dense_gemm_gb300 import linear, linear_backward, rms_norm, rms_norm_backward
+    z = lambda *s, t=torch.float16: torch.zeros(*s).to(t)  # noqa: E731
+    A, B, E = z(4, 8), z(8, 16), torch.float8_e4m3fn
+    with pytest.raises(ValueError, match="CUDA"):
+        linear(A, B)
+    with pytest.raises(ValueError, match="chain"):
+        linear(A, z(9, 16))
+    with pytest.raises(ValueError, match="activation"):
+        linear(A, B, activation="tanh")
+    with pytest.raises(ValueError, match="scale"):
+        linear(A.to(E), B.to(E))
+    for bad in (lambda: linear(A, z(8, 16, t=torch.bfloat16)), lambda: linear(A.float(), B.float()), lambda: linear(A, 3),
+                lambda: linear(None, B), lambda: linear(A, B, out_dtype=torch.int32), lambda: linear(A, B, 1.0),
+                lambda: linear_backward(None, A, B), lambda: rms_norm(A.double(), z(8)), lambda: rms_norm(A, None),
+                lambda: rms_norm(A, z(8), eps="x"), lambda: rms_norm_backward(A, A, z(8), None)):
+        with pytest.raises((TypeError, ValueError)):
+            bad()
+    with pytest.raises(ValueError, match="CUDA"):
+        rms_norm(A, z(8))
+    with pytest.raises(ValueError, match="CUDA"):
+        rms_norm_backward(A, A, z(8), torch.zeros(4))
