@@ -613,67 +613,115 @@ namespace {
 constexpr int64_t kNormParts = 608;  // blocks of the backward pass at most: 4 per SM
 
 struct RowShape {
-    bool vec;       // 16-byte vectors (8 elements), else single elements
-    int nv;         // loads per thread
-    int tpr, rpb;   // threads per row, rows per block
-    bool fits;      // the row fits its threads' registers
+    int nv;        // loads of 8 elements per thread
+    int tpr, rpb;  // threads per row, rows per block
+    bool fits;     // the row fits its threads' registers
 };
 
-// Threads per row: enough for one load each where possible, at most 1024; short
+// One load per thread where 1024 threads hold the row so, else the fewest; short
 // rows share a block of 256 threads.
-RowShape row_shape(int64_t width, bool vec, const int *nvs, int count) {
-    RowShape s{vec, nvs[0], 32, 1, false};
-    const int64_t v = vec ? 8 : 1;
-    for (int i = 0; i < count; ++i) {
-        s.nv = nvs[i];
-        const int64_t t = cdiv(cdiv(width, v * s.nv), 32) * 32;
-        const int64_t most = i + 1 < count ? 512 : 1024;
-        if (t <= most) {
-            s.tpr = int(t);
-            s.fits = true;
-            break;
-        }
+RowShape row_shape(int64_t width) {
+    RowShape s{1, 32, 1, false};
+    for (int nv : {1, 2, 4}) {
+        const int64_t t = cdiv(cdiv(width, 8 * nv), 32) * 32;
+        if (t > 1024) continue;
+        s.nv = nv;
+        s.tpr = int(t);
+        s.fits = true;
+        break;
     }
     if (s.fits && s.tpr <= 128) s.rpb = 256 / s.tpr;
     return s;
 }
 
-template <typename T>
-cudaError_t launch_norm(const NormParams &p, bool vec, bool quant, cudaStream_t stream) {
-    static const int kVecNv[] = {1, 2, 4}, kOneNv[] = {4, 16, 32};
-    const RowShape s = row_shape(p.width, vec, vec ? kVecNv : kOneNv, 3);
-    if (!s.fits) {
-        if (p.rows > kMaxDim) return cudaErrorInvalidValue;
-        return launch_shape(rms_norm_long_kernel<T>, dim3(unsigned(p.rows)), dim3(1024), 0, 1, stream, p, int32_t(quant));
+// The persistent form's block: 256 threads (rows of up to 8192 elements), else
+// 512; nv is the number of loads of 8 elements per thread. Two blocks of 256
+// share an SM, each with half the shared memory for its ring.
+struct RingPlan {
+    bool ok;
+    int tpr, rpb, nv;  // threads per row, rows per block, loads per thread
+    int smem, grid;
+    RingShape ring;
+};
+
+// `sums`: the backward pass, which adds up dweight over the block's rows: in
+// shared memory behind the ring (any alignment), or, with vectors, in registers
+// and at the end in the ring's place.
+RingPlan ring_plan(int64_t rows, int64_t width, int es, int arrays, bool vec, bool sums, int num_sms) {
+    RingPlan r{};
+    const int threads = width <= 8192 ? 256 : 512;
+    const int64_t loads = cdiv(width, 8);
+    r.nv = int(cdiv(loads, threads));
+    if (r.nv > 4) return r;  // ok stays false
+    r.tpr = int(cdiv(cdiv(loads, r.nv), 32) * 32);
+    while (threads % r.tpr) r.tpr += 32;
+    r.rpb = threads / r.tpr;
+    r.ring.pitch = int((width * es + 15) / 16 * 16 + 16);
+    r.ring.array_bytes = r.rpb * r.ring.pitch;
+    r.ring.slot_bytes = arrays * r.ring.array_bytes;
+    const int blocks_per_sm = threads == 256 ? 2 : 1;
+    const int behind = sums && !vec ? int(r.rpb * width * 4) : 0;
+    const int budget = (blocks_per_sm == 2 ? 113 : 226) * 1024 - 2048 - behind;
+    r.ring.slots = std::min(kRingSlots, budget / r.ring.slot_bytes);
+    if (r.ring.slots < 2) return r;
+    r.smem = r.ring.slots * r.ring.slot_bytes + behind;
+    if (sums && vec && r.rpb > 1) r.smem = std::max(r.smem, r.rpb * r.tpr * 8 * r.nv * 4);
+    r.grid = int(std::min<int64_t>(cdiv(rows, r.rpb), int64_t(blocks_per_sm) * num_sms));
+    r.ok = true;
+    return r;
+}
+
+// Launches one ring kernel; its shared-memory limit is raised by its first
+// launch on a device.
+template <auto Kernel, typename P>
+cudaError_t launch_ring(const RingPlan &r, const P &p, int dev, cudaStream_t stream) {
+    static std::atomic<uint64_t> raised{0};  // one bit per device
+    static_assert(kMaxDevices <= 64, "one bit per device");
+    const uint64_t bit = uint64_t(1) << dev;
+    if (!(raised.load(std::memory_order_acquire) & bit)) {
+        const cudaError_t e = allow_smem(Kernel, 226 * 1024);
+        if (e != cudaSuccess) {
+            (void)cudaGetLastError();
+            return e;
+        }
+        raised.fetch_or(bit, std::memory_order_release);
     }
-    using Kernel = void (*)(const NormParams);
-    Kernel k;
-    if (vec) {
-        k = s.nv == 1 ? (quant ? rms_norm_kernel<T, 8, 1, true> : rms_norm_kernel<T, 8, 1, false>)
-            : s.nv == 2 ? (quant ? rms_norm_kernel<T, 8, 2, true> : rms_norm_kernel<T, 8, 2, false>)
-                        : (quant ? rms_norm_kernel<T, 8, 4, true> : rms_norm_kernel<T, 8, 4, false>);
-    } else {
-        k = s.nv == 4 ? (quant ? rms_norm_kernel<T, 1, 4, true> : rms_norm_kernel<T, 1, 4, false>)
-            : s.nv == 16 ? (quant ? rms_norm_kernel<T, 1, 16, true> : rms_norm_kernel<T, 1, 16, false>)
-                         : (quant ? rms_norm_kernel<T, 1, 32, true> : rms_norm_kernel<T, 1, 32, false>);
+    return launch_shape(Kernel, dim3(unsigned(r.grid)), dim3(unsigned(r.tpr), unsigned(r.rpb)), r.smem, 1, stream, p, r.ring);
+}
+
+template <typename T, bool kQ>
+cudaError_t launch_norm(const NormParams &p, bool vec, int dev, int num_sms, cudaStream_t stream) {
+    const RingPlan r = ring_plan(p.rows, p.width, int(sizeof(T)), p.r != nullptr ? 2 : 1, vec, false, num_sms);
+    if (r.ok && !vec) return launch_ring<rms_norm_rows_any_kernel<T, kQ>>(r, p, dev, stream);
+    if (r.ok && cdiv(p.rows, r.rpb) >= 6 * r.grid) {
+        switch (r.nv) {
+            case 1: return launch_ring<rms_norm_rows_kernel<T, 8, 1, kQ>>(r, p, dev, stream);
+            case 2: return launch_ring<rms_norm_rows_kernel<T, 8, 2, kQ>>(r, p, dev, stream);
+            case 3: return launch_ring<rms_norm_rows_kernel<T, 8, 3, kQ>>(r, p, dev, stream);
+            default: return launch_ring<rms_norm_rows_kernel<T, 8, 4, kQ>>(r, p, dev, stream);
+        }
     }
+    const RowShape s = row_shape(p.width);
+    if (!vec || !s.fits)
+        return launch_shape(rms_norm_long_kernel<T>, dim3(unsigned(p.rows)), dim3(1024), 0, 1, stream, p, int32_t(kQ));
+    auto *k = s.nv == 1 ? rms_norm_kernel<T, 8, 1, kQ> : s.nv == 2 ? rms_norm_kernel<T, 8, 2, kQ> : rms_norm_kernel<T, 8, 4, kQ>;
     return launch_shape(k, dim3(unsigned(cdiv(p.rows, s.rpb))), dim3(unsigned(s.tpr), unsigned(s.rpb)), 0, 1, stream, p);
 }
 
 template <typename T>
-cudaError_t launch_norm_backward(NormBackwardParams p, bool vec, float *dweight, float *partial, cudaStream_t stream) {
-    static const int kVecNv[] = {1, 2}, kOneNv[] = {4, 16};
-    const RowShape s = row_shape(p.width, vec, vec ? kVecNv : kOneNv, 2);
+cudaError_t launch_norm_backward(NormBackwardParams p, bool vec, float *dweight, float *partial, int dev, int num_sms,
+                                 cudaStream_t stream) {
     p.partial = dweight != nullptr ? partial : nullptr;
     int64_t parts;
     cudaError_t e;
-    if (s.fits) {
-        using Kernel = void (*)(const NormBackwardParams);
-        Kernel k = vec ? (s.nv == 1 ? rms_norm_backward_kernel<T, 8, 1> : rms_norm_backward_kernel<T, 8, 2>)
-                       : (s.nv == 4 ? rms_norm_backward_kernel<T, 1, 4> : rms_norm_backward_kernel<T, 1, 16>);
-        parts = std::min<int64_t>(cdiv(p.rows, s.rpb), kNormParts);
-        const int smem = s.rpb > 1 ? s.rpb * s.tpr * (vec ? 8 : 1) * s.nv * 4 : 0;
-        e = launch_shape(k, dim3(unsigned(parts)), dim3(unsigned(s.tpr), unsigned(s.rpb)), smem, 1, stream, p);
+    const RingPlan r = ring_plan(p.rows, p.width, int(sizeof(T)), p.dh != nullptr ? 3 : 2, vec, true, num_sms);
+    if (r.ok) {
+        parts = r.grid;
+        if (!vec) e = launch_ring<rms_norm_backward_rows_any_kernel<T>>(r, p, dev, stream);
+        else if (r.nv == 1) e = launch_ring<rms_norm_backward_rows_kernel<T, 8, 1>>(r, p, dev, stream);
+        else if (r.nv == 2) e = launch_ring<rms_norm_backward_rows_kernel<T, 8, 2>>(r, p, dev, stream);
+        else if (r.nv == 3) e = launch_ring<rms_norm_backward_rows_kernel<T, 8, 3>>(r, p, dev, stream);
+        else e = launch_ring<rms_norm_backward_rows_kernel<T, 8, 4>>(r, p, dev, stream);
     } else {
         e = launch_shape(rms_norm_backward_long_kernel<T>, dim3(unsigned(p.rows)), dim3(1024), 0, 1, stream, p);
         const int64_t rows_per_block = cdiv(p.rows, kNormParts);
@@ -714,7 +762,8 @@ gemm_status_t gemm_rms_norm(const gemm_matrix_t *x, const gemm_matrix_t *residua
         if (st != GEMM_OK) return st;
     }
     DeviceState *ds = nullptr;
-    if (device_state(&ds) < 0) return GEMM_ERR_CUDA;
+    const int dev = device_state(&ds);
+    if (dev < 0) return GEMM_ERR_CUDA;
     NormParams p;
     std::memset(&p, 0, sizeof(p));
     p.x = x->data;
@@ -733,15 +782,19 @@ gemm_status_t gemm_rms_norm(const gemm_matrix_t *x, const gemm_matrix_t *residua
     p.width = width;
     p.eps = eps;
     p.inv_width = 1.0f / float(width);
+    p.wait.timeout_ns = g_timeout_ns.load();
+    p.wait.epoch = next_epoch();
     const int es = type_bytes(x->type);
     bool vec = width % 8 == 0 && aligned16(weight) && vec16(p.x, p.ldx, es);
     if (p.r != nullptr) vec = vec && vec16(p.r, p.ldr, es);
     if (p.h != nullptr) vec = vec && vec16(p.h, p.ldh, es);
     vec = vec && (quant ? (reinterpret_cast<uintptr_t>(p.y) & 7u) == 0 && p.ldy % 8 == 0 : vec16(p.y, p.ldy, es));
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    const cudaError_t e = x->type == GEMM_TYPE_F32   ? launch_norm<float>(p, vec, quant, stream)
-                          : x->type == GEMM_TYPE_F16 ? launch_norm<__half>(p, vec, quant, stream)
-                                                     : launch_norm<__nv_bfloat16>(p, vec, quant, stream);
+    auto launch = [&](auto *k) { return k(p, vec, dev, ds->num_sms, stream); };
+    const cudaError_t e =
+        x->type == GEMM_TYPE_F32   ? launch(quant ? launch_norm<float, true> : launch_norm<float, false>)
+        : x->type == GEMM_TYPE_F16 ? launch(quant ? launch_norm<__half, true> : launch_norm<__half, false>)
+                                   : launch(quant ? launch_norm<__nv_bfloat16, true> : launch_norm<__nv_bfloat16, false>);
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
@@ -778,7 +831,8 @@ gemm_status_t gemm_rms_norm_backward(const gemm_matrix_t *grad, const gemm_matri
     if (st != GEMM_OK) return st;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     DeviceState *ds = nullptr;
-    if (device_state(&ds) < 0) return GEMM_ERR_CUDA;
+    const int dev = device_state(&ds);
+    if (dev < 0) return GEMM_ERR_CUDA;
     if (rows == 0) {
         if (dweight != nullptr && cudaMemsetAsync(dweight, 0, size_t(width) * 4u, stream) != cudaSuccess) return GEMM_ERR_CUDA;
         return GEMM_OK;
@@ -799,14 +853,16 @@ gemm_status_t gemm_rms_norm_backward(const gemm_matrix_t *grad, const gemm_matri
     p.rows = rows;
     p.width = width;
     p.inv_width = 1.0f / float(width);
+    p.wait.timeout_ns = g_timeout_ns.load();
+    p.wait.epoch = next_epoch();
     const int es = type_bytes(grad->type);
     bool vec = width % 8 == 0 && aligned16(weight) && vec16(p.g, p.ldg, es) && vec16(p.h, p.ldh, es) &&
                vec16(p.dx, p.lddx, es);
     if (p.dh != nullptr) vec = vec && vec16(p.dh, p.lddh, es);
     float *part = static_cast<float *>(workspace);
-    const cudaError_t e = grad->type == GEMM_TYPE_F32   ? launch_norm_backward<float>(p, vec, dweight, part, stream)
-                          : grad->type == GEMM_TYPE_F16 ? launch_norm_backward<__half>(p, vec, dweight, part, stream)
-                                                        : launch_norm_backward<__nv_bfloat16>(p, vec, dweight, part, stream);
+    const cudaError_t e = grad->type == GEMM_TYPE_F32   ? launch_norm_backward<float>(p, vec, dweight, part, dev, ds->num_sms, stream)
+                          : grad->type == GEMM_TYPE_F16 ? launch_norm_backward<__half>(p, vec, dweight, part, dev, ds->num_sms, stream)
+                                                        : launch_norm_backward<__nv_bfloat16>(p, vec, dweight, part, dev, ds->num_sms, stream);
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 

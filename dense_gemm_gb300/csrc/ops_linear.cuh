@@ -954,24 +954,27 @@ struct GradParams {
 };
 constexpr int kGradGroups = 8;
 
+template <uint32_t ACT>
+__device__ __forceinline__ float2 slope_of(float2 x) { return make_float2(act_slope<ACT>(x.x), act_slope<ACT>(x.y)); }
+template <uint32_t ACT>
+__device__ __forceinline__ float slope_of(float x) { return act_slope<ACT>(x); }
+
 template <uint32_t ACT, typename T, int VEC>
-__device__ __forceinline__ void grad_rows(const GradParams &p, int64_t col, int64_t r0, int64_t r1, float (&sum)[VEC]) {
+__device__ __forceinline__ void grad_rows(const GradParams &p, int64_t col, int64_t r0, int64_t r1, F32<VEC> &sum) {
     const T *g = static_cast<const T *>(p.g), *pre = static_cast<const T *>(p.pre);
     T *d = static_cast<T *>(p.d);
 #pragma unroll 4
     for (int64_t r = r0 + threadIdx.y; r < r1; r += kGradGroups) {
-        const Raw<T, VEC> a = load_raw<T, VEC>(g + r * p.ldg + col);
-        float x[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) x[i] = to_f32<T>(a.v[i]);
+        F32<VEC> x = widen<T, VEC>(load_raw<T, VEC>(g + r * p.ldg + col));
         if constexpr (ACT != kActNone) {
-            const Raw<T, VEC> b = load_raw<T, VEC>(pre + r * p.ldp + col);
+            const F32<VEC> b = widen<T, VEC>(load_raw<T, VEC>(pre + r * p.ldp + col));
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) x[i] *= act_slope<ACT>(to_f32<T>(b.v[i]));
+            for (int i = 0; i < F32<VEC>::PAIRS; ++i)
+                x.p[i] = mul2(x.p[i], slope_of<ACT>(b.p[i]));
         }
         if (d != nullptr) store_f32<T, VEC>(d + r * p.ldd + col, x);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) sum[i] += x[i];
+        for (int i = 0; i < F32<VEC>::PAIRS; ++i) sum.p[i] = add2(sum.p[i], x.p[i]);
     }
 }
 
@@ -983,9 +986,9 @@ __global__ void __launch_bounds__(32 * kGradGroups) linear_grad_kernel(const Gra
     const int64_t col = (int64_t(blockIdx.x) * 32 + threadIdx.x) * VEC;
     const int64_t r0 = int64_t(blockIdx.y) * p.rows_per_block;
     const int64_t r1 = r0 + p.rows_per_block < p.M ? r0 + p.rows_per_block : p.M;
-    float sum[VEC];
+    F32<VEC> sum;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) sum[i] = 0.0f;
+    for (int i = 0; i < F32<VEC>::PAIRS; ++i) sum.p[i] = splat<VEC>(0.0f);
     if (col < p.N) {
         switch (p.act) {
             case kActRelu: grad_rows<kActRelu, T, VEC>(p, col, r0, r1, sum); break;
@@ -997,7 +1000,14 @@ __global__ void __launch_bounds__(32 * kGradGroups) linear_grad_kernel(const Gra
     }
     if (p.partial == nullptr) return;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) s[threadIdx.y][threadIdx.x * VEC + i] = sum[i];
+    for (int i = 0; i < F32<VEC>::PAIRS; ++i) {
+        if constexpr (VEC == 8) {
+            s[threadIdx.y][threadIdx.x * VEC + 2 * i] = sum.p[i].x;
+            s[threadIdx.y][threadIdx.x * VEC + 2 * i + 1] = sum.p[i].y;
+        } else {
+            s[threadIdx.y][threadIdx.x] = sum.p[0];
+        }
+    }
     __syncthreads();
     for (int c = threadIdx.y * 32 + threadIdx.x; c < 32 * VEC; c += 32 * kGradGroups) {
         const int64_t at = int64_t(blockIdx.x) * 32 * VEC + c;

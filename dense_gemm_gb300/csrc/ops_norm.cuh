@@ -29,72 +29,164 @@ __device__ __forceinline__ T from_f32(float v) {  // round to nearest even
     else return __float2bfloat16_rn(v);
 }
 
-// A register image of VEC consecutive elements (16 bytes at least with VEC = 8).
+// VEC consecutive elements as they lie in memory: 16 bytes (32 for fp32) with
+// VEC = 8, one element with VEC = 1.
 template <typename T, int VEC>
 struct Raw {
-    static_assert(VEC == 1 || VEC == 8, "one element, or 16-byte vectors");
-    T v[VEC];
+    static_assert(VEC == 8, "one element, or 16-byte vectors");
+    uint4 q[sizeof(T) / 2];
 };
 template <typename T>
-struct alignas(16) Raw<T, 8> {
-    T v[8];
+struct Raw<T, 1> {
+    T v;
 };
 
 template <typename T, int VEC>
 __device__ __forceinline__ Raw<T, VEC> load_raw(const T *p) {
+    Raw<T, VEC> r;
     if constexpr (VEC == 1) {
-        Raw<T, 1> r;
-        r.v[0] = *p;
-        return r;
+        r.v = *p;
     } else {
-        Raw<T, VEC> r;
 #pragma unroll
-        for (int i = 0; i < int(sizeof(r) / 16); ++i)
-            reinterpret_cast<uint4 *>(&r)[i] = reinterpret_cast<const uint4 *>(p)[i];
-        return r;
+        for (int i = 0; i < int(sizeof(r) / 16); ++i) r.q[i] = reinterpret_cast<const uint4 *>(p)[i];
     }
+    return r;
+}
+
+// The same from a shared-memory address (VEC = 8: 16-byte aligned).
+template <typename T, int VEC>
+__device__ __forceinline__ Raw<T, VEC> load_raw_shared(uint32_t addr) {
+    Raw<T, VEC> r;
+    if constexpr (VEC == 8) {
+#pragma unroll
+        for (int i = 0; i < int(sizeof(r) / 16); ++i) ld_shared_v4(addr + 16u * i, r.q[i].x, r.q[i].y, r.q[i].z, r.q[i].w);
+    } else if constexpr (sizeof(T) == 4) {
+        const uint32_t w = ld_shared_b32(addr);
+        r.v = *reinterpret_cast<const T *>(&w);
+    } else {
+        uint16_t w = 0;
+        if (G16_CHECK(smem_window_ok(addr, 2))) asm volatile("ld.shared.b16 %0, [%1];" : "=h"(w) : "r"(addr) : "memory");
+        r.v = *reinterpret_cast<const T *>(&w);
+    }
+    return r;
+}
+
+// fp32 values in pairs: the arithmetic of a pair is one instruction
+// (fma.rn.f32x2 and its like). These kernels spend as many issue slots as the
+// memory system leaves them, so VEC = 8 works on 4 pairs; VEC = 1 on one value.
+template <int VEC>
+struct F32 {
+    using E = float2;
+    static constexpr int PAIRS = 4;
+    E p[PAIRS];
+};
+template <>
+struct F32<1> {
+    using E = float;
+    static constexpr int PAIRS = 1;
+    E p[PAIRS];
+};
+
+__device__ __forceinline__ uint64_t bits2(float2 a) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ float2 pair2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return pair2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair2(r);
+}
+__device__ __forceinline__ float fma2(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float mul2(float a, float b) { return a * b; }
+__device__ __forceinline__ float add2(float a, float b) { return a + b; }
+__device__ __forceinline__ float total(float2 a) { return a.x + a.y; }
+__device__ __forceinline__ float total(float a) { return a; }
+
+template <int VEC>
+__device__ __forceinline__ typename F32<VEC>::E splat(float v) {
+    if constexpr (VEC == 8) return make_float2(v, v);
+    else return v;
+}
+
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if constexpr (std::is_same_v<T, __half>) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    else return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));  // bf16: the high half of an fp32
 }
 
 template <typename T, int VEC>
-__device__ __forceinline__ void store_f32(T *p, const float (&v)[VEC]) {
+__device__ __forceinline__ F32<VEC> widen(const Raw<T, VEC> &r) {
+    F32<VEC> v;
     if constexpr (VEC == 1) {
-        *p = from_f32<T>(v[0]);
+        v.p[0] = to_f32<T>(r.v);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v.p[2 * i] = make_float2(__uint_as_float(r.q[i].x), __uint_as_float(r.q[i].y));
+            v.p[2 * i + 1] = make_float2(__uint_as_float(r.q[i].z), __uint_as_float(r.q[i].w));
+        }
     } else {
-        Raw<T, VEC> r;
+        v.p[0] = unpack2<T>(r.q[0].x);
+        v.p[1] = unpack2<T>(r.q[0].y);
+        v.p[2] = unpack2<T>(r.q[0].z);
+        v.p[3] = unpack2<T>(r.q[0].w);
+    }
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+    return pack_16x2(v.x, v.y, std::is_same_v<T, __half> ? 1u : 2u);
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void store_f32(T *p, const F32<VEC> &v) {
+    if constexpr (VEC == 1) {
+        *p = from_f32<T>(v.p[0]);
+    } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) r.v[i] = from_f32<T>(v[i]);
-#pragma unroll
-        for (int i = 0; i < int(sizeof(r) / 16); ++i)
-            reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<const uint4 *>(&r)[i];
+        for (int i = 0; i < 2; ++i)
+            reinterpret_cast<float4 *>(p)[i] = make_float4(v.p[2 * i].x, v.p[2 * i].y, v.p[2 * i + 1].x, v.p[2 * i + 1].y);
+    } else {
+        *reinterpret_cast<uint4 *>(p) =
+            make_uint4(pack2<T>(v.p[0]), pack2<T>(v.p[1]), pack2<T>(v.p[2]), pack2<T>(v.p[3]));
     }
 }
 
-// Weights: T or fp32, VEC of them as fp32.
+// Weights: T or fp32.
 template <typename T, int VEC>
-__device__ __forceinline__ void load_weight(const void *w, bool w_f32, int64_t at, float (&v)[VEC]) {
-    if (w_f32) {
-        const Raw<float, VEC> r = load_raw<float, VEC>(static_cast<const float *>(w) + at);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = r.v[i];
-    } else {
-        const Raw<T, VEC> r = load_raw<T, VEC>(static_cast<const T *>(w) + at);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = to_f32<T>(r.v[i]);
-    }
+__device__ __forceinline__ F32<VEC> load_weight(const void *w, bool w_f32, int64_t at) {
+    if (w_f32) return widen<float, VEC>(load_raw<float, VEC>(static_cast<const float *>(w) + at));
+    return widen<T, VEC>(load_raw<T, VEC>(static_cast<const T *>(w) + at));
 }
 
 // fp32 -> e4m3, nearest even; |v| <= 448 up to rounding, a NaN stays one.
 template <int VEC>
-__device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&v)[VEC]) {
+__device__ __forceinline__ void store_e4m3(uint8_t *p, const F32<VEC> &v) {
     if constexpr (VEC == 1) {
-        *p = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+        *p = __nv_cvt_float_to_fp8(v.p[0], __NV_SATFINITE, __NV_E4M3);
     } else {
         uint32_t w[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i], v[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi =
-                __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2], v[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(v.p[2 * i], __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(v.p[2 * i + 1], __NV_SATFINITE, __NV_E4M3);
             w[i] = lo | (hi << 16);
         }
         *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
@@ -103,46 +195,86 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const float (&v)[VEC]) {
 
 // ------------------------------------------------------------------ row reductions
 // A block holds blockDim.y rows of blockDim.x threads each (blockDim.x a
-// multiple of 32: a warp never spans two rows). Every thread of a row gets the
-// row's sum, its warps' sums added in warp order. `red`: 32 floats, one use per
-// call (a second call in the same kernel passes another array).
+// multiple of 32: a warp never spans two rows). `red`: 32 words, one use between
+// two barriers.
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
+// Every thread of a row gets the row's sum: each warp's sum goes through shared
+// memory, and every warp adds the row's warps' sums by the same tree. One
+// barrier, also for rows of one warp where `always` (callers use it to know that
+// all threads have left the step before).
+template <bool kAlways>
 __device__ __forceinline__ float row_sum(float v, float *red) {
     v = warp_sum(v);
     const int wpr = blockDim.x >> 5;
-    if (wpr == 1) return v;
-    const int w = threadIdx.x >> 5, base = int(threadIdx.y) * wpr;
-    if ((threadIdx.x & 31) == 0) red[base + w] = v;
+    if (!kAlways && wpr == 1) return v;
+    const int lane = threadIdx.x & 31, base = int(threadIdx.y) * wpr;
+    if (lane == 0) red[base + (threadIdx.x >> 5)] = v;
     __syncthreads();
-    float s = red[base];
-    for (int i = 1; i < wpr; ++i) s += red[base + i];
-    return s;
+    if (wpr == 1) return v;
+    return warp_sum(lane < wpr ? red[base + lane] : 0.0f);
 }
 
-// Largest |value| of a row, as bits: the order of the bits of non-negative
-// floats is theirs, infinity above every number and a NaN above infinity, so a
-// NaN anywhere in the row is the result.
-__device__ __forceinline__ uint32_t row_max_bits(uint32_t v, uint32_t *red) {
-    v = __reduce_max_sync(0xffffffffu, v);
+// The largest |value|, NaN if there is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// A row's sum and largest value (>= 0 or NaN: their bits are in their order, a
+// NaN's above infinity's); one barrier.
+__device__ __forceinline__ void row_sum_max(float &v, float &m, float *red, uint32_t *redq) {
+    v = warp_sum(v);
+    uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m) & 0x7fffffffu);
     const int wpr = blockDim.x >> 5;
-    if (wpr == 1) return v;
-    const int w = threadIdx.x >> 5, base = int(threadIdx.y) * wpr;
-    if ((threadIdx.x & 31) == 0) red[base + w] = v;
+    const int lane = threadIdx.x & 31, base = int(threadIdx.y) * wpr;
+    if (lane == 0) {
+        red[base + (threadIdx.x >> 5)] = v;
+        redq[base + (threadIdx.x >> 5)] = mb;
+    }
     __syncthreads();
-    uint32_t m = red[base];
-    for (int i = 1; i < wpr; ++i) m = max(m, red[base + i]);
-    return m;
+    if (wpr > 1) {
+        v = warp_sum(lane < wpr ? red[base + lane] : 0.0f);
+        mb = __reduce_max_sync(0xffffffffu, lane < wpr ? redq[base + lane] : 0u);
+    }
+    m = __uint_as_float(mb);
 }
 
 // Rows whose largest |y| is below this (zero rows among them) are stored as
 // zeros with scale 1: their 448 / a would leave fp32's range.
 constexpr float kQuantTiny = 7.7e-34f;
 constexpr float kE4m3Max = 448.0f;
+
+// With t = w h, y = t rstd and a = max|y| = rstd max|t|, so y 448 / a = t 448 /
+// max|t|: the row's factor for t and its scale, from max|t|. One pass over the
+// row then gives both its sum and its maximum.
+__device__ __forceinline__ void quant_factors(float tmax, float rstd, float &mul, float &scale) {
+    const float a = tmax * rstd;
+    if (a < kQuantTiny) {
+        mul = 0.0f;
+        scale = 1.0f;
+    } else {  // a NaN (also from an infinity, whose rstd is 0) makes the row NaN
+        mul = a == a ? kE4m3Max / tmax : a;
+        scale = a * (1.0f / kE4m3Max);
+    }
+}
+
+// t = w h of VEC elements; adds h^2 to ss and takes |t| into tmax.
+template <int VEC, bool kQ>
+__device__ __forceinline__ void square_and_weigh(F32<VEC> &t, const F32<VEC> &w, typename F32<VEC>::E &ss, float &tmax) {
+#pragma unroll
+    for (int i = 0; i < F32<VEC>::PAIRS; ++i) {
+        ss = fma2(t.p[i], t.p[i], ss);
+        t.p[i] = mul2(t.p[i], w.p[i]);
+        if constexpr (kQ && VEC == 8) tmax = max_nan(max_nan(tmax, fabsf(t.p[i].x)), fabsf(t.p[i].y));
+        else if constexpr (kQ) tmax = max_nan(tmax, fabsf(t.p[i]));
+    }
+}
 
 struct NormParams {
     const void *x, *r;  // r == nullptr: no residual
@@ -153,18 +285,8 @@ struct NormParams {
     int64_t ldx, ldr, ldy, ldh;
     float eps, inv_width;
     int32_t w_f32;
+    WaitCtl wait;
 };
-
-__device__ __forceinline__ void quant_factors(uint32_t amax_bits, float &mul, float &scale) {
-    const float a = __uint_as_float(amax_bits);
-    if (a < kQuantTiny) {
-        mul = 0.0f;
-        scale = 1.0f;
-    } else {  // a NaN makes both NaN
-        mul = kE4m3Max / a;
-        scale = a * (1.0f / kE4m3Max);
-    }
-}
 
 // One row per blockDim.x threads, held in registers: element (j * blockDim.x +
 // t) * VEC + i of the row is value i of load j of thread t.
@@ -176,74 +298,56 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
     const bool live = row < p.rows;
     griddep_wait();
     griddep_launch_dependents();
-    float h[NV][VEC];
+    const int width = int(p.width);
+    auto at_of = [&](int j) { return (j * int(blockDim.x) + int(threadIdx.x)) * VEC; };
+    F32<VEC> t[NV];
     {
         Raw<T, VEC> a[NV], b[NV];
         const T *x = static_cast<const T *>(p.x) + row * p.ldx;
         const T *r = static_cast<const T *>(p.r) + row * p.ldr;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int64_t at = (int64_t(j) * blockDim.x + threadIdx.x) * VEC;
-            if (live && at < p.width) {
-                a[j] = load_raw<T, VEC>(x + at);
-                if (p.r != nullptr) b[j] = load_raw<T, VEC>(r + at);
-            }
+            if (!live || at_of(j) >= width) continue;
+            a[j] = load_raw<T, VEC>(x + at_of(j));
+            if (p.r != nullptr) b[j] = load_raw<T, VEC>(r + at_of(j));
         }
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const bool in = live && (int64_t(j) * blockDim.x + threadIdx.x) * VEC < p.width;
+            if (!live || at_of(j) >= width) continue;
+            t[j] = widen<T, VEC>(a[j]);
+            if (p.r == nullptr) continue;
+            const F32<VEC> f = widen<T, VEC>(b[j]);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                h[j][i] = in ? to_f32<T>(a[j].v[i]) : 0.0f;
-                if (in && p.r != nullptr) h[j][i] += to_f32<T>(b[j].v[i]);
-            }
+            for (int i = 0; i < F32<VEC>::PAIRS; ++i) t[j].p[i] = add2(t[j].p[i], f.p[i]);
         }
     }
-    float ss = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) ss = fmaf(h[j][i], h[j][i], ss);
-    if (p.h != nullptr) {
-        T *hp = static_cast<T *>(p.h) + row * p.ldh;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int64_t at = (int64_t(j) * blockDim.x + threadIdx.x) * VEC;
-            if (live && at < p.width) store_f32<T, VEC>(hp + at, h[j]);
-        }
-    }
-    const float rstd = rsqrtf(fmaf(row_sum(ss, red), p.inv_width, p.eps));
-    if (live && p.rstd != nullptr && threadIdx.x == 0) p.rstd[row] = rstd;
-    uint32_t amax = 0;
+    auto ss2 = splat<VEC>(0.0f);
+    float tmax = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int64_t at = (int64_t(j) * blockDim.x + threadIdx.x) * VEC;
-        if (live && at < p.width) {
-            float w[VEC];
-            load_weight<T, VEC>(p.w, p.w_f32 != 0, at, w);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                h[j][i] = h[j][i] * rstd * w[i];
-                if (kQ) amax = max(amax, __float_as_uint(h[j][i]) & 0x7fffffffu);
-            }
-            if (!kQ) store_f32<T, VEC>(static_cast<T *>(p.y) + row * p.ldy + at, h[j]);
-        }
+        if (!live || at_of(j) >= width) continue;
+        if (p.h != nullptr) store_f32<T, VEC>(static_cast<T *>(p.h) + row * p.ldh + at_of(j), t[j]);
+        square_and_weigh<VEC, kQ>(t[j], load_weight<T, VEC>(p.w, p.w_f32 != 0, at_of(j)), ss2, tmax);
     }
+    float ss = total(ss2);
+    if constexpr (kQ) row_sum_max(ss, tmax, red, redq);
+    else ss = row_sum<false>(ss, red);
+    const float rstd = rsqrtf(fmaf(ss, p.inv_width, p.eps));
+    if (!live) return;
+    if (p.rstd != nullptr && threadIdx.x == 0) p.rstd[row] = rstd;
+    float mul = rstd;
     if constexpr (kQ) {
-        float mul, scale;
-        quant_factors(row_max_bits(amax, redq), mul, scale);
-        if (!live) return;
+        float scale;
+        quant_factors(tmax, rstd, mul, scale);
         if (threadIdx.x == 0) p.scale[row] = scale;
-        uint8_t *q = static_cast<uint8_t *>(p.y) + row * p.ldy;
+    }
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int64_t at = (int64_t(j) * blockDim.x + threadIdx.x) * VEC;
-            if (at < p.width) {
+    for (int j = 0; j < NV; ++j) {
+        if (at_of(j) >= width) continue;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) h[j][i] *= mul;
-                store_e4m3<VEC>(q + at, h[j]);
-            }
-        }
+        for (int i = 0; i < F32<VEC>::PAIRS; ++i) t[j].p[i] = mul2(t[j].p[i], splat<VEC>(mul));
+        if constexpr (kQ) store_e4m3<VEC>(static_cast<uint8_t *>(p.y) + row * p.ldy + at_of(j), t[j]);
+        else store_f32<T, VEC>(static_cast<T *>(p.y) + row * p.ldy + at_of(j), t[j]);
     }
 }
 
@@ -260,37 +364,253 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const NormParams p,
     const T *x = static_cast<const T *>(p.x) + row * p.ldx;
     const T *r = p.r != nullptr ? static_cast<const T *>(p.r) + row * p.ldr : nullptr;
     auto sum = [&](int64_t at) { return to_f32<T>(x[at]) + (r != nullptr ? to_f32<T>(r[at]) : 0.0f); };
-    float ss = 0.0f;
+    float ss = 0.0f, tmax = 0.0f;
     for (int64_t at = threadIdx.x; at < p.width; at += blockDim.x) {
         const float h = sum(at);
         ss = fmaf(h, h, ss);
+        if (quant) tmax = max_nan(tmax, fabsf(h * load_weight<T, 1>(p.w, p.w_f32 != 0, at).p[0]));
     }
-    const float rstd = rsqrtf(fmaf(row_sum(ss, red), p.inv_width, p.eps));
+    row_sum_max(ss, tmax, red, redq);
+    const float rstd = rsqrtf(fmaf(ss, p.inv_width, p.eps));
     if (p.rstd != nullptr && threadIdx.x == 0) p.rstd[row] = rstd;
-    float mul = 1.0f, scale = 1.0f;
+    float mul = rstd, scale = 1.0f;
     if (quant) {
-        uint32_t amax = 0;
-        for (int64_t at = threadIdx.x; at < p.width; at += blockDim.x) {
-            float w[1];
-            load_weight<T, 1>(p.w, p.w_f32 != 0, at, w);
-            amax = max(amax, __float_as_uint(sum(at) * rstd * w[0]) & 0x7fffffffu);
-        }
-        quant_factors(row_max_bits(amax, redq), mul, scale);
+        quant_factors(tmax, rstd, mul, scale);
         if (threadIdx.x == 0) p.scale[row] = scale;
     }
     for (int64_t at = threadIdx.x; at < p.width; at += blockDim.x) {
-        float w[1];
-        load_weight<T, 1>(p.w, p.w_f32 != 0, at, w);
         const float h = sum(at);
-        float y[1] = {h * rstd * w[0]};
+        F32<1> y;
+        y.p[0] = h * load_weight<T, 1>(p.w, p.w_f32 != 0, at).p[0] * mul;
         if (p.h != nullptr) static_cast<T *>(p.h)[row * p.ldh + at] = from_f32<T>(h);
-        if (quant) {
-            y[0] *= mul;
-            store_e4m3<1>(static_cast<uint8_t *>(p.y) + row * p.ldy + at, y);
-        } else {
-            static_cast<T *>(p.y)[row * p.ldy + at] = from_f32<T>(y[0]);
-        }
+        if (quant) store_e4m3<1>(static_cast<uint8_t *>(p.y) + row * p.ldy + at, y);
+        else store_f32<T, 1>(static_cast<T *>(p.y) + row * p.ldy + at, y);
     }
+}
+
+// ------------------------------------------------------------------ rows through shared memory
+// The persistent form: each block walks rows base + threadIdx.y, base = blockIdx.x
+// * blockDim.y, then every gridDim.x * blockDim.y further on. The rows of the next
+// steps are on their way into a ring of shared-memory slots (bulk copies) while
+// this one is summed and written, so the memory system stays busy through the
+// barriers of the reductions. A copy starts and ends on 16-byte boundaries: it
+// takes the bytes that share a granule with the row's first and last element
+// too, and the row's elements are found from the offset in that granule.
+constexpr int kRingSlots = 8;      // at most
+constexpr int kRingThreads = 512;  // at most: 128 registers each, so two blocks of 256 share an SM
+
+struct RingShape {
+    int32_t slots;
+    int32_t pitch;        // bytes between the rows of one array in a slot
+    int32_t array_bytes;  // blockDim.y * pitch
+    int32_t slot_bytes;   // arrays * array_bytes
+};
+
+template <typename T>
+struct RowSource {
+    const T *data;
+    int64_t ld;
+    __device__ __forceinline__ uint32_t in_slot(uint32_t place, int64_t row) const {
+        return place + (uint32_t(reinterpret_cast<uintptr_t>(data + row * ld)) & 15u);
+    }
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    if (!G16_CHECK((bytes & 15u) == 0 && smem_window_ok(dst, bytes))) return;
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Warp 0 of the block starts the copies of rows base .. base + blockDim.y - 1 of
+// every array into a slot; one lane per copy.
+template <typename T>
+__device__ __forceinline__ void fill_slot(const RowSource<T> *src, int arrays, const RingShape &ring, uint8_t *slots, int slot,
+                                          uint32_t bar, int64_t base, int64_t rows, int64_t width) {
+    if (threadIdx.y != 0 || threadIdx.x >= 32) return;
+    const int lane = threadIdx.x, nrows = int(blockDim.y);
+    const int a = lane / nrows, y = lane - a * nrows;
+    uint32_t bytes = 0, dst = 0;
+    const void *from = nullptr;
+    if (a < arrays && base + y < rows) {
+        const RowSource<T> s = a == 0 ? src[0] : a == 1 ? src[1] : src[2];
+        const uintptr_t at = reinterpret_cast<uintptr_t>(s.data + (base + y) * s.ld);
+        from = reinterpret_cast<const void *>(at & ~uintptr_t(15));
+        bytes = (uint32_t(at & 15u) + uint32_t(width) * uint32_t(sizeof(T)) + 15u) & ~15u;
+        dst = smem_addr(slots) + uint32_t(slot * ring.slot_bytes + a * ring.array_bytes + y * ring.pitch);
+    }
+    const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+    if (lane == 0) mbar_arrive_expect_tx(bar, total);
+    __syncwarp();
+    if (bytes > 0) bulk_load(dst, from, bytes, bar);
+}
+
+// After a wait ran out (the status is set, the results are not to be used): time
+// for copies already started, rows of some 64 KiB at most, to land before the
+// block's shared memory is given away.
+__device__ __forceinline__ void let_copies_land() {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 200000ull) {
+    }
+}
+
+template <typename T, int VEC, int NV, bool kQ>
+__global__ void __launch_bounds__(kRingThreads) rms_norm_rows_kernel(const NormParams p, const RingShape ring) {
+    __shared__ float red[2][32];
+    __shared__ uint32_t redq[2][32];
+    __shared__ __align__(8) uint64_t full[kRingSlots];
+    extern __shared__ __align__(16) uint8_t rows[];
+    if (threadIdx.y == 0 && threadIdx.x == 0) {
+        for (int s = 0; s < ring.slots; ++s) mbar_init(smem_addr(&full[s]), 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t step = int64_t(gridDim.x) * blockDim.y;
+    const int64_t first = int64_t(blockIdx.x) * blockDim.y;
+    const RowSource<T> src[3] = {{static_cast<const T *>(p.x), p.ldx}, {static_cast<const T *>(p.r), p.ldr}, {nullptr, 0}};
+    const int arrays = p.r != nullptr ? 2 : 1;
+    auto refill = [&](int64_t base, int slot) {
+        if (base < p.rows) fill_slot(src, arrays, ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
+    };
+    for (int s = 0; s < ring.slots; ++s) refill(first + s * step, s);
+    auto at_of = [&](int j) { return (j * int(blockDim.x) + int(threadIdx.x)) * VEC; };
+    const int width = int(p.width);
+    Raw<T, VEC> w16[NV];  // a weight of T's type; fp32 weights are read again for each row
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (at_of(j) < width && !p.w_f32) w16[j] = load_raw<T, VEC>(static_cast<const T *>(p.w) + at_of(j));
+    const uint32_t ring0 = smem_addr(rows) + uint32_t(int(threadIdx.y) * ring.pitch);
+    const bool has_r = p.r != nullptr, has_h = p.h != nullptr;
+    int slot = 0, flip = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t base = first; base < p.rows; base += step, flip ^= 1) {
+        const int64_t row = base + threadIdx.y;
+        const bool live = row < p.rows;
+        ok = mbar_wait(smem_addr(&full[slot]), phase, p.wait) && ok;
+        const uint32_t mine = ring0 + uint32_t(slot * ring.slot_bytes);
+        const uint32_t x = src[0].in_slot(mine, row), r = src[1].in_slot(mine + uint32_t(ring.array_bytes), row);
+        T *h = static_cast<T *>(p.h) + row * p.ldh;
+        F32<VEC> t[NV];
+        auto ss2 = splat<VEC>(0.0f);
+        float tmax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (!live || at_of(j) >= width) continue;
+            t[j] = widen<T, VEC>(load_raw_shared<T, VEC>(x + uint32_t(at_of(j)) * uint32_t(sizeof(T))));
+            if (has_r) {
+                const F32<VEC> f = widen<T, VEC>(load_raw_shared<T, VEC>(r + uint32_t(at_of(j)) * uint32_t(sizeof(T))));
+#pragma unroll
+                for (int i = 0; i < F32<VEC>::PAIRS; ++i) t[j].p[i] = add2(t[j].p[i], f.p[i]);
+                if (has_h) store_f32<T, VEC>(h + at_of(j), t[j]);
+            }
+            square_and_weigh<VEC, kQ>(t[j], p.w_f32 ? load_weight<T, VEC>(p.w, true, at_of(j)) : widen<T, VEC>(w16[j]), ss2, tmax);
+        }
+        float ss = total(ss2);
+        if constexpr (kQ) row_sum_max(ss, tmax, red[flip], redq[flip]);
+        else ss = row_sum<true>(ss, red[flip]);
+        refill(base + int64_t(ring.slots) * step, slot);  // every thread has its values of this slot in registers
+        const float rstd = rsqrtf(fmaf(ss, p.inv_width, p.eps));
+        float mul = rstd;
+        if constexpr (kQ) {
+            float scale;
+            quant_factors(tmax, rstd, mul, scale);
+            if (live && threadIdx.x == 0) p.scale[row] = scale;
+        }
+        if (live && p.rstd != nullptr && threadIdx.x == 0) p.rstd[row] = rstd;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (!live || at_of(j) >= width) continue;
+#pragma unroll
+            for (int i = 0; i < F32<VEC>::PAIRS; ++i) t[j].p[i] = mul2(t[j].p[i], splat<VEC>(mul));
+            if constexpr (kQ) store_e4m3<VEC>(static_cast<uint8_t *>(p.y) + row * p.ldy + at_of(j), t[j]);
+            else store_f32<T, VEC>(static_cast<T *>(p.y) + row * p.ldy + at_of(j), t[j]);
+        }
+        if (++slot == ring.slots) { slot = 0; phase ^= 1u; }
+    }
+    if (!ok) let_copies_land();
+}
+
+// Rows that are not all on 16-byte boundaries (or a width that is no multiple of
+// 8): element by element out of the slots, lane by lane along the row, so that
+// the stores of a warp stay contiguous. A slot is read twice and refilled after
+// the next step's barrier.
+template <typename T>
+__device__ __forceinline__ float lds_elem(uint32_t row, int c) {
+    return to_f32<T>(load_raw_shared<T, 1>(row + uint32_t(c) * uint32_t(sizeof(T))).v);
+}
+
+template <typename T, bool kQ>
+__global__ void __launch_bounds__(kRingThreads) rms_norm_rows_any_kernel(const NormParams p, const RingShape ring) {
+    __shared__ float red[2][32];
+    __shared__ uint32_t redq[2][32];
+    __shared__ __align__(8) uint64_t full[kRingSlots];
+    extern __shared__ __align__(16) uint8_t rows[];
+    if (threadIdx.y == 0 && threadIdx.x == 0) {
+        for (int s = 0; s < ring.slots; ++s) mbar_init(smem_addr(&full[s]), 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t step = int64_t(gridDim.x) * blockDim.y;
+    const int64_t first = int64_t(blockIdx.x) * blockDim.y;
+    const RowSource<T> src[3] = {{static_cast<const T *>(p.x), p.ldx}, {static_cast<const T *>(p.r), p.ldr}, {nullptr, 0}};
+    const bool has_r = p.r != nullptr, has_h = p.h != nullptr;
+    auto refill = [&](int64_t base, int slot) {
+        if (base < p.rows) fill_slot(src, has_r ? 2 : 1, ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
+    };
+    for (int s = 0; s < ring.slots; ++s) refill(first + s * step, s);
+    const int width = int(p.width), tpr = int(blockDim.x);
+    const uint32_t ring0 = smem_addr(rows) + uint32_t(int(threadIdx.y) * ring.pitch);
+    int slot = 0, last = ring.slots - 1, flip = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int64_t base = first; base < p.rows; base += step, flip ^= 1) {
+        const int64_t row = base + threadIdx.y;
+        const bool live = row < p.rows;
+        ok = mbar_wait(smem_addr(&full[slot]), phase, p.wait) && ok;
+        const uint32_t mine = ring0 + uint32_t(slot * ring.slot_bytes);
+        const uint32_t x = src[0].in_slot(mine, row), r = src[1].in_slot(mine + uint32_t(ring.array_bytes), row);
+        auto sum = [&](int c) { return lds_elem<T>(x, c) + (has_r ? lds_elem<T>(r, c) : 0.0f); };
+        float ss = 0.0f, tmax = 0.0f;
+        if (live) {
+#pragma unroll 4
+            for (int c = threadIdx.x; c < width; c += tpr) {
+                const float h = sum(c);
+                ss = fmaf(h, h, ss);
+                if (kQ) tmax = max_nan(tmax, fabsf(h * load_weight<T, 1>(p.w, p.w_f32 != 0, c).p[0]));
+            }
+        }
+        if constexpr (kQ) row_sum_max(ss, tmax, red[flip], redq[flip]);
+        else ss = row_sum<true>(ss, red[flip]);
+        if (base >= first + step) refill(base + int64_t(ring.slots - 1) * step, last);  // all have left the step before
+        const float rstd = rsqrtf(fmaf(ss, p.inv_width, p.eps));
+        float mul = rstd;
+        if constexpr (kQ) {
+            float scale;
+            quant_factors(tmax, rstd, mul, scale);
+            if (live && threadIdx.x == 0) p.scale[row] = scale;
+        }
+        if (live && p.rstd != nullptr && threadIdx.x == 0) p.rstd[row] = rstd;
+        if (live) {
+            T *ho = static_cast<T *>(p.h) + row * p.ldh;
+#pragma unroll 4
+            for (int c = threadIdx.x; c < width; c += tpr) {
+                const float h = sum(c);
+                if (has_h) ho[c] = from_f32<T>(h);
+                F32<1> y;
+                y.p[0] = h * load_weight<T, 1>(p.w, p.w_f32 != 0, c).p[0] * mul;
+                if constexpr (kQ) store_e4m3<1>(static_cast<uint8_t *>(p.y) + row * p.ldy + c, y);
+                else store_f32<T, 1>(static_cast<T *>(p.y) + row * p.ldy + c, y);
+            }
+        }
+        last = slot;
+        if (++slot == ring.slots) { slot = 0; phase ^= 1u; }
+    }
+    if (!ok) let_copies_land();
 }
 
 // ------------------------------------------------------------------ backward
@@ -304,98 +624,194 @@ struct NormBackwardParams {
     int64_t ldg, ldh, lddh, lddx;
     float inv_width;
     int32_t w_f32;
+    WaitCtl wait;
 };
 
-// Rows blockIdx.x * blockDim.y + threadIdx.y, then every gridDim.x * blockDim.y
-// further on: a thread keeps its columns, so their dweight sums stay in its
-// registers and each block writes one row of partial sums at its end. The next
-// row's loads are issued before this row's reduction, whose barrier would
-// otherwise leave the block with nothing in flight.
+// The persistent form, as rms_norm_rows_kernel: rows arrive through a ring of
+// shared-memory slots, and a thread keeps its columns, so that their dweight
+// sums stay in its registers and each block writes one row of partial sums at
+// its end. A slot is read twice (for the row's dot product and for dx) and
+// refilled after the next step's barrier.
 template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(1024) rms_norm_backward_kernel(const NormBackwardParams p) {
+__global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_kernel(const NormBackwardParams p, const RingShape ring) {
     __shared__ float red[2][32];
-    extern __shared__ float dw_rows[];  // blockDim.y > 1: [blockDim.y][blockDim.x * VEC * NV]
+    __shared__ __align__(8) uint64_t full[kRingSlots];
+    extern __shared__ __align__(16) uint8_t rows[];
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+    if (tid == 0) {
+        for (int s = 0; s < ring.slots; ++s) mbar_init(smem_addr(&full[s]), 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
     const int64_t step = int64_t(gridDim.x) * blockDim.y;
-    // the block's rows advance together, so that the barriers below are met by all
     const int64_t first = int64_t(blockIdx.x) * blockDim.y;
-    float w[NV][VEC], dw[NV][VEC];
-    Raw<T, VEC> rg[NV], rh[NV], rd[NV];
-    float rstd = 0.0f;
-    auto at_of = [&](int j) { return (int64_t(j) * blockDim.x + threadIdx.x) * VEC; };
-    auto fetch = [&](int64_t row) {
-        if (row >= p.rows) return;
-        rstd = p.rstd[row];
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (at_of(j) >= p.width) continue;
-            rg[j] = load_raw<T, VEC>(static_cast<const T *>(p.g) + row * p.ldg + at_of(j));
-            rh[j] = load_raw<T, VEC>(static_cast<const T *>(p.h) + row * p.ldh + at_of(j));
-            if (p.dh != nullptr) rd[j] = load_raw<T, VEC>(static_cast<const T *>(p.dh) + row * p.lddh + at_of(j));
-        }
+    const RowSource<T> src[3] = {{static_cast<const T *>(p.g), p.ldg}, {static_cast<const T *>(p.h), p.ldh},
+                                 {static_cast<const T *>(p.dh), p.lddh}};
+    const int arrays = p.dh != nullptr ? 3 : 2;
+    auto refill = [&](int64_t base, int slot) {
+        if (base < p.rows) fill_slot(src, arrays, ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
     };
-    fetch(first + threadIdx.y);
+    for (int s = 0; s < ring.slots; ++s) refill(first + s * step, s);
+    auto at_of = [&](int j) { return (j * int(blockDim.x) + int(threadIdx.x)) * VEC; };
+    const int width = int(p.width);
+    F32<VEC> dw[NV];
+    Raw<T, VEC> w16[NV];  // a weight of T's type; fp32 weights are read again for each row
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) w[j][i] = dw[j][i] = 0.0f;
-        if (at_of(j) < p.width) load_weight<T, VEC>(p.w, p.w_f32 != 0, at_of(j), w[j]);
+        for (int i = 0; i < F32<VEC>::PAIRS; ++i) dw[j].p[i] = splat<VEC>(0.0f);
+        if (at_of(j) < width && !p.w_f32) w16[j] = load_raw<T, VEC>(static_cast<const T *>(p.w) + at_of(j));
     }
+    auto weight = [&](int j) { return p.w_f32 ? load_weight<T, VEC>(p.w, true, at_of(j)) : widen<T, VEC>(w16[j]); };
+    const uint32_t ring0 = smem_addr(rows) + uint32_t(int(threadIdx.y) * ring.pitch);
+    const bool has_d = p.dh != nullptr;
+    int slot = 0, last = ring.slots - 1;  // `last`: the slot before it in the ring
+    uint32_t phase = 0;
     int flip = 0;
+    bool ok = true;
+    auto rstd_of = [&](int64_t row) { return row < p.rows ? p.rstd[row] : 0.0f; };
+    float rs_next = rstd_of(first + threadIdx.y);
     for (int64_t base = first; base < p.rows; base += step, flip ^= 1) {
         const int64_t row = base + threadIdx.y;
         const bool live = row < p.rows;
-        const float rs = rstd;
-        float g[NV][VEC], u[NV][VEC], d[NV][VEC];
-        float dot = 0.0f;
+        const float rs = rs_next;
+        rs_next = rstd_of(row + step);
+        ok = mbar_wait(smem_addr(&full[slot]), phase, p.wait) && ok;
+        const uint32_t mine = ring0 + uint32_t(slot * ring.slot_bytes);
+        const uint32_t g = src[0].in_slot(mine, row), h = src[1].in_slot(mine + uint32_t(ring.array_bytes), row),
+                       d = src[2].in_slot(mine + 2u * uint32_t(ring.array_bytes), row);
+        Raw<T, VEC> rg[NV], rh[NV];
+        auto dot2 = splat<VEC>(0.0f);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const bool in = live && at_of(j) < p.width;
+            if (!live || at_of(j) >= width) continue;
+            rg[j] = load_raw_shared<T, VEC>(g + uint32_t(at_of(j)) * uint32_t(sizeof(T)));
+            rh[j] = load_raw_shared<T, VEC>(h + uint32_t(at_of(j)) * uint32_t(sizeof(T)));
+            const F32<VEC> fg = widen<T, VEC>(rg[j]), fh = widen<T, VEC>(rh[j]), w = weight(j);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float dy = in ? to_f32<T>(rg[j].v[i]) : 0.0f;
-                u[j][i] = in ? to_f32<T>(rh[j].v[i]) * rs : 0.0f;
-                d[j][i] = in && p.dh != nullptr ? to_f32<T>(rd[j].v[i]) : 0.0f;
-                g[j][i] = dy * w[j][i];
-                dw[j][i] = fmaf(dy, u[j][i], dw[j][i]);
-                dot = fmaf(g[j][i], u[j][i], dot);
-            }
+            for (int i = 0; i < F32<VEC>::PAIRS; ++i) dot2 = fma2(mul2(fg.p[i], w.p[i]), fh.p[i], dot2);
         }
-        fetch(row + step);
-        const float m = row_sum(dot, red[flip]) * p.inv_width;
-        if (live) {
+        const float sum = row_sum<true>(total(dot2), red[flip]);
+        if (base >= first + step) refill(base + int64_t(ring.slots - 1) * step, last);  // all have left the step before
+        // dx = rstd g + (-rstd mean(g u)) u + dh, with g = dy w, u = h rstd
+        const auto rs2 = splat<VEC>(rs), c2 = splat<VEC>(-rs * (sum * rs * p.inv_width));
+        T *dx = static_cast<T *>(p.dx) + row * p.lddx;
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                if (at_of(j) >= p.width) continue;
-                float o[VEC];
+        for (int j = 0; j < NV; ++j) {
+            if (!live || at_of(j) >= width) continue;
+            const F32<VEC> fg = widen<T, VEC>(rg[j]), fh = widen<T, VEC>(rh[j]), w = weight(j);
+            F32<VEC> o;
+            if (has_d) o = widen<T, VEC>(load_raw_shared<T, VEC>(d + uint32_t(at_of(j)) * uint32_t(sizeof(T))));
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = fmaf(rs, fmaf(-u[j][i], m, g[j][i]), d[j][i]);
-                store_f32<T, VEC>(static_cast<T *>(p.dx) + row * p.lddx + at_of(j), o);
+            for (int i = 0; i < F32<VEC>::PAIRS; ++i) {
+                const auto u = mul2(fh.p[i], rs2);
+                dw[j].p[i] = fma2(fg.p[i], u, dw[j].p[i]);
+                const auto wg = mul2(fg.p[i], w.p[i]);
+                o.p[i] = fma2(u, c2, has_d ? fma2(wg, rs2, o.p[i]) : mul2(wg, rs2));
             }
+            store_f32<T, VEC>(dx + at_of(j), o);
         }
+        last = slot;
+        if (++slot == ring.slots) { slot = 0; phase ^= 1u; }
     }
+    if (!ok) let_copies_land();
     if (p.partial == nullptr) return;
-    if (blockDim.y > 1) {
+    float *out = p.partial + int64_t(blockIdx.x) * p.width;
+    if (blockDim.y > 1) {  // the block's rows first, in order (the ring holds no copy in flight any more)
+        float *dw_rows = reinterpret_cast<float *>(rows);
         const int span = blockDim.x * VEC * NV;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) dw_rows[int(threadIdx.y) * span + int(at_of(j)) + i] = dw[j][i];
         __syncthreads();
-        const int t = threadIdx.y * blockDim.x + threadIdx.x;
-        for (int c = t; c < span && c < p.width; c += blockDim.x * blockDim.y) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) store_f32<float, VEC>(dw_rows + int(threadIdx.y) * span + at_of(j), dw[j]);
+        __syncthreads();
+        for (int c = tid; c < span && c < width; c += blockDim.x * blockDim.y) {
             float s = dw_rows[c];
             for (int y = 1; y < int(blockDim.y); ++y) s += dw_rows[y * span + c];
-            p.partial[int64_t(blockIdx.x) * p.width + c] = s;
+            out[c] = s;
         }
         return;
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        if (at_of(j) >= p.width) continue;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) p.partial[int64_t(blockIdx.x) * p.width + at_of(j) + i] = dw[j][i];
+        if (at_of(j) >= width) continue;
+        store_f32<float, VEC>(out + at_of(j), dw[j]);  // VEC = 8: width is a multiple of 8, the workspace aligned
+    }
+}
+
+// Any alignment and width, as rms_norm_rows_any_kernel; the dweight sums are in
+// shared memory behind the ring, one row of them per row of the block, each
+// column touched by its own thread only.
+template <typename T>
+__global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_any_kernel(const NormBackwardParams p, const RingShape ring) {
+    __shared__ float red[2][32];
+    __shared__ __align__(8) uint64_t full[kRingSlots];
+    extern __shared__ __align__(16) uint8_t rows[];
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x, width = int(p.width), tpr = int(blockDim.x);
+    float *dw_rows = reinterpret_cast<float *>(rows + ring.slots * ring.slot_bytes);
+    float *dw = dw_rows + int(threadIdx.y) * width;
+    if (tid == 0) {
+        for (int s = 0; s < ring.slots; ++s) mbar_init(smem_addr(&full[s]), 1);
+        fence_mbar_init();
+    }
+    for (int c = threadIdx.x; c < width; c += tpr) dw[c] = 0.0f;
+    __syncthreads();
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t step = int64_t(gridDim.x) * blockDim.y;
+    const int64_t first = int64_t(blockIdx.x) * blockDim.y;
+    const RowSource<T> src[3] = {{static_cast<const T *>(p.g), p.ldg}, {static_cast<const T *>(p.h), p.ldh},
+                                 {static_cast<const T *>(p.dh), p.lddh}};
+    const bool has_d = p.dh != nullptr;
+    auto refill = [&](int64_t base, int slot) {
+        if (base < p.rows) fill_slot(src, has_d ? 3 : 2, ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
+    };
+    for (int s = 0; s < ring.slots; ++s) refill(first + s * step, s);
+    const uint32_t ring0 = smem_addr(rows) + uint32_t(int(threadIdx.y) * ring.pitch);
+    int slot = 0, last = ring.slots - 1, flip = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    auto rstd_of = [&](int64_t row) { return row < p.rows ? p.rstd[row] : 0.0f; };
+    float rs_next = rstd_of(first + threadIdx.y);
+    for (int64_t base = first; base < p.rows; base += step, flip ^= 1) {
+        const int64_t row = base + threadIdx.y;
+        const bool live = row < p.rows;
+        const float rs = rs_next;
+        rs_next = rstd_of(row + step);
+        ok = mbar_wait(smem_addr(&full[slot]), phase, p.wait) && ok;
+        const uint32_t mine = ring0 + uint32_t(slot * ring.slot_bytes);
+        const uint32_t g = src[0].in_slot(mine, row), h = src[1].in_slot(mine + uint32_t(ring.array_bytes), row),
+                       d = src[2].in_slot(mine + 2u * uint32_t(ring.array_bytes), row);
+        float dot = 0.0f;
+        if (live) {
+#pragma unroll 4
+            for (int c = threadIdx.x; c < width; c += tpr)
+                dot = fmaf(lds_elem<T>(g, c) * load_weight<T, 1>(p.w, p.w_f32 != 0, c).p[0], lds_elem<T>(h, c), dot);
+        }
+        const float sum = row_sum<true>(dot, red[flip]);
+        if (base >= first + step) refill(base + int64_t(ring.slots - 1) * step, last);  // all have left the step before
+        if (live) {
+            const float m = -rs * (sum * rs * p.inv_width);
+            T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+#pragma unroll 4
+            for (int c = threadIdx.x; c < width; c += tpr) {
+                const float dy = lds_elem<T>(g, c), u = lds_elem<T>(h, c) * rs;
+                const float wg = dy * load_weight<T, 1>(p.w, p.w_f32 != 0, c).p[0];
+                dw[c] = fmaf(dy, u, dw[c]);
+                dx[c] = from_f32<T>(fmaf(u, m, fmaf(wg, rs, has_d ? lds_elem<T>(d, c) : 0.0f)));
+            }
+        }
+        last = slot;
+        if (++slot == ring.slots) { slot = 0; phase ^= 1u; }
+    }
+    if (!ok) let_copies_land();
+    if (p.partial == nullptr) return;
+    __syncthreads();
+    for (int c = tid; c < width; c += int(blockDim.x * blockDim.y)) {
+        float s = dw_rows[c];
+        for (int y = 1; y < int(blockDim.y); ++y) s += dw_rows[y * width + c];
+        p.partial[int64_t(blockIdx.x) * p.width + c] = s;
     }
 }
 
@@ -410,19 +826,13 @@ __global__ void __launch_bounds__(1024) rms_norm_backward_long_kernel(const Norm
     const T *g = static_cast<const T *>(p.g) + row * p.ldg, *h = static_cast<const T *>(p.h) + row * p.ldh;
     const T *dh = p.dh != nullptr ? static_cast<const T *>(p.dh) + row * p.lddh : nullptr;
     const float rs = p.rstd[row];
+    auto wg = [&](int64_t at) { return to_f32<T>(g[at]) * load_weight<T, 1>(p.w, p.w_f32 != 0, at).p[0]; };
     float dot = 0.0f;
+    for (int64_t at = threadIdx.x; at < p.width; at += blockDim.x) dot = fmaf(wg(at), to_f32<T>(h[at]), dot);
+    const float c = -rs * (row_sum<false>(dot, red) * rs * p.inv_width);
     for (int64_t at = threadIdx.x; at < p.width; at += blockDim.x) {
-        float w[1];
-        load_weight<T, 1>(p.w, p.w_f32 != 0, at, w);
-        dot = fmaf(to_f32<T>(g[at]) * w[0], to_f32<T>(h[at]) * rs, dot);
-    }
-    const float m = row_sum(dot, red) * p.inv_width;
-    for (int64_t at = threadIdx.x; at < p.width; at += blockDim.x) {
-        float w[1];
-        load_weight<T, 1>(p.w, p.w_f32 != 0, at, w);
-        const float u = to_f32<T>(h[at]) * rs;
         const float d = dh != nullptr ? to_f32<T>(dh[at]) : 0.0f;
-        static_cast<T *>(p.dx)[row * p.lddx + at] = from_f32<T>(fmaf(rs, fmaf(-u, m, to_f32<T>(g[at]) * w[0]), d));
+        static_cast<T *>(p.dx)[row * p.lddx + at] = from_f32<T>(fmaf(to_f32<T>(h[at]) * rs, c, fmaf(wg(at), rs, d)));
     }
 }
 
