@@ -187,30 +187,65 @@ uint32_t linear_idesc(int32_t type, bool a_mn, bool b_mn, uint32_t m, uint32_t n
 // ------------------------------------------------------------------ linear: which kernel
 struct LinearPlan {
     bool pair;
-    int T, split, stages;
+    int T, split, stages;   // linear_split
+    int64_t whole, units;   // linear_pair: whole tiles, and units in all
 };
 
-// linear_split's shape for M rows. T is the smallest row count that holds them
-// (an M-major A comes in chunks of 64 rows). Up to 64 rows a CTA's ring is
-// kept under half the SM's shared memory, so that two CTAs share an SM and one's
-// set-up and sum overlap the other's stream.
-LinearPlan plan_split(int64_t M, int64_t N, int64_t num_kb, bool a_mn, int num_sms) {
-    LinearPlan pl{false, 16, 1, 6};
-    while (pl.T < 256 && (pl.T < M || (a_mn && pl.T < 64))) pl.T *= 2;
-    const bool two = pl.T <= 64;
-    pl.stages = pl.T <= 16 ? 6 : pl.T <= 32 ? 5 : pl.T <= 64 ? 4 : pl.T <= 128 ? 6 : 4;
-    const int64_t tiles = cdiv(N, lin::SPLIT_ROWS) * cdiv(M, pl.T);
-    const int64_t slots = two ? 2 * int64_t(num_sms) : num_sms;
-    while (pl.split < lin::MAX_SPLIT && tiles * pl.split * 2 <= slots && pl.split * 2 * 4 <= num_kb) pl.split *= 2;
-    return pl;
+// Estimated SM cycles, from rates measured on GB300: an SM fills shared memory
+// with about 60 bytes a cycle, the tensor core takes 2 cycles per column of a
+// 128-row, 128-byte-deep step, and a CTA's set-up and drain take some microseconds.
+constexpr double kFillBytes = 60.0, kLatency = 2800.0, kSplitFixed = 4500.0, kPairFixed = 6000.0, kPairStep = 560.0;
+
+// linear_split's ring depth: up to 64 rows it is kept under half the SM's shared
+// memory, so that two CTAs share an SM and one's set-up and sum overlap the
+// other's stream.
+int split_stages(int T) { return T <= 16 ? 6 : T <= 32 ? 5 : T <= 64 ? 4 : T <= 128 ? 6 : 4; }
+
+// linear_split's shape, rows per CTA T (an M-major A comes in chunks of 64 rows)
+// and K slices S, by the estimate. What one CTA draws is bound by its ring over
+// the memory latency as well: 32 x 8 CTAs read 4096 x 4096 weights for one token
+// faster than 32 x 4 (9.5 against 11.0 us).
+double plan_split(int64_t M, int64_t N, int64_t num_kb, bool a_mn, int num_sms, LinearPlan *pl) {
+    double best = 1e300;
+    for (int T = a_mn ? 64 : 16; T <= 256; T *= 2) {
+        const int64_t tiles = cdiv(N, lin::SPLIT_ROWS) * cdiv(M, T);
+        const int per_sm = T <= 64 ? 2 : 1;
+        const double stage = lin::W_STAGE_BYTES + 128.0 * T;
+        for (int S = 1; S <= lin::MAX_SPLIT && (S == 1 || S * 2 <= num_kb); S *= 2) {
+            const int64_t ctas = tiles * S, slots = int64_t(per_sm) * num_sms;
+            const double resident = ctas <= num_sms ? 1.0 : double(per_sm);  // CTAs that share an SM's rates
+            const double fill = std::min(kFillBytes / resident, split_stages(T) * stage / kLatency);
+            const double step = std::max(2.0 * T * resident, stage / fill);
+            const double cost = double(cdiv(ctas, slots)) * (double(cdiv(num_kb, S)) * step + kSplitFixed + (S > 1 ? 500.0 : 0.0) + 6.0 * T);
+            if (cost < best) {
+                best = cost;
+                pl->T = T;
+                pl->split = S;
+            }
+        }
+        if (T >= M) break;
+    }
+    pl->stages = split_stages(pl->T);
+    return best;
+}
+
+// linear_pair's units: whole tiles for as many full rounds of the GPU's pairs as
+// there are, then, where the tiles that remain fit into one round as halves, those.
+// (4096 x 4096 x 8192: 256 tiles on 76 pairs are 3 rounds and 56 halves.)
+double plan_pair(int64_t M, int64_t N, int64_t num_kb, int max_pairs, LinearPlan *pl) {
+    const int64_t tiles = cdiv(M, pair::TILE_M) * cdiv(N, pair::TILE_N), rest = tiles % max_pairs;
+    const bool halves = rest > 0 && 2 * rest <= max_pairs;
+    pl->whole = halves ? tiles - rest : tiles;
+    pl->units = pl->whole + (halves ? 2 * rest : 0);
+    const double rounds = double(cdiv(pl->whole, max_pairs)) + (halves ? 0.58 : 0.0);
+    return rounds * double(num_kb) * kPairStep + kPairFixed;
 }
 
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t num_kb, bool a_mn, uint32_t flags, const DeviceState &ds) {
-    LinearPlan pl = plan_split(M, N, num_kb, a_mn, ds.num_sms);
-    const int64_t pair_tiles = cdiv(M, pair::TILE_M) * cdiv(N, pair::TILE_N);
-    if (flags & GEMM_LINEAR_PAIR) pl.pair = true;
-    else if (flags & GEMM_LINEAR_SPLIT) pl.pair = false;
-    else pl.pair = M > 256 && pair_tiles * 4 >= 3 * int64_t(ds.max_pairs);
+    LinearPlan pl{};
+    const double split = plan_split(M, N, num_kb, a_mn, ds.num_sms, &pl);
+    const double pair = plan_pair(M, N, num_kb, ds.max_pairs, &pl);
+    pl.pair = (flags & GEMM_LINEAR_PAIR) || (!(flags & GEMM_LINEAR_SPLIT) && pair <= split);
     return pl;
 }
 
@@ -242,14 +277,16 @@ gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t 
     p.wait.timeout_ns = g_timeout_ns.load();
     p.wait.epoch = next_epoch();
     const LinearPlan pl = plan_linear(M, N, p.num_kb, A.mn_major, flags, *ds);
-    CUtensorMap tmA, tmB, tmC, tmR, tmP;
+    CUtensorMap tmA, tmB, tmBhalf, tmC, tmR, tmP;
     cudaError_t err;
     if (pl.pair) {
         const int64_t nm = cdiv(M, pair::TILE_M), nn = cdiv(N, pair::TILE_N);
         if (nm * nn > kMaxDim / 2) return GEMM_ERR_UNSUPPORTED;
         std::memset(&tmC, 0, sizeof(tmC));
         tmR = tmP = tmC;
-        if (!encode_operand(&tmA, A, pair::CTA_M) || !encode_operand(&tmB, B, pair::CTA_N)) return GEMM_ERR_CUDA;
+        if (!encode_operand(&tmA, A, pair::CTA_M) || !encode_operand(&tmB, B, pair::CTA_N) ||
+            !encode_operand(&tmBhalf, B, pair::CTA_N / 2))
+            return GEMM_ERR_CUDA;
         // a clipped TMA store writes whole 16-byte granules: C's and pre's rows must end on one
         const bool ends = (N * es) % 16 == 0;
         p.e.c_tma = ends && tma_ok(e.c, N, e.ldc, es);
@@ -263,35 +300,40 @@ gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t 
         p.sched.nn = int32_t(nn);
         p.sched.group_m = 8;
         p.sched.grouped = 1;
-        p.num_tiles = int32_t(nm * nn);
+        p.num_units = int32_t(pl.units);
+        p.whole = int32_t(pl.whole);
         p.idesc = linear_idesc(A.type, A.mn_major, B.mn_major, 2 * pair::CTA_M, pair::TILE_N);
+        p.idesc_half = linear_idesc(A.type, A.mn_major, B.mn_major, 2 * pair::CTA_M, pair::TILE_N / 2);
         p.bufs = e.r != nullptr || e.pre != nullptr ? 2 : 1;
         p.stages = p.bufs == 2 ? 5 : 6;
-        const dim3 grid(unsigned(2 * std::min<int64_t>(p.num_tiles, ds->max_pairs)));
+        const dim3 grid(unsigned(2 * std::min<int64_t>(p.num_units, ds->max_pairs)));
         auto *kernel = f8 ? (es == 4 ? linear_pair<true, 4> : linear_pair<true, 2>)
                           : (es == 4 ? linear_pair<false, 4> : linear_pair<false, 2>);
-        err = launch_shape(kernel, grid, dim3(lin::PAIR_THREADS), lin::PAIR_SMEM, 1, stream, tmA, tmB, tmC, tmR, tmP, p);
+        err = launch_shape(kernel, grid, dim3(lin::PAIR_THREADS), lin::PAIR_SMEM, 1, stream, tmA, tmB, tmBhalf, tmC, tmR,
+                           tmP, p);
     } else {
         const int64_t nm = cdiv(M, pl.T), nn = cdiv(N, lin::SPLIT_ROWS);
         if (nm * nn > kMaxDim / lin::MAX_SPLIT) return GEMM_ERR_UNSUPPORTED;
         if (!encode_operand(&tmA, A, pl.T) || !encode_operand(&tmB, B, lin::SPLIT_ROWS)) return GEMM_ERR_CUDA;
         p.sched.nm = int32_t(nm);
         p.sched.nn = int32_t(nn);
-        p.num_tiles = int32_t(nm * nn);
+        p.num_units = int32_t(nm * nn);
         p.T = pl.T;
         p.tmem_cols = pl.T < 32 ? 32 : pl.T;
         p.split = pl.split;
         p.stages = pl.stages;
         // transposed product: the weights are the 128-row operand
         p.idesc = linear_idesc(A.type, B.mn_major, A.mn_major, lin::SPLIT_ROWS, uint32_t(pl.T));
-        p.e.vec4 = quad_aligned(e.c, e.ldc, es) && (e.pre == nullptr || quad_aligned(e.pre, e.ldp, es));
-        const dim3 grid(unsigned(int64_t(p.num_tiles) * pl.split));
+        p.e.vec4 = quad_aligned(e.c, e.ldc, es) && (e.pre == nullptr || quad_aligned(e.pre, e.ldp, es)) &&
+                   (e.r == nullptr || quad_aligned(e.r, e.ldr, es));
+        const dim3 grid(unsigned(int64_t(p.num_units) * pl.split));
         err = launch_shape(f8 ? linear_split<true> : linear_split<false>, grid, dim3(lin::SPLIT_THREADS),
                            lin::split_smem(pl.stages, pl.T), pl.split, stream, tmB, tmA, p);
     }
     if (log_enabled())
-        std::fprintf(stderr, "[gemm_linear] M=%lld N=%lld K=%lld kernel=%s T=%d split=%d stages=%d tiles=%d\n", (long long)M,
-                     (long long)N, (long long)K, pl.pair ? "pair" : "split", p.T, p.split, p.stages, p.num_tiles);
+        std::fprintf(stderr, "[gemm_linear] M=%lld N=%lld K=%lld kernel=%s T=%d split=%d stages=%d units=%d whole=%d\n", (long long)M,
+                     (long long)N, (long long)K, pl.pair ? "pair" : "split", p.T, p.split, p.stages, p.num_units,
+                     p.whole);
     return err == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 

@@ -44,20 +44,36 @@ __device__ __forceinline__ void mma_f8_pair_elect(uint32_t d_tmem, uint64_t a_de
 }
 
 // ------------------------------------------------------------------ activations
-// The library's exponential (__expf) is within 2 + |1.2 x| units in the last
-// place and the quotients within 2, far inside the 16-bit outputs' rounding
-// and about 1e-6 for fp32 ones; the erf is CUDA's erff.
+// __expf is within 2 + |1.2 x| units in the last place and the quotients within
+// 2, far inside the 16-bit outputs' rounding and about 1e-6 for fp32 ones. The
+// normal distribution's cumulative function is Abramowitz & Stegun 26.2.17: for
+// x >= 0, 1 - Z(x) (b1 t + ... + b5 t^5) with t = 1 / (1 + 0.2316419 x) and Z the
+// density, off by less than 7.5e-8; the density is what gelu's slope needs too.
+// With CUDA's erff and __expf instead, D = G gelu'(P) of 4096 x 8192 took 82 us.
 constexpr uint32_t kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4;  // GEMM_ACT_*
-constexpr float kSqrtHalf = 0.70710678118654752f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTwoSqrt2OverPi = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+
+__device__ __forceinline__ void normal_parts(float x, float &cdf, float &density) {
+    density = kInvSqrt2Pi * __expf(-0.5f * x * x);
+    const float t = __fdividef(1.0f, fmaf(0.2316419f, fabsf(x), 1.0f));
+    float q = fmaf(t, 1.330274429f, -1.821255978f);
+    q = fmaf(t, q, 1.781477937f);
+    q = fmaf(t, q, -0.356563782f);
+    q = fmaf(t, q, 0.319381530f);
+    q = q * t * density;
+    cdf = x < 0.0f ? q : 1.0f - q;
+}
 
 template <uint32_t ACT>
 __device__ __forceinline__ float act_value(float x) {
     if constexpr (ACT == kActRelu) return x < 0.0f ? 0.0f : x;
     else if constexpr (ACT == kActSilu) return __fdividef(x, 1.0f + __expf(-x));
-    else if constexpr (ACT == kActGelu) return 0.5f * x * (1.0f + erff(x * kSqrtHalf));
-    else if constexpr (ACT == kActGeluTanh)
+    else if constexpr (ACT == kActGelu) {
+        float cdf, density;
+        normal_parts(x, cdf, density);
+        return x * cdf;
+    } else if constexpr (ACT == kActGeluTanh)
         return __fdividef(x, 1.0f + __expf(-kTwoSqrt2OverPi * fmaf(0.044715f * x * x, x, x)));
     else return x;
 }
@@ -69,7 +85,9 @@ __device__ __forceinline__ float act_slope(float x) {
         const float s = __fdividef(1.0f, 1.0f + __expf(-x));
         return s * fmaf(x, 1.0f - s, 1.0f);
     } else if constexpr (ACT == kActGelu) {
-        return fmaf(x * kInvSqrt2Pi, __expf(-0.5f * x * x), 0.5f * (1.0f + erff(x * kSqrtHalf)));
+        float cdf, density;
+        normal_parts(x, cdf, density);
+        return fmaf(x, density, cdf);
     } else if constexpr (ACT == kActGeluTanh) {
         // x s(z) with z = c (x + 0.044715 x^3): s + x s (1 - s) z'
         const float s = __fdividef(1.0f, 1.0f + __expf(-kTwoSqrt2OverPi * fmaf(0.044715f * x * x, x, x)));
@@ -137,8 +155,12 @@ struct EpilogueParams {
 struct LinearParams {
     int64_t M, N;
     Sched sched;
-    int32_t num_tiles, num_kb;
+    int32_t num_kb;
     uint32_t a_mn, b_mn, idesc;
+    // linear_pair: units below `whole` are tiles; from there on, halves (128
+    // columns) of the tiles `whole`, whole + 1, ...
+    int32_t num_units, whole;
+    uint32_t idesc_half;
     int32_t stages, bufs;     // linear_pair: ring depth, staging buffers per epilogue warp
     int32_t T, tmem_cols;     // linear_split: rows of C per CTA, TMEM columns
     int32_t split;            // linear_split: CTAs of a cluster along K
@@ -163,32 +185,57 @@ constexpr int PAIR_SMEM = PAIR_OFF_SLOT + 16 + 1024;
 static_assert(PAIR_SMEM <= 232448, "exceeds the 227 KiB per-CTA shared memory limit");
 }  // namespace lin
 
-// The epilogue of one warp: 32 rows (TMEM lanes) by the 128 columns of its half.
-// OB: bytes per element of C. A chunk is 128 bytes of each row.
+// A unit of linear_pair: the first row and column of this CTA's part of the
+// output and the unit's columns (256, or 128 for half a tile).
+struct Unit {
+    int64_t row0, col0;
+    int32_t cols;
+};
+__device__ __forceinline__ Unit unit_of(const LinearParams &p, int32_t u, uint32_t rank) {
+    const bool half = u >= p.whole;
+    const int32_t v = u - p.whole;
+    int32_t tm, tn;
+    tile_coords(half ? p.whole + (v >> 1) : u, p.sched, tm, tn);
+    return Unit{int64_t(tm) * pair::TILE_M + int64_t(rank) * pair::CTA_M,
+                int64_t(tn) * pair::TILE_N + (half && (v & 1) ? pair::TILE_N / 2 : 0), half ? pair::TILE_N / 2 : pair::TILE_N};
+}
+
+// The epilogue of one warp: 32 rows (TMEM lanes) by half the unit's columns.
+// OB: bytes per element of C. A chunk is 128 bytes of each row; the warp's chunks
+// take its staging buffers in turn.
 template <bool kF8, int OB>
 struct PairEpilogue {
-    static constexpr int CHUNK = 128 / OB;       // columns: 64 or 32
-    static constexpr int PER_TILE = 128 / CHUNK;  // chunks of the warp's half: 2 or 4
+    static constexpr int CHUNK = 128 / OB;  // columns: 64 or 32
     const LinearParams &p;
     const CUtensorMap *tmC, *tmR, *tmP;
     uint32_t stg, rbar;  // this warp's staging buffers and residual barriers (2)
-    int lane;
-    uint32_t r_issued[2], r_used[2];
+    int lane, q, half;   // TMEM lane quarter, column half
+    uint32_t rank;
+    int32_t next_u, next_c, step;  // the next chunk to fetch the residual of; units between this CTA's
+    uint32_t fetched, used;        // residual chunks asked for and taken
 
-    __device__ __forceinline__ uint32_t buf(int b) const { return stg + uint32_t(b) * lin::BUF_BYTES; }
+    __device__ __forceinline__ uint32_t buf(uint32_t b) const { return stg + b * lin::BUF_BYTES; }
     __device__ __forceinline__ bool prefetches() const { return p.e.r != nullptr && p.e.r_tma && p.e.pre == nullptr; }
 
-    // Start fetching the residual's 32 rows x CHUNK columns into buffer b (whole warp).
-    __device__ __forceinline__ void fetch_residual(int b, int64_t row0, int64_t col0) {
+    // Start fetching the residual's 32 rows x CHUNK columns of the next chunk that
+    // has not been asked for into its buffer (whole warp; two buffers).
+    __device__ __forceinline__ void fetch_residual() {
+        if (next_u >= p.num_units) return;
+        const Unit u = unit_of(p, next_u, rank);
         if (lane == 0) {
+            const uint32_t b = fetched & 1u;
             mbar_arrive_expect_tx(rbar + 8u * b, lin::BUF_BYTES);
-            tma_load_2d(buf(b), tmR, int32_t(col0), int32_t(row0), rbar + 8u * b);
+            tma_load_2d(buf(b), tmR, int32_t(u.col0) + half * (u.cols / 2) + next_c * CHUNK, int32_t(u.row0) + q * 32, rbar + 8u * b);
         }
-        ++r_issued[b];
+        ++fetched;
+        if (++next_c * CHUNK == u.cols / 2) {
+            next_c = 0;
+            next_u += step;
+        }
     }
 
     // Buffer b <- the residual's 32 rows x CHUNK columns, with plain loads.
-    __device__ __forceinline__ void load_residual(int b, int64_t row0, int64_t col0) {
+    __device__ __forceinline__ void load_residual(uint32_t b, int64_t row0, int64_t col0) {
         const int64_t rows = p.M - row0;
         constexpr int PER_LANE = CHUNK / 32;
         const int64_t col = col0 + PER_LANE * lane;
@@ -210,7 +257,7 @@ struct PairEpilogue {
     }
 
     // Buffer b -> 32 rows x CHUNK columns of `dst`, by TMA or plain stores.
-    __device__ __forceinline__ void store(int b, void *dst, int64_t ld, const CUtensorMap *map, bool tma, int64_t row0,
+    __device__ __forceinline__ void store(uint32_t b, void *dst, int64_t ld, const CUtensorMap *map, bool tma, int64_t row0,
                                           int64_t col0) {
         if (tma) {
             fence_proxy_async_smem();
@@ -244,8 +291,8 @@ struct PairEpilogue {
         fence_proxy_async_smem();  // before a TMA fetch writes it
     }
 
-    // x -> units of this lane's row of buffer b; `half` of the chunk (16-bit: two halves of 32 columns)
-    __device__ __forceinline__ void put(int b, int half, const float (&x)[32]) {
+    // x -> this lane's row of buffer b; `part`: which 32 columns of a 16-bit chunk
+    __device__ __forceinline__ void put(uint32_t b, int part, const float (&x)[32]) {
         if constexpr (OB == 4) {
 #pragma unroll
             for (int u = 0; u < 8; ++u)
@@ -254,14 +301,14 @@ struct PairEpilogue {
         } else {
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                st_shared_v4(buf(b) + swz128(lane, 4 * half + u), pack_16x2(x[8 * u], x[8 * u + 1], p.e.type),
+                st_shared_v4(buf(b) + swz128(lane, 4 * part + u), pack_16x2(x[8 * u], x[8 * u + 1], p.e.type),
                              pack_16x2(x[8 * u + 2], x[8 * u + 3], p.e.type),
                              pack_16x2(x[8 * u + 4], x[8 * u + 5], p.e.type),
                              pack_16x2(x[8 * u + 6], x[8 * u + 7], p.e.type));
         }
     }
 
-    __device__ __forceinline__ void add_residual(int b, int half, float (&x)[32]) {
+    __device__ __forceinline__ void add_residual(uint32_t b, int part, float (&x)[32]) {
         if constexpr (OB == 4) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -274,7 +321,7 @@ struct PairEpilogue {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 uint32_t w[4];
-                ld_shared_v4(buf(b) + swz128(lane, 4 * half + u), w[0], w[1], w[2], w[3]);
+                ld_shared_v4(buf(b) + swz128(lane, 4 * part + u), w[0], w[1], w[2], w[3]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 f = unpack_16x2(w[i], p.e.type);
@@ -285,12 +332,11 @@ struct PairEpilogue {
         }
     }
 
-    // One tile: rows row0 .. row0 + 31, columns col0 .. col0 + 127. `next`: the
-    // same for this warp's next tile (next_row0 < 0: none). False if a wait ran out.
+    // One unit's part of this warp: rows row0 .. row0 + 31, `groups` (4 or 2) times
+    // 32 columns from col0 on. False if a wait ran out.
     template <typename Drained>
-    __device__ __forceinline__ bool tile(uint32_t t_addr, int64_t row0, int64_t col0, int64_t next_row0,
-                                         int64_t next_col0, const float (&bias)[4], const float (&sb)[4], float sa,
-                                         Drained drained) {
+    __device__ __forceinline__ bool unit(uint32_t t_addr, int64_t row0, int64_t col0, int groups, const float (&bias)[4],
+                                         const float (&sb)[4], float sa, Drained drained) {
         const bool has_r = p.e.r != nullptr, has_p = p.e.pre != nullptr, pref = prefetches();
         const bool two = p.bufs == 2;
         bool ok = true;
@@ -298,23 +344,21 @@ struct PairEpilogue {
         tmem_ld_32x32b_x32(t_addr, v[0]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            if (j >= groups) break;
             const int c = j * 32 / CHUNK;
-            const int half = OB == 4 ? 0 : (j & 1);
-            const int b = has_p ? 1 : (two ? (c & 1) : 0);  // C's buffer; pre's is 0
+            const int part = OB == 4 ? 0 : (j & 1);  // which 32 columns of a 16-bit chunk
+            // C's buffer: with pre, 0 is pre's; chunks of a unit come in pairs except for
+            // half a tile in 16 bits, so with prefetches the count of chunks decides
+            const uint32_t b = has_p ? 1u : !two ? 0u : pref ? (used & 1u) : uint32_t(c & 1);
             tmem_ld_wait();
-            if (j < 3) tmem_ld_32x32b_x32(t_addr + (j + 1) * 32, v[(j + 1) & 1]);
+            if (j + 1 < groups) tmem_ld_32x32b_x32(t_addr + (j + 1) * 32, v[(j + 1) & 1]);
             else drained();
-            if (half == 0) {  // the buffers of a new chunk
-                if (pref) {  // two buffers, taken in turn
-                    if (!__all_sync(0xffffffffu, mbar_wait(rbar + 8u * (c & 1), r_used[c & 1] & 1u, p.wait))) ok = false;
-                    else ++r_used[c & 1];
+            if (part == 0) {  // the buffers of a new chunk
+                if (pref) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(rbar + 8u * b, (used >> 1) & 1u, p.wait))) ok = false;
                 } else {
-                    // the buffer's previous store has read it; with two buffers taken in turn,
-                    // only the store before the last must have (pre and C go out as two stores)
-                    if (lane == 0) {
-                        if (two && !has_p) bulk_wait_group_read<1>();
-                        else bulk_wait_group_read<0>();
-                    }
+                    // the buffer's previous store has read it
+                    if (lane == 0) bulk_wait_group_read<0>();
                     __syncwarp();
                     if (has_r) load_residual(b, row0, col0 + c * CHUNK);
                 }
@@ -330,45 +374,36 @@ struct PairEpilogue {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] += __shfl_sync(0xffffffffu, bias[j], i);
             }
-            if (has_p) put(0, half, x);
+            if (has_p) put(0, part, x);
             apply_act(p.e.act, x);
-            if (has_r) add_residual(b, half, x);
-            put(b, half, x);
-            if (half == (OB == 4 ? 0 : 1)) {
+            if (has_r) add_residual(b, part, x);
+            put(b, part, x);
+            if (part == (OB == 4 ? 0 : 1)) {
                 if (has_p) store(0, p.e.pre, p.e.ldp, tmP, p.e.p_tma != 0, row0, col0 + c * CHUNK);
                 store(b, p.e.c, p.e.ldc, tmC, p.e.c_tma != 0, row0, col0 + c * CHUNK);
-                if (pref) {  // refill this buffer for the chunk after the next, of this tile or the next one
-                    const int cn = c + 2;
-                    const bool here = cn < PER_TILE;
-                    if (here || next_row0 >= 0) {
-                        if (lane == 0) bulk_wait_group_read<0>();
-                        __syncwarp();
-                        fetch_residual(c & 1, here ? row0 : next_row0,
-                                       (here ? col0 : next_col0) + (here ? cn : cn - PER_TILE) * CHUNK);
-                    }
+                if (pref) {  // this buffer takes the chunk after the next
+                    ++used;
+                    if (lane == 0) bulk_wait_group_read<0>();
+                    __syncwarp();
+                    if (ok) fetch_residual();
                 }
             }
         }
         return ok;
     }
 
-    // Before the first tile.
-    __device__ __forceinline__ void begin(int64_t row0, int64_t col0) {
-        r_issued[0] = r_issued[1] = r_used[0] = r_used[1] = 0;
+    // Before the first unit.
+    __device__ __forceinline__ void begin() {
         if (!prefetches()) return;
-        fetch_residual(0, row0, col0);
-        fetch_residual(1, row0, col0 + CHUNK);
+        fetch_residual();
+        fetch_residual();
     }
 
-    // After the last tile, or after a wait ran out: no copy may still be on its
+    // After the last unit, or after a wait ran out: no copy may still be on its
     // way into or out of this warp's buffers when the CTA ends.
     __device__ __forceinline__ void end() {
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-            while (r_used[b] < r_issued[b]) {
-                mbar_wait_slow(rbar + 8u * b, r_used[b] & 1u, cleanup_wait(p.wait), false);
-                ++r_used[b];
-            }
+        for (; used < fetched; ++used)
+            mbar_wait_slow(rbar + 8u * (used & 1u), (used >> 1) & 1u, cleanup_wait(p.wait), false);
         if (lane == 0) bulk_wait_group<0>();
         __syncwarp();
     }
@@ -377,8 +412,8 @@ struct PairEpilogue {
 template <bool kF8, int OB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1)
     linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmR,
-                const __grid_constant__ CUtensorMap tmP, const LinearParams p) {
+                const __grid_constant__ CUtensorMap tmBhalf, const __grid_constant__ CUtensorMap tmC,
+                const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmP, const LinearParams p) {
     constexpr int MAXST = lin::PAIR_STAGES;
     constexpr int BKE = kF8 ? 128 : 64;  // K per stage, elements
     constexpr int MMA_WARP = 1, EPI_WARP0 = 2;
@@ -449,18 +484,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
         uint32_t stage = 0, phase = 0, issued = 0;
         bool ok = true;
         const int na = p.a_mn ? pair::CTA_M / MN_CHUNK : 1;  // copies of A per stage
-        const int nb = p.b_mn ? pair::CTA_N / MN_CHUNK : 1;  // copies of B per stage
-        for (int32_t u = pair_id; ok && u < p.num_tiles; u += num_pairs) {
-            int32_t tm, tn;
-            tile_coords(u, p.sched, tm, tn);
-            const int32_t m0 = tm * pair::TILE_M + int32_t(rank) * pair::CTA_M;
-            const int32_t n0 = tn * pair::TILE_N + int32_t(rank) * pair::CTA_N;
+        // All k-blocks of one unit. kHalf is a template argument because a map chosen at
+        // run time in the inner loop costs 6 % of the whole kernel (4096 x 8192 x 8192
+        // e4m3: 161 -> 171 us).
+        auto load_unit = [&](const Unit &un, auto is_half) {
+            constexpr bool kHalf = decltype(is_half)::value;
+            constexpr int CTA_COLS = kHalf ? pair::CTA_N / 2 : pair::CTA_N;  // columns of B this CTA loads
+            constexpr uint32_t TX = 2u * uint32_t(pair::A_STAGE_BYTES + CTA_COLS * 128);
+            const int nb = p.b_mn ? CTA_COLS / MN_CHUNK : 1;  // copies of B per stage
+            const int32_t m0 = int32_t(un.row0), n0 = int32_t(un.col0) + int32_t(rank) * CTA_COLS;
             for (int32_t kb = 0; kb < num_kb; ++kb) {
                 if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, p.wait))) {
                     ok = false;
                     break;
                 }
-                if (lane == 0 && rank == 0) mbar_arrive_expect_tx(full_bar(stage), pair::PAIR_TX_BYTES);
+                if (lane == 0 && rank == 0) mbar_arrive_expect_tx(full_bar(stage), TX);
                 const uint32_t fb = mapa_shared(full_bar(stage), 0);
                 const int32_t k0 = kb * BKE;
                 if (lane < na + nb) {  // lane: copy `lane` of A, or copy `lane - na` of B
@@ -470,12 +508,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
                                          uint32_t(c) * MN_CHUNK_BYTES;
                     const bool mn_major = (is_a ? p.a_mn : p.b_mn) != 0;
                     const int32_t mn = (is_a ? m0 : n0) + c * MN_CHUNK;
-                    tma_load_2d_pair(dst, is_a ? &tmA : &tmB, mn_major ? mn : k0, mn_major ? k0 : mn, fb);
+                    tma_load_2d_pair(dst, is_a ? &tmA : kHalf ? &tmBhalf : &tmB, mn_major ? mn : k0, mn_major ? k0 : mn, fb);
                 }
                 ++issued;
                 if (++stage == uint32_t(NST)) { stage = 0; phase ^= 1u; }
             }
-        }
+        };
+        int32_t u = pair_id;
+        for (; ok && u < p.whole; u += num_pairs) load_unit(unit_of(p, u, rank), std::false_type());
+        for (; ok && u < p.num_units; u += num_pairs) load_unit(unit_of(p, u, rank), std::true_type());
         if (!ok && lane == 0) {
             if (rank == 0) {
                 // Let the copies counted on this CTA's barriers land before exiting.
@@ -497,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
             // One release at cluster scope per tile tells CTA 0 that all of this CTA's
             // epilogue warps have drained the accumulator.
             int32_t it = 0;
-            for (int32_t u = pair_id; u < p.num_tiles; u += num_pairs, ++it) {
+            for (int32_t u = pair_id; u < p.num_units; u += num_pairs, ++it) {
                 const uint32_t acc = it & 1;
                 if (!__all_sync(0xffffffffu, mbar_wait(tdone_bar(acc), (uint32_t(it) >> 1) & 1u, p.wait))) break;
                 if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar(acc), 0));
@@ -510,8 +551,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
             int32_t it = 0;
             const DescStep da = make_desc_step(sA, p.a_mn, pair::A_STAGE_BYTES);
             const DescStep db = make_desc_step(sB, p.b_mn, pair::B_STAGE_BYTES);
-            const uint32_t idesc = p.idesc;
-            for (int32_t u = pair_id; ok && u < p.num_tiles; u += num_pairs, ++it) {
+            for (int32_t u = pair_id; ok && u < p.num_units; u += num_pairs, ++it) {
+                const uint32_t idesc = u < p.whole ? p.idesc : p.idesc_half;
                 const uint32_t acc = it & 1, use = it >> 1;
                 if (!__all_sync(0xffffffffu, mbar_wait_cluster(tempty_bar(acc), (use & 1u) ^ 1u, p.wait))) {
                     ok = false;
@@ -548,30 +589,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const int ew = warp - EPI_WARP0;
         const int half = ew / 4;  // columns [128 half, 128 half + 128) of the tile
-        PairEpilogue<kF8, OB> ep{p, &tmC, &tmR, &tmP, sE + uint32_t(ew) * uint32_t(p.bufs) * lin::BUF_BYTES,
-                                 res_bar0 + 16u * ew, lane, {0, 0}, {0, 0}};
-        auto place = [&](int32_t u, int64_t &row0, int64_t &col0) {
-            int32_t tm, tn;
-            tile_coords(u, p.sched, tm, tn);
-            row0 = int64_t(tm) * pair::TILE_M + int64_t(rank) * pair::CTA_M + q * 32;
-            col0 = int64_t(tn) * pair::TILE_N + half * 128;
-        };
-        int64_t row0 = -1, col0 = 0;
-        if (pair_id < p.num_tiles) {
-            place(pair_id, row0, col0);
-            ep.begin(row0, col0);
-        }
+        PairEpilogue<kF8, OB> ep{p,    &tmC, &tmR, &tmP,    sE + uint32_t(ew) * uint32_t(p.bufs) * lin::BUF_BYTES,
+                                 res_bar0 + 16u * ew, lane, q, half, rank, pair_id, 0, num_pairs, 0, 0};
+        ep.begin();
         int32_t it = 0;
-        for (int32_t u = pair_id; u < p.num_tiles; u += num_pairs, ++it) {
+        for (int32_t u = pair_id; u < p.num_units; u += num_pairs, ++it) {
             const uint32_t acc = it & 1, use = it >> 1;
-            int64_t nrow = -1, ncol = 0;
-            if (u + num_pairs < p.num_tiles) place(u + num_pairs, nrow, ncol);
+            const Unit un = unit_of(p, u, rank);
+            const int32_t first = half * (un.cols / 2);  // this warp's first column of the unit
+            const int64_t row0 = un.row0 + q * 32, col0 = un.col0 + first;
+            const int groups = un.cols / 64;
             // column factors and the row's, one column of each 32 per lane
             float bias[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {1.f, 1.f, 1.f, 1.f}, sa = 1.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int64_t col = col0 + 32 * j + lane;
-                if (col < p.N) {
+                if (j < groups && col < p.N) {
                     if (p.e.bias != nullptr) bias[j] = load_elem(p.e.bias, p.e.bias_type, col);
                     if (kF8) sb[j] = p.e.sb[col];
                 }
@@ -587,11 +620,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
                     if (rank == 0) mbar_arrive(tempty_bar(acc));  // the MMA warp is in this CTA
                 }
             };
-            if (!ep.tile(tmem_base + (uint32_t(q * 32) << 16) + acc * pair::TILE_N + half * 128, row0, col0, nrow, ncol,
-                         bias, sb, sa, release))
+            if (!ep.unit(tmem_base + (uint32_t(q * 32) << 16) + acc * pair::TILE_N + first, row0, col0, groups, bias, sb, sa,
+                         release))
                 break;
-            row0 = nrow;
-            col0 = ncol;
         }
         ep.end();
     }
@@ -627,11 +658,103 @@ __device__ __forceinline__ float4 ld_dsmem_v4(uint32_t cluster_addr) {
     return v;
 }
 
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
 // The epilogue on one value of C.
 __device__ __forceinline__ float act_one(uint32_t act, float x) {
     float v[1] = {x};
     apply_act(act, v);
     return v[0];
+}
+
+// Sums the S partial tiles' rows that fall to warp `ew` of CTA `rank` and runs
+// the epilogue on them. A lane holds four columns: consecutive ones where C, pre
+// and residual take vectors of four, else 32 apart, so that the stores of a warp
+// are contiguous either way.
+template <bool kF8, int S>
+__device__ __forceinline__ void split_rows(const LinearParams &p, uint32_t base, uint32_t rank, int ew, int lane, int32_t m0,
+                                           int32_t n0, int valid) {
+    constexpr int U = lin::MAX_SPLIT / S;  // rows at a time
+    const EpilogueParams &e = p.e;
+    const bool vec = e.vec4 && n0 + lin::SPLIT_ROWS <= p.N;
+    int col[4];
+    float bias[4], sb[4];
+    bool in[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        col[i] = vec ? lane * 4 + i : lane + 32 * i;
+        const int64_t n = int64_t(n0) + col[i];
+        in[i] = n < p.N;
+        bias[i] = in[i] && e.bias != nullptr ? load_elem(e.bias, e.bias_type, n) : 0.0f;
+        sb[i] = kF8 && in[i] ? e.sb[n] : 1.0f;
+    }
+    for (int t0 = int(rank) + S * (ew * U); t0 < valid; t0 += S * U * EPI_WARPS) {
+        float part[U][S][4];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + S * u;
+            if (t >= valid) continue;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const uint32_t row = base + uint32_t(t * lin::SPLIT_ROWS) * 4u;
+                const uint32_t at = S == 1 ? row : mapa_shared(row, uint32_t(s));
+                if (vec) {
+                    const float4 f = ld_dsmem_v4(at + uint32_t(col[0]) * 4u);
+                    part[u][s][0] = f.x, part[u][s][1] = f.y, part[u][s][2] = f.z, part[u][s][3] = f.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) part[u][s][i] = ld_dsmem_f32(at + uint32_t(col[i]) * 4u);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = t0 + S * u;
+            if (t >= valid) continue;
+            const int64_t m = int64_t(m0) + t;
+            float x[4];
+            const float sa = kF8 ? e.sa[m] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = part[u][0][i];
+#pragma unroll
+                for (int s = 1; s < S; ++s) x[i] += part[u][s][i];  // in rank order
+                x[i] = (kF8 ? x[i] * (sa * sb[i]) : x[i]) + bias[i];
+            }
+            auto put = [&](void *dst, int64_t ld) {
+                const int64_t row = m * ld + n0;
+                if (vec && e.type == 0) {
+                    *reinterpret_cast<float4 *>(static_cast<float *>(dst) + row + col[0]) = make_float4(x[0], x[1], x[2], x[3]);
+                } else if (vec) {
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst) + row + col[0]) =
+                        make_uint2(pack_16x2(x[0], x[1], e.type), pack_16x2(x[2], x[3], e.type));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (in[i] && G16_CHECK(m < p.M)) store_elem(dst, e.type, row + col[i], x[i]);
+                }
+            };
+            if (e.pre != nullptr) put(e.pre, e.ldp);
+            apply_act(e.act, x);
+            if (e.r != nullptr) {
+                const int64_t row = m * e.ldr + n0;
+                if (vec && e.type != 0) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(e.r) + row + col[0]);
+                    const float2 a = unpack_16x2(w.x, e.type), b = unpack_16x2(w.y, e.type);
+                    x[0] += a.x, x[1] += a.y, x[2] += b.x, x[3] += b.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (in[i]) x[i] += load_elem(e.r, e.type, row + col[i]);
+                }
+            }
+            put(e.c, e.ldc);
+        }
+    }
 }
 
 // Cluster of p.split CTAs (1..8) along x, all on the same tile; CTA r sums the
@@ -666,39 +789,35 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     const int32_t tn = tile / p.sched.nm, tm = tile - tn * p.sched.nm;
     const int32_t m0 = tm * T, n0 = tn * lin::SPLIT_ROWS;
     const int32_t kb0 = int32_t(int64_t(p.num_kb) * rank / S), kb1 = int32_t(int64_t(p.num_kb) * (rank + 1) / S);
+    const int valid = int(p.M - m0 < T ? p.M - m0 : T);  // rows of C in this tile
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < NST; ++s) {
-            mbar_init(full_bar(s), 1);
-            mbar_init(empty_bar(s), 1);
-        }
-        mbar_init(done_bar, 1);
-        fence_mbar_init();
-    }
-    if (warp == MMA_WARP) {
-        tmem_alloc(smem_addr(tmem_slot), uint32_t(p.tmem_cols));
-        tmem_relinquish();
-    }
-    if (warp == 0 && lane == 0) {
-        prefetch_tensormap(&tmW);
-        prefetch_tensormap(&tmX);
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    griddep_wait();
-    griddep_launch_dependents();
-    const uint32_t tmem_base = *tmem_slot;
     bool ready = false;  // epilogue warps: the accumulator is complete
+    uint32_t tmem_base = 0;
 
     if (warp == 0) {
         // ============================================================ producer
+        // This warp sets up the barriers and starts the first stages by itself, while
+        // the others set up tensor memory; only then it meets them.
+        if (lane == 0) {
+            prefetch_tensormap(&tmW);
+            prefetch_tensormap(&tmX);
+            for (int s = 0; s < NST; ++s) {
+                mbar_init(full_bar(s), 1);
+                mbar_init(empty_bar(s), 1);
+            }
+            mbar_init(done_bar, 1);
+            fence_mbar_init();
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+        griddep_wait();
         uint32_t stage = 0, phase = 0, issued = 0;
         bool ok = true;
         const int nw = p.b_mn ? lin::SPLIT_ROWS / MN_CHUNK : 1;
         const int nx = p.a_mn ? T / MN_CHUNK : 1;
         for (int32_t kb = kb0; kb < kb1; ++kb) {
-            if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, p.wait))) {
+            if (kb - kb0 == NST) __syncthreads();  // the others are set up
+            if (kb - kb0 >= NST && !__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, p.wait))) {
                 ok = false;
                 break;
             }
@@ -717,13 +836,28 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
             ++issued;
             if (++stage == uint32_t(NST)) { stage = 0; phase ^= 1u; }
         }
+        if (kb1 - kb0 <= NST) __syncthreads();
+        griddep_launch_dependents();
         if (!ok && lane == 0) {  // let the copies this warp started land before the CTA exits
             const uint32_t n = issued < uint32_t(NST) ? issued : uint32_t(NST);
             for (uint32_t q = issued - n; q < issued; ++q)
                 mbar_wait_slow(full_bar(q % NST), (q / NST) & 1u, cleanup_wait(p.wait), false);
         }
         __syncwarp();
-    } else if (warp == MMA_WARP) {
+    } else {
+        if (warp == MMA_WARP) {
+            tmem_alloc(smem_addr(tmem_slot), uint32_t(p.tmem_cols));
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        griddep_wait();
+        griddep_launch_dependents();
+        tmem_base = *tmem_slot;
+    }
+
+    if (warp == MMA_WARP) {
         // ============================================================ MMA issuer
         uint32_t stage = 0, phase = 0;
         const DescStep dw = make_desc_step(sW, p.b_mn, lin::W_STAGE_BYTES);
@@ -747,127 +881,49 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         // still be writing TMEM when it is freed
         mma_commit_elect(done_bar);
         __all_sync(0xffffffffu, mbar_wait_slow(done_bar, 0, cleanup_wait(p.wait), false));
-    } else {
-        // ============================================================ epilogue
+    } else if (warp >= EPI_WARP0) {
+        // ============================================================ partial tile -> shared memory
+        // fp32 [row of C][128 columns], in the ring's place: every copy into it has
+        // been consumed once the accumulator is complete.
         const int q = warp & 3;
-        const int ew = warp - EPI_WARP0;
-        const int half = ew / 4;
+        const int half = (warp - EPI_WARP0) / 4;
         ready = __all_sync(0xffffffffu, mbar_wait(done_bar, 0, p.wait));
         tc_fence_after();
         if (ready) {
             // two warps per TMEM lane quarter: rows [0, T/2) and [T/2, T) of the tile
-            const int t0 = half * (T / 2), t1 = t0 + T / 2;
-            const int col = q * 32 + lane;  // column of the tile
-            const int64_t n = int64_t(n0) + col;
-            const int valid = int(p.M - m0 < T ? p.M - m0 : T);
-            const bool col_ok = n < p.N;
-            const float bias = S == 1 && col_ok && p.e.bias != nullptr ? load_elem(p.e.bias, p.e.bias_type, n) : 0.0f;
-            const float sb = kF8 && S == 1 && col_ok ? p.e.sb[n] : 1.0f;
-            for (int t = t0; t < t1 && t < valid; t += 32) {
+            const int t0 = half * (T / 2), t1 = min(t0 + T / 2, valid);
+            const uint32_t col = base + uint32_t(q * 32 + lane) * 4u;
+            for (int t = t0; t < t1; t += 32) {
                 uint32_t v[32];
-                tmem_ld_32x32b_x32(tmem_base + (uint32_t(q * 32) << 16) + min(t, p.tmem_cols - 32), v);
+                const int at = min(t, p.tmem_cols - 32);  // T = 16: one load of 32 columns holds all
+                tmem_ld_32x32b_x32(tmem_base + (uint32_t(q * 32) << 16) + uint32_t(at), v);
                 tmem_ld_wait();
-                const int lead = t - min(t, p.tmem_cols - 32);  // T = 16: columns 8.. of the one 32-column load
-                const int cnt = min(32, min(t1, valid) - t);
-                if (S > 1) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i >= lead && i - lead < cnt)
-                            st_shared_s32(base + uint32_t((t - lead + i) * lin::SPLIT_ROWS + col) * 4u, int32_t(v[i]));
-                } else {
-                    float x[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        x[i] = __uint_as_float(v[i]);
-                        if (kF8) x[i] *= sb * (i >= lead && i - lead < cnt ? p.e.sa[m0 + t - lead + i] : 1.0f);
-                        x[i] += bias;
-                    }
-                    if (p.e.pre != nullptr) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (col_ok && i >= lead && i - lead < cnt)
-                                store_elem(p.e.pre, p.e.type, int64_t(m0 + t - lead + i) * p.e.ldp + n, x[i]);
-                    }
-                    apply_act(p.e.act, x);
-                    if (p.e.r != nullptr) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (col_ok && i >= lead && i - lead < cnt)
-                                x[i] += load_elem(p.e.r, p.e.type, int64_t(m0 + t - lead + i) * p.e.ldr + n);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (col_ok && i >= lead && i - lead < cnt && G16_CHECK(m0 + t - lead + i < p.M))
-                            store_elem(p.e.c, p.e.type, int64_t(m0 + t - lead + i) * p.e.ldc + n, x[i]);
-                }
+                for (int i = 0; i < 32; ++i)
+                    if (at + i >= t && at + i < t1) st_shared_s32(col + uint32_t((at + i) * lin::SPLIT_ROWS) * 4u, int32_t(v[i]));
             }
         }
         tc_fence_before();
     }
 
-    // ---------------------------------------------------------------- the cluster's sum
+    // ---------------------------------------------------------------- the cluster's sum and the epilogue
+    // Row t of the tile belongs to CTA t % S; there a warp takes 8 / S of them at a
+    // time, so that 8 loads are in flight whatever S.
+    __syncwarp();
+    if (S > 1) cluster_sync();  // every CTA's partial tile is in its shared memory
+    else __syncthreads();
+    if (ready) {
+        const int ew = warp - EPI_WARP0;
+        switch (S) {
+            case 1: split_rows<kF8, 1>(p, base, rank, ew, lane, m0, n0, valid); break;
+            case 2: split_rows<kF8, 2>(p, base, rank, ew, lane, m0, n0, valid); break;
+            case 4: split_rows<kF8, 4>(p, base, rank, ew, lane, m0, n0, valid); break;
+            default: split_rows<kF8, 8>(p, base, rank, ew, lane, m0, n0, valid); break;
+        }
+    }
     if (S > 1) {
         __syncwarp();
-        cluster_sync();  // every CTA's partial tile is in its shared memory
-        if (ready) {
-            const int ew = warp - EPI_WARP0;
-            const int valid = int(p.M - m0 < T ? p.M - m0 : T);
-            const int64_t n = int64_t(n0) + lane * 4;
-            const int cols = n < p.N ? int(p.N - n < 4 ? p.N - n : 4) : 0;
-            const bool vec = p.e.vec4 && cols == 4;
-            float bias[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {1.f, 1.f, 1.f, 1.f};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i < cols && p.e.bias != nullptr) bias[i] = load_elem(p.e.bias, p.e.bias_type, n + i);
-                if (kF8 && i < cols) sb[i] = p.e.sb[n + i];
-            }
-            // row t of the tile belongs to CTA t % S, and there to warp (t / S) % 8
-            for (int t = int(rank) + S * ew; t < valid; t += S * EPI_WARPS) {
-                const uint32_t at = base + uint32_t(t * lin::SPLIT_ROWS + lane * 4) * 4u;
-                float4 part[lin::MAX_SPLIT];
-#pragma unroll
-                for (int s = 0; s < lin::MAX_SPLIT; ++s)
-                    if (s < S) part[s] = ld_dsmem_v4(mapa_shared(at, uint32_t(s)));
-                float x[4] = {part[0].x, part[0].y, part[0].z, part[0].w};
-#pragma unroll
-                for (int s = 1; s < lin::MAX_SPLIT; ++s)
-                    if (s < S) {
-                        x[0] += part[s].x;
-                        x[1] += part[s].y;
-                        x[2] += part[s].z;
-                        x[3] += part[s].w;
-                    }
-                const int64_t m = int64_t(m0) + t;
-                const float sa = kF8 ? p.e.sa[m] : 1.0f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = (kF8 ? x[i] * (sa * sb[i]) : x[i]) + bias[i];
-                auto put = [&](void *dst, int64_t ld) {
-                    if (vec && p.e.type == 0) {
-                        *reinterpret_cast<float4 *>(static_cast<float *>(dst) + m * ld + n) = make_float4(x[0], x[1], x[2], x[3]);
-                    } else if (vec) {
-                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst) + m * ld + n) =
-                            make_uint2(pack_16x2(x[0], x[1], p.e.type), pack_16x2(x[2], x[3], p.e.type));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (i < cols && G16_CHECK(m < p.M && n + i < p.N)) store_elem(dst, p.e.type, m * ld + n + i, x[i]);
-                    }
-                };
-                if (p.e.pre != nullptr) put(p.e.pre, p.e.ldp);
-                apply_act(p.e.act, x);
-                if (p.e.r != nullptr) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < cols) x[i] += load_elem(p.e.r, p.e.type, m * p.e.ldr + n + i);
-                }
-                put(p.e.c, p.e.ldc);
-            }
-        }
-        __syncwarp();
         cluster_sync();  // no CTA leaves while others read its shared memory
-    } else {
-        __syncwarp();
-        __syncthreads();
     }
     if (warp == MMA_WARP) {
         tc_fence_after();
