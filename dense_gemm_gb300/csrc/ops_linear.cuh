@@ -649,19 +649,9 @@ constexpr int split_ring(int stages, int T) { return stages * (W_STAGE_BYTES + T
 constexpr int split_smem(int stages, int T) { return split_ring(stages, T) + SPLIT_BARS * 8 + 16 + 1024; }
 }  // namespace lin
 
-__device__ __forceinline__ float4 ld_dsmem_v4(uint32_t cluster_addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(cluster_addr)
-                 : "memory");
-    return v;
-}
-
-__device__ __forceinline__ float ld_dsmem_f32(uint32_t cluster_addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
-    return v;
+// Stores into the shared memory of a CTA of the cluster.
+__device__ __forceinline__ void st_dsmem_b32(uint32_t cluster_addr, uint32_t v) {
+    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 
 // The epilogue on one value of C.
@@ -671,89 +661,113 @@ __device__ __forceinline__ float act_one(uint32_t act, float x) {
     return v[0];
 }
 
-// Sums the S partial tiles' rows that fall to warp `ew` of CTA `rank` and runs
-// the epilogue on them. A lane holds four columns: consecutive ones where C, pre
-// and residual take vectors of four, else 32 apart, so that the stores of a warp
-// are contiguous either way.
-template <bool kF8, int S>
+// Rows [t, t1) of the tile from TMEM (`t_addr`: this warp's lanes, column 0) to the
+// CTAs they belong to: row r to CTA r mod S, place r / S, there [place][source
+// CTA][128] floats from `base` on. `col`: this lane's column of the tile.
+template <int S>
+__device__ __forceinline__ void split_send(uint32_t t_addr, uint32_t base, uint32_t rank, int col, int t, int t1, int tmem_cols) {
+    uint32_t to[S];  // place 0 of each CTA, from this one
+#pragma unroll
+    for (int d = 0; d < S; ++d) to[d] = mapa_shared(base + (rank * lin::SPLIT_ROWS + uint32_t(col)) * 4u, uint32_t(d));
+#pragma unroll 1
+    for (; t < t1; t += 32) {
+        uint32_t v[32];
+        const int at = min(t, tmem_cols - 32);  // T = 16: one load of 32 columns holds all
+        tmem_ld_32x32b_x32(t_addr + uint32_t(at), v);
+        tmem_ld_wait();
+        const uint32_t off = uint32_t(at) * (lin::SPLIT_ROWS * 4u);  // at is a multiple of S
+        if (at == t && t + 32 <= t1) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) st_dsmem_b32(to[i % S] + off + uint32_t(i / S * S * lin::SPLIT_ROWS * 4), v[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (at + i >= t && at + i < t1) st_dsmem_b32(to[i % S] + off + uint32_t(i / S * S * lin::SPLIT_ROWS * 4), v[i]);
+        }
+    }
+}
+
+// Sums the S partial rows of each row of C that falls to warp `ew` of CTA `rank`
+// (row t belongs to CTA t mod S, and there to warp (t / S) mod 8), in rank order,
+// and runs the epilogue on them. A lane holds four columns: consecutive ones where
+// C, pre and residual take vectors of four (VEC), else 32 apart, so that a warp's
+// stores are contiguous either way.
+template <bool kF8, int S, bool VEC>
 __device__ __forceinline__ void split_rows(const LinearParams &p, uint32_t base, uint32_t rank, int ew, int lane, int32_t m0,
                                            int32_t n0, int valid) {
-    constexpr int U = lin::MAX_SPLIT / S;  // rows at a time
     const EpilogueParams &e = p.e;
-    const bool vec = e.vec4 && n0 + lin::SPLIT_ROWS <= p.N;
     int col[4];
     float bias[4], sb[4];
     bool in[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        col[i] = vec ? lane * 4 + i : lane + 32 * i;
+        col[i] = VEC ? lane * 4 + i : lane + 32 * i;
         const int64_t n = int64_t(n0) + col[i];
-        in[i] = n < p.N;
+        in[i] = VEC || n < p.N;
         bias[i] = in[i] && e.bias != nullptr ? load_elem(e.bias, e.bias_type, n) : 0.0f;
         sb[i] = kF8 && in[i] ? e.sb[n] : 1.0f;
     }
-    for (int t0 = int(rank) + S * (ew * U); t0 < valid; t0 += S * U * EPI_WARPS) {
-        float part[U][S][4];
+#pragma unroll 1
+    for (int k = ew; k * S + int(rank) < valid; k += EPI_WARPS) {
+        const uint32_t row = base + uint32_t(k * S * lin::SPLIT_ROWS) * 4u;
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = t0 + S * u;
-            if (t >= valid) continue;
+        for (int s = 0; s < S; ++s) {
+            const uint32_t at = row + uint32_t(s * lin::SPLIT_ROWS) * 4u;
+            uint32_t w[4];
+            if constexpr (VEC) {
+                ld_shared_v4(at + uint32_t(lane) * 16u, w[0], w[1], w[2], w[3]);
+            } else {
 #pragma unroll
-            for (int s = 0; s < S; ++s) {
-                const uint32_t row = base + uint32_t(t * lin::SPLIT_ROWS) * 4u;
-                const uint32_t at = S == 1 ? row : mapa_shared(row, uint32_t(s));
-                if (vec) {
-                    const float4 f = ld_dsmem_v4(at + uint32_t(col[0]) * 4u);
-                    part[u][s][0] = f.x, part[u][s][1] = f.y, part[u][s][2] = f.z, part[u][s][3] = f.w;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) part[u][s][i] = ld_dsmem_f32(at + uint32_t(col[i]) * 4u);
-                }
+                for (int i = 0; i < 4; ++i) w[i] = ld_shared_b32(at + uint32_t(col[i]) * 4u);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] += __uint_as_float(w[i]);
         }
+        const int64_t m = int64_t(m0) + k * S + int(rank);
+        const float sa = kF8 ? e.sa[m] : 1.0f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int t = t0 + S * u;
-            if (t >= valid) continue;
-            const int64_t m = int64_t(m0) + t;
-            float x[4];
-            const float sa = kF8 ? e.sa[m] : 1.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = part[u][0][i];
-#pragma unroll
-                for (int s = 1; s < S; ++s) x[i] += part[u][s][i];  // in rank order
-                x[i] = (kF8 ? x[i] * (sa * sb[i]) : x[i]) + bias[i];
-            }
-            auto put = [&](void *dst, int64_t ld) {
-                const int64_t row = m * ld + n0;
-                if (vec && e.type == 0) {
-                    *reinterpret_cast<float4 *>(static_cast<float *>(dst) + row + col[0]) = make_float4(x[0], x[1], x[2], x[3]);
-                } else if (vec) {
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst) + row + col[0]) =
+        for (int i = 0; i < 4; ++i) x[i] = (kF8 ? x[i] * (sa * sb[i]) : x[i]) + bias[i];
+        auto put = [&](void *dst, int64_t ld) {
+            const int64_t at = m * ld + n0 + col[0];
+            if constexpr (VEC) {
+                if (e.type == 0)
+                    *reinterpret_cast<float4 *>(static_cast<float *>(dst) + at) = make_float4(x[0], x[1], x[2], x[3]);
+                else
+                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst) + at) =
                         make_uint2(pack_16x2(x[0], x[1], e.type), pack_16x2(x[2], x[3], e.type));
-                } else {
+            } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (in[i] && G16_CHECK(m < p.M)) store_elem(dst, e.type, row + col[i], x[i]);
-                }
-            };
-            if (e.pre != nullptr) put(e.pre, e.ldp);
-            apply_act(e.act, x);
-            if (e.r != nullptr) {
-                const int64_t row = m * e.ldr + n0;
-                if (vec && e.type != 0) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(e.r) + row + col[0]);
-                    const float2 a = unpack_16x2(w.x, e.type), b = unpack_16x2(w.y, e.type);
-                    x[0] += a.x, x[1] += a.y, x[2] += b.x, x[3] += b.y;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (in[i]) x[i] += load_elem(e.r, e.type, row + col[i]);
-                }
+                for (int i = 0; i < 4; ++i)
+                    if (in[i] && G16_CHECK(m < p.M)) store_elem(dst, e.type, at + 32 * i, x[i]);
             }
-            put(e.c, e.ldc);
+        };
+        if (e.pre != nullptr) put(e.pre, e.ldp);
+        apply_act(e.act, x);
+        if (e.r != nullptr) {
+            const int64_t at = m * e.ldr + n0 + col[0];
+            if (VEC && e.type != 0) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(e.r) + at);
+                const float2 a = unpack_16x2(w.x, e.type), b = unpack_16x2(w.y, e.type);
+                x[0] += a.x, x[1] += a.y, x[2] += b.x, x[3] += b.y;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (in[i]) x[i] += load_elem(e.r, e.type, at + (VEC ? i : 32 * i));
+            }
         }
+        put(e.c, e.ldc);
+    }
+}
+
+// Calls f with S as a template argument.
+template <typename F>
+__device__ __forceinline__ void with_split(int S, F f) {
+    switch (S) {
+        case 1: f(std::integral_constant<int, 1>()); break;
+        case 2: f(std::integral_constant<int, 2>()); break;
+        case 4: f(std::integral_constant<int, 4>()); break;
+        default: f(std::integral_constant<int, 8>()); break;
     }
 }
 
@@ -882,48 +896,40 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         mma_commit_elect(done_bar);
         __all_sync(0xffffffffu, mbar_wait_slow(done_bar, 0, cleanup_wait(p.wait), false));
     } else if (warp >= EPI_WARP0) {
-        // ============================================================ partial tile -> shared memory
-        // fp32 [row of C][128 columns], in the ring's place: every copy into it has
-        // been consumed once the accumulator is complete.
-        const int q = warp & 3;
-        const int half = (warp - EPI_WARP0) / 4;
         ready = __all_sync(0xffffffffu, mbar_wait(done_bar, 0, p.wait));
         tc_fence_after();
-        if (ready) {
-            // two warps per TMEM lane quarter: rows [0, T/2) and [T/2, T) of the tile
-            const int t0 = half * (T / 2), t1 = min(t0 + T / 2, valid);
-            const uint32_t col = base + uint32_t(q * 32 + lane) * 4u;
-            for (int t = t0; t < t1; t += 32) {
-                uint32_t v[32];
-                const int at = min(t, p.tmem_cols - 32);  // T = 16: one load of 32 columns holds all
-                tmem_ld_32x32b_x32(tmem_base + (uint32_t(q * 32) << 16) + uint32_t(at), v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (at + i >= t && at + i < t1) st_shared_s32(col + uint32_t((at + i) * lin::SPLIT_ROWS) * 4u, int32_t(v[i]));
-            }
-        }
-        tc_fence_before();
     }
 
     // ---------------------------------------------------------------- the cluster's sum and the epilogue
-    // Row t of the tile belongs to CTA t % S; there a warp takes 8 / S of them at a
-    // time, so that 8 loads are in flight whatever S.
+    // Each CTA sends the rows of its partial tile to the CTAs they belong to, into
+    // the place of their rings: those hold nothing any more once every CTA has met
+    // the barrier with its accumulator complete. After the next barrier each CTA
+    // finds all it has to add in its own shared memory. (Reading the others' rows
+    // instead, after one barrier, left each row waiting for the cluster's latency:
+    // 1000 x 640 x 256 9.7 us.)
+    const int ew = warp - EPI_WARP0;
     __syncwarp();
-    if (S > 1) cluster_sync();  // every CTA's partial tile is in its shared memory
+    if (S > 1) cluster_sync();
     else __syncthreads();
     if (ready) {
-        const int ew = warp - EPI_WARP0;
-        switch (S) {
-            case 1: split_rows<kF8, 1>(p, base, rank, ew, lane, m0, n0, valid); break;
-            case 2: split_rows<kF8, 2>(p, base, rank, ew, lane, m0, n0, valid); break;
-            case 4: split_rows<kF8, 4>(p, base, rank, ew, lane, m0, n0, valid); break;
-            default: split_rows<kF8, 8>(p, base, rank, ew, lane, m0, n0, valid); break;
-        }
+        // two warps per TMEM lane quarter: rows [0, T/2) and [T/2, T) of the tile
+        const int q = warp & 3, t0 = (ew / 4) * (T / 2);
+        with_split(S, [&](auto s) {
+            split_send<decltype(s)::value>(tmem_base + (uint32_t(q * 32) << 16), base, rank, q * 32 + lane, t0,
+                                           min(t0 + T / 2, valid), p.tmem_cols);
+        });
+        tc_fence_before();
     }
-    if (S > 1) {
-        __syncwarp();
-        cluster_sync();  // no CTA leaves while others read its shared memory
+    __syncwarp();
+    if (S > 1) cluster_sync();
+    else __syncthreads();
+    if (ready) {
+        const bool vec = p.e.vec4 && n0 + lin::SPLIT_ROWS <= p.N;
+        with_split(S, [&](auto s) {
+            constexpr int SPLIT = decltype(s)::value;
+            if (vec) split_rows<kF8, SPLIT, true>(p, base, rank, ew, lane, m0, n0, valid);
+            else split_rows<kF8, SPLIT, false>(p, base, rank, ew, lane, m0, n0, valid);
+        });
     }
     if (warp == MMA_WARP) {
         tc_fence_after();
