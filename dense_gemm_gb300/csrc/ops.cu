@@ -31,37 +31,6 @@ int device_state(DeviceState **ds) {
     return dev;
 }
 
-// Dynamic shared memory limits of this file's kernels, set once per device.
-struct OpsState {
-    std::mutex mu;
-    std::atomic<bool> ready{false};
-};
-OpsState g_ops[kMaxDevices];
-
-template <typename K>
-cudaError_t allow_smem(K *kernel, int bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
-bool ops_init(int dev) {
-    OpsState &o = g_ops[dev];
-    if (o.ready.load(std::memory_order_acquire)) return true;
-    std::lock_guard<std::mutex> lock(o.mu);
-    if (o.ready.load(std::memory_order_relaxed)) return true;
-    cudaError_t e = allow_smem(linear_pair<false, 2>, lin::PAIR_SMEM);
-    if (e == cudaSuccess) e = allow_smem(linear_pair<false, 4>, lin::PAIR_SMEM);
-    if (e == cudaSuccess) e = allow_smem(linear_pair<true, 2>, lin::PAIR_SMEM);
-    if (e == cudaSuccess) e = allow_smem(linear_pair<true, 4>, lin::PAIR_SMEM);
-    if (e == cudaSuccess) e = allow_smem(linear_split<false>, 232448);
-    if (e == cudaSuccess) e = allow_smem(linear_split<true>, 232448);
-    if (e != cudaSuccess) {
-        (void)cudaGetLastError();
-        return false;
-    }
-    o.ready.store(true, std::memory_order_release);
-    return true;
-}
-
 // launch_overlapped with a 2-D grid and block, and a cluster along x where
 // `cluster` > 1.
 template <typename... KArgs, typename... Args>
@@ -84,6 +53,75 @@ cudaError_t launch_shape(void (*kernel)(KArgs...), dim3 grid, dim3 block, int sm
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
     if (e != cudaSuccess) (void)cudaGetLastError();
     return e;
+}
+
+// ------------------------------------------------------------------ per-device set-up
+// linear_split's shapes: T = 16 << t rows of C, S = 1 << s CTAs along K.
+constexpr int kSplitTs = 5, kSplitSs = 4;
+
+// Ring depth by T: up to 64 rows the ring is kept under half the SM's shared
+// memory, so that two CTAs share an SM and one's set-up and sum overlap the
+// other's stream.
+constexpr int split_stages(int T) { return T == 16 || T == 128 ? 3 : 2; }
+
+// Done once per device: this file's kernels' shared-memory limits, and how many
+// CTAs of each linear_split shape are resident at once (clusters of 8 do not fill
+// every GPC).
+struct OpsState {
+    std::mutex mu;
+    std::atomic<bool> ready{false};
+    int split_slots[kSplitTs][kSplitSs];
+};
+OpsState g_ops[kMaxDevices];
+
+template <typename K>
+cudaError_t allow_smem(K *kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+const OpsState *ops_init(int dev, int num_sms) {
+    OpsState &o = g_ops[dev];
+    if (o.ready.load(std::memory_order_acquire)) return &o;
+    std::lock_guard<std::mutex> lock(o.mu);
+    if (o.ready.load(std::memory_order_relaxed)) return &o;
+    cudaError_t e = allow_smem(linear_pair<false, 2>, lin::PAIR_SMEM);
+    if (e == cudaSuccess) e = allow_smem(linear_pair<false, 4>, lin::PAIR_SMEM);
+    if (e == cudaSuccess) e = allow_smem(linear_pair<true, 2>, lin::PAIR_SMEM);
+    if (e == cudaSuccess) e = allow_smem(linear_pair<true, 4>, lin::PAIR_SMEM);
+    if (e == cudaSuccess) e = allow_smem(linear_split<false>, 232448);
+    if (e == cudaSuccess) e = allow_smem(linear_split<true>, 232448);
+    for (int t = 0; e == cudaSuccess && t < kSplitTs; ++t) {
+        const int T = 16 << t;
+        o.split_slots[t][0] = (T <= 64 ? 2 : 1) * num_sms;
+        for (int s = 1; e == cudaSuccess && s < kSplitSs; ++s) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1u << s;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(unsigned(2 * num_sms) >> s << s);
+            cfg.blockDim = dim3(lin::SPLIT_THREADS);
+            cfg.dynamicSmemBytes = size_t(lin::split_smem(split_stages(T), T));
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            e = cudaOccupancyMaxActiveClusters(&n, linear_split<false>, &cfg);
+            // the query counts one CTA per SM for these shapes, also where two fit and run
+            // (16384 x 4096 weights, 64 tokens, 128 clusters of 2: 25.6 us, in one round)
+            o.split_slots[t][s] = (T <= 64 ? 2 : 1) * std::max(n, 1) << s;
+        }
+    }
+    if (e != cudaSuccess) {
+        (void)cudaGetLastError();
+        return nullptr;
+    }
+    if (log_enabled())
+        for (int t = 0; t < kSplitTs; ++t)
+            std::fprintf(stderr, "[gemm_linear] T=%d resident CTAs by K slices 1/2/4/8: %d %d %d %d\n", 16 << t, o.split_slots[t][0],
+                         o.split_slots[t][1], o.split_slots[t][2], o.split_slots[t][3]);
+    o.ready.store(true, std::memory_order_release);
+    return &o;
 }
 
 // ------------------------------------------------------------------ linear: operands
@@ -167,14 +205,31 @@ cudaError_t pack_operands(Operand *a, void *dst_a, Operand *b, void *dst_b, int 
     return e;
 }
 
-bool encode_operand(CUtensorMap *map, const Operand &o, int rows_per_copy) {
-    const int es = type_bytes(o.type);
+// The tensor map of an operand for stages of `kbs` k-blocks of 128 bytes and `mn`
+// rows (or columns) per CTA, and how a stage is fetched through it (OperandLoad).
+// Rows of the third dimension are whole pieces of one row of the operand: it is
+// used only where the row's extent is a multiple of the piece, so that nothing
+// but the operand is read.
+bool encode_operand(CUtensorMap *map, OperandLoad *load, const Operand &o, int kbs, int mn) {
+    EncodeTiledFn enc = encode_fn();
+    if (enc == nullptr) return false;
+    const int es = type_bytes(o.type), be = 128 / es;
     const CUtensorMapDataType dt = o.type == GEMM_TYPE_E4M3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : o.type == GEMM_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    return o.mn_major ? encode_2d(map, dt, o.data, uint64_t(o.inner), uint64_t(o.rows), uint64_t(o.ld) * es, MN_CHUNK, BK)
-                      : encode_2d(map, dt, o.data, uint64_t(o.inner), uint64_t(o.rows), uint64_t(o.ld) * es, 128 / es,
-                                  rows_per_copy);
+    const int pieces = o.mn_major ? mn / be : kbs;
+    load->mn = o.mn_major;
+    load->mode = pieces == 1 ? kLoadOne : o.inner % be == 0 ? kLoadBoxed : kLoadLanes;
+    load->copies = pieces;
+    const uint32_t outer_box = uint32_t(o.mn_major ? kbs * be : mn);
+    if (load->mode != kLoadBoxed)
+        return encode_2d(map, dt, o.data, uint64_t(o.inner), uint64_t(o.rows), uint64_t(o.ld) * es, uint32_t(be), outer_box);
+    const cuuint64_t dims[3] = {cuuint64_t(be), cuuint64_t(o.rows), cuuint64_t(o.inner / be)};
+    const cuuint64_t strides[2] = {cuuint64_t(o.ld) * es, 128u};
+    const cuuint32_t box[3] = {cuuint32_t(be), outer_box, cuuint32_t(pieces)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, dt, 3, const_cast<void *>(o.data), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The same descriptor fields as make_idesc with the operands' format: fp16 0,
@@ -191,36 +246,33 @@ struct LinearPlan {
     int64_t whole, units;   // linear_pair: whole tiles, and units in all
 };
 
-// Estimated SM cycles, from rates measured on GB300: an SM fills shared memory
-// with about 60 bytes a cycle, the tensor core takes 2 cycles per column of a
-// 128-row, 128-byte-deep step, and a CTA's set-up and drain take some microseconds.
-constexpr double kFillBytes = 60.0, kLatency = 2800.0, kSplitFixed = 4500.0, kPairFixed = 6000.0, kPairStep = 560.0;
-
-// linear_split's ring depth: up to 64 rows it is kept under half the SM's shared
-// memory, so that two CTAs share an SM and one's set-up and sum overlap the
-// other's stream.
-int split_stages(int T) { return T <= 16 ? 6 : T <= 32 ? 5 : T <= 64 ? 4 : T <= 128 ? 6 : 4; }
+// Estimated microseconds, from what was measured on GB300 (a step is a k-block of
+// 128 bytes): loads come back after kLatency, so a ring of n stages takes a step
+// every kLatency / n at best; weights come from DRAM at kDramBytes a microsecond;
+// linear_split sets up and ends in about 3.3, and sends and sums its partial rows
+// in the time given per row; linear_pair starts and ends in 3.9.
+constexpr double kLatency = 1.75, kStep = 0.33, kDramBytes = 6.6e6, kSplitFixed = 3.0, kSplitCluster = 0.3, kSplitSend = 0.008,
+                 kSplitRow = 0.018, kPairFixed = 3.9, kPairStep = 0.29, kPairFirst = 0.33, kPairHalf = 0.285;
 
 // linear_split's shape, rows per CTA T (an M-major A comes in chunks of 64 rows)
-// and K slices S, by the estimate. What one CTA draws is bound by its ring over
-// the memory latency as well: 32 x 8 CTAs read 4096 x 4096 weights for one token
-// faster than 32 x 4 (9.5 against 11.0 us).
-double plan_split(int64_t M, int64_t N, int64_t num_kb, bool a_mn, int num_sms, LinearPlan *pl) {
+// and K slices S. (4096 x 4096 weights, one token: S = 8 8.9 us, 4 9.7, 2 15.2,
+// 1 26.2; 256 tokens: T = 256, S = 4 15.2, T = 128, S = 2 17.5, pairs 22.3.)
+double plan_split(int64_t M, int64_t N, int64_t num_kb, bool a_mn, const OpsState &o, LinearPlan *pl) {
     double best = 1e300;
-    for (int T = a_mn ? 64 : 16; T <= 256; T *= 2) {
+    for (int t = a_mn ? 2 : 0; t < kSplitTs; ++t) {
+        const int T = 16 << t;
         const int64_t tiles = cdiv(N, lin::SPLIT_ROWS) * cdiv(M, T);
-        const int per_sm = T <= 64 ? 2 : 1;
-        const double stage = lin::W_STAGE_BYTES + 128.0 * T;
-        for (int S = 1; S <= lin::MAX_SPLIT && (S == 1 || S * 2 <= num_kb); S *= 2) {
-            const int64_t ctas = tiles * S, slots = int64_t(per_sm) * num_sms;
-            const double resident = ctas <= num_sms ? 1.0 : double(per_sm);  // CTAs that share an SM's rates
-            const double fill = std::min(kFillBytes / resident, split_stages(T) * stage / kLatency);
-            const double step = std::max(2.0 * T * resident, stage / fill);
-            const double cost = double(cdiv(ctas, slots)) * (double(cdiv(num_kb, S)) * step + kSplitFixed + (S > 1 ? 500.0 : 0.0) + 6.0 * T);
+        const double step = std::max(kStep, kLatency / split_stages(T));
+        for (int s = 0; s < kSplitSs && (s == 0 || (int64_t(2) << s) <= num_kb); ++s) {
+            const int64_t S = int64_t(1) << s, ctas = tiles * S;
+            const double one = kSplitFixed + (s > 0 ? kSplitCluster : 0.0) + kSplitSend * T + kSplitRow * T / double(S);
+            const double stream = kLatency + double(cdiv(cdiv(num_kb, lin::KPS), S) - 1) * step;
+            double cost = double(cdiv(ctas, o.split_slots[t][s])) * (one + stream);
+            cost = std::max(cost, one + double(N) * double(num_kb) * 128.0 / kDramBytes);
             if (cost < best) {
                 best = cost;
                 pl->T = T;
-                pl->split = S;
+                pl->split = int(S);
             }
         }
         if (T >= M) break;
@@ -230,20 +282,22 @@ double plan_split(int64_t M, int64_t N, int64_t num_kb, bool a_mn, int num_sms, 
 }
 
 // linear_pair's units: whole tiles for as many full rounds of the GPU's pairs as
-// there are, then, where the tiles that remain fit into one round as halves, those.
-// (4096 x 4096 x 8192: 256 tiles on 76 pairs are 3 rounds and 56 halves.)
+// there are, then, where the tiles that remain fit into one round as halves, those
+// (4000 x 5000 x 3000: 4 rounds of 76 and 32 halves, 96.5 us; as 16 tiles 99.7).
 double plan_pair(int64_t M, int64_t N, int64_t num_kb, int max_pairs, LinearPlan *pl) {
     const int64_t tiles = cdiv(M, pair::TILE_M) * cdiv(N, pair::TILE_N), rest = tiles % max_pairs;
     const bool halves = rest > 0 && 2 * rest <= max_pairs;
     pl->whole = halves ? tiles - rest : tiles;
     pl->units = pl->whole + (halves ? 2 * rest : 0);
-    const double rounds = double(cdiv(pl->whole, max_pairs)) + (halves ? 0.58 : 0.0);
-    return rounds * double(num_kb) * kPairStep + kPairFixed;
+    const double rounds = double(cdiv(pl->whole, max_pairs));
+    const double step = rounds == 1.0 ? kPairFirst : rounds * kPairStep;
+    return kPairFixed + double(num_kb) * (step + (halves ? kPairHalf : 0.0));
 }
 
-LinearPlan plan_linear(int64_t M, int64_t N, int64_t num_kb, bool a_mn, uint32_t flags, const DeviceState &ds) {
+LinearPlan plan_linear(int64_t M, int64_t N, int64_t num_kb, bool a_mn, uint32_t flags, const DeviceState &ds,
+                       const OpsState &o) {
     LinearPlan pl{};
-    const double split = plan_split(M, N, num_kb, a_mn, ds.num_sms, &pl);
+    const double split = plan_split(M, N, num_kb, a_mn, o, &pl);
     const double pair = plan_pair(M, N, num_kb, ds.max_pairs, &pl);
     pl.pair = (flags & GEMM_LINEAR_PAIR) || (!(flags & GEMM_LINEAR_SPLIT) && pair <= split);
     return pl;
@@ -263,7 +317,7 @@ bool quad_aligned(const void *p, int64_t ld, int es) {
 
 // The product and its epilogue on operands that TMA can describe. K >= 1.
 gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t N, int64_t K, const EpilogueParams &e,
-                         uint32_t flags, DeviceState *ds, cudaStream_t stream) {
+                         uint32_t flags, const DeviceState *ds, const OpsState *ops, cudaStream_t stream) {
     const bool f8 = A.type == GEMM_TYPE_E4M3;
     const int es = e.type == 0 ? 4 : 2;
     LinearParams p;
@@ -272,11 +326,9 @@ gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t 
     p.N = N;
     p.e = e;
     p.num_kb = int32_t(cdiv(K, f8 ? 128 : 64));
-    p.a_mn = A.mn_major;
-    p.b_mn = B.mn_major;
     p.wait.timeout_ns = g_timeout_ns.load();
     p.wait.epoch = next_epoch();
-    const LinearPlan pl = plan_linear(M, N, p.num_kb, A.mn_major, flags, *ds);
+    const LinearPlan pl = plan_linear(M, N, p.num_kb, A.mn_major, flags, *ds, *ops);
     CUtensorMap tmA, tmB, tmBhalf, tmC, tmR, tmP;
     cudaError_t err;
     if (pl.pair) {
@@ -284,8 +336,8 @@ gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t 
         if (nm * nn > kMaxDim / 2) return GEMM_ERR_UNSUPPORTED;
         std::memset(&tmC, 0, sizeof(tmC));
         tmR = tmP = tmC;
-        if (!encode_operand(&tmA, A, pair::CTA_M) || !encode_operand(&tmB, B, pair::CTA_N) ||
-            !encode_operand(&tmBhalf, B, pair::CTA_N / 2))
+        if (!encode_operand(&tmA, &p.a, A, 1, pair::CTA_M) || !encode_operand(&tmB, &p.b, B, 1, pair::CTA_N) ||
+            !encode_operand(&tmBhalf, &p.b_half, B, 1, pair::CTA_N / 2))
             return GEMM_ERR_CUDA;
         // a clipped TMA store writes whole 16-byte granules: C's and pre's rows must end on one
         const bool ends = (N * es) % 16 == 0;
@@ -314,7 +366,8 @@ gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t 
     } else {
         const int64_t nm = cdiv(M, pl.T), nn = cdiv(N, lin::SPLIT_ROWS);
         if (nm * nn > kMaxDim / lin::MAX_SPLIT) return GEMM_ERR_UNSUPPORTED;
-        if (!encode_operand(&tmA, A, pl.T) || !encode_operand(&tmB, B, lin::SPLIT_ROWS)) return GEMM_ERR_CUDA;
+        if (!encode_operand(&tmA, &p.a, A, lin::KPS, pl.T) || !encode_operand(&tmB, &p.b, B, lin::KPS, lin::SPLIT_ROWS))
+            return GEMM_ERR_CUDA;
         p.sched.nm = int32_t(nm);
         p.sched.nn = int32_t(nn);
         p.num_units = int32_t(nm * nn);
@@ -411,7 +464,8 @@ gemm_status_t gemm_linear(const gemm_matrix_t *A, const gemm_matrix_t *B, const 
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     DeviceState *ds = nullptr;
     const int dev = device_state(&ds);
-    if (dev < 0 || !ops_init(dev)) return GEMM_ERR_CUDA;
+    const OpsState *ops = dev < 0 ? nullptr : ops_init(dev, ds->num_sms);
+    if (ops == nullptr) return GEMM_ERR_CUDA;
     EpilogueParams e;
     std::memset(&e, 0, sizeof(e));
     e.c = C->data;
@@ -438,7 +492,7 @@ gemm_status_t gemm_linear(const gemm_matrix_t *A, const gemm_matrix_t *B, const 
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     if (na + nb > 0 && pack_operands(&a, na ? ws : nullptr, &b, nb ? ws + na : nullptr, ds->num_sms, stream) != cudaSuccess)
         return GEMM_ERR_CUDA;
-    return run_linear(a, b, M, N, K, e, flags, ds, stream);
+    return run_linear(a, b, M, N, K, e, flags, ds, ops, stream);
 }
 
 }  // extern "C"
@@ -571,7 +625,8 @@ gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     DeviceState *ds = nullptr;
     const int dev = device_state(&ds);
-    if (dev < 0 || !ops_init(dev)) return GEMM_ERR_CUDA;
+    const OpsState *ops = dev < 0 ? nullptr : ops_init(dev, ds->num_sms);
+    if (ops == nullptr) return GEMM_ERR_CUDA;
     if (M == 0 || N == 0) {  // empty sums
         if (present(dA) && zero_matrix(dA, dA_t, M, K, ds->num_sms, stream) != cudaSuccess) return GEMM_ERR_CUDA;
         if (present(dB) && zero_matrix(dB, dB_t, K, N, ds->num_sms, stream) != cudaSuccess) return GEMM_ERR_CUDA;
@@ -635,14 +690,14 @@ gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *
     };
     if (present(dA)) {  // dA = D B^T, or its transpose B D^T
         const Operand w = turned(b);
-        st = dA_t ? run_linear(w, d_rows, K, M, N, out(dA, true), flags, ds, stream)
-                  : run_linear(d_rows, w, M, K, N, out(dA, false), flags, ds, stream);
+        st = dA_t ? run_linear(w, d_rows, K, M, N, out(dA, true), flags, ds, ops, stream)
+                  : run_linear(d_rows, w, M, K, N, out(dA, false), flags, ds, ops, stream);
         if (st != GEMM_OK) return st;
     }
     if (present(dB)) {  // dB = A^T D, or its transpose D^T A
         const Operand x = turned(a), d = turned(d_rows);
-        st = dB_t ? run_linear(d, x, N, K, M, out(dB, true), flags, ds, stream)
-                  : run_linear(x, d, K, N, M, out(dB, false), flags, ds, stream);
+        st = dB_t ? run_linear(d, x, N, K, M, out(dB, true), flags, ds, ops, stream)
+                  : run_linear(x, d, K, N, M, out(dB, false), flags, ds, ops, stream);
     }
     return st;
 }

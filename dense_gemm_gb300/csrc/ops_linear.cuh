@@ -152,11 +152,114 @@ struct EpilogueParams {
     uint32_t vec4;                 // four consecutive columns of C, R and pre are aligned to their size together
 };
 
+// How one operand's part of a stage is fetched. Issuing a copy costs its warp some
+// hundred cycles, and more when the operands of the instruction are not uniform
+// over the warp, so each operand has a producer warp of its own and, where that is
+// possible, a stage is one copy, issued by an elected lane from uniform values:
+// kLoadOne is a box of a two-dimensional map. kLoadBoxed brings several pieces, the
+// k-blocks of a stage one after the other (K-major) or the 64-wide chunks
+// (MN-major), through a third dimension of the map; that needs rows that are a
+// multiple of the piece, since the third dimension would run into the next row
+// otherwise. kLoadLanes issues each piece from a lane of its own.
+constexpr uint32_t kLoadOne = 0, kLoadBoxed = 1, kLoadLanes = 2;
+struct OperandLoad {
+    uint32_t mn;    // 1: MN-major in memory and in shared memory
+    uint32_t mode;  // kLoad*
+    int32_t copies;  // kLoadLanes: pieces of a stage
+};
+
+// kPair: counted on an mbarrier of the pair's CTA 0 (shared::cluster address).
+template <bool kPair>
+__device__ __forceinline__ void tma_load_2d_elect(uint32_t dst, const void *tmap, int32_t x, int32_t y, uint32_t bar) {
+    if (!G16_CHECK((x & 7) == 0 && smem_window_ok(dst, 16))) return;
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred pe;\n\t"
+            "elect.sync _|pe, 0xffffffff;\n\t"
+            "@pe cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+            "l"(tmap), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred pe;\n\t"
+            "elect.sync _|pe, 0xffffffff;\n\t"
+            "@pe cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+            "l"(tmap), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+
+template <bool kPair>
+__device__ __forceinline__ void tma_load_3d_elect(uint32_t dst, const void *tmap, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+    if (!G16_CHECK((x & 7) == 0 && smem_window_ok(dst, 16))) return;
+    if constexpr (kPair)
+        asm volatile(
+            "{\n\t.reg .pred pe;\n\t"
+            "elect.sync _|pe, 0xffffffff;\n\t"
+            "@pe cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+            "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred pe;\n\t"
+            "elect.sync _|pe, 0xffffffff;\n\t"
+            "@pe cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+            "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+}
+
+__device__ __forceinline__ void mbar_expect_tx_elect(uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred pe;\n\t"
+        "elect.sync _|pe, 0xffffffff;\n\t"
+        "@pe mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes)
+        : "memory");
+}
+
+// The copies of the stage that starts at k-block kb (of `be` elements), for the
+// rows or columns from `mn` on. Whole warp; pieces lie `piece` bytes apart.
+template <uint32_t MODE, bool kMn, bool kPair>
+__device__ __forceinline__ void issue_copies(const CUtensorMap *map, uint32_t dst, uint32_t piece, int32_t copies, int32_t kb,
+                                             int32_t be, int32_t mn, uint32_t bar, int lane) {
+    const int32_t k0 = kb * be;
+    if constexpr (MODE == kLoadOne) {
+        tma_load_2d_elect<kPair>(dst, map, kMn ? mn : k0, kMn ? k0 : mn, bar);
+    } else if constexpr (MODE == kLoadBoxed) {
+        tma_load_3d_elect<kPair>(dst, map, 0, kMn ? k0 : mn, kMn ? mn / MN_CHUNK : kb, bar);
+    } else if (lane < copies) {
+        const int32_t x = kMn ? mn + lane * MN_CHUNK : k0 + lane * be, y = kMn ? k0 : mn;
+        if constexpr (kPair) tma_load_2d_pair(dst + uint32_t(lane) * piece, map, x, y, bar);
+        else tma_load_2d(dst + uint32_t(lane) * piece, map, x, y, bar);
+    }
+}
+
+// Calls f with the mode and the major-ness as template arguments.
+template <typename F>
+__device__ __forceinline__ void with_load(const OperandLoad &o, F f) {
+    using std::integral_constant;
+    using One = integral_constant<uint32_t, kLoadOne>;
+    using Boxed = integral_constant<uint32_t, kLoadBoxed>;
+    using Lanes = integral_constant<uint32_t, kLoadLanes>;
+    if (o.mn) {
+        if (o.mode == kLoadBoxed) f(Boxed(), std::true_type());
+        else if (o.mode == kLoadOne) f(One(), std::true_type());
+        else f(Lanes(), std::true_type());
+    } else {
+        if (o.mode == kLoadBoxed) f(Boxed(), std::false_type());
+        else if (o.mode == kLoadOne) f(One(), std::false_type());
+        else f(Lanes(), std::false_type());
+    }
+}
+
 struct LinearParams {
     int64_t M, N;
     Sched sched;
     int32_t num_kb;
-    uint32_t a_mn, b_mn, idesc;
+    OperandLoad a, b, b_half;  // b_half: linear_pair's half tiles
+    uint32_t idesc;
     // linear_pair: units below `whole` are tiles; from there on, halves (128
     // columns) of the tiles `whole`, whole + 1, ...
     int32_t num_units, whole;
@@ -172,7 +275,7 @@ struct LinearParams {
 namespace lin {
 constexpr int PAIR_STAGES = 6;  // at most; 5 when two staging buffers per warp are needed
 constexpr int STAGE_BYTES = pair::A_STAGE_BYTES + pair::B_STAGE_BYTES;
-constexpr int PAIR_THREADS = (2 + EPI_WARPS) * 32;
+constexpr int PAIR_THREADS = (3 + EPI_WARPS) * 32;  // A's and B's producers, MMA, epilogue
 constexpr int BUF_BYTES = 4096;  // 32 rows of 128 bytes
 // full[6], empty[6], tfull[2], tempty[2], tdone[2], drain, residual[8 warps][2]
 constexpr int PAIR_BARS = 2 * PAIR_STAGES + 3 * NUM_ACC + 1 + 2 * EPI_WARPS;
@@ -416,7 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
                 const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmP, const LinearParams p) {
     constexpr int MAXST = lin::PAIR_STAGES;
     constexpr int BKE = kF8 ? 128 : 64;  // K per stage, elements
-    constexpr int MMA_WARP = 1, EPI_WARP0 = 2;
+    constexpr int MMA_WARP = 1, EPI_WARP0 = 2, B_WARP = EPI_WARP0 + EPI_WARPS;
     const int NST = p.stages;
 
     extern __shared__ uint8_t smem_raw[];
@@ -460,9 +563,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
         tmem_alloc_pair(smem_addr(tmem_slot), TMEM_COLS);
         tmem_relinquish_pair();
     }
-    if (warp == 0 && lane == 0) {
-        prefetch_tensormap(&tmA);
+    if (warp == 0 && lane == 0) prefetch_tensormap(&tmA);
+    if (warp == B_WARP && lane == 0) {
         prefetch_tensormap(&tmB);
+        if (p.whole < p.num_units) prefetch_tensormap(&tmBhalf);
     }
     if (warp == EPI_WARP0 && lane == 0) {
         if (p.e.c_tma) prefetch_tensormap(&tmC);
@@ -479,53 +583,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
     const uint32_t tmem_base = *tmem_slot;
     const int32_t num_kb = p.num_kb;
 
-    if (warp == 0) {
-        // ============================================================ producer (both CTAs)
+    if (warp == 0 || warp == B_WARP) {
+        // ============================================================ producers (both CTAs)
+        // One warp per operand; A's announces a stage's bytes (both operands', both
+        // CTAs') on CTA 0's barrier. Copies may land before the announcement: a phase
+        // ends only after it.
         uint32_t stage = 0, phase = 0, issued = 0;
         bool ok = true;
-        const int na = p.a_mn ? pair::CTA_M / MN_CHUNK : 1;  // copies of A per stage
-        // All k-blocks of one unit. kHalf is a template argument because a map chosen at
-        // run time in the inner loop costs 6 % of the whole kernel (4096 x 8192 x 8192
-        // e4m3: 161 -> 171 us).
-        auto load_unit = [&](const Unit &un, auto is_half) {
-            constexpr bool kHalf = decltype(is_half)::value;
-            constexpr int CTA_COLS = kHalf ? pair::CTA_N / 2 : pair::CTA_N;  // columns of B this CTA loads
-            constexpr uint32_t TX = 2u * uint32_t(pair::A_STAGE_BYTES + CTA_COLS * 128);
-            const int nb = p.b_mn ? CTA_COLS / MN_CHUNK : 1;  // copies of B per stage
-            const int32_t m0 = int32_t(un.row0), n0 = int32_t(un.col0) + int32_t(rank) * CTA_COLS;
+        const bool is_a = warp == 0;
+        // All k-blocks of one unit; what does not change over them is a template argument.
+        auto load_unit = [&](const Unit &un, const CUtensorMap *map, auto mode, auto mn_major, auto announces, uint32_t tx) {
+            const int32_t mn = is_a ? int32_t(un.row0) : int32_t(un.col0) + int32_t(rank) * (un.cols / 2);
+            const int32_t copies = is_a ? p.a.copies : un.cols == pair::TILE_N ? p.b.copies : p.b_half.copies;
+            const uint32_t s0 = is_a ? sA : sB;
             for (int32_t kb = 0; kb < num_kb; ++kb) {
                 if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, p.wait))) {
                     ok = false;
                     break;
                 }
-                if (lane == 0 && rank == 0) mbar_arrive_expect_tx(full_bar(stage), TX);
-                const uint32_t fb = mapa_shared(full_bar(stage), 0);
-                const int32_t k0 = kb * BKE;
-                if (lane < na + nb) {  // lane: copy `lane` of A, or copy `lane - na` of B
-                    const bool is_a = lane < na;
-                    const int c = is_a ? lane : lane - na;
-                    const uint32_t dst = (is_a ? sA + stage * pair::A_STAGE_BYTES : sB + stage * pair::B_STAGE_BYTES) +
-                                         uint32_t(c) * MN_CHUNK_BYTES;
-                    const bool mn_major = (is_a ? p.a_mn : p.b_mn) != 0;
-                    const int32_t mn = (is_a ? m0 : n0) + c * MN_CHUNK;
-                    tma_load_2d_pair(dst, is_a ? &tmA : kHalf ? &tmBhalf : &tmB, mn_major ? mn : k0, mn_major ? k0 : mn, fb);
-                }
+                if constexpr (decltype(announces)::value) mbar_expect_tx_elect(full_bar(stage), tx);
+                issue_copies<decltype(mode)::value, decltype(mn_major)::value, true>(
+                    map, s0 + stage * pair::A_STAGE_BYTES, MN_CHUNK_BYTES, copies, kb, BKE, mn, mapa_shared(full_bar(stage), 0), lane);
                 ++issued;
                 if (++stage == uint32_t(NST)) { stage = 0; phase ^= 1u; }
             }
         };
+        static_assert(pair::A_STAGE_BYTES == pair::B_STAGE_BYTES, "one stage pitch for both operands");
+        constexpr uint32_t TX_HALF = 2u * (pair::A_STAGE_BYTES + pair::B_STAGE_BYTES / 2);
         int32_t u = pair_id;
-        for (; ok && u < p.whole; u += num_pairs) load_unit(unit_of(p, u, rank), std::false_type());
-        for (; ok && u < p.num_units; u += num_pairs) load_unit(unit_of(p, u, rank), std::true_type());
+        if (is_a) {
+            with_load(p.a, [&](auto mode, auto mn_major) {
+                for (; ok && u < p.num_units; u += num_pairs) {
+                    const uint32_t tx = u < p.whole ? pair::PAIR_TX_BYTES : TX_HALF;
+                    if (rank == 0) load_unit(unit_of(p, u, rank), &tmA, mode, mn_major, std::true_type(), tx);
+                    else load_unit(unit_of(p, u, rank), &tmA, mode, mn_major, std::false_type(), tx);
+                }
+            });
+        } else {
+            with_load(p.b, [&](auto mode, auto mn_major) {
+                for (; ok && u < p.whole; u += num_pairs)
+                    load_unit(unit_of(p, u, rank), &tmB, mode, mn_major, std::false_type(), 0u);
+            });
+            with_load(p.b_half, [&](auto mode, auto mn_major) {
+                for (; ok && u < p.num_units; u += num_pairs)
+                    load_unit(unit_of(p, u, rank), &tmBhalf, mode, mn_major, std::false_type(), 0u);
+            });
+        }
         if (!ok && lane == 0) {
-            if (rank == 0) {
+            if (rank == 0 && is_a) {
                 // Let the copies counted on this CTA's barriers land before exiting.
                 const uint32_t n = issued < uint32_t(NST) ? issued : uint32_t(NST);
                 for (uint32_t q = issued - n; q < issued; ++q)
                     mbar_wait_slow(full_bar(q % NST), (q / NST) & 1u, cleanup_wait(p.wait), false);
             } else {
-                // The peer's copies count on CTA 0's barriers, which it cannot wait on; give
-                // copies already issued time to land (16 KiB reads, microseconds at most).
+                // Copies issued by the other producers are not known here, and CTA 1's count
+                // on CTA 0's barriers, which it cannot wait on; give copies already issued
+                // time to land (16 KiB reads, microseconds at most).
                 const uint64_t t0 = global_timer_ns();
                 while (global_timer_ns() - t0 < 200000ull) {
                 }
@@ -549,8 +662,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
             uint32_t stage = 0, phase = 0;
             bool ok = true;
             int32_t it = 0;
-            const DescStep da = make_desc_step(sA, p.a_mn, pair::A_STAGE_BYTES);
-            const DescStep db = make_desc_step(sB, p.b_mn, pair::B_STAGE_BYTES);
+            const DescStep da = make_desc_step(sA, p.a.mn, pair::A_STAGE_BYTES);
+            const DescStep db = make_desc_step(sB, p.b.mn, pair::B_STAGE_BYTES);
             for (int32_t u = pair_id; ok && u < p.num_units; u += num_pairs, ++it) {
                 const uint32_t idesc = u < p.whole ? p.idesc : p.idesc_half;
                 const uint32_t acc = it & 1, use = it >> 1;
@@ -640,12 +753,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
 namespace lin {
 constexpr int SPLIT_THREADS = (2 + EPI_WARPS) * 32;
 constexpr int SPLIT_ROWS = 128;                     // columns of C per CTA (TMEM lanes)
-constexpr int W_STAGE_BYTES = SPLIT_ROWS * 128;     // 16 KiB
-constexpr int SPLIT_MAX_STAGES = 8;
+constexpr int KPS = 2;                              // k-blocks per stage
+constexpr int W_STAGE_BYTES = KPS * SPLIT_ROWS * 128;  // 32 KiB
+constexpr int SPLIT_MAX_STAGES = 3;
 constexpr int MAX_SPLIT = 8;
 // full[S], empty[S], done
 constexpr int SPLIT_BARS = 2 * SPLIT_MAX_STAGES + 1;
-constexpr int split_ring(int stages, int T) { return stages * (W_STAGE_BYTES + T * 128); }
+constexpr int split_ring(int stages, int T) { return stages * (W_STAGE_BYTES + KPS * T * 128); }
 constexpr int split_smem(int stages, int T) { return split_ring(stages, T) + SPLIT_BARS * 8 + 16 + 1024; }
 }  // namespace lin
 
@@ -772,7 +886,7 @@ __device__ __forceinline__ void with_split(int S, F f) {
 }
 
 // Cluster of p.split CTAs (1..8) along x, all on the same tile; CTA r sums the
-// k-blocks [r num_kb / split, (r + 1) num_kb / split).
+// pairs of k-blocks r n / split ... (r + 1) n / split of n.
 template <bool kF8>
 __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     linear_split(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const LinearParams p) {
@@ -784,7 +898,7 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     const uint32_t raw = smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;  // same offset in every CTA of the cluster
     uint8_t *smem = smem_raw + (base - raw);
-    const uint32_t x_stage = uint32_t(T) * 128u;
+    const uint32_t x_stage = uint32_t(lin::KPS * T) * 128u;
     const uint32_t sW = base;
     const uint32_t sX = base + uint32_t(NST) * lin::W_STAGE_BYTES;
     const uint32_t ring = uint32_t(NST) * (lin::W_STAGE_BYTES + x_stage);
@@ -802,14 +916,41 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     const int32_t tile = int32_t(blockIdx.x) / S;
     const int32_t tn = tile / p.sched.nm, tm = tile - tn * p.sched.nm;
     const int32_t m0 = tm * T, n0 = tn * lin::SPLIT_ROWS;
-    const int32_t kb0 = int32_t(int64_t(p.num_kb) * rank / S), kb1 = int32_t(int64_t(p.num_kb) * (rank + 1) / S);
+    // this CTA's stages: of the pairs of k-blocks (a last odd one is completed with zeros)
+    const int32_t steps = (p.num_kb + lin::KPS - 1) / lin::KPS;
+    const int32_t st0 = int32_t(int64_t(steps) * rank / S), st1 = int32_t(int64_t(steps) * (rank + 1) / S);
     const int valid = int(p.M - m0 < T ? p.M - m0 : T);  // rows of C in this tile
 
     bool ready = false;  // epilogue warps: the accumulator is complete
     uint32_t tmem_base = 0;
 
+    const uint32_t w_piece = p.b.mn ? lin::KPS * MN_CHUNK_BYTES : lin::SPLIT_ROWS * 128;  // between an operand's copies
+    const uint32_t x_piece = p.a.mn ? lin::KPS * MN_CHUNK_BYTES : uint32_t(T) * 128u;
+    auto load_w = [&](auto mode, auto mn, int32_t st, uint32_t stage) {
+        issue_copies<decltype(mode)::value, decltype(mn)::value, false>(&tmW, sW + stage * lin::W_STAGE_BYTES, w_piece, p.b.copies,
+                                                                        st * lin::KPS, BKE, n0, full_bar(stage), lane);
+    };
+    auto load_x = [&](auto mode, auto mn, int32_t st, uint32_t stage) {
+        issue_copies<decltype(mode)::value, decltype(mn)::value, false>(&tmX, sX + stage * x_stage, x_piece, p.a.copies,
+                                                                        st * lin::KPS, BKE, m0, full_bar(stage), lane);
+    };
+    // The stages after the first NST, each once the MMAs have freed its place. After
+    // a wait ran out, copies already issued get time to land before the CTA ends.
+    auto later_stages = [&](auto load) {
+        uint32_t stage = 0, phase = 0;
+        for (int32_t st = st0 + NST; st < st1; ++st) {
+            if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase, p.wait))) {
+                let_copies_land();
+                break;
+            }
+            load(st, stage);
+            if (++stage == uint32_t(NST)) { stage = 0; phase ^= 1u; }
+        }
+        __syncwarp();
+    };
+
     if (warp == 0) {
-        // ============================================================ producer
+        // ============================================================ producer (weights)
         // This warp sets up the barriers and starts the first stages by itself, while
         // the others set up tensor memory; only then it meets them.
         if (lane == 0) {
@@ -825,39 +966,23 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         }
         __syncwarp();
         griddep_wait();
-        uint32_t stage = 0, phase = 0, issued = 0;
-        bool ok = true;
-        const int nw = p.b_mn ? lin::SPLIT_ROWS / MN_CHUNK : 1;
-        const int nx = p.a_mn ? T / MN_CHUNK : 1;
-        for (int32_t kb = kb0; kb < kb1; ++kb) {
-            if (kb - kb0 == NST) __syncthreads();  // the others are set up
-            if (kb - kb0 >= NST && !__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, p.wait))) {
-                ok = false;
-                break;
-            }
-            const uint32_t fb = full_bar(stage);
-            if (lane == 0) mbar_arrive_expect_tx(fb, lin::W_STAGE_BYTES + x_stage);
-            __syncwarp();
-            const int32_t k0 = kb * BKE;
-            if (lane < nw + nx) {  // lane: copy `lane` of the weights, or copy `lane - nw` of the tokens
-                const bool is_w = lane < nw;
-                const int c = is_w ? lane : lane - nw;
-                const uint32_t dst = (is_w ? sW + stage * lin::W_STAGE_BYTES : sX + stage * x_stage) + uint32_t(c) * MN_CHUNK_BYTES;
-                const bool mn_major = (is_w ? p.b_mn : p.a_mn) != 0;
-                const int32_t mn = (is_w ? n0 : m0) + c * MN_CHUNK;
-                tma_load_2d(dst, is_w ? &tmW : &tmX, mn_major ? mn : k0, mn_major ? k0 : mn, fb);
-            }
-            ++issued;
-            if (++stage == uint32_t(NST)) { stage = 0; phase ^= 1u; }
-        }
-        if (kb1 - kb0 <= NST) __syncthreads();
+        // the first stages, both operands
+        const int32_t first = min(st0 + NST, st1);
+        for (int32_t st = st0; st < first; ++st) mbar_expect_tx_elect(full_bar(st - st0), lin::W_STAGE_BYTES + x_stage);
+        with_load(p.b, [&](auto mode, auto mn) {
+            for (int32_t st = st0; st < first; ++st) load_w(mode, mn, st, uint32_t(st - st0));
+        });
+        with_load(p.a, [&](auto mode, auto mn) {
+            for (int32_t st = st0; st < first; ++st) load_x(mode, mn, st, uint32_t(st - st0));
+        });
+        __syncthreads();  // the others are set up
         griddep_launch_dependents();
-        if (!ok && lane == 0) {  // let the copies this warp started land before the CTA exits
-            const uint32_t n = issued < uint32_t(NST) ? issued : uint32_t(NST);
-            for (uint32_t q = issued - n; q < issued; ++q)
-                mbar_wait_slow(full_bar(q % NST), (q / NST) & 1u, cleanup_wait(p.wait), false);
-        }
-        __syncwarp();
+        with_load(p.b, [&](auto mode, auto mn) {
+            later_stages([&](int32_t st, uint32_t stage) {
+                mbar_expect_tx_elect(full_bar(stage), lin::W_STAGE_BYTES + x_stage);
+                load_w(mode, mn, st, stage);
+            });
+        });
     } else {
         if (warp == MMA_WARP) {
             tmem_alloc(smem_addr(tmem_slot), uint32_t(p.tmem_cols));
@@ -871,22 +996,35 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         tmem_base = *tmem_slot;
     }
 
+    if (warp == EPI_WARP0) {
+        // ============================================================ producer (tokens), then epilogue
+        with_load(p.a, [&](auto mode, auto mn) {
+            later_stages([&](int32_t st, uint32_t stage) { load_x(mode, mn, st, stage); });
+        });
+    }
     if (warp == MMA_WARP) {
         // ============================================================ MMA issuer
         uint32_t stage = 0, phase = 0;
-        const DescStep dw = make_desc_step(sW, p.b_mn, lin::W_STAGE_BYTES);
-        const DescStep dx = make_desc_step(sX, p.a_mn, x_stage);
+        // descriptors of stage 0; a 32-byte step of K-major K is followed by the next
+        // k-block's rows after four, of MN-major K by the next 16 rows of its chunk
+        auto desc = [](uint32_t at, uint32_t mn) {
+            return mn ? smem_desc(at, lin::KPS * MN_CHUNK_BYTES, 1024) : smem_desc(at, 16, 1024);
+        };
+        const uint64_t dw = desc(sW, p.b.mn), dx = desc(sX, p.a.mn);
+        const uint32_t w_k = (p.b.mn ? UMMA_K * 128u : 32u) >> 4, x_k = (p.a.mn ? UMMA_K * 128u : 32u) >> 4;
+        const uint32_t w_kb = p.b.mn ? 4u * w_k : (lin::SPLIT_ROWS * 128u) >> 4, x_kb = p.a.mn ? 4u * x_k : (uint32_t(T) * 128u) >> 4;
         const uint32_t idesc = p.idesc;
-        for (int32_t kb = kb0; kb < kb1; ++kb) {
+        for (int32_t st = st0; st < st1; ++st) {
             if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, p.wait))) break;
             tc_fence_after();
-            const uint64_t w0 = dw.base + stage * dw.stage;
-            const uint64_t x0 = dx.base + stage * dx.stage;
+            const uint64_t w0 = dw + stage * (lin::W_STAGE_BYTES >> 4);
+            const uint64_t x0 = dx + stage * (x_stage >> 4);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                const uint32_t accumulate = kb != kb0 || ks != 0 ? 1u : 0u;
-                if constexpr (kF8) mma_f8_elect(tmem_base, w0 + ks * dw.k16, x0 + ks * dx.k16, idesc, accumulate);
-                else mma_f16_elect(tmem_base, w0 + ks * dw.k16, x0 + ks * dx.k16, idesc, accumulate);
+            for (int ks = 0; ks < 4 * lin::KPS; ++ks) {
+                const uint32_t accumulate = st != st0 || ks != 0 ? 1u : 0u;
+                const uint64_t wd = w0 + (ks / 4) * w_kb + (ks % 4) * w_k, xd = x0 + (ks / 4) * x_kb + (ks % 4) * x_k;
+                if constexpr (kF8) mma_f8_elect(tmem_base, wd, xd, idesc, accumulate);
+                else mma_f16_elect(tmem_base, wd, xd, idesc, accumulate);
             }
             mma_commit_elect(empty_bar(stage));
             if (++stage == uint32_t(NST)) { stage = 0; phase ^= 1u; }
