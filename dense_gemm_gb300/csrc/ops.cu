@@ -246,29 +246,36 @@ struct LinearPlan {
     int64_t whole, units;   // linear_pair: whole tiles, and units in all
 };
 
-// Estimated microseconds, from what was measured on GB300 (a step is a k-block of
-// 128 bytes): loads come back after kLatency, so a ring of n stages takes a step
-// every kLatency / n at best; weights come from DRAM at kDramBytes a microsecond;
-// linear_split sets up and ends in about 3.3, and sends and sums its partial rows
-// in the time given per row; linear_pair starts and ends in 3.9.
-constexpr double kLatency = 1.75, kStep = 0.33, kDramBytes = 6.6e6, kSplitFixed = 3.0, kSplitCluster = 0.3, kSplitSend = 0.008,
-                 kSplitRow = 0.018, kPairFixed = 3.9, kPairStep = 0.29, kPairFirst = 0.33, kPairHalf = 0.285;
+// Estimated microseconds, from what was measured on GB300. linear_split: set-up
+// and end 3.3, partial rows sent and summed at a time per row, the first loads back
+// after kLatency, a stage of two k-blocks every kSplitStep, and the weights from
+// DRAM at 6.2 bytes a picosecond, less where too few rings are in flight for it, and
+// from L2 at 11, once for every T rows.
+// linear_pair: set-up and end 3.9, a k-block of one round every kPairStep (more
+// where there is only one round, and hardly less for halves of tiles).
+constexpr double kLatency = 1.15, kDramBytes = 6.2e6, kL2Bytes = 11e6, kRingTime = 2.2, kSplitFixed = 3.0, kSplitCluster = 0.3,
+                 kSplitSend = 0.008, kSplitRow = 0.018, kPairFixed = 3.9, kPairStep = 0.29, kPairFirst = 0.34, kPairHalf = 0.275;
+constexpr double kSplitStep[kSplitTs] = {0.36, 0.42, 0.45, 0.37, 0.80};
 
 // linear_split's shape, rows per CTA T (an M-major A comes in chunks of 64 rows)
-// and K slices S. (4096 x 4096 weights, one token: S = 8 8.9 us, 4 9.7, 2 15.2,
-// 1 26.2; 256 tokens: T = 256, S = 4 15.2, T = 128, S = 2 17.5, pairs 22.3.)
+// and K slices S. (4096 x 4096 weights, one token: S = 8 9.0 us, 4 9.3, 2 11.2,
+// 1 15.6; 256 tokens: T = 128, S = 2 14.5, T = 256, S = 4 16.8, pairs 21.2.)
 double plan_split(int64_t M, int64_t N, int64_t num_kb, bool a_mn, const OpsState &o, LinearPlan *pl) {
     double best = 1e300;
     for (int t = a_mn ? 2 : 0; t < kSplitTs; ++t) {
         const int T = 16 << t;
         const int64_t tiles = cdiv(N, lin::SPLIT_ROWS) * cdiv(M, T);
-        const double step = std::max(kStep, kLatency / split_stages(T));
         for (int s = 0; s < kSplitSs && (s == 0 || (int64_t(2) << s) <= num_kb); ++s) {
             const int64_t S = int64_t(1) << s, ctas = tiles * S;
             const double one = kSplitFixed + (s > 0 ? kSplitCluster : 0.0) + kSplitSend * T + kSplitRow * T / double(S);
-            const double stream = kLatency + double(cdiv(cdiv(num_kb, lin::KPS), S) - 1) * step;
-            double cost = double(cdiv(ctas, o.split_slots[t][s])) * (one + stream);
-            cost = std::max(cost, one + double(N) * double(num_kb) * 128.0 / kDramBytes);
+            const double stream = kLatency + double(cdiv(cdiv(num_kb, lin::KPS), S) - 1) * kSplitStep[t];
+            // a few CTAs more than fit start late but end soon after the others
+            const double load = double(ctas) / o.split_slots[t][s];
+            const double rounds = load <= 1.0 ? 1.0 : load <= 1.1 ? load : double(cdiv(ctas, o.split_slots[t][s]));
+            const double rate = std::min(kDramBytes, double(ctas) * lin::split_ring(split_stages(T), T) / kRingTime);
+            const double weights = double(N) * double(num_kb) * 128.0;
+            const double moved = std::max(weights / rate, double(cdiv(M, T)) * weights / kL2Bytes);
+            const double cost = std::max(rounds * (one + stream), one + moved);
             if (cost < best) {
                 best = cost;
                 pl->T = T;
@@ -500,15 +507,17 @@ gemm_status_t gemm_linear(const gemm_matrix_t *A, const gemm_matrix_t *B, const 
 // ------------------------------------------------------------------ linear, backward
 namespace {
 
-// Column sums of D: each block sums a strip of columns over up to this many
-// rows, in kGradGroups interleaved groups.
+// Column sums of D: each block sums a strip of 256 columns (32 where rows are not on
+// 16-byte boundaries) over rows_per_block rows, 64 where that gives the GPU enough
+// blocks, fewer down to 8 (one per row group) where it does not.
 struct GradPlan {
     int64_t rows_per_block, parts;
 };
-GradPlan plan_grad(int64_t M) {
+GradPlan plan_grad(int64_t M, int64_t N) {
     GradPlan g;
     g.rows_per_block = 64;
-    if (cdiv(M, g.rows_per_block) > 512) g.rows_per_block = cdiv(cdiv(M, 512), 8) * 8;
+    while (g.rows_per_block > kGradGroups && cdiv(M, g.rows_per_block) * cdiv(N, 256) < 900) g.rows_per_block /= 2;
+    if (cdiv(M, g.rows_per_block) > 512) g.rows_per_block = cdiv(cdiv(M, 512), kGradGroups) * kGradGroups;
     g.parts = cdiv(M, g.rows_per_block);
     return g;
 }
@@ -529,7 +538,7 @@ gemm_status_t backward_space(const gemm_matrix_t *G, const Operand &a, const Ope
     s->ldd = (N + 63) / 64 * 64;
     if (s->store_d && K > 0) s->d = round256(uint64_t(M) * uint64_t(s->ldd) * 2u);
     if (need_dbias) {
-        const GradPlan g = plan_grad(M);
+        const GradPlan g = plan_grad(M, N);
         if (g.parts > 1) s->partial = round256(uint64_t(g.parts) * uint64_t(N) * 4u);
     }
     if (K > 0) copies_needed(a, b, &s->a, &s->b);
@@ -641,7 +650,7 @@ gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *
     // ---- D and its column sums
     Operand d_rows{G->data, M, N, G->stride_row, G->type, false};
     if ((s.store_d && products) || dbias != nullptr) {
-        const GradPlan gp = plan_grad(M);
+        const GradPlan gp = plan_grad(M, N);
         GradParams p;
         std::memset(&p, 0, sizeof(p));
         p.g = G->data;

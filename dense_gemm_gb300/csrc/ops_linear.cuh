@@ -44,77 +44,112 @@ __device__ __forceinline__ void mma_f8_pair_elect(uint32_t d_tmem, uint64_t a_de
 }
 
 // ------------------------------------------------------------------ activations
-// __expf is within 2 + |1.2 x| units in the last place and the quotients within
-// 2, far inside the 16-bit outputs' rounding and about 1e-6 for fp32 ones. The
-// normal distribution's cumulative function is Abramowitz & Stegun 26.2.17: for
+// Exponentials are 2^(x log2 e) by ex2.approx (2 units in the last place, plus the
+// argument's rounding) and reciprocals rcp.approx (1): far inside the 16-bit
+// outputs' rounding and about 1e-6 for fp32 ones. Work is on pairs of values, one
+// instruction per pair where there is one (fma2 and its like).
+// The normal distribution's cumulative function is Abramowitz & Stegun 26.2.17: for
 // x >= 0, 1 - Z(x) (b1 t + ... + b5 t^5) with t = 1 / (1 + 0.2316419 x) and Z the
 // density, off by less than 7.5e-8; the density is what gelu's slope needs too.
-// With CUDA's erff and __expf instead, D = G gelu'(P) of 4096 x 8192 took 82 us.
+// D = G gelu'(P) of 4096 x 8192 takes 82 us with CUDA's erff and __expf, 57 with the
+// formula value by value, 41 in pairs with four rows loaded ahead.
 constexpr uint32_t kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4;  // GEMM_ACT_*
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTwoSqrt2OverPi = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kLog2E = 1.4426950408889634f;
 
-__device__ __forceinline__ void normal_parts(float x, float &cdf, float &density) {
-    density = kInvSqrt2Pi * __expf(-0.5f * x * x);
-    const float t = __fdividef(1.0f, fmaf(0.2316419f, fabsf(x), 1.0f));
-    float q = fmaf(t, 1.330274429f, -1.821255978f);
-    q = fmaf(t, q, 1.781477937f);
-    q = fmaf(t, q, -0.356563782f);
-    q = fmaf(t, q, 0.319381530f);
-    q = q * t * density;
-    cdf = x < 0.0f ? q : 1.0f - q;
+__device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float2 exp2_approx(float2 x) { return make_float2(exp2_approx(x.x), exp2_approx(x.y)); }
+__device__ __forceinline__ float2 rcp_approx(float2 x) {
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(x.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(x.y));
+    return r;
+}
+
+// 1 / (1 + exp(-z))
+__device__ __forceinline__ float2 logistic(float2 z) {
+    return rcp_approx(add2(pair_of(1.0f), exp2_approx(mul2(z, pair_of(-kLog2E)))));
+}
+
+__device__ __forceinline__ void normal_parts(float2 x, float2 &cdf, float2 &density) {
+    density = mul2(exp2_approx(mul2(mul2(x, x), pair_of(-0.5f * kLog2E))), pair_of(kInvSqrt2Pi));
+    const float2 t = rcp_approx(fma2(make_float2(fabsf(x.x), fabsf(x.y)), pair_of(0.2316419f), pair_of(1.0f)));
+    float2 q = fma2(t, pair_of(1.330274429f), pair_of(-1.821255978f));
+    q = fma2(t, q, pair_of(1.781477937f));
+    q = fma2(t, q, pair_of(-0.356563782f));
+    q = fma2(t, q, pair_of(0.319381530f));
+    q = mul2(mul2(q, t), density);
+    const float2 above = fma2(q, pair_of(-1.0f), pair_of(1.0f));
+    cdf = make_float2(x.x < 0.0f ? q.x : above.x, x.y < 0.0f ? q.y : above.y);
+}
+
+// z with gelu's tanh form = x / (1 + exp(-z))
+__device__ __forceinline__ float2 tanh_argument(float2 x) {
+    const float2 x2 = mul2(x, x);
+    return mul2(mul2(x, pair_of(kTwoSqrt2OverPi)), fma2(x2, pair_of(0.044715f), pair_of(1.0f)));
 }
 
 template <uint32_t ACT>
-__device__ __forceinline__ float act_value(float x) {
-    if constexpr (ACT == kActRelu) return x < 0.0f ? 0.0f : x;
-    else if constexpr (ACT == kActSilu) return __fdividef(x, 1.0f + __expf(-x));
-    else if constexpr (ACT == kActGelu) {
-        float cdf, density;
-        normal_parts(x, cdf, density);
-        return x * cdf;
-    } else if constexpr (ACT == kActGeluTanh)
-        return __fdividef(x, 1.0f + __expf(-kTwoSqrt2OverPi * fmaf(0.044715f * x * x, x, x)));
-    else return x;
-}
-
-template <uint32_t ACT>
-__device__ __forceinline__ float act_slope(float x) {
-    if constexpr (ACT == kActRelu) return x > 0.0f ? 1.0f : 0.0f;
-    else if constexpr (ACT == kActSilu) {
-        const float s = __fdividef(1.0f, 1.0f + __expf(-x));
-        return s * fmaf(x, 1.0f - s, 1.0f);
+__device__ __forceinline__ float2 act_value(float2 x) {
+    if constexpr (ACT == kActRelu) {
+        return make_float2(x.x < 0.0f ? 0.0f : x.x, x.y < 0.0f ? 0.0f : x.y);
+    } else if constexpr (ACT == kActSilu) {
+        return mul2(x, logistic(x));
     } else if constexpr (ACT == kActGelu) {
-        float cdf, density;
+        float2 cdf, density;
         normal_parts(x, cdf, density);
-        return fmaf(x, density, cdf);
+        return mul2(x, cdf);
     } else if constexpr (ACT == kActGeluTanh) {
-        // x s(z) with z = c (x + 0.044715 x^3): s + x s (1 - s) z'
-        const float s = __fdividef(1.0f, 1.0f + __expf(-kTwoSqrt2OverPi * fmaf(0.044715f * x * x, x, x)));
-        const float dz = kTwoSqrt2OverPi * fmaf(0.134145f * x, x, 1.0f);
-        return fmaf(x * s * (1.0f - s), dz, s);
-    } else return 1.0f;
+        return mul2(x, logistic(tanh_argument(x)));
+    } else {
+        return x;
+    }
+}
+
+template <uint32_t ACT>
+__device__ __forceinline__ float2 act_slope(float2 x) {
+    if constexpr (ACT == kActRelu) {
+        return make_float2(x.x > 0.0f ? 1.0f : 0.0f, x.y > 0.0f ? 1.0f : 0.0f);
+    } else if constexpr (ACT == kActSilu) {  // s + x s (1 - s)
+        const float2 s = logistic(x), xs = mul2(x, s);
+        return fma2(xs, fma2(s, pair_of(-1.0f), pair_of(1.0f)), s);
+    } else if constexpr (ACT == kActGelu) {
+        float2 cdf, density;
+        normal_parts(x, cdf, density);
+        return fma2(x, density, cdf);
+    } else if constexpr (ACT == kActGeluTanh) {  // s + x s (1 - s) z'
+        const float2 s = logistic(tanh_argument(x)), xs = mul2(x, s);
+        const float2 dz = fma2(mul2(x, x), pair_of(0.134145f * kTwoSqrt2OverPi), pair_of(kTwoSqrt2OverPi));
+        return fma2(mul2(xs, fma2(s, pair_of(-1.0f), pair_of(1.0f))), dz, s);
+    } else {
+        return pair_of(1.0f);
+    }
+}
+
+template <uint32_t ACT, int N>
+__device__ __forceinline__ void act_all(float (&x)[N]) {
+    static_assert(N % 2 == 0, "pairs");
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+        const float2 v = act_value<ACT>(make_float2(x[i], x[i + 1]));
+        x[i] = v.x;
+        x[i + 1] = v.y;
+    }
 }
 
 template <int N>
 __device__ __forceinline__ void apply_act(uint32_t act, float (&x)[N]) {
     switch (act) {  // uniform
-        case kActRelu:
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = act_value<kActRelu>(x[i]);
-            break;
-        case kActGelu:
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = act_value<kActGelu>(x[i]);
-            break;
-        case kActGeluTanh:
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = act_value<kActGeluTanh>(x[i]);
-            break;
-        case kActSilu:
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = act_value<kActSilu>(x[i]);
-            break;
+        case kActRelu: act_all<kActRelu>(x); break;
+        case kActGelu: act_all<kActGelu>(x); break;
+        case kActGeluTanh: act_all<kActGeluTanh>(x); break;
+        case kActSilu: act_all<kActSilu>(x); break;
         default: break;
     }
 }
@@ -770,7 +805,7 @@ __device__ __forceinline__ void st_dsmem_b32(uint32_t cluster_addr, uint32_t v) 
 
 // The epilogue on one value of C.
 __device__ __forceinline__ float act_one(uint32_t act, float x) {
-    float v[1] = {x};
+    float v[2] = {x, x};
     apply_act(act, v);
     return v[0];
 }
@@ -1155,26 +1190,39 @@ struct GradParams {
 constexpr int kGradGroups = 8;
 
 template <uint32_t ACT>
-__device__ __forceinline__ float2 slope_of(float2 x) { return make_float2(act_slope<ACT>(x.x), act_slope<ACT>(x.y)); }
+__device__ __forceinline__ float2 slope_of(float2 x) { return act_slope<ACT>(x); }
 template <uint32_t ACT>
-__device__ __forceinline__ float slope_of(float x) { return act_slope<ACT>(x); }
+__device__ __forceinline__ float slope_of(float x) { return act_slope<ACT>(pair_of(x)).x; }
 
 template <uint32_t ACT, typename T, int VEC>
 __device__ __forceinline__ void grad_rows(const GradParams &p, int64_t col, int64_t r0, int64_t r1, F32<VEC> &sum) {
     const T *g = static_cast<const T *>(p.g), *pre = static_cast<const T *>(p.pre);
     T *d = static_cast<T *>(p.d);
-#pragma unroll 4
-    for (int64_t r = r0 + threadIdx.y; r < r1; r += kGradGroups) {
-        F32<VEC> x = widen<T, VEC>(load_raw<T, VEC>(g + r * p.ldg + col));
-        if constexpr (ACT != kActNone) {
-            const F32<VEC> b = widen<T, VEC>(load_raw<T, VEC>(pre + r * p.ldp + col));
+    constexpr int AHEAD = 4;  // rows loaded before the first is stored
+#pragma unroll 1
+    for (int64_t r = r0 + threadIdx.y; r < r1; r += AHEAD * kGradGroups) {
+        Raw<T, VEC> a[AHEAD], b[AHEAD];
 #pragma unroll
-            for (int i = 0; i < F32<VEC>::PAIRS; ++i)
-                x.p[i] = mul2(x.p[i], slope_of<ACT>(b.p[i]));
+        for (int k = 0; k < AHEAD; ++k) {
+            const int64_t row = r + k * kGradGroups;
+            if (row >= r1) break;
+            a[k] = load_raw<T, VEC>(g + row * p.ldg + col);
+            if constexpr (ACT != kActNone) b[k] = load_raw<T, VEC>(pre + row * p.ldp + col);
         }
-        if (d != nullptr) store_f32<T, VEC>(d + r * p.ldd + col, x);
 #pragma unroll
-        for (int i = 0; i < F32<VEC>::PAIRS; ++i) sum.p[i] = add2(sum.p[i], x.p[i]);
+        for (int k = 0; k < AHEAD; ++k) {
+            const int64_t row = r + k * kGradGroups;
+            if (row >= r1) break;
+            F32<VEC> x = widen<T, VEC>(a[k]);
+            if constexpr (ACT != kActNone) {
+                const F32<VEC> f = widen<T, VEC>(b[k]);
+#pragma unroll
+                for (int i = 0; i < F32<VEC>::PAIRS; ++i) x.p[i] = mul2(x.p[i], slope_of<ACT>(f.p[i]));
+            }
+            if (d != nullptr) store_f32<T, VEC>(d + row * p.ldd + col, x);
+#pragma unroll
+            for (int i = 0; i < F32<VEC>::PAIRS; ++i) sum.p[i] = add2(sum.p[i], x.p[i]);
+        }
     }
 }
 

@@ -120,7 +120,7 @@ def test_linear_backward_workspace(lib):
     size = lambda *a: (lib.gemm_linear_backward_workspace_size(*a, n), n.value)  # noqa: E731
     assert size(mat(), mat(), mat(), 0, 0, 4, 8, 8) == (0, 0)
     assert size(mat(), mat(), mat(), 2, 0, 4, 8, 8) == (0, 4 * 128)                    # D
-    assert size(mat(r=8), mat(), mat(), 2, 1, 130, 8, 8) == (0, 130 * 128 + 256)       # and 3 blocks of column sums
+    assert size(mat(r=8), mat(), mat(), 2, 1, 130, 8, 8) == (0, 130 * 128 + 768)       # and 17 blocks of 8 rows' sums of 8 columns
     assert size(mat(r=9), mat(), mat(r=9), 0, 0, 4, 9, 8)[1] == 4 * 128 + 1024         # G and B copied
 
 
