@@ -8,13 +8,15 @@ trapping. The binding loads it when GEMM_LIBRARY=debug.
 
 One translation unit, one -gencode, static CUDA runtime; no cmake. The same
 command works on x86-64 and aarch64 hosts. Beside it, the CPython extension
-_native.so (ops.py's argument marshalling) is built with the host compiler.
+_native.so (ops.py's argument marshalling, on PyTorch's C++ API) is built with
+the host compiler, at the same time.
 """
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -57,24 +59,37 @@ def up_to_date(lib: str = LIB, depends=None) -> bool:
     return all(os.path.getmtime(d) <= t for d in (DEPENDS if depends is None else depends))
 
 
+def native_command(out: str):
+    """The host compiler's command for _native.so; found without importing torch
+    (a slow import), which the extension's own process has loaded when it is used."""
+    import importlib.util
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    lib = os.path.join(torch_dir, "lib")
+    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), INCLUDE, sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
+            *(f"-I{d}" for d in inc), "-o", out, NATIVE_DEPENDS[0], f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch",
+            "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+
+
 def build_native(force: bool = False) -> str:
     if not force and up_to_date(NATIVE, NATIVE_DEPENDS):
         return NATIVE
     tmp = NATIVE + f".tmp{os.getpid()}"
-    subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
-                    "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-o", tmp, NATIVE_DEPENDS[0]], check=True)
+    subprocess.run(native_command(tmp), check=True)
     os.replace(tmp, NATIVE)
     return NATIVE
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
     lib = DEBUG_LIB if debug else LIB
-    build_native(force)
-    if not force and up_to_date(lib):
-        return lib
-    tmp = lib + f".tmp{os.getpid()}"
-    subprocess.run(command(tmp, verbose_ptxas, debug), check=True)
-    os.replace(tmp, lib)
+    with ThreadPoolExecutor(1) as beside:
+        native = beside.submit(build_native, force)
+        if force or not up_to_date(lib):
+            tmp = lib + f".tmp{os.getpid()}"
+            subprocess.run(command(tmp, verbose_ptxas, debug), check=True)
+            os.replace(tmp, lib)
+        native.result()
     return lib
 
 

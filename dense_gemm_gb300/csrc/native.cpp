@@ -1,16 +1,27 @@
-// Argument marshalling for ops.py as a CPython extension: tensors' attributes
-// -> gemm_matrix_t, outputs and workspaces from torch.empty, one C call. No
-// arithmetic. The same steps through ctypes took 20 us a call on the GB300's host
-// (three times a small kernel's time); here about 7.
+// Argument marshalling for ops.py as a CPython extension on PyTorch's C++ API:
+// tensors -> gemm_matrix_t, outputs and workspaces allocated, one C call. No
+// arithmetic. The smallest kernels take 2 us on the GPU; through ctypes the same
+// steps took 20 us a call on the GB300's host, through the tensors' Python
+// attributes 7 to 10.
 //
-// Every function works on the current device and its current stream; ops.py
-// makes another device or stream current first. The library's entry points
-// and the torch objects arrive through setup().
+// Every function makes the tensors' device and, where one is given, the stream
+// current for its call, so that what it allocates belongs to the stream it is
+// written on. The library's entry points arrive through setup().
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/Stream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
 #include <cstdint>
 #include <initializer_list>
+#include <optional>
 
 #include "gemm_ops.h"
 
@@ -27,65 +38,50 @@ template <typename F>
 F *entry(Entry e, F *) { return reinterpret_cast<F *>(g_entry[e]); }
 #define CALL(e, fn) (entry(e, &fn))
 
-PyObject *g_empty, *g_raw_stream, *g_error, *g_dtype[4], *g_uint8, *g_device_of;  // owned
-PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_t;          // interned names
-PyObject *g_kw_empty;  // ("dtype", "device")
+PyObject *g_error, *g_norm_result;  // GemmError, RmsNormResult (owned)
 
 const char *const kTypeNames[4] = {"float32", "float16", "bfloat16", "float8_e4m3fn"};
+const at::ScalarType kTypes[4] = {at::kFloat, at::kHalf, at::kBFloat16, at::kFloat8_e4m3fn};
+
+int type_code(at::ScalarType t) {
+    for (int i = 0; i < 4; ++i)
+        if (t == kTypes[i]) return i;
+    return -1;
+}
 
 // ------------------------------------------------------------------ tensors
 struct Tensor {
     PyObject *obj = nullptr;  // borrowed; nullptr: absent
     void *data = nullptr;
     int64_t n[2] = {0, 0}, s[2] = {1, 1};
+    int64_t nbytes = 0;
     int dims = 0;
     int type = -1;  // GEMM_TYPE_*, -1: another one
     int device = -1;
     explicit operator bool() const { return obj != nullptr; }
 };
 
-bool small_ints(PyObject *tuple, int64_t *v, int dims) {
-    for (int i = 0; i < dims; ++i) {
-        v[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(tuple, i));
-        if (v[i] == -1 && PyErr_Occurred()) return false;
-    }
-    return true;
-}
-
-int type_code(PyObject *dtype) {
-    for (int i = 0; i < 4; ++i)
-        if (dtype == g_dtype[i]) return i;
-    return -1;
-}
-
 // False with a Python error set. None is an absent tensor.
 bool read_tensor(PyObject *o, Tensor *t, const char *what) {
     if (o == Py_None) return true;
-    t->obj = o;
-    PyObject *shape = PyObject_GetAttr(o, s_shape);
-    if (shape == nullptr || !PyTuple_Check(shape)) {
-        Py_XDECREF(shape);
+    if (!THPVariable_Check(o)) {
         PyErr_Format(PyExc_TypeError, "%s must be a torch.Tensor", what);
         return false;
     }
-    t->dims = int(PyTuple_GET_SIZE(shape));
-    const int d = t->dims < 2 ? t->dims : 2;
-    bool ok = small_ints(shape, t->n, d);
-    Py_DECREF(shape);
-    PyObject *stride = ok ? PyObject_CallMethodNoArgs(o, s_stride) : nullptr;
-    ok = stride != nullptr && PyTuple_Check(stride) && small_ints(stride, t->s, d);
-    Py_XDECREF(stride);
-    PyObject *dtype = ok ? PyObject_GetAttr(o, s_dtype) : nullptr;
-    ok = dtype != nullptr;
-    if (ok) t->type = type_code(dtype);
-    Py_XDECREF(dtype);
-    PyObject *dev = ok ? PyObject_CallMethodNoArgs(o, s_get_device) : nullptr;
-    if (dev != nullptr) t->device = int(PyLong_AsLong(dev));
-    Py_XDECREF(dev);
-    PyObject *ptr = dev != nullptr ? PyObject_CallMethodNoArgs(o, s_data_ptr) : nullptr;
-    if (ptr != nullptr) t->data = PyLong_AsVoidPtr(ptr);
-    Py_XDECREF(ptr);
-    return !PyErr_Occurred();
+    const at::Tensor &v = THPVariable_Unpack(o);
+    t->obj = o;
+    t->dims = int(v.dim());
+    for (int i = 0; i < t->dims && i < 2; ++i) {
+        t->n[i] = v.size(i);
+        t->s[i] = v.stride(i);
+    }
+    t->type = type_code(v.scalar_type());
+    t->device = v.is_cuda() ? int(v.get_device()) : -1;
+    if (t->device >= 0) {
+        t->data = v.data_ptr();
+        t->nbytes = int64_t(v.nbytes());
+    }
+    return true;
 }
 
 // Dimensions of one element may have any stride in torch, also 0; a stride of 0
@@ -128,62 +124,67 @@ bool is_vector(const Tensor &t, int64_t n, int type, int or_type, const char *wh
     return false;
 }
 
-// New reference: torch.empty(shape, dtype=, device=) on the tensors' device, and its data.
-PyObject *empty(std::initializer_list<int64_t> shape, PyObject *dtype, PyObject *device, void **data) {
-    PyObject *size = PyTuple_New(Py_ssize_t(shape.size()));
-    if (size == nullptr) return nullptr;
-    Py_ssize_t i = 0;
-    for (int64_t n : shape) PyTuple_SET_ITEM(size, i++, PyLong_FromLongLong(n));
-    PyObject *args[3] = {size, dtype, device};
-    PyObject *t = PyObject_Vectorcall(g_empty, args, 1, g_kw_empty);
-    Py_DECREF(size);
-    if (t == nullptr) return nullptr;
-    PyObject *ptr = PyObject_CallMethodNoArgs(t, s_data_ptr);
-    if (ptr == nullptr) {
-        Py_DECREF(t);
-        return nullptr;
-    }
-    *data = PyLong_AsVoidPtr(ptr);
-    Py_DECREF(ptr);
-    return t;
-}
+// ------------------------------------------------------------------ where a call runs
+// The tensors' device and, where one is given, the stream made current.
+struct Place {
+    std::optional<c10::cuda::CUDAGuard> device;
+    std::optional<c10::cuda::CUDAStreamGuard> guard;
+    gemm_stream_t stream = nullptr;
+    at::TensorOptions options;
 
-// An owned reference that may stay empty.
-struct Ref {
-    PyObject *p = nullptr;
-    Ref() = default;
-    Ref(const Ref &) = delete;
-    Ref &operator=(const Ref &) = delete;
-    ~Ref() { Py_XDECREF(p); }
-    PyObject *give() {
-        PyObject *r = p != nullptr ? p : Py_NewRef(Py_None);
-        p = nullptr;
-        return r;
+    // False with a Python error set.
+    bool enter(int index, PyObject *given) {
+        options = at::TensorOptions().device(at::Device(at::kCUDA, at::DeviceIndex(index)));
+        if (given == Py_None) {
+            device.emplace(at::DeviceIndex(index));
+            stream = c10::cuda::getCurrentCUDAStream(at::DeviceIndex(index)).stream();
+            return true;
+        }
+        if (!THPStream_Check(given)) {
+            PyErr_SetString(PyExc_TypeError, "stream must be a torch.cuda.Stream");
+            return false;
+        }
+        const auto *s = reinterpret_cast<const THPStream *>(given);
+        if (s->device_type != int64_t(at::kCUDA) || s->device_index != index) {
+            PyErr_Format(PyExc_ValueError, "stream is on device %lld, the tensors on %d", (long long)s->device_index, index);
+            return false;
+        }
+        const auto cs = c10::cuda::CUDAStream::unpack3(s->stream_id, at::DeviceIndex(index), at::kCUDA);
+        guard.emplace(cs);
+        stream = cs.stream();
+        return true;
     }
+
+    // torch.empty on the call's device and stream.
+    at::Tensor empty(at::IntArrayRef shape, at::ScalarType type) const { return at::empty(shape, options.dtype(type)); }
 };
 
 // The matrix of an output: the given tensor, or a new one stored by rows or (turned) by columns.
-bool output(const Tensor &given, int64_t rows, int64_t cols, int type, bool turned, PyObject *device, Ref *keep,
-            gemm_matrix_t *m) {
-    if (given) {
-        keep->p = Py_NewRef(given.obj);
-        *m = matrix(given);
-        return true;
+struct Output {
+    PyObject *given = nullptr;  // borrowed
+    at::Tensor made;
+    gemm_matrix_t m = {nullptr, 1, 1, 0};
+
+    void set(const Tensor &t, int64_t rows, int64_t cols, int type, bool turned, const Place &place) {
+        if (t) {
+            given = t.obj;
+            m = matrix(t);
+            return;
+        }
+        made = turned ? place.empty({cols, rows}, kTypes[type]).t() : place.empty({rows, cols}, kTypes[type]);
+        m = turned ? gemm_matrix_t{made.data_ptr(), 1, rows > 0 ? rows : 1, type}
+                   : gemm_matrix_t{made.data_ptr(), cols > 0 ? cols : 1, 1, type};
     }
-    void *data = nullptr;
-    PyObject *t = turned ? empty({cols, rows}, g_dtype[type], device, &data) : empty({rows, cols}, g_dtype[type], device, &data);
-    if (t == nullptr) return false;
-    if (turned) {
-        keep->p = PyObject_CallMethodNoArgs(t, s_t);
-        Py_DECREF(t);
-        if (keep->p == nullptr) return false;
-        *m = gemm_matrix_t{data, 1, rows > 0 ? rows : 1, type};
-    } else {
-        keep->p = t;
-        *m = gemm_matrix_t{data, cols > 0 ? cols : 1, 1, type};
+    void set_vector(int64_t n, const Place &place) {
+        made = place.empty({n}, at::kFloat);
+        m.data = made.data_ptr();
     }
-    return true;
-}
+    float *floats() const { return static_cast<float *>(m.data); }
+    PyObject *give() {  // new reference
+        if (given != nullptr) return Py_NewRef(given);
+        return made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(Py_None);
+    }
+};
 
 // Raises for a status other than 0.
 bool passed(int status, const char *what) {
@@ -196,42 +197,31 @@ bool passed(int status, const char *what) {
     return false;
 }
 
-bool current_stream(int device, gemm_stream_t *stream) {
-    PyObject *d = PyLong_FromLong(device);
-    PyObject *s = PyObject_CallOneArg(g_raw_stream, d);
-    Py_DECREF(d);
-    if (s == nullptr) return false;
-    *stream = static_cast<gemm_stream_t>(PyLong_AsVoidPtr(s));
-    Py_DECREF(s);
-    return !PyErr_Occurred();
-}
-
 // The caller's workspace (any CUDA tensor) or one of `need` bytes.
-bool workspace(PyObject *given, uint64_t need, int device_index, PyObject *device, Ref *keep, void **data, uint64_t *bytes) {
-    *data = nullptr;
-    *bytes = 0;
-    if (given == Py_None) {
-        if (need == 0) return true;
-        *bytes = need;
-        keep->p = empty({int64_t(need)}, g_uint8, device, data);
-        return keep->p != nullptr;
-    }
-    Tensor t;
-    if (!read_tensor(given, &t, "workspace")) return false;
-    if (t.device != device_index) {
-        PyErr_SetString(PyExc_ValueError, "the workspace is on another device than the tensors");
-        return false;
-    }
-    PyObject *nbytes = PyObject_GetAttrString(given, "nbytes");
-    if (nbytes == nullptr) return false;
-    *bytes = PyLong_AsUnsignedLongLong(nbytes);
-    Py_DECREF(nbytes);
-    *data = t.data;
-    return !PyErr_Occurred();
-}
+struct Workspace {
+    at::Tensor made;
+    void *data = nullptr;
+    uint64_t bytes = 0;
 
-// The torch.device of a tensor (new reference).
-PyObject *device_of(const Tensor &t) { return PyObject_GetAttr(t.obj, g_device_of); }
+    bool set(PyObject *given, uint64_t need, int device, const Place &place) {
+        if (given == Py_None) {
+            if (need == 0) return true;
+            made = place.empty({int64_t(need)}, at::kByte);
+            data = made.data_ptr();
+            bytes = need;
+            return true;
+        }
+        Tensor t;
+        if (!read_tensor(given, &t, "workspace")) return false;
+        if (t.device != device) {
+            PyErr_SetString(PyExc_ValueError, "the workspace is on another device than the tensors");
+            return false;
+        }
+        data = t.data;
+        bytes = uint64_t(t.nbytes);
+        return true;
+    }
+};
 
 bool arguments(Py_ssize_t got, Py_ssize_t want) {
     if (got == want) return true;
@@ -251,24 +241,32 @@ bool operands(const Tensor &A, const Tensor &B) {
     return true;
 }
 
-bool c_dtype(PyObject *given, int otherwise, int *type, const char *what) {
-    *type = given == Py_None ? otherwise : type_code(given);
-    if (*type >= GEMM_TYPE_F32 && *type <= GEMM_TYPE_BF16) return true;
+// The type code of a torch.dtype argument; None: `otherwise`. -1: not one of the four.
+int dtype_code(PyObject *o, int otherwise) {
+    if (o == Py_None) return otherwise;
+    return THPDtype_Check(o) ? type_code(reinterpret_cast<const THPDtype *>(o)->scalar_type) : -1;
+}
+
+bool is_c_type(int type, const char *what) {
+    if (type >= GEMM_TYPE_F32 && type <= GEMM_TYPE_BF16) return true;
     PyErr_Format(PyExc_TypeError, "%s must be float32, float16 or bfloat16", what);
     return false;
 }
 
-PyObject *pair_or_first(Ref *first, Ref *second) {
-    if (second->p == nullptr) return first->give();
-    PyObject *t = PyTuple_New(2);
-    if (t == nullptr) return nullptr;
-    PyTuple_SET_ITEM(t, 0, first->give());
-    PyTuple_SET_ITEM(t, 1, second->give());
+// A tuple of new references (each taken, also on failure).
+PyObject *tuple_of(std::initializer_list<PyObject *> items) {
+    PyObject *t = PyTuple_New(Py_ssize_t(items.size()));
+    Py_ssize_t i = 0;
+    for (PyObject *o : items) {
+        if (t == nullptr) Py_XDECREF(o);
+        else PyTuple_SET_ITEM(t, i++, o);
+    }
     return t;
 }
 
 // ------------------------------------------------------------------ entry points
 PyObject *py_linear_workspace_size(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
     Tensor A, B;
     if (!arguments(n, 2) || !read_tensor(a[0], &A, "A") || !read_tensor(a[1], &B, "B") || !operands(A, B)) return nullptr;
     const gemm_matrix_t ma = matrix(A), mb = matrix(B);
@@ -276,11 +274,13 @@ PyObject *py_linear_workspace_size(PyObject *, PyObject *const *a, Py_ssize_t n)
     if (!passed(CALL(kLinearSize, gemm_linear_workspace_size)(&ma, &mb, A.n[0], B.n[1], A.n[1], &need), kEntryNames[kLinear]))
         return nullptr;
     return PyLong_FromUnsignedLongLong(need);
+    END_HANDLE_TH_ERRORS
 }
 
-// (A, B, bias, activation, residual, scale_a, scale_b, out, out_dtype, pre, return_pre, flags, workspace)
+// (A, B, bias, activation, residual, scale_a, scale_b, out, out_dtype, pre, return_pre, flags, workspace, stream)
 PyObject *py_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arguments(n, 13)) return nullptr;
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 14)) return nullptr;
     Tensor A, B, bias, res, sa, sb, out, pre;
     if (!read_tensor(a[0], &A, "A") || !read_tensor(a[1], &B, "B") || !operands(A, B) || !read_tensor(a[2], &bias, "bias") ||
         !read_tensor(a[4], &res, "residual") || !read_tensor(a[5], &sa, "scale_a") || !read_tensor(a[6], &sb, "scale_b") ||
@@ -292,28 +292,22 @@ PyObject *py_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
         PyErr_SetString(PyExc_ValueError, "scale_a and scale_b go with float8_e4m3fn operands, and only with them");
         return nullptr;
     }
-    int type = out ? out.type : -1;
-    if (out ? !c_dtype(Py_None, type, &type, "C")
-            : !c_dtype(a[8], res ? res.type : eight ? GEMM_TYPE_BF16 : A.type, &type, "C"))
-        return nullptr;
-    if (!same_device(A, {&B, &bias, &res, &sa, &sb, &out, &pre}) || !is_matrix(out, M, N, type, "out") ||
-        !is_matrix(res, M, N, type, "residual") || !is_matrix(pre, M, N, type, "pre") ||
+    const int type = out ? out.type : dtype_code(a[8], res ? res.type : eight ? GEMM_TYPE_BF16 : A.type);
+    if (!is_c_type(type, "C") || !same_device(A, {&B, &bias, &res, &sa, &sb, &out, &pre}) ||
+        !is_matrix(out, M, N, type, "out") || !is_matrix(res, M, N, type, "residual") || !is_matrix(pre, M, N, type, "pre") ||
         !is_vector(bias, N, GEMM_TYPE_F32, type, "bias") || !is_vector(sa, M, GEMM_TYPE_F32, GEMM_TYPE_F32, "scale_a") ||
         !is_vector(sb, N, GEMM_TYPE_F32, GEMM_TYPE_F32, "scale_b"))
         return nullptr;
     const gemm_matrix_t ma = matrix(A), mb = matrix(B);
-    uint64_t need = 0, bytes = 0;
+    uint64_t need = 0;
     if (!passed(CALL(kLinearSize, gemm_linear_workspace_size)(&ma, &mb, M, N, K, &need), kEntryNames[kLinear])) return nullptr;
-    Ref device, c_ref, pre_ref, ws_ref;
-    device.p = device_of(A);
-    gemm_matrix_t mc, mp = {nullptr, 1, 1, 0};
-    void *ws = nullptr;
-    gemm_stream_t stream;
+    Place place;
+    Workspace ws;
+    if (!place.enter(A.device, a[13]) || !ws.set(a[12], need, A.device, place)) return nullptr;
+    Output c, p;
     const bool want_pre = pre || a[10] == Py_True;
-    if (device.p == nullptr || !output(out, M, N, type, false, device.p, &c_ref, &mc) ||
-        (want_pre && !output(pre, M, N, type, false, device.p, &pre_ref, &mp)) ||
-        !workspace(a[12], need, A.device, device.p, &ws_ref, &ws, &bytes) || !current_stream(A.device, &stream))
-        return nullptr;
+    c.set(out, M, N, type, false, place);
+    if (want_pre) p.set(pre, M, N, type, false, place);
     gemm_epilogue_t ep = {};
     ep.bias = bias.data;
     ep.bias_type = bias ? bias.type : 0;
@@ -321,22 +315,25 @@ PyObject *py_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
     ep.scale_a = static_cast<const float *>(sa.data);
     ep.scale_b = static_cast<const float *>(sb.data);
     ep.residual = matrix(res);
-    ep.pre = mp;
-    if (!passed(CALL(kLinear, gemm_linear)(&ma, &mb, &mc, &ep, M, N, K, uint32_t(PyLong_AsLong(a[11])), ws, bytes, stream),
+    ep.pre = p.m;
+    if (!passed(CALL(kLinear, gemm_linear)(&ma, &mb, &c.m, &ep, M, N, K, uint32_t(PyLong_AsLong(a[11])), ws.data, ws.bytes,
+                                           place.stream),
                 kEntryNames[kLinear]))
         return nullptr;
-    return pair_or_first(&c_ref, &pre_ref);
+    return want_pre ? tuple_of({c.give(), p.give()}) : c.give();
+    END_HANDLE_TH_ERRORS
 }
 
-// (grad, A, B, pre, activation, need_a, need_b, need_bias, grad_dtype, flags, workspace)
+// (grad, A, B, pre, activation, need_a, need_b, need_bias, grad_dtype, flags, workspace, stream)
 PyObject *py_linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arguments(n, 11)) return nullptr;
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 12)) return nullptr;
     Tensor G, A, B, pre;
     if (!read_tensor(a[0], &G, "grad") || !read_tensor(a[1], &A, "A") || !read_tensor(a[2], &B, "B") || !operands(A, B) ||
         !read_tensor(a[3], &pre, "pre"))
         return nullptr;
-    if (A.type == GEMM_TYPE_E4M3) {
-        PyErr_SetString(PyExc_TypeError, "linear_backward takes float16 or bfloat16 operands");
+    if (A.type == GEMM_TYPE_E4M3 || !G) {
+        PyErr_SetString(PyExc_TypeError, "linear_backward takes a gradient and float16 or bfloat16 operands");
         return nullptr;
     }
     const int64_t M = A.n[0], K = A.n[1], N = B.n[1];
@@ -346,48 +343,37 @@ PyObject *py_linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         return nullptr;
     }
     if (act == GEMM_ACT_NONE) pre = Tensor();
-    int type;
-    if (!c_dtype(a[8], A.type, &type, "gradients") || !same_device(A, {&B, &G, &pre}) || !is_matrix(G, M, N, A.type, "grad") ||
+    const int type = dtype_code(a[8], A.type);
+    if (!is_c_type(type, "gradients") || !same_device(A, {&B, &G, &pre}) || !is_matrix(G, M, N, A.type, "grad") ||
         !is_matrix(pre, M, N, A.type, "pre"))
         return nullptr;
-    if (!G) {
-        PyErr_SetString(PyExc_TypeError, "grad must be a torch.Tensor");
-        return nullptr;
-    }
     const bool need_a = a[5] == Py_True, need_b = a[6] == Py_True, need_bias = a[7] == Py_True;
     const gemm_matrix_t mg = matrix(G), ma = matrix(A), mb = matrix(B), mp = matrix(pre);
-    uint64_t need = 0, bytes = 0;
+    uint64_t need = 0;
     if (!passed(CALL(kBackwardSize, gemm_linear_backward_workspace_size)(&mg, &ma, &mb, act, need_bias, M, N, K, &need),
                 kEntryNames[kBackward]))
         return nullptr;
-    Ref device, da_ref, db_ref, bias_ref, ws_ref;
-    device.p = device_of(A);
-    gemm_matrix_t mda = {nullptr, 1, 1, 0}, mdb = mda;
-    void *ws = nullptr, *dbias = nullptr;
-    gemm_stream_t stream;
-    const Tensor none;
+    Place place;
+    Workspace ws;
+    if (!place.enter(A.device, a[11]) || !ws.set(a[10], need, A.device, place)) return nullptr;
+    Output da, db, dbias;
     // gradients are stored as their operands are: by columns where those are
     auto turned = [](const Tensor &t) { return t.s[0] == 1 && t.s[1] != 1 && t.n[0] > 1 && t.n[1] > 1; };
-    if (device.p == nullptr || (need_a && !output(none, M, K, type, turned(A), device.p, &da_ref, &mda)) ||
-        (need_b && !output(none, K, N, type, turned(B), device.p, &db_ref, &mdb)) ||
-        (need_bias && (bias_ref.p = empty({N}, g_dtype[GEMM_TYPE_F32], device.p, &dbias)) == nullptr) ||
-        !workspace(a[10], need, A.device, device.p, &ws_ref, &ws, &bytes) || !current_stream(A.device, &stream))
-        return nullptr;
-    if (!passed(CALL(kBackward, gemm_linear_backward)(&mg, &ma, &mb, &mp, act, &mda, &mdb, static_cast<float *>(dbias), M, N, K,
-                                                      uint32_t(PyLong_AsLong(a[9])), ws, bytes, stream),
+    if (need_a) da.set(Tensor(), M, K, type, turned(A), place);
+    if (need_b) db.set(Tensor(), K, N, type, turned(B), place);
+    if (need_bias) dbias.set_vector(N, place);
+    if (!passed(CALL(kBackward, gemm_linear_backward)(&mg, &ma, &mb, &mp, act, &da.m, &db.m, dbias.floats(), M, N, K,
+                                                      uint32_t(PyLong_AsLong(a[9])), ws.data, ws.bytes, place.stream),
                 kEntryNames[kBackward]))
         return nullptr;
-    PyObject *t = PyTuple_New(3);
-    if (t == nullptr) return nullptr;
-    PyTuple_SET_ITEM(t, 0, da_ref.give());
-    PyTuple_SET_ITEM(t, 1, db_ref.give());
-    PyTuple_SET_ITEM(t, 2, bias_ref.give());
-    return t;
+    return tuple_of({da.give(), db.give(), dbias.give()});
+    END_HANDLE_TH_ERRORS
 }
 
-// (x, weight, residual, eps, out_dtype, return_rstd, out, h_out) -> (y, h, scale, rstd)
+// (x, weight, residual, eps, out_dtype, return_rstd, out, h_out, stream) -> RmsNormResult
 PyObject *py_rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arguments(n, 8)) return nullptr;
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 9)) return nullptr;
     Tensor x, w, r, out, h;
     if (!read_tensor(a[0], &x, "x") || !read_tensor(a[1], &w, "weight") || !read_tensor(a[2], &r, "residual") ||
         !read_tensor(a[6], &out, "out") || !read_tensor(a[7], &h, "h_out"))
@@ -397,7 +383,7 @@ PyObject *py_rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         return nullptr;
     }
     const int64_t rows = x.n[0], width = x.n[1];
-    const int type = out ? out.type : a[4] == Py_None ? x.type : type_code(a[4]);
+    const int type = out ? out.type : dtype_code(a[4], x.type);
     if (type != x.type && type != GEMM_TYPE_E4M3) {
         PyErr_SetString(PyExc_TypeError, "y has x's type or float8_e4m3fn");
         return nullptr;
@@ -412,34 +398,32 @@ PyObject *py_rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         !is_matrix(r, rows, width, x.type, "residual") || !is_matrix(out, rows, width, type, "out") ||
         !is_matrix(h, rows, width, x.type, "h_out"))
         return nullptr;
-    Ref device, y_ref, h_ref, scale_ref, rstd_ref;
-    device.p = device_of(x);
-    gemm_matrix_t my, mh = {nullptr, 1, 1, 0};
-    void *scale = nullptr, *rstd = nullptr;
-    gemm_stream_t stream;
-    if (device.p == nullptr || !output(out, rows, width, type, false, device.p, &y_ref, &my) ||
-        (r && !output(h, rows, width, x.type, false, device.p, &h_ref, &mh)) ||
-        (type == GEMM_TYPE_E4M3 && (scale_ref.p = empty({rows}, g_dtype[GEMM_TYPE_F32], device.p, &scale)) == nullptr) ||
-        (a[5] == Py_True && (rstd_ref.p = empty({rows}, g_dtype[GEMM_TYPE_F32], device.p, &rstd)) == nullptr) ||
-        !current_stream(x.device, &stream))
-        return nullptr;
+    Place place;
+    if (!place.enter(x.device, a[8])) return nullptr;
+    Output y, sum, scale, rstd;
+    y.set(out, rows, width, type, false, place);
+    if (r) sum.set(h, rows, width, x.type, false, place);
+    if (type == GEMM_TYPE_E4M3) scale.set_vector(rows, place);
+    if (a[5] == Py_True) rstd.set_vector(rows, place);
     const gemm_matrix_t mx = matrix(x), mr = matrix(r);
-    if (!passed(CALL(kNorm, gemm_rms_norm)(&mx, &mr, w.data, w.type, &my, &mh, static_cast<float *>(scale),
-                                           static_cast<float *>(rstd), rows, width, float(eps), stream),
+    if (!passed(CALL(kNorm, gemm_rms_norm)(&mx, &mr, w.data, w.type, &y.m, &sum.m, scale.floats(), rstd.floats(), rows, width,
+                                           float(eps), place.stream),
                 kEntryNames[kNorm]))
         return nullptr;
-    PyObject *t = PyTuple_New(4);
+    PyObject *t = tuple_of({y.give(), sum.give(), scale.give(), rstd.give()});
     if (t == nullptr) return nullptr;
-    PyTuple_SET_ITEM(t, 0, y_ref.give());
-    PyTuple_SET_ITEM(t, 1, h_ref.give());
-    PyTuple_SET_ITEM(t, 2, scale_ref.give());
-    PyTuple_SET_ITEM(t, 3, rstd_ref.give());
-    return t;
+    PyObject *args = tuple_of({t});
+    if (args == nullptr) return nullptr;
+    PyObject *result = PyTuple_Type.tp_new(reinterpret_cast<PyTypeObject *>(g_norm_result), args, nullptr);  // as its _make
+    Py_DECREF(args);
+    return result;
+    END_HANDLE_TH_ERRORS
 }
 
-// (grad, h, weight, rstd, grad_h, need_weight, out, workspace) -> (dx, dweight)
+// (grad, h, weight, rstd, grad_h, need_weight, out, workspace, stream) -> (dx, dweight)
 PyObject *py_rms_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    if (!arguments(n, 8)) return nullptr;
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 9)) return nullptr;
     Tensor g, h, w, rstd, gh, out;
     if (!read_tensor(a[0], &g, "grad") || !read_tensor(a[1], &h, "h") || !read_tensor(a[2], &w, "weight") ||
         !read_tensor(a[3], &rstd, "rstd") || !read_tensor(a[4], &gh, "grad_h") || !read_tensor(a[6], &out, "out"))
@@ -454,36 +438,29 @@ PyObject *py_rms_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
         !is_vector(w, width, GEMM_TYPE_F32, h.type, "weight") || !is_vector(rstd, rows, GEMM_TYPE_F32, GEMM_TYPE_F32, "rstd"))
         return nullptr;
     const bool need_weight = a[5] == Py_True;
-    uint64_t need = 0, bytes = 0;
+    uint64_t need = 0;
     if (need_weight &&
         !passed(CALL(kNormBackwardSize, gemm_rms_norm_backward_workspace_size)(rows, width, &need), kEntryNames[kNormBackward]))
         return nullptr;
-    Ref device, dx_ref, dw_ref, ws_ref;
-    device.p = device_of(h);
-    gemm_matrix_t mdx;
-    void *ws = nullptr, *dw = nullptr;
-    gemm_stream_t stream;
-    if (device.p == nullptr || !output(out, rows, width, h.type, false, device.p, &dx_ref, &mdx) ||
-        (need_weight && (dw_ref.p = empty({width}, g_dtype[GEMM_TYPE_F32], device.p, &dw)) == nullptr) ||
-        !workspace(a[7], need, h.device, device.p, &ws_ref, &ws, &bytes) || !current_stream(h.device, &stream))
-        return nullptr;
+    Place place;
+    Workspace ws;
+    if (!place.enter(h.device, a[8]) || !ws.set(a[7], need, h.device, place)) return nullptr;
+    Output dx, dw;
+    dx.set(out, rows, width, h.type, false, place);
+    if (need_weight) dw.set_vector(width, place);
     const gemm_matrix_t mg = matrix(g), mh = matrix(h), mgh = matrix(gh);
     if (!passed(CALL(kNormBackward, gemm_rms_norm_backward)(&mg, &mh, w.data, w.type, static_cast<const float *>(rstd.data), &mgh,
-                                                            &mdx, static_cast<float *>(dw), rows, width, ws, bytes, stream),
+                                                            &dx.m, dw.floats(), rows, width, ws.data, ws.bytes, place.stream),
                 kEntryNames[kNormBackward]))
         return nullptr;
-    PyObject *t = PyTuple_New(2);
-    if (t == nullptr) return nullptr;
-    PyTuple_SET_ITEM(t, 0, dx_ref.give());
-    PyTuple_SET_ITEM(t, 1, dw_ref.give());
-    return t;
+    return tuple_of({dx.give(), dw.give()});
+    END_HANDLE_TH_ERRORS
 }
 
-// setup({entry name: address}, (float32, float16, bfloat16, float8_e4m3fn), uint8, empty, raw_stream, error)
+// setup({entry name: address}, GemmError, RmsNormResult)
 PyObject *py_setup(PyObject *, PyObject *args) {
-    PyObject *entries, *types, *uint8, *empty_fn, *raw, *error;
-    if (!PyArg_ParseTuple(args, "O!O!OOOO", &PyDict_Type, &entries, &PyTuple_Type, &types, &uint8, &empty_fn, &raw, &error))
-        return nullptr;
+    PyObject *entries, *error, *norm_result;
+    if (!PyArg_ParseTuple(args, "O!OO", &PyDict_Type, &entries, &error, &norm_result)) return nullptr;
     for (int i = 0; i < kEntries; ++i) {
         PyObject *p = PyDict_GetItemString(entries, kEntryNames[i]);
         if (p == nullptr) {
@@ -493,15 +470,8 @@ PyObject *py_setup(PyObject *, PyObject *args) {
         g_entry[i] = PyLong_AsVoidPtr(p);
         if (PyErr_Occurred()) return nullptr;
     }
-    if (PyTuple_GET_SIZE(types) != 4) {
-        PyErr_SetString(PyExc_ValueError, "four element types");
-        return nullptr;
-    }
-    for (int i = 0; i < 4; ++i) Py_XSETREF(g_dtype[i], Py_NewRef(PyTuple_GET_ITEM(types, i)));
-    Py_XSETREF(g_uint8, Py_NewRef(uint8));
-    Py_XSETREF(g_empty, Py_NewRef(empty_fn));
-    Py_XSETREF(g_raw_stream, Py_NewRef(raw));
     Py_XSETREF(g_error, Py_NewRef(error));
+    Py_XSETREF(g_norm_result, Py_NewRef(norm_result));
     Py_RETURN_NONE;
 }
 
@@ -522,15 +492,4 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", "Argument marshalling o
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__native() {
-    s_dtype = PyUnicode_InternFromString("dtype");
-    s_shape = PyUnicode_InternFromString("shape");
-    s_stride = PyUnicode_InternFromString("stride");
-    s_data_ptr = PyUnicode_InternFromString("data_ptr");
-    s_get_device = PyUnicode_InternFromString("get_device");
-    s_t = PyUnicode_InternFromString("t");
-    g_device_of = PyUnicode_InternFromString("device");
-    g_kw_empty = Py_BuildValue("(ss)", "dtype", "device");
-    if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_get_device || !s_t || !g_device_of || !g_kw_empty) return nullptr;
-    return PyModule_Create(&kModule);
-}
+PyMODINIT_FUNC PyInit__native() { return PyModule_Create(&kModule); }

@@ -6,7 +6,6 @@ with the library); the arithmetic runs in the library's CUDA kernels. Outputs
 and workspaces that are not given are allocated on the stream the kernels run
 on (``stream``, or the current one).
 """
-import contextlib
 import ctypes
 from typing import NamedTuple, Optional
 
@@ -20,9 +19,14 @@ LINEAR_KERNELS = {"auto": 0, "pair": 1, "split": 2}
 _ENTRIES = ("gemm_linear", "gemm_linear_workspace_size", "gemm_linear_backward", "gemm_linear_backward_workspace_size",
             "gemm_rms_norm", "gemm_rms_norm_backward", "gemm_rms_norm_backward_workspace_size")
 
-# the C-level forms of torch.cuda.current_device / current_stream, 0.1 us against 0.3 and 2
-_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+class RmsNormResult(NamedTuple):
+    """What ``rms_norm`` returns; ``h``, ``scale`` and ``rstd`` are None where they are not made."""
+    y: torch.Tensor
+    h: Optional[torch.Tensor]
+    scale: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]
+
 
 _module = None
 
@@ -36,29 +40,9 @@ def _native():
             from . import _native as module
         except ImportError as e:
             raise GemmError(3, f"dense_gemm_gb300/_native.so ({e}): build it with `python -m dense_gemm_gb300.build`") from e
-        module.setup({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ENTRIES},
-                     (torch.float32, torch.float16, torch.bfloat16, torch.float8_e4m3fn), torch.uint8, torch.empty, _raw_stream,
-                     GemmError)
+        module.setup({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ENTRIES}, GemmError, RmsNormResult)
         _module = module
     return _module
-
-
-@contextlib.contextmanager
-def _current(index: int, stream):
-    """Makes a tensor's device and the call's stream current."""
-    if stream is not None and stream.device.index != index:
-        raise ValueError(f"stream is on {stream.device}, the tensors on device {index}")
-    with torch.cuda.device(index), torch.cuda.stream(stream):
-        yield
-
-
-def _call(name: str, first: torch.Tensor, stream, args):
-    fn = getattr(_module or _native(), name)
-    index = first.get_device() if isinstance(first, torch.Tensor) else -1
-    if index < 0 or (stream is None and index == _current_device()):
-        return fn(*args)  # a tensor that is not on a GPU is refused there
-    with _current(index, stream):
-        return fn(*args)
 
 
 def _code(table: dict, key, what: str) -> int:
@@ -90,8 +74,9 @@ def linear(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor = None, *, activ
     (C, pre) is returned. ``kernel`` chooses between "pair" and "split" by hand
     (gemm_linear in include/gemm_ops.h).
     """
-    return _call("linear", A, stream, (A, B, bias, _code(ACTIVATIONS, activation, "activation"), residual, scale_a, scale_b, out,
-                                       out_dtype, pre, bool(return_pre), _code(LINEAR_KERNELS, kernel, "kernel"), workspace))
+    return (_module or _native()).linear(
+        A, B, bias, _code(ACTIVATIONS, activation, "activation"), residual, scale_a, scale_b, out, out_dtype, pre,
+        bool(return_pre), _code(LINEAR_KERNELS, kernel, "kernel"), workspace, stream)
 
 
 def linear_backward(grad: torch.Tensor, A: torch.Tensor, B: torch.Tensor, *, pre: torch.Tensor = None,
@@ -105,17 +90,9 @@ def linear_backward(grad: torch.Tensor, A: torch.Tensor, B: torch.Tensor, *, pre
     and the memory order of A and B; dbias [N] is float32. The residual's
     gradient is ``grad`` itself.
     """
-    return _call("linear_backward", grad, stream, (grad, A, B, pre, _code(ACTIVATIONS, activation, "activation"), bool(need_a),
-                                                   bool(need_b), bool(need_bias), grad_dtype,
-                                                   _code(LINEAR_KERNELS, kernel, "kernel"), workspace))
-
-
-class RmsNormResult(NamedTuple):
-    """What ``rms_norm`` returns; ``h``, ``scale`` and ``rstd`` are None where they are not made."""
-    y: torch.Tensor
-    h: Optional[torch.Tensor]
-    scale: Optional[torch.Tensor]
-    rstd: Optional[torch.Tensor]
+    return (_module or _native()).linear_backward(
+        grad, A, B, pre, _code(ACTIVATIONS, activation, "activation"), bool(need_a), bool(need_b), bool(need_bias), grad_dtype,
+        _code(LINEAR_KERNELS, kernel, "kernel"), workspace, stream)
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor = None, eps: float = 1e-6,
@@ -130,7 +107,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor = 
     residual is given; ``h_out`` may be x or residual itself. ``return_rstd``
     keeps 1 / sqrt(mean(h^2) + eps) for ``rms_norm_backward``.
     """
-    return RmsNormResult._make(_call("rms_norm", x, stream, (x, weight, residual, eps, out_dtype, bool(return_rstd), out, h_out)))
+    return (_module or _native()).rms_norm(x, weight, residual, eps, out_dtype, bool(return_rstd), out, h_out, stream)
 
 
 def rms_norm_backward(grad: torch.Tensor, h: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, *,
@@ -144,4 +121,4 @@ def rms_norm_backward(grad: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     ``out`` may be grad or grad_h itself. dweight is float32 [width], None
     unless ``need_weight``.
     """
-    return _call("rms_norm_backward", grad, stream, (grad, h, weight, rstd, grad_h, bool(need_weight), out, workspace))
+    return (_module or _native()).rms_norm_backward(grad, h, weight, rstd, grad_h, bool(need_weight), out, workspace, stream)
