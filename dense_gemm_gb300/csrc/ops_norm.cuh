@@ -219,6 +219,28 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
     return warp_sum(lane < wpr ? red[base + lane] : 0.0f);
 }
 
+// row_sum<true> of R rows per thread at a time.
+template <int R>
+__device__ __forceinline__ void rows_sum(float (&v)[R], float (*red)[32]) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
+    const int wpr = blockDim.x >> 5, lane = threadIdx.x & 31, base = int(threadIdx.y) * wpr;
+    if (lane == 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) red[r][base + (threadIdx.x >> 5)] = v[r];
+    }
+    __syncthreads();
+    if (wpr == 1) return;
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = lane < wpr ? red[r][base + lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < R; ++r) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
+}
+
 // The largest |value|, NaN if there is one.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
@@ -402,7 +424,7 @@ constexpr int kRingThreads = 512;  // at most: 128 registers each, so two blocks
 struct RingShape {
     int32_t slots;
     int32_t pitch;        // bytes between the rows of one array in a slot
-    int32_t array_bytes;  // blockDim.y * pitch
+    int32_t array_bytes;  // rows of a slot * pitch
     int32_t slot_bytes;   // arrays * array_bytes
 };
 
@@ -422,13 +444,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// Warp 0 of the block starts the copies of rows base .. base + blockDim.y - 1 of
-// every array into a slot; one lane per copy.
+// Warp 0 of the block starts the copies of rows base .. base + nrows - 1 of every
+// array into a slot; one lane per copy.
 template <typename T>
-__device__ __forceinline__ void fill_slot(const RowSource<T> *src, int arrays, const RingShape &ring, uint8_t *slots, int slot,
-                                          uint32_t bar, int64_t base, int64_t rows, int64_t width) {
+__device__ __forceinline__ void fill_slot(const RowSource<T> *src, int arrays, int nrows, const RingShape &ring, uint8_t *slots,
+                                          int slot, uint32_t bar, int64_t base, int64_t rows, int64_t width) {
     if (threadIdx.y != 0 || threadIdx.x >= 32) return;
-    const int lane = threadIdx.x, nrows = int(blockDim.y);
+    const int lane = threadIdx.x;
     const int a = lane / nrows, y = lane - a * nrows;
     uint32_t bytes = 0, dst = 0;
     const void *from = nullptr;
@@ -472,7 +494,7 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_rows_kernel(const NormP
     const RowSource<T> src[3] = {{static_cast<const T *>(p.x), p.ldx}, {static_cast<const T *>(p.r), p.ldr}, {nullptr, 0}};
     const int arrays = p.r != nullptr ? 2 : 1;
     auto refill = [&](int64_t base, int slot) {
-        if (base < p.rows) fill_slot(src, arrays, ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
+        if (base < p.rows) fill_slot(src, arrays, int(blockDim.y), ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
     };
     for (int s = 0; s < ring.slots; ++s) refill(first + s * step, s);
     auto at_of = [&](int j) { return (j * int(blockDim.x) + int(threadIdx.x)) * VEC; };
@@ -491,7 +513,7 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_rows_kernel(const NormP
         const bool live = row < p.rows;
         ok = mbar_wait(smem_addr(&full[slot]), phase, p.wait) && ok;
         const uint32_t mine = ring0 + uint32_t(slot * ring.slot_bytes);
-        const uint32_t x = src[0].in_slot(mine, row), r = src[1].in_slot(mine + uint32_t(ring.array_bytes), row);
+        const uint32_t x = mine, r = mine + uint32_t(ring.array_bytes);  // rows on 16-byte boundaries
         T *h = static_cast<T *>(p.h) + row * p.ldh;
         F32<VEC> t[NV];
         auto ss2 = splat<VEC>(0.0f);
@@ -560,7 +582,7 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_rows_any_kernel(const N
     const RowSource<T> src[3] = {{static_cast<const T *>(p.x), p.ldx}, {static_cast<const T *>(p.r), p.ldr}, {nullptr, 0}};
     const bool has_r = p.r != nullptr, has_h = p.h != nullptr;
     auto refill = [&](int64_t base, int slot) {
-        if (base < p.rows) fill_slot(src, has_r ? 2 : 1, ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
+        if (base < p.rows) fill_slot(src, has_r ? 2 : 1, int(blockDim.y), ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
     };
     for (int s = 0; s < ring.slots; ++s) refill(first + s * step, s);
     const int width = int(p.width), tpr = int(blockDim.x);
@@ -631,10 +653,13 @@ struct NormBackwardParams {
 // shared-memory slots, and a thread keeps its columns, so that their dweight
 // sums stay in its registers and each block writes one row of partial sums at
 // its end. A slot is read twice (for the row's dot product and for dx) and
-// refilled after the next step's barrier.
-template <typename T, int VEC, int NV>
+// refilled after the next step's barrier. The chain of a row's reduction is long
+// beside its arithmetic, so a thread works on R rows at a time (row base +
+// threadIdx.y * R + r), with one barrier for all of them.
+template <typename T, int NV, int R>
 __global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_kernel(const NormBackwardParams p, const RingShape ring) {
-    __shared__ float red[2][32];
+    constexpr int VEC = 8;
+    __shared__ float red[2][R][32];
     __shared__ __align__(8) uint64_t full[kRingSlots];
     extern __shared__ __align__(16) uint8_t rows[];
     const int tid = threadIdx.y * blockDim.x + threadIdx.x;
@@ -645,13 +670,15 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_kernel(co
     __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t step = int64_t(gridDim.x) * blockDim.y;
-    const int64_t first = int64_t(blockIdx.x) * blockDim.y;
+    const int per_slot = int(blockDim.y) * R;
+    const int64_t step = int64_t(gridDim.x) * per_slot;
+    const int64_t first = int64_t(blockIdx.x) * per_slot;
     const RowSource<T> src[3] = {{static_cast<const T *>(p.g), p.ldg}, {static_cast<const T *>(p.h), p.ldh},
                                  {static_cast<const T *>(p.dh), p.lddh}};
-    const int arrays = p.dh != nullptr ? 3 : 2;
+    const bool has_d = p.dh != nullptr;
     auto refill = [&](int64_t base, int slot) {
-        if (base < p.rows) fill_slot(src, arrays, ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
+        if (base < p.rows)
+            fill_slot(src, has_d ? 3 : 2, per_slot, ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
     };
     for (int s = 0; s < ring.slots; ++s) refill(first + s * step, s);
     auto at_of = [&](int j) { return (j * int(blockDim.x) + int(threadIdx.x)) * VEC; };
@@ -665,53 +692,68 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_kernel(co
         if (at_of(j) < width && !p.w_f32) w16[j] = load_raw<T, VEC>(static_cast<const T *>(p.w) + at_of(j));
     }
     auto weight = [&](int j) { return p.w_f32 ? load_weight<T, VEC>(p.w, true, at_of(j)) : widen<T, VEC>(w16[j]); };
-    const uint32_t ring0 = smem_addr(rows) + uint32_t(int(threadIdx.y) * ring.pitch);
-    const bool has_d = p.dh != nullptr;
+    const uint32_t ring0 = smem_addr(rows) + uint32_t(int(threadIdx.y) * R * ring.pitch);
+    const uint32_t off_h = uint32_t(ring.array_bytes), off_d = 2u * off_h;
     int slot = 0, last = ring.slots - 1;  // `last`: the slot before it in the ring
     uint32_t phase = 0;
     int flip = 0;
     bool ok = true;
-    auto rstd_of = [&](int64_t row) { return row < p.rows ? p.rstd[row] : 0.0f; };
-    float rs_next = rstd_of(first + threadIdx.y);
-    for (int64_t base = first; base < p.rows; base += step, flip ^= 1) {
-        const int64_t row = base + threadIdx.y;
-        const bool live = row < p.rows;
-        const float rs = rs_next;
-        rs_next = rstd_of(row + step);
+    int64_t row = first + int64_t(threadIdx.y) * R;
+    T *dx = static_cast<T *>(p.dx) + row * p.lddx;
+    const int64_t dx_step = step * p.lddx;
+    float rs_next[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) rs_next[r] = row + r < p.rows ? p.rstd[row + r] : 0.0f;
+    for (int64_t base = first; base < p.rows; base += step, row += step, dx += dx_step, flip ^= 1) {
+        float rs[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            rs[r] = rs_next[r];
+            rs_next[r] = row + step + r < p.rows ? p.rstd[row + step + r] : 0.0f;
+        }
         ok = mbar_wait(smem_addr(&full[slot]), phase, p.wait) && ok;
         const uint32_t mine = ring0 + uint32_t(slot * ring.slot_bytes);
-        const uint32_t g = src[0].in_slot(mine, row), h = src[1].in_slot(mine + uint32_t(ring.array_bytes), row),
-                       d = src[2].in_slot(mine + 2u * uint32_t(ring.array_bytes), row);
-        Raw<T, VEC> rg[NV], rh[NV];
-        auto dot2 = splat<VEC>(0.0f);
+        const int left = int(p.rows - row < R ? p.rows - row : R);  // rows of this thread that exist
+        Raw<T, VEC> rg[R][NV], rh[R][NV];
+        float sum[R];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (!live || at_of(j) >= width) continue;
-            rg[j] = load_raw_shared<T, VEC>(g + uint32_t(at_of(j)) * uint32_t(sizeof(T)));
-            rh[j] = load_raw_shared<T, VEC>(h + uint32_t(at_of(j)) * uint32_t(sizeof(T)));
-            const F32<VEC> fg = widen<T, VEC>(rg[j]), fh = widen<T, VEC>(rh[j]), w = weight(j);
+        for (int r = 0; r < R; ++r) {
+            const uint32_t g = mine + uint32_t(r * ring.pitch);
+            auto dot2 = splat<VEC>(0.0f);
 #pragma unroll
-            for (int i = 0; i < F32<VEC>::PAIRS; ++i) dot2 = fma2(mul2(fg.p[i], w.p[i]), fh.p[i], dot2);
+            for (int j = 0; j < NV; ++j) {
+                if (r >= left || at_of(j) >= width) continue;
+                const uint32_t at = g + uint32_t(at_of(j)) * uint32_t(sizeof(T));
+                rg[r][j] = load_raw_shared<T, VEC>(at);
+                rh[r][j] = load_raw_shared<T, VEC>(at + off_h);
+                const F32<VEC> fg = widen<T, VEC>(rg[r][j]), fh = widen<T, VEC>(rh[r][j]), w = weight(j);
+#pragma unroll
+                for (int i = 0; i < F32<VEC>::PAIRS; ++i) dot2 = fma2(mul2(fg.p[i], w.p[i]), fh.p[i], dot2);
+            }
+            sum[r] = total(dot2);
         }
-        const float sum = row_sum<true>(total(dot2), red[flip]);
+        rows_sum<R>(sum, red[flip]);
         if (base >= first + step) refill(base + int64_t(ring.slots - 1) * step, last);  // all have left the step before
         // dx = rstd g + (-rstd mean(g u)) u + dh, with g = dy w, u = h rstd
-        const auto rs2 = splat<VEC>(rs), c2 = splat<VEC>(-rs * (sum * rs * p.inv_width));
-        T *dx = static_cast<T *>(p.dx) + row * p.lddx;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (!live || at_of(j) >= width) continue;
-            const F32<VEC> fg = widen<T, VEC>(rg[j]), fh = widen<T, VEC>(rh[j]), w = weight(j);
-            F32<VEC> o;
-            if (has_d) o = widen<T, VEC>(load_raw_shared<T, VEC>(d + uint32_t(at_of(j)) * uint32_t(sizeof(T))));
+        for (int r = 0; r < R; ++r) {
+            const auto rs2 = splat<VEC>(rs[r]), c2 = splat<VEC>(-rs[r] * (sum[r] * rs[r] * p.inv_width));
+            const uint32_t d = mine + uint32_t(r * ring.pitch) + off_d;
 #pragma unroll
-            for (int i = 0; i < F32<VEC>::PAIRS; ++i) {
-                const auto u = mul2(fh.p[i], rs2);
-                dw[j].p[i] = fma2(fg.p[i], u, dw[j].p[i]);
-                const auto wg = mul2(fg.p[i], w.p[i]);
-                o.p[i] = fma2(u, c2, has_d ? fma2(wg, rs2, o.p[i]) : mul2(wg, rs2));
+            for (int j = 0; j < NV; ++j) {
+                if (r >= left || at_of(j) >= width) continue;
+                const F32<VEC> fg = widen<T, VEC>(rg[r][j]), fh = widen<T, VEC>(rh[r][j]), w = weight(j);
+                F32<VEC> o;
+                if (has_d) o = widen<T, VEC>(load_raw_shared<T, VEC>(d + uint32_t(at_of(j)) * uint32_t(sizeof(T))));
+#pragma unroll
+                for (int i = 0; i < F32<VEC>::PAIRS; ++i) {
+                    const auto u = mul2(fh.p[i], rs2);
+                    dw[j].p[i] = fma2(fg.p[i], u, dw[j].p[i]);
+                    const auto gw = mul2(fg.p[i], w.p[i]);
+                    o.p[i] = fma2(u, c2, has_d ? fma2(gw, rs2, o.p[i]) : mul2(gw, rs2));
+                }
+                store_f32<T, VEC>(dx + r * p.lddx + at_of(j), o);
             }
-            store_f32<T, VEC>(dx + at_of(j), o);
         }
         last = slot;
         if (++slot == ring.slots) { slot = 0; phase ^= 1u; }
@@ -736,7 +778,7 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_kernel(co
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         if (at_of(j) >= width) continue;
-        store_f32<float, VEC>(out + at_of(j), dw[j]);  // VEC = 8: width is a multiple of 8, the workspace aligned
+        store_f32<float, VEC>(out + at_of(j), dw[j]);  // width is a multiple of 8, the workspace aligned
     }
 }
 
@@ -765,7 +807,7 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_any_kerne
                                  {static_cast<const T *>(p.dh), p.lddh}};
     const bool has_d = p.dh != nullptr;
     auto refill = [&](int64_t base, int slot) {
-        if (base < p.rows) fill_slot(src, has_d ? 3 : 2, ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
+        if (base < p.rows) fill_slot(src, has_d ? 3 : 2, int(blockDim.y), ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
     };
     for (int s = 0; s < ring.slots; ++s) refill(first + s * step, s);
     const uint32_t ring0 = smem_addr(rows) + uint32_t(int(threadIdx.y) * ring.pitch);
