@@ -244,6 +244,8 @@ struct LinearPlan {
     bool pair;
     int T, split, stages;   // linear_split
     int64_t whole, units;   // linear_pair: whole tiles, and units in all
+    double split_us, pair_us;
+    double split_load, pair_load;  // shares of the GPU's places that the launch takes
 };
 
 // Estimated microseconds, from what was measured on GB300. linear_split: set-up
@@ -254,7 +256,8 @@ struct LinearPlan {
 // linear_pair: set-up and end 3.9, a k-block of one round every kPairStep (more
 // where there is only one round, and hardly less for halves of tiles).
 constexpr double kLatency = 1.15, kDramBytes = 6.2e6, kL2Bytes = 11e6, kRingTime = 2.2, kSplitFixed = 3.0, kSplitCluster = 0.3,
-                 kSplitSend = 0.008, kSplitRow = 0.018, kPairFixed = 3.9, kPairStep = 0.29, kPairFirst = 0.34, kPairHalf = 0.275;
+                 kSplitSend = 0.008, kSplitRow = 0.018, kPairFixed = 3.9, kPairStep = 0.29, kPairFirst = 0.32, kPairHalf = 0.265, kKernelSwitch = 3.0, kSideBySide = 1.5,
+                 kHiddenStart = 2.0;
 constexpr double kSplitStep[kSplitTs] = {0.36, 0.42, 0.45, 0.37, 0.80};
 
 // linear_split's shape, rows per CTA T (an M-major A comes in chunks of 64 rows)
@@ -280,6 +283,7 @@ double plan_split(int64_t M, int64_t N, int64_t num_kb, bool a_mn, const OpsStat
                 best = cost;
                 pl->T = T;
                 pl->split = int(S);
+                pl->split_load = load;
             }
         }
         if (T >= M) break;
@@ -291,22 +295,23 @@ double plan_split(int64_t M, int64_t N, int64_t num_kb, bool a_mn, const OpsStat
 // linear_pair's units: whole tiles for as many full rounds of the GPU's pairs as
 // there are, then, where the tiles that remain fit into one round as halves, those
 // (4000 x 5000 x 3000: 4 rounds of 76 and 32 halves, 96.5 us; as 16 tiles 99.7).
-double plan_pair(int64_t M, int64_t N, int64_t num_kb, int max_pairs, LinearPlan *pl) {
+double plan_pair(int64_t M, int64_t N, int64_t num_kb, int max_pairs, bool halves_allowed, LinearPlan *pl) {
     const int64_t tiles = cdiv(M, pair::TILE_M) * cdiv(N, pair::TILE_N), rest = tiles % max_pairs;
-    const bool halves = rest > 0 && 2 * rest <= max_pairs;
+    const bool halves = halves_allowed && rest > 0 && 2 * rest <= max_pairs;
     pl->whole = halves ? tiles - rest : tiles;
     pl->units = pl->whole + (halves ? 2 * rest : 0);
+    pl->pair_load = double(pl->units) / max_pairs;
     const double rounds = double(cdiv(pl->whole, max_pairs));
     const double step = rounds == 1.0 ? kPairFirst : rounds * kPairStep;
     return kPairFixed + double(num_kb) * (step + (halves ? kPairHalf : 0.0));
 }
 
-LinearPlan plan_linear(int64_t M, int64_t N, int64_t num_kb, bool a_mn, uint32_t flags, const DeviceState &ds,
+LinearPlan plan_linear(int64_t M, int64_t N, int64_t num_kb, bool a_mn, bool alone, uint32_t flags, const DeviceState &ds,
                        const OpsState &o) {
     LinearPlan pl{};
-    const double split = plan_split(M, N, num_kb, a_mn, o, &pl);
-    const double pair = plan_pair(M, N, num_kb, ds.max_pairs, &pl);
-    pl.pair = (flags & GEMM_LINEAR_PAIR) || (!(flags & GEMM_LINEAR_SPLIT) && pair <= split);
+    pl.split_us = plan_split(M, N, num_kb, a_mn, o, &pl);
+    pl.pair_us = plan_pair(M, N, num_kb, ds.max_pairs, alone, &pl);
+    pl.pair = (flags & GEMM_LINEAR_PAIR) || (!(flags & GEMM_LINEAR_SPLIT) && pl.pair_us <= pl.split_us);
     return pl;
 }
 
@@ -322,9 +327,17 @@ bool quad_aligned(const void *p, int64_t ld, int es) {
     return (reinterpret_cast<uintptr_t>(p) & uintptr_t(4 * es - 1)) == 0 && ld % 4 == 0;
 }
 
+// Two products of one call that do not need each other run one into the other:
+// the second's tiles start where the first's last round leaves SMs idle
+// (griddep_enter), so neither ends in halves of tiles (gradients of 257 x 1000 x
+// 513: 26.7 us one after the other, 21.7 us so; of 4096 x 8192 x 4096 the same
+// either way, since an SM that waits leaves the others its power).
+enum class Order { kAlone, kFirst, kSecond };
+
 // The product and its epilogue on operands that TMA can describe. K >= 1.
 gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t N, int64_t K, const EpilogueParams &e,
-                         uint32_t flags, const DeviceState *ds, const OpsState *ops, cudaStream_t stream) {
+                         uint32_t flags, const DeviceState *ds, const OpsState *ops, cudaStream_t stream,
+                         Order order = Order::kAlone) {
     const bool f8 = A.type == GEMM_TYPE_E4M3;
     const int es = e.type == 0 ? 4 : 2;
     LinearParams p;
@@ -335,7 +348,8 @@ gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t 
     p.num_kb = int32_t(cdiv(K, f8 ? 128 : 64));
     p.wait.timeout_ns = g_timeout_ns.load();
     p.wait.epoch = next_epoch();
-    const LinearPlan pl = plan_linear(M, N, p.num_kb, A.mn_major, flags, *ds, *ops);
+    const LinearPlan pl = plan_linear(M, N, p.num_kb, A.mn_major, order == Order::kAlone, flags, *ds, *ops);
+    p.late = order == Order::kSecond;
     CUtensorMap tmA, tmB, tmBhalf, tmC, tmR, tmP;
     cudaError_t err;
     if (pl.pair) {
@@ -647,10 +661,14 @@ gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *
     float *ws_part = reinterpret_cast<float *>(ws + s.d);
     const bool products = K > 0 && (present(dA) || present(dB));
 
-    // ---- D and its column sums
+    // ---- operand copies; D and its column sums beside them
+    const bool pack_a = products && present(dB) && s.a > 0, pack_b = products && present(dA) && s.b > 0;
+    const bool packs = pack_a || pack_b;
+    if (packs && pack_operands(&a, pack_a ? ws_a : nullptr, &b, pack_b ? ws_b : nullptr, ds->num_sms, stream) != cudaSuccess)
+        return GEMM_ERR_CUDA;
     Operand d_rows{G->data, M, N, G->stride_row, G->type, false};
+    const GradPlan gp = plan_grad(M, N);
     if ((s.store_d && products) || dbias != nullptr) {
-        const GradPlan gp = plan_grad(M, N);
         GradParams p;
         std::memset(&p, 0, sizeof(p));
         p.g = G->data;
@@ -664,25 +682,25 @@ gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *
         p.N = N;
         p.rows_per_block = gp.rows_per_block;
         p.act = uint32_t(activation);
+        p.late = packs;
         const bool vec = N % 8 == 0 && vec16(p.g, p.ldg, 2) && (!has_pre || vec16(p.pre, p.ldp, 2));
-        cudaError_t e = G->type == GEMM_TYPE_F16 ? launch_grad<__half>(p, vec, gp.parts, stream)
-                                                 : launch_grad<__nv_bfloat16>(p, vec, gp.parts, stream);
-        if (e == cudaSuccess && dbias != nullptr && gp.parts > 1)
-            e = launch_shape(sum_partials_kernel, dim3(unsigned(cdiv(N, 32))), dim3(32, kPartGroups), 0, 1, stream,
-                             static_cast<const float *>(ws_part), dbias, gp.parts, N);
+        const cudaError_t e = G->type == GEMM_TYPE_F16 ? launch_grad<__half>(p, vec, gp.parts, stream)
+                                                       : launch_grad<__nv_bfloat16>(p, vec, gp.parts, stream);
         if (e != cudaSuccess) return GEMM_ERR_CUDA;
         if (p.d != nullptr) {
             d_rows.data = ws_d;
             d_rows.ld = s.ldd;
         }
     }
-    if (!products) {
-        return GEMM_OK;
-    }
-    const bool pack_a = present(dB) && s.a > 0, pack_b = present(dA) && s.b > 0;
-    if ((pack_a || pack_b) &&
-        pack_operands(&a, pack_a ? ws_a : nullptr, &b, pack_b ? ws_b : nullptr, ds->num_sms, stream) != cudaSuccess)
-        return GEMM_ERR_CUDA;
+    // the column sums' last step; after the products, it needs nothing of the one before it
+    auto finish_dbias = [&] {
+        if (dbias == nullptr || gp.parts == 1) return GEMM_OK;
+        return launch_shape(sum_partials_kernel, dim3(unsigned(cdiv(N, 32))), dim3(32, kPartGroups), 0, 1, stream,
+                            static_cast<const float *>(ws_part), dbias, gp.parts, N, uint32_t(products)) == cudaSuccess
+                   ? GEMM_OK
+                   : GEMM_ERR_CUDA;
+    };
+    if (!products) return finish_dbias();
     auto out = [](const gemm_matrix_t *m, bool turned) {
         EpilogueParams e;
         std::memset(&e, 0, sizeof(e));
@@ -697,18 +715,39 @@ gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *
         o.mn_major = !o.mn_major;
         return o;
     };
+    const bool two = present(dA) && present(dB);
+    if (two && flags == 0) {
+        // One kernel for both, unless two pay for the change: a kernel whose code is not on
+        // the SMs yet starts kKernelSwitch later (257 x 1000 x 512: 12.9 us with one of
+        // each, 8.6 with linear_split twice; 2048 x 2048 x 1024: 24.6, 18.3 with pairs).
+        const LinearPlan pa = plan_linear(dA_t ? K : M, dA_t ? M : K, cdiv(N, 64), dA_t ? turned(b).mn_major : d_rows.mn_major,
+                                          false, 0, *ds, *ops);
+        const LinearPlan pb = plan_linear(dB_t ? N : K, dB_t ? K : N, cdiv(M, 64), dB_t ? true : turned(a).mn_major, false, 0,
+                                          *ds, *ops);
+        // side by side where both fit the GPU at once, else the second's set-up is hidden
+        auto both = [](double a, double b, double load) {
+            return load <= 1.0 ? std::max(a, b) + kSideBySide : a + b - kHiddenStart;
+        };
+        const double pairs = both(pa.pair_us, pb.pair_us, pa.pair_load + pb.pair_load);
+        const double splits = both(pa.split_us, pb.split_us, pa.split_load + pb.split_load);
+        const double each = std::min(pa.pair_us, pa.split_us) + std::min(pb.pair_us, pb.split_us) + kKernelSwitch;
+        if (std::min(pairs, splits) <= each) flags = pairs <= splits ? GEMM_LINEAR_PAIR : GEMM_LINEAR_SPLIT;
+    }
     if (present(dA)) {  // dA = D B^T, or its transpose B D^T
         const Operand w = turned(b);
-        st = dA_t ? run_linear(w, d_rows, K, M, N, out(dA, true), flags, ds, ops, stream)
-                  : run_linear(d_rows, w, M, K, N, out(dA, false), flags, ds, ops, stream);
+        const Order order = two ? Order::kFirst : Order::kAlone;
+        st = dA_t ? run_linear(w, d_rows, K, M, N, out(dA, true), flags, ds, ops, stream, order)
+                  : run_linear(d_rows, w, M, K, N, out(dA, false), flags, ds, ops, stream, order);
         if (st != GEMM_OK) return st;
     }
     if (present(dB)) {  // dB = A^T D, or its transpose D^T A
         const Operand x = turned(a), d = turned(d_rows);
-        st = dB_t ? run_linear(d, x, N, K, M, out(dB, true), flags, ds, ops, stream)
-                  : run_linear(x, d, K, N, M, out(dB, false), flags, ds, ops, stream);
+        const Order order = two ? Order::kSecond : Order::kAlone;
+        st = dB_t ? run_linear(d, x, N, K, M, out(dB, true), flags, ds, ops, stream, order)
+                  : run_linear(x, d, K, N, M, out(dB, false), flags, ds, ops, stream, order);
+        if (st != GEMM_OK) return st;
     }
-    return st;
+    return finish_dbias();
 }
 
 }  // extern "C"
@@ -848,7 +887,7 @@ cudaError_t launch_norm_backward(NormBackwardParams p, bool vec, float *dweight,
     }
     if (e == cudaSuccess && dweight != nullptr)
         e = launch_shape(sum_partials_kernel, dim3(unsigned(cdiv(p.width, 32))), dim3(32, kPartGroups), 0, 1, stream,
-                         static_cast<const float *>(partial), dweight, parts, p.width);
+                         static_cast<const float *>(partial), dweight, parts, p.width, 0u);
     return e;
 }
 

@@ -302,6 +302,7 @@ struct LinearParams {
     int32_t stages, bufs;     // linear_pair: ring depth, staging buffers per epilogue warp
     int32_t T, tmem_cols;     // linear_split: rows of C per CTA, TMEM columns
     int32_t split;            // linear_split: CTAs of a cluster along K
+    uint32_t late;            // griddep_enter
     EpilogueParams e;
     WaitCtl wait;
 };
@@ -613,8 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
     tc_fence_after();
     // The set-up above may overlap the end of the previous kernel on the
     // stream; nothing below touches global memory before that kernel is done.
-    griddep_wait();
-    griddep_launch_dependents();
+    griddep_enter(p.late);
     const uint32_t tmem_base = *tmem_slot;
     const int32_t num_kb = p.num_kb;
 
@@ -776,6 +776,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
     }
 
     // ---------------------------------------------------------------- teardown
+    griddep_leave(p.late);
     tc_fence_before();
     cluster_sync();  // no CTA leaves while its peer may still use its smem or barriers
     if (warp == MMA_WARP) {
@@ -1000,7 +1001,7 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
             fence_proxy_async_smem();
         }
         __syncwarp();
-        griddep_wait();
+        if (!p.late) griddep_wait();
         // the first stages, both operands
         const int32_t first = min(st0 + NST, st1);
         for (int32_t st = st0; st < first; ++st) mbar_expect_tx_elect(full_bar(st - st0), lin::W_STAGE_BYTES + x_stage);
@@ -1010,7 +1011,7 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         with_load(p.a, [&](auto mode, auto mn) {
             for (int32_t st = st0; st < first; ++st) load_x(mode, mn, st, uint32_t(st - st0));
         });
-        __syncthreads();  // the others are set up
+        __syncthreads();  // the others are set up; tensor memory is allocated
         griddep_launch_dependents();
         with_load(p.b, [&](auto mode, auto mn) {
             later_stages([&](int32_t st, uint32_t stage) {
@@ -1026,8 +1027,7 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        griddep_wait();
-        griddep_launch_dependents();
+        griddep_enter(p.late);
         tmem_base = *tmem_slot;
     }
 
@@ -1104,6 +1104,7 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
             else split_rows<kF8, SPLIT, false>(p, base, rank, ew, lane, m0, n0, valid);
         });
     }
+    griddep_leave(p.late);
     if (warp == MMA_WARP) {
         tc_fence_after();
         tmem_dealloc(tmem_base, uint32_t(p.tmem_cols));
@@ -1185,7 +1186,7 @@ struct GradParams {
     float *partial;       // [gridDim.y][N] or nullptr
     int64_t M, N, ldg, ldp, ldd;
     int64_t rows_per_block;
-    uint32_t act;
+    uint32_t act, late;
 };
 constexpr int kGradGroups = 8;
 
@@ -1229,8 +1230,7 @@ __device__ __forceinline__ void grad_rows(const GradParams &p, int64_t col, int6
 template <typename T, int VEC>
 __global__ void __launch_bounds__(32 * kGradGroups) linear_grad_kernel(const GradParams p) {
     __shared__ float s[kGradGroups][32 * VEC + 1];
-    griddep_wait();
-    griddep_launch_dependents();
+    griddep_enter(p.late);
     const int64_t col = (int64_t(blockIdx.x) * 32 + threadIdx.x) * VEC;
     const int64_t r0 = int64_t(blockIdx.y) * p.rows_per_block;
     const int64_t r1 = r0 + p.rows_per_block < p.M ? r0 + p.rows_per_block : p.M;
@@ -1246,6 +1246,7 @@ __global__ void __launch_bounds__(32 * kGradGroups) linear_grad_kernel(const Gra
             default: grad_rows<kActNone, T, VEC>(p, col, r0, r1, sum); break;
         }
     }
+    griddep_leave(p.late);
     if (p.partial == nullptr) return;
 #pragma unroll
     for (int i = 0; i < F32<VEC>::PAIRS; ++i) {

@@ -14,6 +14,21 @@
 
 namespace g16 {
 
+// ------------------------------------------------------------------ launches that overlap
+// A kernel of a call that needs nothing of the kernel right before it (late != 0)
+// does not wait for it before its work but before it ends. What it does read was
+// written by kernels that had completed before that one's own wait returned, and
+// so before this one could be scheduled; and whatever follows on the stream still
+// finds both complete. In gradients the second product's tiles so fill the SMs
+// that the first one's last round leaves idle.
+__device__ __forceinline__ void griddep_enter(uint32_t late) {
+    if (!late) griddep_wait();
+    griddep_launch_dependents();
+}
+__device__ __forceinline__ void griddep_leave(uint32_t late) {
+    if (late) griddep_wait();
+}
+
 // ------------------------------------------------------------------ elements
 template <typename T>
 __device__ __forceinline__ float to_f32(T v) {
@@ -898,10 +913,9 @@ __global__ void __launch_bounds__(256) rms_norm_dweight_long_kernel(const NormBa
 constexpr int kPartGroups = 32;
 __global__ void __launch_bounds__(32 * kPartGroups) sum_partials_kernel(const float *__restrict__ partial,
                                                                         float *__restrict__ out, int64_t parts,
-                                                                        int64_t width) {
+                                                                        int64_t width, uint32_t late) {
     __shared__ float s[kPartGroups][33];
-    griddep_wait();
-    griddep_launch_dependents();
+    griddep_enter(late);
     const int64_t col = int64_t(blockIdx.x) * 32 + threadIdx.x;
     float v = 0.0f;
     if (col < width) {
@@ -909,6 +923,7 @@ __global__ void __launch_bounds__(32 * kPartGroups) sum_partials_kernel(const fl
         for (int64_t r = threadIdx.y; r < parts; r += kPartGroups) v += partial[r * width + col];
     }
     s[threadIdx.y][threadIdx.x] = v;
+    griddep_leave(late);
     __syncthreads();
     if (threadIdx.y != 0 || col >= width) return;
     for (int g = 1; g < kPartGroups; ++g) v += s[g][threadIdx.x];
