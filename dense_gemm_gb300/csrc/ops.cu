@@ -249,20 +249,24 @@ struct LinearPlan {
 };
 
 // Estimated microseconds, from what was measured on GB300. linear_split: set-up
-// and end 3.3, partial rows sent and summed at a time per row, the first loads back
-// after kLatency, a stage of two k-blocks every kSplitStep, and the weights from
-// DRAM at 6.2 bytes a picosecond, less where too few rings are in flight for it, and
-// from L2 at 11, once for every T rows.
-// linear_pair: set-up and end 3.9, a k-block of one round every kPairStep (more
-// where there is only one round, and hardly less for halves of tiles).
-constexpr double kLatency = 1.15, kDramBytes = 6.2e6, kL2Bytes = 11e6, kRingTime = 2.2, kSplitFixed = 3.0, kSplitCluster = 0.3,
-                 kSplitSend = 0.008, kSplitRow = 0.018, kPairFixed = 3.9, kPairStep = 0.29, kPairFirst = 0.32, kPairHalf = 0.265, kKernelSwitch = 3.0, kSideBySide = 1.5,
-                 kHiddenStart = 2.0;
+// and end kSplitFixed, partial rows sent and summed at a time per row, the first
+// loads back after kLatency, a stage of two k-blocks every kSplitStep, and the
+// weights from DRAM at 6.2 bytes a picosecond, or at what the rings in flight carry
+// where that is less (a ring's bytes every kRingTime), and from L2 at 11, once for
+// every T rows.
+// linear_pair: set-up and end kPairFixed, a k-block of one round every kPairStep
+// (more where there is only one round, and hardly less for halves of tiles), and
+// the weights at what the rings carry (4 x 16384 x 4096: pairs 35.4 us,
+// linear_split 25.1; 200 x 16384 x 4096: 32.4 and 40.3).
+constexpr double kLatency = 1.15, kDramBytes = 6.2e6, kL2Bytes = 11e6, kRingTime = 2.6, kSplitFixed = 3.0, kSplitCluster = 0.3,
+                 kSplitSend = 0.008, kSplitRow = 0.018, kPairFixed = 3.9, kPairStep = 0.29, kPairFirst = 0.32, kPairHalf = 0.265,
+                 kPairRingTime = 2.9, kKernelSwitch = 3.0, kSideBySide = 1.5, kHiddenStart = 2.0;
 constexpr double kSplitStep[kSplitTs] = {0.36, 0.42, 0.45, 0.37, 0.80};
 
 // linear_split's shape, rows per CTA T (an M-major A comes in chunks of 64 rows)
-// and K slices S. (4096 x 4096 weights, one token: S = 8 9.0 us, 4 9.3, 2 11.2,
-// 1 15.6; 256 tokens: T = 128, S = 2 14.5, T = 256, S = 4 16.8, pairs 21.2.)
+// and K slices S. (4096 x 4096 weights, one token: S = 8 8.4 us, 4 9.8, 2 11.6,
+// 1 15.8; 256 tokens: T = 128, S = 2 14.6, T = 256, S = 4 16.6, pairs 21.1; 64 x
+// 16384 x 4096: T = 64, S = 2 25.4, S = 4 29.9, T = 32, S = 1 28.9.)
 double plan_split(int64_t M, int64_t N, int64_t num_kb, bool a_mn, const OpsState &o, LinearPlan *pl) {
     double best = 1e300;
     for (int t = a_mn ? 2 : 0; t < kSplitTs; ++t) {
@@ -278,7 +282,7 @@ double plan_split(int64_t M, int64_t N, int64_t num_kb, bool a_mn, const OpsStat
             const double rate = std::min(kDramBytes, double(ctas) * lin::split_ring(split_stages(T), T) / kRingTime);
             const double weights = double(N) * double(num_kb) * 128.0;
             const double moved = std::max(weights / rate, double(cdiv(M, T)) * weights / kL2Bytes);
-            const double cost = std::max(rounds * (one + stream), one + moved);
+            const double cost = rounds * one + std::max(rounds * stream, moved);
             if (cost < best) {
                 best = cost;
                 pl->T = T;
@@ -303,7 +307,9 @@ double plan_pair(int64_t M, int64_t N, int64_t num_kb, int max_pairs, bool halve
     pl->pair_load = double(pl->units) / max_pairs;
     const double rounds = double(cdiv(pl->whole, max_pairs));
     const double step = rounds == 1.0 ? kPairFirst : rounds * kPairStep;
-    return kPairFixed + double(num_kb) * (step + (halves ? kPairHalf : 0.0));
+    // few rows: bound by how many bytes of weights the rings keep in flight
+    const double rate = double(std::min<int64_t>(pl->units, max_pairs)) * 2 * lin::PAIR_STAGES * pair::B_STAGE_BYTES / kPairRingTime;
+    return kPairFixed + std::max(double(num_kb) * (step + (halves ? kPairHalf : 0.0)), double(N) * double(num_kb) * 128.0 / rate);
 }
 
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t num_kb, bool a_mn, bool alone, uint32_t flags, const DeviceState &ds,

@@ -271,6 +271,29 @@ __device__ __forceinline__ void issue_copies(const CUtensorMap *map, uint32_t ds
     }
 }
 
+// Asks for the same copies' lines in L2 only. Nothing is read by it, so it may come
+// before the kernel that the launch depends on has ended: a line that is written
+// after all is written in L2. (kLoadLanes: not worth its code.)
+template <uint32_t MODE, bool kMn>
+__device__ __forceinline__ void prefetch_copies(const CUtensorMap *map, int32_t kb, int32_t be, int32_t mn) {
+    const int32_t k0 = kb * be;
+    if constexpr (MODE == kLoadOne) {
+        asm volatile(
+            "{\n\t.reg .pred pe;\n\t"
+            "elect.sync _|pe, 0xffffffff;\n\t"
+            "@pe cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n\t}" ::"l"(map),
+            "r"(kMn ? mn : k0), "r"(kMn ? k0 : mn)
+            : "memory");
+    } else if constexpr (MODE == kLoadBoxed) {
+        asm volatile(
+            "{\n\t.reg .pred pe;\n\t"
+            "elect.sync _|pe, 0xffffffff;\n\t"
+            "@pe cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n\t}" ::"l"(map),
+            "r"(0), "r"(kMn ? k0 : mn), "r"(kMn ? mn / MN_CHUNK : kb)
+            : "memory");
+    }
+}
+
 // Calls f with the mode and the major-ness as template arguments.
 template <typename F>
 __device__ __forceinline__ void with_load(const OperandLoad &o, F f) {
@@ -1001,9 +1024,14 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
             fence_proxy_async_smem();
         }
         __syncwarp();
+        const int32_t first = min(st0 + NST, st1);
+        // the first stages' weights are on their way into L2 while the kernel before ends
+        with_load(p.b, [&](auto mode, auto mn) {
+            for (int32_t st = st0; st < first; ++st)
+                prefetch_copies<decltype(mode)::value, decltype(mn)::value>(&tmW, st * lin::KPS, BKE, n0);
+        });
         if (!p.late) griddep_wait();
         // the first stages, both operands
-        const int32_t first = min(st0 + NST, st1);
         for (int32_t st = st0; st < first; ++st) mbar_expect_tx_elect(full_bar(st - st0), lin::W_STAGE_BYTES + x_stage);
         with_load(p.b, [&](auto mode, auto mn) {
             for (int32_t st = st0; st < first; ++st) load_w(mode, mn, st, uint32_t(st - st0));
