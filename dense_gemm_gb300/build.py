@@ -43,7 +43,7 @@ def nvcc() -> str:
 
 
 def command(out: str, verbose_ptxas: bool = False, debug: bool = False):
-    cmd = [nvcc(), *ARCH, "-O3", "-split-compile=0", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
            "-Xcompiler", "-Wall", "-I", INCLUDE, "-I", CSRC, "-o", out, *SOURCES]
     if verbose_ptxas:
         cmd.insert(1, "-Xptxas=-v")
