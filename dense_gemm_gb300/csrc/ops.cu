@@ -850,13 +850,24 @@ cudaError_t launch_ring(const RingPlan &r, const P &p, int dev, cudaStream_t str
     return launch_shape(Kernel, dim3(unsigned(r.grid)), dim3(unsigned(r.tpr), unsigned(r.rpb)), r.smem, 1, stream, p, r.ring);
 }
 
+// The persistent form or one block per row(s), both on 16-byte vectors. The ring
+// pays where a thread has two loads or more of a row and a block long enough to
+// work (direct / ring, bf16: 8192 x 4096 without residual 30.3 / 28.2 us, 4096 x 8192
+// 34.7 / 25.8, with a residual and 8 bits 43.1 / 40.7, 2048 x 12288 with a residual
+// 40.6 / 35.1; but 16384 x 2048 27.1 / 47.6, 2048 x 4096 9.7 / 10.0), except for two
+// 16-bit inputs and two 16-bit outputs of rows that 256 threads hold, which either
+// form moves at the memory's rate (4096 x 8192 43.3 / 45.8 us).
+bool ring_pays(const RingPlan &r, const NormParams &p, bool quant) {
+    if (!r.ok || r.nv < 2 || p.rows * p.width < int64_t(48 * 1024) * r.grid) return false;
+    return quant || p.r == nullptr || p.width > 8192;
+}
+
 template <typename T, bool kQ>
 cudaError_t launch_norm(const NormParams &p, bool vec, int dev, int num_sms, cudaStream_t stream) {
     const RingPlan r = ring_plan(p.rows, p.width, int(sizeof(T)), p.r != nullptr ? 2 : 1, vec, false, num_sms);
     if (r.ok && !vec) return launch_ring<rms_norm_rows_any_kernel<T, kQ>>(r, p, dev, stream);
-    if (r.ok && cdiv(p.rows, r.rpb) >= 6 * int64_t(r.grid)) {
+    if (ring_pays(r, p, kQ)) {
         switch (r.nv) {
-            case 1: return launch_ring<rms_norm_rows_kernel<T, 8, 1, kQ>>(r, p, dev, stream);
             case 2: return launch_ring<rms_norm_rows_kernel<T, 8, 2, kQ>>(r, p, dev, stream);
             case 3: return launch_ring<rms_norm_rows_kernel<T, 8, 3, kQ>>(r, p, dev, stream);
             default: return launch_ring<rms_norm_rows_kernel<T, 8, 4, kQ>>(r, p, dev, stream);
