@@ -496,6 +496,9 @@ struct PairEpilogue {
 
     // One unit's part of this warp: rows row0 .. row0 + 31, `groups` (4 or 2) times
     // 32 columns from col0 on. False if a wait ran out.
+    // Two 32-column turns are unrolled, not four: the code of five activations in
+    // each is fetched more slowly than it runs (1024 x 4096 x 1024: 13.9 us with
+    // four, 11.6 with two and the set-up before griddep_enter).
     template <typename Drained>
     __device__ __forceinline__ bool unit(uint32_t t_addr, int64_t row0, int64_t col0, int groups, const float (&bias)[4],
                                          const float (&sb)[4], float sa, Drained drained) {
@@ -504,16 +507,16 @@ struct PairEpilogue {
         bool ok = true;
         uint32_t v[2][32];
         tmem_ld_32x32b_x32(t_addr, v[0]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j >= groups) break;
+#pragma unroll 2
+        for (int j = 0; j < groups; ++j) {
+            const int i0 = j & 1, j0 = j - i0;
             const int c = j * 32 / CHUNK;
-            const int part = OB == 4 ? 0 : (j & 1);  // which 32 columns of a 16-bit chunk
+            const int part = OB == 4 ? 0 : i0;  // which 32 columns of a 16-bit chunk
             // C's buffer: with pre, 0 is pre's; chunks of a unit come in pairs except for
             // half a tile in 16 bits, so with prefetches the count of chunks decides
             const uint32_t b = has_p ? 1u : !two ? 0u : pref ? (used & 1u) : uint32_t(c & 1);
             tmem_ld_wait();
-            if (j + 1 < groups) tmem_ld_32x32b_x32(t_addr + (j + 1) * 32, v[(j + 1) & 1]);
+            if (j + 1 < groups) tmem_ld_32x32b_x32(t_addr + (j + 1) * 32, v[i0 ^ 1]);
             else drained();
             if (part == 0) {  // the buffers of a new chunk
                 if (pref) {
@@ -527,14 +530,14 @@ struct PairEpilogue {
             }
             float x[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[j & 1][i]);
+            for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i0][i]);
             if constexpr (kF8) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] *= sa * __shfl_sync(0xffffffffu, sb[j], i);
+                for (int i = 0; i < 32; ++i) x[i] *= sa * __shfl_sync(0xffffffffu, j0 == 0 ? sb[i0] : sb[i0 + 2], i);
             }
             if (p.e.bias != nullptr) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] += __shfl_sync(0xffffffffu, bias[j], i);
+                for (int i = 0; i < 32; ++i) x[i] += __shfl_sync(0xffffffffu, j0 == 0 ? bias[i0] : bias[i0 + 2], i);
             }
             if (has_p) put(0, part, x);
             apply_act(p.e.act, x);
@@ -635,9 +638,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
     tc_fence_before();
     cluster_sync();  // barriers initialised and TMEM allocated in both CTAs
     tc_fence_after();
-    // The set-up above may overlap the end of the previous kernel on the
-    // stream; nothing below touches global memory before that kernel is done.
-    griddep_enter(p.late);
+    // Each role waits for the previous kernel on the stream (griddep_enter) right
+    // before its first access to global memory: by then its parameters are read and
+    // its code is fetched, which took 1.4 us between the wait and the first copy.
     const uint32_t tmem_base = *tmem_slot;
     const int32_t num_kb = p.num_kb;
 
@@ -669,23 +672,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
         static_assert(pair::A_STAGE_BYTES == pair::B_STAGE_BYTES, "one stage pitch for both operands");
         constexpr uint32_t TX_HALF = 2u * (pair::A_STAGE_BYTES + pair::B_STAGE_BYTES / 2);
         int32_t u = pair_id;
+        Unit un = unit_of(p, u, rank);
+        bool entered = false;
+        auto enter = [&] {
+            if (!entered) griddep_enter(p.late);
+            entered = true;
+        };
+        auto next = [&] {
+            u += num_pairs;
+            if (u < p.num_units) un = unit_of(p, u, rank);
+        };
         if (is_a) {
             with_load(p.a, [&](auto mode, auto mn_major) {
-                for (; ok && u < p.num_units; u += num_pairs) {
-                    const uint32_t tx = u < p.whole ? pair::PAIR_TX_BYTES : TX_HALF;
-                    if (rank == 0) load_unit(unit_of(p, u, rank), &tmA, mode, mn_major, std::true_type(), tx);
-                    else load_unit(unit_of(p, u, rank), &tmA, mode, mn_major, std::false_type(), tx);
-                }
+                auto all = [&](auto announces) {
+                    enter();
+                    for (; ok && u < p.num_units; next())
+                        load_unit(un, &tmA, mode, mn_major, announces, u < p.whole ? pair::PAIR_TX_BYTES : TX_HALF);
+                };
+                if (rank == 0) all(std::true_type());
+                else all(std::false_type());
             });
         } else {
-            with_load(p.b, [&](auto mode, auto mn_major) {
-                for (; ok && u < p.whole; u += num_pairs)
-                    load_unit(unit_of(p, u, rank), &tmB, mode, mn_major, std::false_type(), 0u);
-            });
-            with_load(p.b_half, [&](auto mode, auto mn_major) {
-                for (; ok && u < p.num_units; u += num_pairs)
-                    load_unit(unit_of(p, u, rank), &tmBhalf, mode, mn_major, std::false_type(), 0u);
-            });
+            if (u < p.whole)
+                with_load(p.b, [&](auto mode, auto mn_major) {
+                    enter();
+                    for (; ok && u < p.whole; next()) load_unit(un, &tmB, mode, mn_major, std::false_type(), 0u);
+                });
+            if (u < p.num_units)
+                with_load(p.b_half, [&](auto mode, auto mn_major) {
+                    enter();
+                    for (; ok && u < p.num_units; next()) load_unit(un, &tmBhalf, mode, mn_major, std::false_type(), 0u);
+                });
         }
         if (!ok && lane == 0) {
             if (rank == 0 && is_a) {
@@ -704,6 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
         }
         __syncwarp();
     } else if (warp == MMA_WARP) {
+        griddep_enter(p.late);
         if (rank == 1) {
             // ======================================================== relay (CTA 1)
             // One release at cluster scope per tile tells CTA 0 that all of this CTA's
@@ -762,6 +780,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
         const int half = ew / 4;  // columns [128 half, 128 half + 128) of the tile
         PairEpilogue<kF8, OB> ep{p,    &tmC, &tmR, &tmP,    sE + uint32_t(ew) * uint32_t(p.bufs) * lin::BUF_BYTES,
                                  res_bar0 + 16u * ew, lane, q, half, rank, pair_id, 0, num_pairs, 0, 0};
+        griddep_enter(p.late);
         ep.begin();
         int32_t it = 0;
         for (int32_t u = pair_id; u < p.num_units; u += num_pairs, ++it) {
@@ -860,73 +879,123 @@ __device__ __forceinline__ void split_send(uint32_t t_addr, uint32_t base, uint3
     }
 }
 
-// Sums the S partial rows of each row of C that falls to warp `ew` of CTA `rank`
-// (row t belongs to CTA t mod S, and there to warp (t / S) mod 8), in rank order,
-// and runs the epilogue on them. A lane holds four columns: consecutive ones where
-// C, pre and residual take vectors of four (VEC), else 32 apart, so that a warp's
-// stores are contiguous either way.
-template <bool kF8, int S, bool VEC>
-__device__ __forceinline__ void split_rows(const LinearParams &p, uint32_t base, uint32_t rank, int ew, int lane, int32_t m0,
-                                           int32_t n0, int valid) {
-    const EpilogueParams &e = p.e;
-    int col[4];
+// What an epilogue warp of linear_split holds of its columns and of the residual of
+// its first rows: fetched while the products run, since nothing hides the latency
+// of a load at the end (200 x 4096 x 8192 with a residual: 24.4 us, so 23.2). A lane
+// holds four columns: consecutive ones where C, pre and residual take vectors of
+// four (vec), else 32 apart, so that a warp's stores are contiguous either way.
+constexpr int kSplitRows = 4;  // rows of a warp at a time
+struct SplitColumns {
     float bias[4], sb[4];
-    bool in[4];
+    float r[kSplitRows][4];
+};
+
+template <bool VEC>
+__device__ __forceinline__ int split_col(int lane, int i) {
+    return VEC ? lane * 4 + i : lane + 32 * i;
+}
+
+// The residual of row m at this lane's columns.
+template <bool VEC>
+__device__ __forceinline__ void split_residual(const LinearParams &p, int64_t m, int32_t n0, int lane, float (&r)[4]) {
+    const int64_t at = m * p.e.ldr + n0;
+    if (VEC && p.e.type != 0) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.e.r) + at + lane * 4);
+        const float2 a = unpack_16x2(w.x, p.e.type), b = unpack_16x2(w.y, p.e.type);
+        r[0] = a.x, r[1] = a.y, r[2] = b.x, r[3] = b.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = split_col<VEC>(lane, i);
+            r[i] = VEC || n0 + int64_t(c) < p.N ? load_elem(p.e.r, p.e.type, at + c) : 0.0f;
+        }
+    }
+}
+
+// Warp `ew` of CTA `rank` has rows k S + rank of the tile, k = ew, ew + 8, ...; this
+// fetches its columns' factors and the residual of the first kSplitRows of them.
+template <bool kF8, bool VEC>
+__device__ __forceinline__ void split_columns(const LinearParams &p, int S, uint32_t rank, int ew, int lane, int32_t m0,
+                                              int32_t n0, int valid, SplitColumns &h) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        col[i] = VEC ? lane * 4 + i : lane + 32 * i;
-        const int64_t n = int64_t(n0) + col[i];
-        in[i] = VEC || n < p.N;
-        bias[i] = in[i] && e.bias != nullptr ? load_elem(e.bias, e.bias_type, n) : 0.0f;
-        sb[i] = kF8 && in[i] ? e.sb[n] : 1.0f;
+        const int64_t n = int64_t(n0) + split_col<VEC>(lane, i);
+        const bool in = VEC || n < p.N;
+        h.bias[i] = in && p.e.bias != nullptr ? load_elem(p.e.bias, p.e.bias_type, n) : 0.0f;
+        h.sb[i] = kF8 && in ? p.e.sb[n] : 1.0f;
     }
+    if (p.e.r == nullptr) return;
+#pragma unroll
+    for (int u = 0; u < kSplitRows; ++u) {
+        const int t = (ew + u * EPI_WARPS) * S + int(rank);
+        if (t < valid) split_residual<VEC>(p, int64_t(m0) + t, n0, lane, h.r[u]);
+    }
+}
+
+// Sums the S partial rows of this warp's rows of C, in rank order, and runs the
+// epilogue on them, R rows at a time.
+template <bool kF8, int S, bool VEC, int R>
+__device__ __forceinline__ void split_rows(const LinearParams &p, uint32_t base, uint32_t rank, int ew, int lane, int32_t m0,
+                                           int32_t n0, int valid, SplitColumns &h) {
+    const EpilogueParams &e = p.e;
 #pragma unroll 1
-    for (int k = ew; k * S + int(rank) < valid; k += EPI_WARPS) {
-        const uint32_t row = base + uint32_t(k * S * lin::SPLIT_ROWS) * 4u;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = ew; k * S + int(rank) < valid; k += R * EPI_WARPS) {
+        float x[4 * R], sa[R];
+        auto tile_row = [&](int u) { return (k + u * EPI_WARPS) * S + int(rank); };
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            const uint32_t at = row + uint32_t(s * lin::SPLIT_ROWS) * 4u;
-            uint32_t w[4];
-            if constexpr (VEC) {
-                ld_shared_v4(at + uint32_t(lane) * 16u, w[0], w[1], w[2], w[3]);
-            } else {
+        for (int u = 0; u < R; ++u) sa[u] = kF8 && tile_row(u) < valid ? e.sa[int64_t(m0) + tile_row(u)] : 1.0f;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = ld_shared_b32(at + uint32_t(col[i]) * 4u);
+        for (int u = 0; u < R; ++u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[4 * u + i] = 0.0f;
+            if (R > 1 && tile_row(u) >= valid) continue;
+            const uint32_t row = base + uint32_t((k + u * EPI_WARPS) * S * lin::SPLIT_ROWS) * 4u;
+#pragma unroll
+            for (int s = 0; s < S; ++s) {
+                const uint32_t at = row + uint32_t(s * lin::SPLIT_ROWS) * 4u;
+                uint32_t w[4];
+                if constexpr (VEC) {
+                    ld_shared_v4(at + uint32_t(lane) * 16u, w[0], w[1], w[2], w[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = ld_shared_b32(at + uint32_t(split_col<VEC>(lane, i)) * 4u);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[4 * u + i] += __uint_as_float(w[i]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] += __uint_as_float(w[i]);
+            for (int i = 0; i < 4; ++i) x[4 * u + i] = (kF8 ? x[4 * u + i] * (sa[u] * h.sb[i]) : x[4 * u + i]) + h.bias[i];
         }
-        const int64_t m = int64_t(m0) + k * S + int(rank);
-        const float sa = kF8 ? e.sa[m] : 1.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = (kF8 ? x[i] * (sa * sb[i]) : x[i]) + bias[i];
         auto put = [&](void *dst, int64_t ld) {
-            const int64_t at = m * ld + n0 + col[0];
-            if constexpr (VEC) {
-                if (e.type == 0)
-                    *reinterpret_cast<float4 *>(static_cast<float *>(dst) + at) = make_float4(x[0], x[1], x[2], x[3]);
-                else
-                    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst) + at) =
-                        make_uint2(pack_16x2(x[0], x[1], e.type), pack_16x2(x[2], x[3], e.type));
-            } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (in[i] && G16_CHECK(m < p.M)) store_elem(dst, e.type, at + 32 * i, x[i]);
+            for (int u = 0; u < R; ++u) {
+                if (R > 1 && tile_row(u) >= valid) continue;
+                const float *v = x + 4 * u;
+                const int64_t at = (int64_t(m0) + tile_row(u)) * ld + n0 + split_col<VEC>(lane, 0);
+                if constexpr (VEC) {
+                    if (e.type == 0)
+                        *reinterpret_cast<float4 *>(static_cast<float *>(dst) + at) = make_float4(v[0], v[1], v[2], v[3]);
+                    else
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(dst) + at) =
+                            make_uint2(pack_16x2(v[0], v[1], e.type), pack_16x2(v[2], v[3], e.type));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n0 + int64_t(split_col<VEC>(lane, i)) < p.N && G16_CHECK(m0 + tile_row(u) < p.M))
+                            store_elem(dst, e.type, at + 32 * i, v[i]);
+                }
             }
         };
         if (e.pre != nullptr) put(e.pre, e.ldp);
         apply_act(e.act, x);
         if (e.r != nullptr) {
-            const int64_t at = m * e.ldr + n0 + col[0];
-            if (VEC && e.type != 0) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(e.r) + at);
-                const float2 a = unpack_16x2(w.x, e.type), b = unpack_16x2(w.y, e.type);
-                x[0] += a.x, x[1] += a.y, x[2] += b.x, x[3] += b.y;
-            } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (in[i]) x[i] += load_elem(e.r, e.type, at + (VEC ? i : 32 * i));
+            for (int u = 0; u < R; ++u) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[4 * u + i] += h.r[u][i];
+                // for the next rows, while these are stored
+                const int t = tile_row(u) + R * EPI_WARPS * S;
+                if (t < valid) split_residual<VEC>(p, int64_t(m0) + t, n0, lane, h.r[u]);
             }
         }
         put(e.c, e.ldc);
@@ -982,6 +1051,9 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
 
     bool ready = false;  // epilogue warps: the accumulator is complete
     uint32_t tmem_base = 0;
+    const int ew = warp - EPI_WARP0;
+    const bool vec = p.e.vec4 && n0 + lin::SPLIT_ROWS <= p.N;
+    SplitColumns columns = {};
 
     const uint32_t w_piece = p.b.mn ? lin::KPS * MN_CHUNK_BYTES : lin::SPLIT_ROWS * 128;  // between an operand's copies
     const uint32_t x_piece = p.a.mn ? lin::KPS * MN_CHUNK_BYTES : uint32_t(T) * 128u;
@@ -1097,6 +1169,8 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         mma_commit_elect(done_bar);
         __all_sync(0xffffffffu, mbar_wait_slow(done_bar, 0, cleanup_wait(p.wait), false));
     } else if (warp >= EPI_WARP0) {
+        if (vec) split_columns<kF8, true>(p, S, rank, ew, lane, m0, n0, valid, columns);
+        else split_columns<kF8, false>(p, S, rank, ew, lane, m0, n0, valid, columns);
         ready = __all_sync(0xffffffffu, mbar_wait(done_bar, 0, p.wait));
         tc_fence_after();
     }
@@ -1108,7 +1182,6 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     // finds all it has to add in its own shared memory. (Reading the others' rows
     // instead, after one barrier, left each row waiting for the cluster's latency:
     // 1000 x 640 x 256 9.7 us.)
-    const int ew = warp - EPI_WARP0;
     __syncwarp();
     if (S > 1) cluster_sync();
     else __syncthreads();
@@ -1125,11 +1198,12 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     if (S > 1) cluster_sync();
     else __syncthreads();
     if (ready) {
-        const bool vec = p.e.vec4 && n0 + lin::SPLIT_ROWS <= p.N;
+        const bool one = valid <= EPI_WARPS * S;  // a row for each warp at most
         with_split(S, [&](auto s) {
             constexpr int SPLIT = decltype(s)::value;
-            if (vec) split_rows<kF8, SPLIT, true>(p, base, rank, ew, lane, m0, n0, valid);
-            else split_rows<kF8, SPLIT, false>(p, base, rank, ew, lane, m0, n0, valid);
+            if (vec && one) split_rows<kF8, SPLIT, true, 1>(p, base, rank, ew, lane, m0, n0, valid, columns);
+            else if (vec) split_rows<kF8, SPLIT, true, kSplitRows>(p, base, rank, ew, lane, m0, n0, valid, columns);
+            else split_rows<kF8, SPLIT, false, kSplitRows>(p, base, rank, ew, lane, m0, n0, valid, columns);
         });
     }
     griddep_leave(p.late);
