@@ -602,6 +602,13 @@ cudaError_t launch_grad(const GradParams &p, bool vec, int64_t parts, cudaStream
                : launch_shape(linear_grad_kernel<T, 1>, grid, block, 0, 1, stream, p);
 }
 
+// Rows of a second 16-bit (or, `es` = 1, 8-bit) matrix that start at the same place in
+// a granule of 8 elements as the first's, row by row.
+bool same_places(const void *a, int64_t lda, const void *b, int64_t ldb, int es, int64_t rows) {
+    return ((reinterpret_cast<uintptr_t>(a) / 2 - reinterpret_cast<uintptr_t>(b) / uintptr_t(es)) & 7u) == 0 &&
+           (rows == 1 || (lda - ldb) % 8 == 0);
+}
+
 bool vec16(const void *p, int64_t ld, int es) { return aligned16(p) && (ld * es) % 16 == 0; }
 
 }  // namespace
@@ -799,10 +806,12 @@ struct RingPlan {
 // `sums`: the backward pass, which adds up dweight over the block's rows: in
 // shared memory behind the ring (any alignment), or, with vectors, in registers
 // and at the end in the ring's place.
-RingPlan ring_plan(int64_t rows, int64_t width, int es, int arrays, bool vec, bool sums, int num_sms) {
+// `shift`: vectors of rows off 16-byte boundaries, which have up to 7 foreign
+// elements in front.
+RingPlan ring_plan(int64_t rows, int64_t width, int es, int arrays, bool vec, bool shift, bool sums, int num_sms) {
     RingPlan r{};
-    const int threads = width <= 8192 ? 256 : 512;
-    const int64_t loads = cdiv(width, 8);
+    const int threads = width + (shift ? 7 : 0) <= 8192 ? 256 : 512;
+    const int64_t loads = cdiv(width + (shift ? 7 : 0), 8);
     r.nv = int(cdiv(loads, threads));
     if (r.nv > 4) return r;  // ok stays false
     r.tpr = int(cdiv(cdiv(loads, r.nv), 32) * 32);
@@ -811,10 +820,12 @@ RingPlan ring_plan(int64_t rows, int64_t width, int es, int arrays, bool vec, bo
     r.ring.pitch = int((width * es + 15) / 16 * 16 + 16);
     // two rows at a time in the backward pass, where the registers and a slot's copies
     // (one lane each) allow it (8192 x 4096: 58.7 us with one, 54.4 with two)
-    r.rpt = sums && vec && r.nv <= 2 && arrays * r.rpb * 2 <= 32 ? 2 : 1;
+    const int blocks_per_sm = threads == 256 ? 2 : 1, most = blocks_per_sm * num_sms;
+    // shifted: a thread's rows are 8 k apart, or it has one row only
+    const bool one_row = shift && cdiv(rows, r.rpb) <= most;
+    r.rpt = sums && vec && r.nv <= 2 && arrays * r.rpb * 2 <= 32 && !one_row ? 2 : 1;
     r.ring.array_bytes = r.rpb * r.rpt * r.ring.pitch;
     r.ring.slot_bytes = arrays * r.ring.array_bytes;
-    const int blocks_per_sm = threads == 256 ? 2 : 1;
     const int behind = sums && !vec ? int(r.rpb * width * 4) : 0;
     const int budget = (blocks_per_sm == 2 ? 113 : 226) * 1024 - 2048 - behind;
     r.ring.slots = std::min(kRingSlots, budget / r.ring.slot_bytes);
@@ -826,8 +837,12 @@ RingPlan ring_plan(int64_t rows, int64_t width, int es, int arrays, bool vec, bo
     }
     if (r.ring.slots < 2) return r;
     r.smem = r.ring.slots * r.ring.slot_bytes + behind;
-    if (sums && vec && r.rpb > 1) r.smem = std::max(r.smem, r.rpb * r.tpr * 8 * std::max(r.nv, 2) * 4);
-    r.grid = int(std::min<int64_t>(cdiv(rows, r.rpb * r.rpt), int64_t(blocks_per_sm) * num_sms));
+    if (sums && vec && (r.rpb > 1 || shift)) r.smem = std::max(r.smem, r.rpb * r.tpr * 8 * std::max(r.nv, 2) * 4);
+    r.grid = int(std::min<int64_t>(cdiv(rows, r.rpb * r.rpt), most));
+    if (shift && !one_row) {
+        if (most < 8) return r;
+        r.grid = int(std::min<int64_t>(cdiv(r.grid, 8) * 8, most / 8 * 8));
+    }
     r.ok = true;
     return r;
 }
@@ -863,8 +878,17 @@ bool ring_pays(const RingPlan &r, const NormParams &p, bool quant) {
 }
 
 template <typename T, bool kQ>
-cudaError_t launch_norm(const NormParams &p, bool vec, int dev, int num_sms, cudaStream_t stream) {
-    const RingPlan r = ring_plan(p.rows, p.width, int(sizeof(T)), p.r != nullptr ? 2 : 1, vec, false, num_sms);
+cudaError_t launch_norm(const NormParams &p, bool vec, bool shift, int dev, int num_sms, cudaStream_t stream) {
+    if constexpr (sizeof(T) == 2) {
+        const RowShape s = row_shape(p.width + 7);
+        if (shift && s.fits) {
+            auto *k = s.nv == 1   ? rms_norm_kernel<T, 8, 1, kQ, true>
+                      : s.nv == 2 ? rms_norm_kernel<T, 8, 2, kQ, true>
+                                  : rms_norm_kernel<T, 8, 4, kQ, true>;
+            return launch_shape(k, dim3(unsigned(cdiv(p.rows, s.rpb))), dim3(unsigned(s.tpr), unsigned(s.rpb)), 0, 1, stream, p);
+        }
+    }
+    const RingPlan r = ring_plan(p.rows, p.width, int(sizeof(T)), p.r != nullptr ? 2 : 1, vec, false, false, num_sms);
     if (r.ok && !vec) return launch_ring<rms_norm_rows_any_kernel<T, kQ>>(r, p, dev, stream);
     if (ring_pays(r, p, kQ)) {
         switch (r.nv) {
@@ -876,24 +900,40 @@ cudaError_t launch_norm(const NormParams &p, bool vec, int dev, int num_sms, cud
     const RowShape s = row_shape(p.width);
     if (!vec || !s.fits)
         return launch_shape(rms_norm_long_kernel<T>, dim3(unsigned(p.rows)), dim3(1024), 0, 1, stream, p, int32_t(kQ));
-    auto *k = s.nv == 1 ? rms_norm_kernel<T, 8, 1, kQ> : s.nv == 2 ? rms_norm_kernel<T, 8, 2, kQ> : rms_norm_kernel<T, 8, 4, kQ>;
+    auto *k = s.nv == 1   ? rms_norm_kernel<T, 8, 1, kQ, false>
+              : s.nv == 2 ? rms_norm_kernel<T, 8, 2, kQ, false>
+                          : rms_norm_kernel<T, 8, 4, kQ, false>;
     return launch_shape(k, dim3(unsigned(cdiv(p.rows, s.rpb))), dim3(unsigned(s.tpr), unsigned(s.rpb)), 0, 1, stream, p);
 }
 
+template <typename T, bool kShift>
+cudaError_t launch_norm_backward_rows(const RingPlan &r, const NormBackwardParams &p, int dev, cudaStream_t stream) {
+    if (r.nv == 1 && r.rpt == 2) return launch_ring<rms_norm_backward_rows_kernel<T, 1, 2, kShift>>(r, p, dev, stream);
+    if (r.nv == 2 && r.rpt == 2) return launch_ring<rms_norm_backward_rows_kernel<T, 2, 2, kShift>>(r, p, dev, stream);
+    if (r.nv <= 2) return launch_ring<rms_norm_backward_rows_kernel<T, 2, 1, kShift>>(r, p, dev, stream);
+    if (r.nv == 3) return launch_ring<rms_norm_backward_rows_kernel<T, 3, 1, kShift>>(r, p, dev, stream);
+    return launch_ring<rms_norm_backward_rows_kernel<T, 4, 1, kShift>>(r, p, dev, stream);
+}
+
 template <typename T>
-cudaError_t launch_norm_backward(NormBackwardParams p, bool vec, float *dweight, float *partial, int dev, int num_sms,
+cudaError_t launch_norm_backward(NormBackwardParams p, bool vec, bool shift, float *dweight, float *partial, int dev, int num_sms,
                                  cudaStream_t stream) {
     p.partial = dweight != nullptr ? partial : nullptr;
     int64_t parts;
     cudaError_t e;
-    const RingPlan r = ring_plan(p.rows, p.width, int(sizeof(T)), p.dh != nullptr ? 3 : 2, vec, true, num_sms);
+    const int arrays = p.dh != nullptr ? 3 : 2;
+    RingPlan r{};
+    if constexpr (sizeof(T) == 2) {
+        if (shift) r = ring_plan(p.rows, p.width, int(sizeof(T)), arrays, true, true, true, num_sms);
+    }
+    shift = r.ok;
+    if (!r.ok) r = ring_plan(p.rows, p.width, int(sizeof(T)), arrays, vec, false, true, num_sms);
     if (r.ok) {
         parts = r.grid;
-        if (!vec) e = launch_ring<rms_norm_backward_rows_any_kernel<T>>(r, p, dev, stream);
-        else if (r.nv == 1 && r.rpt == 2) e = launch_ring<rms_norm_backward_rows_kernel<T, 1, 2>>(r, p, dev, stream);
-        else if (r.nv == 2 && r.rpt == 2) e = launch_ring<rms_norm_backward_rows_kernel<T, 2, 2>>(r, p, dev, stream);
-        else if (r.nv <= 2) e = launch_ring<rms_norm_backward_rows_kernel<T, 2, 1>>(r, p, dev, stream);
-        else e = launch_ring<rms_norm_backward_rows_kernel<T, 4, 1>>(r, p, dev, stream);
+        if (vec) e = launch_norm_backward_rows<T, false>(r, p, dev, stream);
+        else if (!shift) e = launch_ring<rms_norm_backward_rows_any_kernel<T>>(r, p, dev, stream);
+        else if constexpr (sizeof(T) == 2) e = launch_norm_backward_rows<T, true>(r, p, dev, stream);
+        else e = cudaErrorInvalidValue;  // shift is for 16-bit types
     } else {
         e = launch_shape(rms_norm_backward_long_kernel<T>, dim3(unsigned(p.rows)), dim3(1024), 0, 1, stream, p);
         const int64_t rows_per_block = cdiv(p.rows, kNormParts);
@@ -961,8 +1001,12 @@ gemm_status_t gemm_rms_norm(const gemm_matrix_t *x, const gemm_matrix_t *residua
     if (p.r != nullptr) vec = vec && vec16(p.r, p.ldr, es);
     if (p.h != nullptr) vec = vec && vec16(p.h, p.ldh, es);
     vec = vec && (quant ? (reinterpret_cast<uintptr_t>(p.y) & 7u) == 0 && p.ldy % 8 == 0 : vec16(p.y, p.ldy, es));
+    bool shift = !vec && es == 2 && weight_type == x->type && aligned16(weight) &&
+                 same_places(p.x, p.ldx, p.y, p.ldy, quant ? 1 : 2, rows);
+    if (p.r != nullptr) shift = shift && same_places(p.x, p.ldx, p.r, p.ldr, 2, rows);
+    if (p.h != nullptr) shift = shift && same_places(p.x, p.ldx, p.h, p.ldh, 2, rows);
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    auto launch = [&](auto *k) { return k(p, vec, dev, ds->num_sms, stream); };
+    auto launch = [&](auto *k) { return k(p, vec, shift, dev, ds->num_sms, stream); };
     const cudaError_t e =
         x->type == GEMM_TYPE_F32   ? launch(quant ? launch_norm<float, true> : launch_norm<float, false>)
         : x->type == GEMM_TYPE_F16 ? launch(quant ? launch_norm<__half, true> : launch_norm<__half, false>)
@@ -1031,10 +1075,13 @@ gemm_status_t gemm_rms_norm_backward(const gemm_matrix_t *grad, const gemm_matri
     bool vec = width % 8 == 0 && aligned16(weight) && vec16(p.g, p.ldg, es) && vec16(p.h, p.ldh, es) &&
                vec16(p.dx, p.lddx, es);
     if (p.dh != nullptr) vec = vec && vec16(p.dh, p.lddh, es);
+    bool shift = !vec && es == 2 && weight_type == grad->type && aligned16(weight) &&
+                 same_places(p.g, p.ldg, p.h, p.ldh, 2, rows) && same_places(p.g, p.ldg, p.dx, p.lddx, 2, rows);
+    if (p.dh != nullptr) shift = shift && same_places(p.g, p.ldg, p.dh, p.lddh, 2, rows);
     float *part = static_cast<float *>(workspace);
-    const cudaError_t e = grad->type == GEMM_TYPE_F32   ? launch_norm_backward<float>(p, vec, dweight, part, dev, ds->num_sms, stream)
-                          : grad->type == GEMM_TYPE_F16 ? launch_norm_backward<__half>(p, vec, dweight, part, dev, ds->num_sms, stream)
-                                                        : launch_norm_backward<__nv_bfloat16>(p, vec, dweight, part, dev, ds->num_sms, stream);
+    const cudaError_t e = grad->type == GEMM_TYPE_F32   ? launch_norm_backward<float>(p, vec, shift, dweight, part, dev, ds->num_sms, stream)
+                          : grad->type == GEMM_TYPE_F16 ? launch_norm_backward<__half>(p, vec, shift, dweight, part, dev, ds->num_sms, stream)
+                                                        : launch_norm_backward<__nv_bfloat16>(p, vec, shift, dweight, part, dev, ds->num_sms, stream);
     return e == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 

@@ -208,6 +208,76 @@ __device__ __forceinline__ void store_e4m3(uint8_t *p, const F32<VEC> &v) {
     }
 }
 
+// ------------------------------------------------------------------ rows off 16-byte boundaries
+// 16-bit rows whose arrays all start at the same place in a granule of 8 elements
+// (a contiguous matrix of odd width: every row at another place) are worked on in
+// whole granules all the same: `o` elements of the row's first granule are not its
+// own, so group i holds the columns 8 i - o ... and the first and last groups are
+// cut. A granule with one byte of an allocation lies in its pages, so reading the
+// rest of it is safe; its foreign elements are cleared, and never written.
+// Element by element, the same rows take 2 to 4 times as long (4096 x 4095 forward
+// 65.4 us, so 20.9; backward 66.1 and 36.2).
+template <typename T>
+__device__ __forceinline__ int place_in_granule(const T *p) {
+    return int(reinterpret_cast<uintptr_t>(p) / sizeof(T)) & 7;
+}
+
+// Clears the elements outside [lo, hi).
+template <typename T>
+__device__ __forceinline__ void keep_elems(Raw<T, 8> &r, int lo, int hi) {
+    static_assert(sizeof(T) == 2, "eight 16-bit elements");
+    uint32_t *w = reinterpret_cast<uint32_t *>(&r.q[0]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] &= (2 * i >= lo && 2 * i < hi ? 0x0000ffffu : 0u) | (2 * i + 1 >= lo && 2 * i + 1 < hi ? 0xffff0000u : 0u);
+}
+
+// Elements at .. at + 7 of w[0 .. width) (16-byte aligned; -8 < at < width), zero
+// outside: two granules shifted into one.
+template <typename T>
+__device__ __forceinline__ Raw<T, 8> load_shifted(const T *w, int at, int width) {
+    const int a = at & ~7, s = at & 7;
+    Raw<T, 8> lo, hi, r;
+    lo.q[0] = hi.q[0] = make_uint4(0u, 0u, 0u, 0u);
+    if (a >= 0) lo = load_raw<T, 8>(w + a);
+    if (s != 0 && a + 8 < width) hi = load_raw<T, 8>(w + a + 8);
+    const uint32_t x[8] = {lo.q[0].x, lo.q[0].y, lo.q[0].z, lo.q[0].w, hi.q[0].x, hi.q[0].y, hi.q[0].z, hi.q[0].w};
+    uint32_t y[6], z[5], o[4];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) y[i] = (s & 4) ? x[i + 2] : x[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) z[i] = (s & 2) ? y[i + 1] : y[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = (s & 1) ? __funnelshift_r(z[i], z[i + 1], 16) : z[i];
+    r.q[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    if (at + 8 > width) keep_elems<T>(r, 0, width - at);
+    return r;
+}
+
+__device__ __forceinline__ void store_elems(float *p, const F32<8> &v, int lo, int hi) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i >= lo && i < hi) p[i] = i & 1 ? v.p[i / 2].y : v.p[i / 2].x;
+}
+
+// v's elements [lo, hi) -> p[lo .. hi): a vector where they are all of them.
+template <typename T>
+__device__ __forceinline__ void store_some(T *p, const F32<8> &v, int lo, int hi) {
+    if (lo <= 0 && hi >= 8) {
+        if constexpr (sizeof(T) == 1) store_e4m3<8>(reinterpret_cast<uint8_t *>(p), v);
+        else store_f32<T, 8>(p, v);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (i < lo || i >= hi) continue;
+        F32<1> e;
+        e.p[0] = i & 1 ? v.p[i / 2].y : v.p[i / 2].x;
+        if constexpr (sizeof(T) == 1) store_e4m3<1>(reinterpret_cast<uint8_t *>(p) + i, e);
+        else store_f32<T, 1>(p + i, e);
+    }
+}
+
 // ------------------------------------------------------------------ row reductions
 // A block holds blockDim.y rows of blockDim.x threads each (blockDim.x a
 // multiple of 32: a warp never spans two rows). `red`: 32 words, one use between
@@ -327,7 +397,8 @@ struct NormParams {
 
 // One row per blockDim.x threads, held in registers: element (j * blockDim.x +
 // t) * VEC + i of the row is value i of load j of thread t.
-template <typename T, int VEC, int NV, bool kQ>
+// kShift: rows off 16-byte boundaries, their first element `o` into a granule.
+template <typename T, int VEC, int NV, bool kQ, bool kShift>
 __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
     __shared__ float red[32];
     __shared__ uint32_t redq[32];
@@ -336,7 +407,8 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
     griddep_wait();
     griddep_launch_dependents();
     const int width = int(p.width);
-    auto at_of = [&](int j) { return (j * int(blockDim.x) + int(threadIdx.x)) * VEC; };
+    const int o = kShift && live ? place_in_granule(static_cast<const T *>(p.x) + row * p.ldx) : 0;
+    auto at_of = [&](int j) { return (j * int(blockDim.x) + int(threadIdx.x)) * VEC - o; };
     F32<VEC> t[NV];
     {
         Raw<T, VEC> a[NV], b[NV];
@@ -351,6 +423,12 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             if (!live || at_of(j) >= width) continue;
+            if constexpr (kShift) {
+                if (at_of(j) < 0 || at_of(j) + VEC > width) {
+                    keep_elems<T>(a[j], -at_of(j), width - at_of(j));
+                    if (p.r != nullptr) keep_elems<T>(b[j], -at_of(j), width - at_of(j));
+                }
+            }
             t[j] = widen<T, VEC>(a[j]);
             if (p.r == nullptr) continue;
             const F32<VEC> f = widen<T, VEC>(b[j]);
@@ -363,8 +441,14 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         if (!live || at_of(j) >= width) continue;
-        if (p.h != nullptr) store_f32<T, VEC>(static_cast<T *>(p.h) + row * p.ldh + at_of(j), t[j]);
-        square_and_weigh<VEC, kQ>(t[j], load_weight<T, VEC>(p.w, p.w_f32 != 0, at_of(j)), ss2, tmax);
+        if constexpr (kShift) {
+            if (p.h != nullptr)
+                store_some<T>(static_cast<T *>(p.h) + row * p.ldh + at_of(j), t[j], -at_of(j), width - at_of(j));
+            square_and_weigh<VEC, kQ>(t[j], widen<T, VEC>(load_shifted<T>(static_cast<const T *>(p.w), at_of(j), width)), ss2, tmax);
+        } else {
+            if (p.h != nullptr) store_f32<T, VEC>(static_cast<T *>(p.h) + row * p.ldh + at_of(j), t[j]);
+            square_and_weigh<VEC, kQ>(t[j], load_weight<T, VEC>(p.w, p.w_f32 != 0, at_of(j)), ss2, tmax);
+        }
     }
     float ss = total(ss2);
     if constexpr (kQ) row_sum_max(ss, tmax, red, redq);
@@ -383,7 +467,10 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
         if (at_of(j) >= width) continue;
 #pragma unroll
         for (int i = 0; i < F32<VEC>::PAIRS; ++i) t[j].p[i] = mul2(t[j].p[i], splat<VEC>(mul));
-        if constexpr (kQ) store_e4m3<VEC>(static_cast<uint8_t *>(p.y) + row * p.ldy + at_of(j), t[j]);
+        if constexpr (kShift)
+            store_some<std::conditional_t<kQ, uint8_t, T>>(static_cast<std::conditional_t<kQ, uint8_t, T> *>(p.y) + row * p.ldy + at_of(j),
+                                                           t[j], -at_of(j), width - at_of(j));
+        else if constexpr (kQ) store_e4m3<VEC>(static_cast<uint8_t *>(p.y) + row * p.ldy + at_of(j), t[j]);
         else store_f32<T, VEC>(static_cast<T *>(p.y) + row * p.ldy + at_of(j), t[j]);
     }
 }
@@ -459,19 +546,21 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// Warp 0 of the block starts the copies of rows base .. base + nrows - 1 of every
-// array into a slot; one lane per copy.
-template <typename T>
+// Warp 0 of the block starts the copies of a slot's rows of every array, one lane
+// per copy: rows base .. base + nrows - 1 or, where R rows of a thread are `apart`
+// rows from each other, row q of the slot is base + q / R + (q mod R) apart.
+template <typename T, int R = 1>
 __device__ __forceinline__ void fill_slot(const RowSource<T> *src, int arrays, int nrows, const RingShape &ring, uint8_t *slots,
-                                          int slot, uint32_t bar, int64_t base, int64_t rows, int64_t width) {
+                                          int slot, uint32_t bar, int64_t base, int64_t rows, int64_t width, int64_t apart = 1) {
     if (threadIdx.y != 0 || threadIdx.x >= 32) return;
     const int lane = threadIdx.x;
     const int a = lane / nrows, y = lane - a * nrows;
+    const int64_t row = apart == 1 ? base + y : base + y / R + (y % R) * apart;
     uint32_t bytes = 0, dst = 0;
     const void *from = nullptr;
-    if (a < arrays && base + y < rows) {
+    if (a < arrays && row < rows) {
         const RowSource<T> s = a == 0 ? src[0] : a == 1 ? src[1] : src[2];
-        const uintptr_t at = reinterpret_cast<uintptr_t>(s.data + (base + y) * s.ld);
+        const uintptr_t at = reinterpret_cast<uintptr_t>(s.data + row * s.ld);
         from = reinterpret_cast<const void *>(at & ~uintptr_t(15));
         bytes = (uint32_t(at & 15u) + uint32_t(width) * uint32_t(sizeof(T)) + 15u) & ~15u;
         dst = smem_addr(slots) + uint32_t(slot * ring.slot_bytes + a * ring.array_bytes + y * ring.pitch);
@@ -671,7 +760,10 @@ struct NormBackwardParams {
 // refilled after the next step's barrier. The chain of a row's reduction is long
 // beside its arithmetic, so a thread works on R rows at a time (row base +
 // threadIdx.y * R + r), with one barrier for all of them.
-template <typename T, int NV, int R>
+// kShift: rows off 16-byte boundaries. A thread's rows are then a multiple of 8
+// rows apart (its block's next ones, the grid being a multiple of 8), so that all of
+// them start at the same place in a granule and a thread keeps its columns.
+template <typename T, int NV, int R, bool kShift>
 __global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_kernel(const NormBackwardParams p, const RingShape ring) {
     constexpr int VEC = 8;
     __shared__ float red[2][R][32];
@@ -687,48 +779,55 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_kernel(co
     griddep_launch_dependents();
     const int per_slot = int(blockDim.y) * R;
     const int64_t step = int64_t(gridDim.x) * per_slot;
-    const int64_t first = int64_t(blockIdx.x) * per_slot;
+    const int64_t first = int64_t(blockIdx.x) * (kShift ? int(blockDim.y) : per_slot);
+    const int64_t apart = kShift && R > 1 ? int64_t(gridDim.x) * blockDim.y : 1;  // rows between a thread's R rows
     const RowSource<T> src[3] = {{static_cast<const T *>(p.g), p.ldg}, {static_cast<const T *>(p.h), p.ldh},
                                  {static_cast<const T *>(p.dh), p.lddh}};
     const bool has_d = p.dh != nullptr;
     auto refill = [&](int64_t base, int slot) {
         if (base < p.rows)
-            fill_slot(src, has_d ? 3 : 2, per_slot, ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
+            fill_slot<T, R>(src, has_d ? 3 : 2, per_slot, ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width, apart);
     };
     for (int s = 0; s < ring.slots; ++s) refill(first + s * step, s);
-    auto at_of = [&](int j) { return (j * int(blockDim.x) + int(threadIdx.x)) * VEC; };
+    int64_t row = first + int64_t(threadIdx.y) * (kShift ? 1 : R);
+    const int o = kShift && row < p.rows ? place_in_granule(static_cast<const T *>(p.g) + row * p.ldg) : 0;
+    auto at_of = [&](int j) { return (j * int(blockDim.x) + int(threadIdx.x)) * VEC - o; };
     const int width = int(p.width);
+    auto cut = [&](int j) { return kShift && (at_of(j) < 0 || at_of(j) + VEC > width); };
     F32<VEC> dw[NV];
     Raw<T, VEC> w16[NV];  // a weight of T's type; fp32 weights are read again for each row
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
         for (int i = 0; i < F32<VEC>::PAIRS; ++i) dw[j].p[i] = splat<VEC>(0.0f);
-        if (at_of(j) < width && !p.w_f32) w16[j] = load_raw<T, VEC>(static_cast<const T *>(p.w) + at_of(j));
+        if (at_of(j) >= width || p.w_f32) continue;
+        if constexpr (kShift) w16[j] = load_shifted<T>(static_cast<const T *>(p.w), at_of(j), width);
+        else w16[j] = load_raw<T, VEC>(static_cast<const T *>(p.w) + at_of(j));
     }
-    auto weight = [&](int j) { return p.w_f32 ? load_weight<T, VEC>(p.w, true, at_of(j)) : widen<T, VEC>(w16[j]); };
+    auto weight = [&](int j) { return !kShift && p.w_f32 ? load_weight<T, VEC>(p.w, true, at_of(j)) : widen<T, VEC>(w16[j]); };
     const uint32_t ring0 = smem_addr(rows) + uint32_t(int(threadIdx.y) * R * ring.pitch);
     const uint32_t off_h = uint32_t(ring.array_bytes), off_d = 2u * off_h;
     int slot = 0, last = ring.slots - 1;  // `last`: the slot before it in the ring
     uint32_t phase = 0;
     int flip = 0;
     bool ok = true;
-    int64_t row = first + int64_t(threadIdx.y) * R;
     T *dx = static_cast<T *>(p.dx) + row * p.lddx;
     const int64_t dx_step = step * p.lddx;
     float rs_next[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) rs_next[r] = row + r < p.rows ? p.rstd[row + r] : 0.0f;
+    for (int r = 0; r < R; ++r) rs_next[r] = row + r * apart < p.rows ? p.rstd[row + r * apart] : 0.0f;
     for (int64_t base = first; base < p.rows; base += step, row += step, dx += dx_step, flip ^= 1) {
         float rs[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             rs[r] = rs_next[r];
-            rs_next[r] = row + step + r < p.rows ? p.rstd[row + step + r] : 0.0f;
+            rs_next[r] = row + step + r * apart < p.rows ? p.rstd[row + step + r * apart] : 0.0f;
         }
         ok = mbar_wait(smem_addr(&full[slot]), phase, p.wait) && ok;
         const uint32_t mine = ring0 + uint32_t(slot * ring.slot_bytes);
-        const int left = int(p.rows - row < R ? p.rows - row : R);  // rows of this thread that exist
+        int left = 0;  // rows of this thread that exist
+#pragma unroll
+        for (int r = 0; r < R; ++r) left += row + r * apart < p.rows;
         Raw<T, VEC> rg[R][NV], rh[R][NV];
         float sum[R];
 #pragma unroll
@@ -738,9 +837,15 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_kernel(co
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 if (r >= left || at_of(j) >= width) continue;
-                const uint32_t at = g + uint32_t(at_of(j)) * uint32_t(sizeof(T));
+                const uint32_t at = g + uint32_t(at_of(j) + o) * uint32_t(sizeof(T));
                 rg[r][j] = load_raw_shared<T, VEC>(at);
                 rh[r][j] = load_raw_shared<T, VEC>(at + off_h);
+                if constexpr (kShift) {
+                    if (cut(j)) {
+                        keep_elems<T>(rg[r][j], -at_of(j), width - at_of(j));
+                        keep_elems<T>(rh[r][j], -at_of(j), width - at_of(j));
+                    }
+                }
                 const F32<VEC> fg = widen<T, VEC>(rg[r][j]), fh = widen<T, VEC>(rh[r][j]), w = weight(j);
 #pragma unroll
                 for (int i = 0; i < F32<VEC>::PAIRS; ++i) dot2 = fma2(mul2(fg.p[i], w.p[i]), fh.p[i], dot2);
@@ -758,16 +863,18 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_kernel(co
             for (int j = 0; j < NV; ++j) {
                 if (r >= left || at_of(j) >= width) continue;
                 const F32<VEC> fg = widen<T, VEC>(rg[r][j]), fh = widen<T, VEC>(rh[r][j]), w = weight(j);
-                F32<VEC> o;
-                if (has_d) o = widen<T, VEC>(load_raw_shared<T, VEC>(d + uint32_t(at_of(j)) * uint32_t(sizeof(T))));
+                F32<VEC> v;
+                if (has_d) v = widen<T, VEC>(load_raw_shared<T, VEC>(d + uint32_t(at_of(j) + o) * uint32_t(sizeof(T))));
 #pragma unroll
                 for (int i = 0; i < F32<VEC>::PAIRS; ++i) {
                     const auto u = mul2(fh.p[i], rs2);
                     dw[j].p[i] = fma2(fg.p[i], u, dw[j].p[i]);
                     const auto gw = mul2(fg.p[i], w.p[i]);
-                    o.p[i] = fma2(u, c2, has_d ? fma2(gw, rs2, o.p[i]) : mul2(gw, rs2));
+                    v.p[i] = fma2(u, c2, has_d ? fma2(gw, rs2, v.p[i]) : mul2(gw, rs2));
                 }
-                store_f32<T, VEC>(dx + r * p.lddx + at_of(j), o);
+                T *to = dx + r * apart * p.lddx + at_of(j);
+                if constexpr (kShift) store_some<T>(to, v, -at_of(j), width - at_of(j));
+                else store_f32<T, VEC>(to, v);
             }
         }
         last = slot;
@@ -776,12 +883,17 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_kernel(co
     if (!ok) let_copies_land();
     if (p.partial == nullptr) return;
     float *out = p.partial + int64_t(blockIdx.x) * p.width;
-    if (blockDim.y > 1) {  // the block's rows first, in order (the ring holds no copy in flight any more)
+    if (kShift || blockDim.y > 1) {
+        // through shared memory (the ring holds no copy in flight any more): the block's
+        // rows added up in order, and stores that are contiguous over a warp
         float *dw_rows = reinterpret_cast<float *>(rows);
         const int span = blockDim.x * VEC * NV;
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < NV; ++j) store_f32<float, VEC>(dw_rows + int(threadIdx.y) * span + at_of(j), dw[j]);
+        for (int j = 0; j < NV; ++j) {
+            if constexpr (kShift) store_elems(dw_rows + int(threadIdx.y) * span + at_of(j), dw[j], -at_of(j), width - at_of(j));
+            else store_f32<float, VEC>(dw_rows + int(threadIdx.y) * span + at_of(j), dw[j]);
+        }
         __syncthreads();
         for (int c = tid; c < span && c < width; c += blockDim.x * blockDim.y) {
             float s = dw_rows[c];
@@ -790,10 +902,12 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_kernel(co
         }
         return;
     }
+    if constexpr (!kShift) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        if (at_of(j) >= width) continue;
-        store_f32<float, VEC>(out + at_of(j), dw[j]);  // width is a multiple of 8, the workspace aligned
+        for (int j = 0; j < NV; ++j) {
+            if (at_of(j) >= width) continue;
+            store_f32<float, VEC>(out + at_of(j), dw[j]);  // width is a multiple of 8, the workspace aligned
+        }
     }
 }
 
