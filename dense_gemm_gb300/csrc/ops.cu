@@ -298,7 +298,8 @@ double plan_split(int64_t M, int64_t N, int64_t num_kb, bool a_mn, const OpsStat
 
 // linear_pair's units: whole tiles for as many full rounds of the GPU's pairs as
 // there are, then, where the tiles that remain fit into one round as halves, those
-// (4000 x 5000 x 3000: 4 rounds of 76 and 32 halves, 96.5 us; as 16 tiles 99.7).
+// (512 x 4096 x 4096: 64 halves 19.6 us, 32 tiles 23.0; 4000 x 5000 x 3000: 4 rounds
+// of 76 and 32 halves 95.6 us, with 16 tiles 96.5).
 double plan_pair(int64_t M, int64_t N, int64_t num_kb, int max_pairs, bool halves_allowed, LinearPlan *pl) {
     const int64_t tiles = cdiv(M, pair::TILE_M) * cdiv(N, pair::TILE_N), rest = tiles % max_pairs;
     const bool halves = halves_allowed && rest > 0 && 2 * rest <= max_pairs;
@@ -335,9 +336,12 @@ bool quad_aligned(const void *p, int64_t ld, int es) {
 
 // Two products of one call that do not need each other run one into the other:
 // the second's tiles start where the first's last round leaves SMs idle
-// (griddep_enter), so neither ends in halves of tiles (gradients of 257 x 1000 x
-// 513: 26.7 us one after the other, 21.7 us so; of 4096 x 8192 x 4096 the same
-// either way, since an SM that waits leaves the others its power).
+// (griddep_enter), so neither ends in halves of tiles. Not for many rounds of
+// tiles, where little of that is left to gain and the power limit sets the pace
+// (gradients, one into the other / one after the other: 257 x 1000 x 520 15.3 /
+// 17.7 us, 2048 x 2048 x 1024 25.1 / 32.6, 4000 x 5000 x 3000, 5.7 rounds, 192 / 207,
+// 4096 x 4096 x 4096, 6.7 rounds, 163 / 166, 8192 x 4096 x 4096, 10.1 rounds, 340 / 329).
+constexpr double kOverlapRounds = 8.0;
 enum class Order { kAlone, kFirst, kSecond };
 
 // The product and its epilogue on operands that TMA can describe. K >= 1.
@@ -527,9 +531,9 @@ gemm_status_t gemm_linear(const gemm_matrix_t *A, const gemm_matrix_t *B, const 
 // ------------------------------------------------------------------ linear, backward
 namespace {
 
-// Column sums of D: each block sums a strip of 256 columns (32 where rows are not on
-// 16-byte boundaries) over rows_per_block rows, 64 where that gives the GPU enough
-// blocks, fewer down to 8 (one per row group) where it does not.
+// Column sums of D: each block sums a strip of 256 columns over rows_per_block
+// rows, 64 where that gives the GPU enough blocks, fewer down to 8 (one per row
+// group) where it does not.
 struct GradPlan {
     int64_t rows_per_block, parts;
 };
@@ -596,10 +600,9 @@ cudaError_t zero_matrix(const gemm_matrix_t *m, bool turned, int64_t rows, int64
 
 template <typename T>
 cudaError_t launch_grad(const GradParams &p, bool vec, int64_t parts, cudaStream_t stream) {
-    const int64_t strip = vec ? 256 : 32;
-    const dim3 grid(unsigned(cdiv(p.N, strip)), unsigned(parts)), block(32, kGradGroups);
-    return vec ? launch_shape(linear_grad_kernel<T, 8>, grid, block, 0, 1, stream, p)
-               : launch_shape(linear_grad_kernel<T, 1>, grid, block, 0, 1, stream, p);
+    const dim3 grid(unsigned(cdiv(p.N, 256)), unsigned(parts)), block(32, kGradGroups);
+    return vec ? launch_shape(linear_grad_kernel<T, false>, grid, block, 0, 1, stream, p)
+               : launch_shape(linear_grad_kernel<T, true>, grid, block, 0, 1, stream, p);
 }
 
 // Rows of a second 16-bit (or, `es` = 1, 8-bit) matrix that start at the same place in
@@ -729,14 +732,16 @@ gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *
         return o;
     };
     const bool two = present(dA) && present(dB);
-    if (two && flags == 0) {
+    bool overlap = false;
+    if (two) {
         // One kernel for both, unless two pay for the change: a kernel whose code is not on
-        // the SMs yet starts kKernelSwitch later (257 x 1000 x 512: 12.9 us with one of
-        // each, 8.6 with linear_split twice; 2048 x 2048 x 1024: 24.6, 18.3 with pairs).
+        // the SMs yet starts kKernelSwitch later (257 x 1000 x 512: 15.4 us with one of
+        // each, 12.2 with one kernel; 2048 x 2048 x 1024: 30.4 and 26.4).
         const LinearPlan pa = plan_linear(dA_t ? K : M, dA_t ? M : K, cdiv(N, 64), dA_t ? turned(b).mn_major : d_rows.mn_major,
                                           false, 0, *ds, *ops);
         const LinearPlan pb = plan_linear(dB_t ? N : K, dB_t ? K : N, cdiv(M, 64), dB_t ? true : turned(a).mn_major, false, 0,
                                           *ds, *ops);
+        overlap = pa.pair_load + pb.pair_load <= kOverlapRounds;
         // side by side where both fit the GPU at once, else the second's set-up is hidden
         auto both = [](double a, double b, double load) {
             return load <= 1.0 ? std::max(a, b) + kSideBySide : a + b - kHiddenStart;
@@ -744,18 +749,18 @@ gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *
         const double pairs = both(pa.pair_us, pb.pair_us, pa.pair_load + pb.pair_load);
         const double splits = both(pa.split_us, pb.split_us, pa.split_load + pb.split_load);
         const double each = std::min(pa.pair_us, pa.split_us) + std::min(pb.pair_us, pb.split_us) + kKernelSwitch;
-        if (std::min(pairs, splits) <= each) flags = pairs <= splits ? GEMM_LINEAR_PAIR : GEMM_LINEAR_SPLIT;
+        if (flags == 0 && std::min(pairs, splits) <= each) flags = pairs <= splits ? GEMM_LINEAR_PAIR : GEMM_LINEAR_SPLIT;
     }
     if (present(dA)) {  // dA = D B^T, or its transpose B D^T
         const Operand w = turned(b);
-        const Order order = two ? Order::kFirst : Order::kAlone;
+        const Order order = overlap ? Order::kFirst : Order::kAlone;
         st = dA_t ? run_linear(w, d_rows, K, M, N, out(dA, true), flags, ds, ops, stream, order)
                   : run_linear(d_rows, w, M, K, N, out(dA, false), flags, ds, ops, stream, order);
         if (st != GEMM_OK) return st;
     }
     if (present(dB)) {  // dB = A^T D, or its transpose D^T A
         const Operand x = turned(a), d = turned(d_rows);
-        const Order order = two ? Order::kSecond : Order::kAlone;
+        const Order order = overlap ? Order::kSecond : Order::kAlone;
         st = dB_t ? run_linear(d, x, N, K, M, out(dB, true), flags, ds, ops, stream, order)
                   : run_linear(x, d, K, N, M, out(dB, false), flags, ds, ops, stream, order);
         if (st != GEMM_OK) return st;

@@ -52,7 +52,7 @@ __device__ __forceinline__ void mma_f8_pair_elect(uint32_t d_tmem, uint64_t a_de
 // x >= 0, 1 - Z(x) (b1 t + ... + b5 t^5) with t = 1 / (1 + 0.2316419 x) and Z the
 // density, off by less than 7.5e-8; the density is what gelu's slope needs too.
 // D = G gelu'(P) of 4096 x 8192 takes 82 us with CUDA's erff and __expf, 57 with the
-// formula value by value, 41 in pairs with four rows loaded ahead.
+// formula value by value, 36.5 in pairs with four rows loaded ahead.
 constexpr uint32_t kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4;  // GEMM_ACT_*
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kTwoSqrt2OverPi = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -574,6 +574,14 @@ struct PairEpilogue {
     }
 };
 
+// Bound by the tensor cores, over many rounds of tiles by the clock the power limit
+// leaves: 8192 x 16384 x 4096 bf16 with gelu and pre 596 us (1.85 PFLOP/s) a call in
+// short runs, 617 to 690 in long ones; 4096 x 8192 x 8192 e4m3 145 us (3.78 PFLOP/s).
+// Where tiles fill few rounds, by what a tile costs around its k-blocks (4000 x 5000
+// x 3000, 4.2 rounds: 95 us, tensor pipe 61 % active) and, with halves, by the copies'
+// issue (0.23 us a k-block and CTA for 0.12 us of products). Two staging buffers per
+// warp instead of one only where the residual or pre needs them: the sixth stage is
+// worth more (8192 x 8192 x 4096: 315 us with one buffer, 340 with two and 5 stages).
 template <bool kF8, int OB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1)
     linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -1015,6 +1023,10 @@ __device__ __forceinline__ void with_split(int S, F f) {
 
 // Cluster of p.split CTAs (1..8) along x, all on the same tile; CTA r sums the
 // pairs of k-blocks r n / split ... (r + 1) n / split of n.
+// Bound by the weights' stream from DRAM where N K is large (4 x 16384 x 4096: 134
+// MB in 23.3 us, 5.8 TB/s), else by the chain first copy - products - cluster barrier
+// - partial rows - sum, 5 us of which hold no stream (one token 4096 x 4096: 33.6 MB
+// in 7.9 us; 48 x 4096 x 8192: 68 MB in 14.4 us).
 template <bool kF8>
 __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     linear_split(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const LinearParams p) {
@@ -1214,7 +1226,8 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
 }
 
 // ================================================================== K = 0
-// The sum is empty: C = act(bias) + R.
+// The sum is empty: C = act(bias) + R, element by element (4096 x 8192 fp16: 101 us,
+// bound by the indices' divisions; a case of the definition, not of any model).
 __global__ void linear_empty_kernel(const LinearParams p) {
     griddep_wait();
     griddep_launch_dependents();
@@ -1233,7 +1246,9 @@ __global__ void linear_empty_kernel(const LinearParams p) {
 // Rows of `inner` bytes, any base and pitch -> rows on 128-byte lines (dst 128-byte
 // aligned, ld_dst a multiple of 128), zero past `inner`. One 16-byte granule of
 // the copy per thread and step, from the one or two aligned source granules that
-// hold its bytes (a granule is read only when it holds a byte of the row).
+// hold its bytes (a granule is read only when it holds a byte of the row). Bound by
+// latency and DRAM (4096 x 8191 and 128 x 8191: 69 MB moved in about 13 us of the 23.3 of
+// a product with them; without copies, at K = 8192, it takes 9.8).
 struct PackBytesJob {
     const uint8_t *src;
     uint8_t *dst;
@@ -1281,7 +1296,11 @@ __global__ void pack_bytes_kernel(PackBytesJob a, PackBytesJob b) {
 // ================================================================== backward, elementwise part
 // D = G act'(P) and the column sums of D over blocks of rows. A block is 32
 // lanes x 8 row groups on a strip of 256 columns (8 per lane); the sums use D
-// before its rounding.
+// before its rounding. 4096 x 8192 bf16 with gelu: 201 MB in 36.5 us (5.5 TB/s),
+// bound by DRAM and, half of the cycles, by the slope's arithmetic; without activation
+// (the sums alone, 67 MB) 16.3 us. Rows off 16-byte boundaries are put together from
+// the two granules that hold eight elements (kShift): 4096 x 8191 49.7 us, element
+// by element 76.2.
 struct GradParams {
     const void *g, *pre;  // pre == nullptr: D = G
     void *d;              // nullptr: not stored
@@ -1292,76 +1311,98 @@ struct GradParams {
 };
 constexpr int kGradGroups = 8;
 
-template <uint32_t ACT>
-__device__ __forceinline__ float2 slope_of(float2 x) { return act_slope<ACT>(x); }
-template <uint32_t ACT>
-__device__ __forceinline__ float slope_of(float x) { return act_slope<ACT>(pair_of(x)).x; }
+// Eight elements of a row from `at` on as they come: the one or, kShift, two
+// granules that hold them.
+template <typename T, bool kShift>
+struct GradLoad {
+    Raw<T, 8> lo, hi;
+    __device__ __forceinline__ void fetch(const T *row, int64_t at, int64_t n) {
+        if constexpr (kShift) {
+            const int s = place_in_granule(row + at);
+            lo = load_raw<T, 8>(row + at - s);
+            hi.q[0] = make_uint4(0u, 0u, 0u, 0u);
+            if (s != 0 && at + 8 - s < n) hi = load_raw<T, 8>(row + at - s + 8);  // only where the row reaches into it
+        } else {
+            lo = load_raw<T, 8>(row + at);
+        }
+    }
+    // the values, zero from column n on
+    __device__ __forceinline__ F32<8> values(const T *row, int64_t at, int64_t n) const {
+        if constexpr (kShift) {
+            Raw<T, 8> r = shift_granules<T>(lo, hi, place_in_granule(row + at));
+            if (at + 8 > n) keep_elems<T>(r, 0, int(n - at));
+            return widen<T, 8>(r);
+        } else {
+            return widen<T, 8>(lo);
+        }
+    }
+};
 
-template <uint32_t ACT, typename T, int VEC>
-__device__ __forceinline__ void grad_rows(const GradParams &p, int64_t col, int64_t r0, int64_t r1, F32<VEC> &sum) {
+template <uint32_t ACT, typename T, bool kShift>
+__device__ __forceinline__ void grad_rows(const GradParams &p, int64_t col, int64_t r0, int64_t r1, F32<8> &sum) {
     const T *g = static_cast<const T *>(p.g), *pre = static_cast<const T *>(p.pre);
     T *d = static_cast<T *>(p.d);
-    constexpr int AHEAD = 4;  // rows loaded before the first is stored
+    constexpr int AHEAD = kShift ? 2 : 4;  // rows loaded before the first is stored
 #pragma unroll 1
     for (int64_t r = r0 + threadIdx.y; r < r1; r += AHEAD * kGradGroups) {
-        Raw<T, VEC> a[AHEAD], b[AHEAD];
+        GradLoad<T, kShift> a[AHEAD], b[AHEAD];
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
             const int64_t row = r + k * kGradGroups;
             if (row >= r1) break;
-            a[k] = load_raw<T, VEC>(g + row * p.ldg + col);
-            if constexpr (ACT != kActNone) b[k] = load_raw<T, VEC>(pre + row * p.ldp + col);
+            a[k].fetch(g + row * p.ldg, col, p.N);
+            if constexpr (ACT != kActNone) b[k].fetch(pre + row * p.ldp, col, p.N);
         }
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
             const int64_t row = r + k * kGradGroups;
             if (row >= r1) break;
-            F32<VEC> x = widen<T, VEC>(a[k]);
+            F32<8> x = a[k].values(g + row * p.ldg, col, p.N);
             if constexpr (ACT != kActNone) {
-                const F32<VEC> f = widen<T, VEC>(b[k]);
+                const F32<8> f = b[k].values(pre + row * p.ldp, col, p.N);
 #pragma unroll
-                for (int i = 0; i < F32<VEC>::PAIRS; ++i) x.p[i] = mul2(x.p[i], slope_of<ACT>(f.p[i]));
+                for (int i = 0; i < F32<8>::PAIRS; ++i) x.p[i] = mul2(x.p[i], act_slope<ACT>(f.p[i]));
             }
-            if (d != nullptr) store_f32<T, VEC>(d + row * p.ldd + col, x);
+            if (d != nullptr) {
+                if constexpr (kShift) store_some<T>(d + row * p.ldd + col, x, 0, int(p.N - col < 8 ? p.N - col : 8));
+                else store_f32<T, 8>(d + row * p.ldd + col, x);
+            }
 #pragma unroll
-            for (int i = 0; i < F32<VEC>::PAIRS; ++i) sum.p[i] = add2(sum.p[i], x.p[i]);
+            for (int i = 0; i < F32<8>::PAIRS; ++i) sum.p[i] = add2(sum.p[i], x.p[i]);
         }
     }
 }
 
-template <typename T, int VEC>
+// kShift: G's or pre's rows off 16-byte boundaries, or N no multiple of 8.
+template <typename T, bool kShift>
 __global__ void __launch_bounds__(32 * kGradGroups) linear_grad_kernel(const GradParams p) {
-    __shared__ float s[kGradGroups][32 * VEC + 1];
+    __shared__ float s[kGradGroups][32 * 8 + 1];
     griddep_enter(p.late);
-    const int64_t col = (int64_t(blockIdx.x) * 32 + threadIdx.x) * VEC;
+    const int64_t col = (int64_t(blockIdx.x) * 32 + threadIdx.x) * 8;
     const int64_t r0 = int64_t(blockIdx.y) * p.rows_per_block;
     const int64_t r1 = r0 + p.rows_per_block < p.M ? r0 + p.rows_per_block : p.M;
-    F32<VEC> sum;
+    F32<8> sum;
 #pragma unroll
-    for (int i = 0; i < F32<VEC>::PAIRS; ++i) sum.p[i] = splat<VEC>(0.0f);
+    for (int i = 0; i < F32<8>::PAIRS; ++i) sum.p[i] = splat<8>(0.0f);
     if (col < p.N) {
         switch (p.act) {
-            case kActRelu: grad_rows<kActRelu, T, VEC>(p, col, r0, r1, sum); break;
-            case kActGelu: grad_rows<kActGelu, T, VEC>(p, col, r0, r1, sum); break;
-            case kActGeluTanh: grad_rows<kActGeluTanh, T, VEC>(p, col, r0, r1, sum); break;
-            case kActSilu: grad_rows<kActSilu, T, VEC>(p, col, r0, r1, sum); break;
-            default: grad_rows<kActNone, T, VEC>(p, col, r0, r1, sum); break;
+            case kActRelu: grad_rows<kActRelu, T, kShift>(p, col, r0, r1, sum); break;
+            case kActGelu: grad_rows<kActGelu, T, kShift>(p, col, r0, r1, sum); break;
+            case kActGeluTanh: grad_rows<kActGeluTanh, T, kShift>(p, col, r0, r1, sum); break;
+            case kActSilu: grad_rows<kActSilu, T, kShift>(p, col, r0, r1, sum); break;
+            default: grad_rows<kActNone, T, kShift>(p, col, r0, r1, sum); break;
         }
     }
     griddep_leave(p.late);
     if (p.partial == nullptr) return;
 #pragma unroll
-    for (int i = 0; i < F32<VEC>::PAIRS; ++i) {
-        if constexpr (VEC == 8) {
-            s[threadIdx.y][threadIdx.x * VEC + 2 * i] = sum.p[i].x;
-            s[threadIdx.y][threadIdx.x * VEC + 2 * i + 1] = sum.p[i].y;
-        } else {
-            s[threadIdx.y][threadIdx.x] = sum.p[0];
-        }
+    for (int i = 0; i < F32<8>::PAIRS; ++i) {
+        s[threadIdx.y][threadIdx.x * 8 + 2 * i] = sum.p[i].x;
+        s[threadIdx.y][threadIdx.x * 8 + 2 * i + 1] = sum.p[i].y;
     }
     __syncthreads();
-    for (int c = threadIdx.y * 32 + threadIdx.x; c < 32 * VEC; c += 32 * kGradGroups) {
-        const int64_t at = int64_t(blockIdx.x) * 32 * VEC + c;
+    for (int c = threadIdx.y * 32 + threadIdx.x; c < 32 * 8; c += 32 * kGradGroups) {
+        const int64_t at = int64_t(blockIdx.x) * 32 * 8 + c;
         if (at >= p.N) continue;
         float v = s[0][c];
         for (int y = 1; y < kGradGroups; ++y) v += s[y][c];

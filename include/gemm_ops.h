@@ -93,6 +93,8 @@ typedef struct {
  * short prompts; few output tiles) tiles of 128 columns by 16..256 rows with K
  * split over a cluster of up to 8 CTAs, whose partial sums are added in rank
  * order through distributed shared memory. Every result is deterministic.
+ * The second kernel may ask for lines of B in L2 before the kernels before it on
+ * the stream have ended; it uses no data of theirs before they have.
  */
 gemm_status_t gemm_linear(const gemm_matrix_t *A, const gemm_matrix_t *B, const gemm_matrix_t *C,
                           const gemm_epilogue_t *epilogue, int64_t M, int64_t N, int64_t K, uint32_t flags,
@@ -119,7 +121,8 @@ gemm_status_t gemm_linear_workspace_size(const gemm_matrix_t *A, const gemm_matr
  * workspace: 128-byte aligned, gemm_linear_backward_workspace_size() bytes; it
  * holds D, copies of unaligned operands and partial column sums. Sizes and
  * layouts as gemm_linear. M == 0 or K == 0, N == 0: the gradients that exist
- * are zero-filled.
+ * are zero-filled. The call's kernels may run at the same time where one needs
+ * nothing of the other; what follows on the stream finds all of them complete.
  */
 gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *A, const gemm_matrix_t *B,
                                    const gemm_matrix_t *pre, int32_t activation, const gemm_matrix_t *dA,
