@@ -578,10 +578,11 @@ struct PairEpilogue {
 // leaves: 8192 x 16384 x 4096 bf16 with gelu and pre 596 us (1.85 PFLOP/s) a call in
 // short runs, 617 to 690 in long ones; 4096 x 8192 x 8192 e4m3 145 us (3.78 PFLOP/s).
 // Where tiles fill few rounds, by what a tile costs around its k-blocks (4000 x 5000
-// x 3000, 4.2 rounds: 95 us, tensor pipe 61 % active) and, with halves, by the copies'
-// issue (0.23 us a k-block and CTA for 0.12 us of products). Two staging buffers per
-// warp instead of one only where the residual or pre needs them: the sixth stage is
-// worth more (8192 x 8192 x 4096: 315 us with one buffer, 340 with two and 5 stages).
+// x 3000, 4.2 rounds: 95 us, tensor pipe 61 % active) and, with halves, by what L2
+// delivers (512 x 4096 x 4096: 0.22 us a k-block, 14 TB/s, for 0.12 us of products; 8
+// stages instead of 6 change nothing). Two staging buffers per warp instead of one
+// only where the residual or pre needs them: the sixth stage is worth more (8192 x
+// 8192 x 4096: 315 us with one buffer, 340 with two and 5 stages).
 template <bool kF8, int OB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1)
     linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
