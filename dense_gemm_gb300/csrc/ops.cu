@@ -344,6 +344,12 @@ bool quad_aligned(const void *p, int64_t ld, int es) {
 constexpr double kOverlapRounds = 8.0;
 enum class Order { kAlone, kFirst, kSecond };
 
+// linear_pair's residual and C share one staging buffer per warp, which leaves the
+// ring a sixth stage, where a tile's products take long enough to hide that (one
+// buffer / two: 4096 x 8192 x 8192 e4m3 152 / 162 us, 8192 x 8192 x 4096 bf16 317 / 325,
+// 2048 157 / 162, 1024 98.8 / 96.6; 8192 x 8192 x 2048 e4m3 111 / 108).
+constexpr int kOneBufferKb = 32;
+
 // The product and its epilogue on operands that TMA can describe. K >= 1.
 gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t N, int64_t K, const EpilogueParams &e,
                          uint32_t flags, const DeviceState *ds, const OpsState *ops, cudaStream_t stream,
@@ -387,7 +393,7 @@ gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t 
         p.whole = int32_t(pl.whole);
         p.idesc = linear_idesc(A.type, A.mn_major, B.mn_major, 2 * pair::CTA_M, pair::TILE_N);
         p.idesc_half = linear_idesc(A.type, A.mn_major, B.mn_major, 2 * pair::CTA_M, pair::TILE_N / 2);
-        p.bufs = e.r != nullptr || e.pre != nullptr ? 2 : 1;
+        p.bufs = e.pre != nullptr || (e.r != nullptr && p.num_kb < kOneBufferKb) ? 2 : 1;
         p.stages = p.bufs == 2 ? 5 : 6;
         const dim3 grid(unsigned(2 * std::min<int64_t>(p.num_units, ds->max_pairs)));
         auto *kernel = f8 ? (es == 4 ? linear_pair<true, 4> : linear_pair<true, 2>)
@@ -517,8 +523,11 @@ gemm_status_t gemm_linear(const gemm_matrix_t *A, const gemm_matrix_t *B, const 
         p.M = M;
         p.N = N;
         p.e = e;
-        const int blocks = int(std::min<int64_t>(cdiv(M * N, 256), 8 * int64_t(ds->num_sms)));
-        return launch_overlapped(linear_empty_kernel, blocks, 256, 0, stream, p) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+        const int64_t strips = std::min<int64_t>(cdiv(N, 256), 1 << 20);
+        const int64_t rows = std::min<int64_t>(M, std::max<int64_t>(1, 16 * int64_t(ds->num_sms) / strips));
+        return launch_shape(linear_empty_kernel, dim3(unsigned(strips), unsigned(rows)), dim3(256), 0, 1, stream, p) == cudaSuccess
+                   ? GEMM_OK
+                   : GEMM_ERR_CUDA;
     }
     unsigned char *ws = static_cast<unsigned char *>(workspace);
     if (na + nb > 0 && pack_operands(&a, na ? ws : nullptr, &b, nb ? ws + na : nullptr, ds->num_sms, stream) != cudaSuccess)

@@ -377,15 +377,22 @@ struct PairEpilogue {
     uint32_t fetched, used;        // residual chunks asked for and taken
 
     __device__ __forceinline__ uint32_t buf(uint32_t b) const { return stg + b * lin::BUF_BYTES; }
-    __device__ __forceinline__ bool prefetches() const { return p.e.r != nullptr && p.e.r_tma && p.e.pre == nullptr; }
+    __device__ __forceinline__ bool prefetches() const { return p.e.r != nullptr && p.e.r_tma; }
+
+    // The buffer of the n-th residual chunk, where C's will be (with pre that is the
+    // second one), and the phase of its barrier. (Plain loads next to pre, instead:
+    // 8192 x 8192 x 128 499 us, so 102.)
+    __device__ __forceinline__ bool in_turns() const { return p.bufs == 2 && p.e.pre == nullptr; }
+    __device__ __forceinline__ uint32_t residual_buf(uint32_t n) const { return p.e.pre != nullptr ? 1u : in_turns() ? n & 1u : 0u; }
+    __device__ __forceinline__ uint32_t residual_phase(uint32_t n) const { return (in_turns() ? n >> 1 : n) & 1u; }
 
     // Start fetching the residual's 32 rows x CHUNK columns of the next chunk that
-    // has not been asked for into its buffer (whole warp; two buffers).
+    // has not been asked for into its buffer (whole warp).
     __device__ __forceinline__ void fetch_residual() {
         if (next_u >= p.num_units) return;
         const Unit u = unit_of(p, next_u, rank);
         if (lane == 0) {
-            const uint32_t b = fetched & 1u;
+            const uint32_t b = residual_buf(fetched);
             mbar_arrive_expect_tx(rbar + 8u * b, lin::BUF_BYTES);
             tma_load_2d(buf(b), tmR, int32_t(u.col0) + half * (u.cols / 2) + next_c * CHUNK, int32_t(u.row0) + q * 32, rbar + 8u * b);
         }
@@ -401,7 +408,7 @@ struct PairEpilogue {
         const int64_t rows = p.M - row0;
         constexpr int PER_LANE = CHUNK / 32;
         const int64_t col = col0 + PER_LANE * lane;
-#pragma unroll 8
+#pragma unroll 16
         for (int r = 0; r < 32; ++r) {
             uint32_t w = 0;
             if (r < rows && col < p.N) {
@@ -514,13 +521,13 @@ struct PairEpilogue {
             const int part = OB == 4 ? 0 : i0;  // which 32 columns of a 16-bit chunk
             // C's buffer: with pre, 0 is pre's; chunks of a unit come in pairs except for
             // half a tile in 16 bits, so with prefetches the count of chunks decides
-            const uint32_t b = has_p ? 1u : !two ? 0u : pref ? (used & 1u) : uint32_t(c & 1);
+            const uint32_t b = has_p ? 1u : !two ? 0u : pref ? residual_buf(used) : uint32_t(c & 1);
             tmem_ld_wait();
             if (j + 1 < groups) tmem_ld_32x32b_x32(t_addr + (j + 1) * 32, v[i0 ^ 1]);
             else drained();
             if (part == 0) {  // the buffers of a new chunk
                 if (pref) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(rbar + 8u * b, (used >> 1) & 1u, p.wait))) ok = false;
+                    if (!__all_sync(0xffffffffu, mbar_wait(rbar + 8u * b, residual_phase(used), p.wait))) ok = false;
                 } else {
                     // the buffer's previous store has read it
                     if (lane == 0) bulk_wait_group_read<0>();
@@ -546,7 +553,7 @@ struct PairEpilogue {
             if (part == (OB == 4 ? 0 : 1)) {
                 if (has_p) store(0, p.e.pre, p.e.ldp, tmP, p.e.p_tma != 0, row0, col0 + c * CHUNK);
                 store(b, p.e.c, p.e.ldc, tmC, p.e.c_tma != 0, row0, col0 + c * CHUNK);
-                if (pref) {  // this buffer takes the chunk after the next
+                if (pref) {  // this buffer takes the next chunk, or in turns the one after
                     ++used;
                     if (lane == 0) bulk_wait_group_read<0>();
                     __syncwarp();
@@ -561,14 +568,14 @@ struct PairEpilogue {
     __device__ __forceinline__ void begin() {
         if (!prefetches()) return;
         fetch_residual();
-        fetch_residual();
+        if (in_turns()) fetch_residual();
     }
 
     // After the last unit, or after a wait ran out: no copy may still be on its
     // way into or out of this warp's buffers when the CTA ends.
     __device__ __forceinline__ void end() {
         for (; used < fetched; ++used)
-            mbar_wait_slow(rbar + 8u * (used & 1u), (used >> 1) & 1u, cleanup_wait(p.wait), false);
+            mbar_wait_slow(rbar + 8u * residual_buf(used), residual_phase(used), cleanup_wait(p.wait), false);
         if (lane == 0) bulk_wait_group<0>();
         __syncwarp();
     }
@@ -1227,19 +1234,19 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
 }
 
 // ================================================================== K = 0
-// The sum is empty: C = act(bias) + R, element by element (4096 x 8192 fp16: 101 us,
-// bound by the indices' divisions; a case of the definition, not of any model).
+// The sum is empty: C = act(bias) + R, a strip of columns per block, whose bias is
+// read once, on every gridDim.y-th row (4096 x 8192 fp16: 21.3 us; a case of the
+// definition, not of any model).
 __global__ void linear_empty_kernel(const LinearParams p) {
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t total = p.M * p.N;
-    for (int64_t e = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; e < total; e += int64_t(gridDim.x) * blockDim.x) {
-        const int64_t i = e / p.N, j = e - i * p.N;
-        float x = p.e.bias != nullptr ? load_elem(p.e.bias, p.e.bias_type, j) : 0.0f;
-        if (p.e.pre != nullptr) store_elem(p.e.pre, p.e.type, i * p.e.ldp + j, x);
-        x = act_one(p.e.act, x);
-        if (p.e.r != nullptr) x += load_elem(p.e.r, p.e.type, i * p.e.ldr + j);
-        store_elem(p.e.c, p.e.type, i * p.e.ldc + j, x);
+    for (int64_t j = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; j < p.N; j += int64_t(gridDim.x) * blockDim.x) {
+        const float x = p.e.bias != nullptr ? load_elem(p.e.bias, p.e.bias_type, j) : 0.0f;
+        const float y = act_one(p.e.act, x);
+        for (int64_t i = blockIdx.y; i < p.M; i += gridDim.y) {
+            if (p.e.pre != nullptr) store_elem(p.e.pre, p.e.type, i * p.e.ldp + j, x);
+            store_elem(p.e.c, p.e.type, i * p.e.ldc + j, p.e.r != nullptr ? y + load_elem(p.e.r, p.e.type, i * p.e.ldr + j) : y);
+        }
     }
 }
 

@@ -14,7 +14,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("module", ["test_linear_gpu.py", "test_linear_places_gpu.py", "test_rms_norm_gpu.py", "test_norm_places_gpu.py", "test_mlp_block_gpu.py"])
+@pytest.mark.parametrize("module", ["test_linear_gpu.py", "test_linear_places_gpu.py", "test_linear_epilogue_gpu.py", "test_rms_norm_gpu.py", "test_norm_places_gpu.py", "test_mlp_block_gpu.py"])
 def test_checked_library_runs_the_operators(module):
     require_gpu()
     subprocess.run([sys.executable, "-m", "dense_gemm_gb300.build", "--debug"], cwd=ROOT, check=True)
