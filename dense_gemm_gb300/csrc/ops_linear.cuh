@@ -403,24 +403,32 @@ struct PairEpilogue {
         }
     }
 
-    // Buffer b <- the residual's 32 rows x CHUNK columns, with plain loads.
+    // Buffer b <- the residual's 32 rows x CHUNK columns, with plain loads. Places
+    // past the last row or column get its value, which goes nowhere: without
+    // conditions, and with a batch's loads before its first store to shared memory,
+    // they are in flight together (8192 x 8191 x 128: row by row 440 us, so 183).
     __device__ __forceinline__ void load_residual(uint32_t b, int64_t row0, int64_t col0) {
-        const int64_t rows = p.M - row0;
-        constexpr int PER_LANE = CHUNK / 32;
-        const int64_t col = col0 + PER_LANE * lane;
-#pragma unroll 16
-        for (int r = 0; r < 32; ++r) {
-            uint32_t w = 0;
-            if (r < rows && col < p.N) {
+        constexpr int PER_LANE = CHUNK / 32, BATCH = 16;
+        const int64_t last = p.N - 1, c = col0 + PER_LANE * lane;
+        const int64_t at0 = c < last ? c : last, at1 = c + 1 < last ? c + 1 : last;
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += BATCH) {
+            uint32_t w[BATCH], hi[BATCH];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int64_t r = row0 + r0 + i, at = (r < p.M ? r : p.M - 1) * p.e.ldr;
                 if constexpr (OB == 4) {
-                    w = static_cast<const uint32_t *>(p.e.r)[(row0 + r) * p.e.ldr + col];
+                    w[i] = static_cast<const uint32_t *>(p.e.r)[at + at0];
                 } else {
-                    const uint16_t *src = static_cast<const uint16_t *>(p.e.r) + (row0 + r) * p.e.ldr + col;
-                    w = src[0];
-                    if (col + 1 < p.N) w |= uint32_t(src[1]) << 16;
+                    w[i] = static_cast<const uint16_t *>(p.e.r)[at + at0];
+                    hi[i] = static_cast<const uint16_t *>(p.e.r)[at + at1];
                 }
             }
-            st_shared_s32(buf(b) + swz128(r, lane >> 2) + (lane & 3) * 4, int32_t(w));
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                if constexpr (OB == 2) w[i] |= hi[i] << 16;
+                st_shared_s32(buf(b) + swz128(r0 + i, lane >> 2) + (lane & 3) * 4, int32_t(w[i]));
+            }
         }
         __syncwarp();
     }
@@ -443,16 +451,23 @@ struct PairEpilogue {
         constexpr int PER_LANE = CHUNK / 32;
         const int64_t col = col0 + PER_LANE * lane;
         if (col < p.N) {
-#pragma unroll 8
-            for (int r = 0; r < 32; ++r) {
-                const uint32_t w = ld_shared_b32(buf(b) + swz128(r, lane >> 2) + (lane & 3) * 4);
-                if (r >= rows || !G16_CHECK(row0 + r < p.M && col >= 0)) continue;
-                if constexpr (OB == 4) {
-                    static_cast<uint32_t *>(dst)[(row0 + r) * ld + col] = w;
-                } else {
-                    uint16_t *d = static_cast<uint16_t *>(dst) + (row0 + r) * ld + col;
-                    d[0] = uint16_t(w & 0xffffu);
-                    if (col + 1 < p.N) d[1] = uint16_t(w >> 16);
+            constexpr int BATCH = 8;
+#pragma unroll 1
+            for (int r0 = 0; r0 < 32; r0 += BATCH) {
+                uint32_t w[BATCH];
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) w[i] = ld_shared_b32(buf(b) + swz128(r0 + i, lane >> 2) + (lane & 3) * 4);
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int r = r0 + i;
+                    if (r >= rows || !G16_CHECK(row0 + r < p.M && col >= 0)) continue;
+                    if constexpr (OB == 4) {
+                        static_cast<uint32_t *>(dst)[(row0 + r) * ld + col] = w[i];
+                    } else {
+                        uint16_t *d = static_cast<uint16_t *>(dst) + (row0 + r) * ld + col;
+                        d[0] = uint16_t(w[i] & 0xffffu);
+                        if (col + 1 < p.N) d[1] = uint16_t(w[i] >> 16);
+                    }
                 }
             }
         }
