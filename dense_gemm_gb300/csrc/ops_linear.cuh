@@ -912,13 +912,13 @@ __device__ __forceinline__ void split_send(uint32_t t_addr, uint32_t base, uint3
 
 // What an epilogue warp of linear_split holds of its columns and of the residual of
 // its first rows: fetched while the products run, since nothing hides the latency
-// of a load at the end (200 x 4096 x 8192 with a residual: 24.4 us, so 23.2). A lane
+// of a load at the end (200 x 4096 x 8192 with a residual: 24.4 us, so 21.7). A lane
 // holds four columns: consecutive ones where C, pre and residual take vectors of
 // four (vec), else 32 apart, so that a warp's stores are contiguous either way.
 constexpr int kSplitRows = 4;  // rows of a warp at a time
 struct SplitColumns {
     float bias[4], sb[4];
-    float r[kSplitRows][4];
+    uint32_t r[kSplitRows][4];  // as loaded: two or four words
 };
 
 template <bool VEC>
@@ -926,20 +926,43 @@ __device__ __forceinline__ int split_col(int lane, int i) {
     return VEC ? lane * 4 + i : lane + 32 * i;
 }
 
-// The residual of row m at this lane's columns.
+// The residual of row m at this lane's columns as it lies in memory, converted only
+// where it is added, so that several rows' loads are in flight together. A column
+// past the last gets its value, which goes nowhere.
 template <bool VEC>
-__device__ __forceinline__ void split_residual(const LinearParams &p, int64_t m, int32_t n0, int lane, float (&r)[4]) {
-    const int64_t at = m * p.e.ldr + n0;
+__device__ __forceinline__ void split_residual(const LinearParams &p, int64_t m, int32_t n0, int lane, uint32_t (&r)[4]) {
+    const int64_t at = m * p.e.ldr;
     if (VEC && p.e.type != 0) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.e.r) + at + lane * 4);
-        const float2 a = unpack_16x2(w.x, p.e.type), b = unpack_16x2(w.y, p.e.type);
-        r[0] = a.x, r[1] = a.y, r[2] = b.x, r[3] = b.y;
+        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.e.r) + at + n0 + lane * 4);
+        r[0] = w.x, r[1] = w.y;
+        return;
+    }
+    int64_t col[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t c = int64_t(n0) + split_col<VEC>(lane, i);
+        col[i] = at + (VEC || c < p.N ? c : p.N - 1);
+    }
+    if (p.e.type == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = static_cast<const uint32_t *>(p.e.r)[col[i]];
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = split_col<VEC>(lane, i);
-            r[i] = VEC || n0 + int64_t(c) < p.N ? load_elem(p.e.r, p.e.type, at + c) : 0.0f;
-        }
+        for (int i = 0; i < 4; ++i) r[i] = static_cast<const uint16_t *>(p.e.r)[col[i]];
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void add_split_residual(uint32_t type, const uint32_t (&r)[4], float *x) {
+    if (type == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] += __uint_as_float(r[i]);
+    } else if constexpr (VEC) {
+        const float2 a = unpack_16x2(r[0], type), b = unpack_16x2(r[1], type);
+        x[0] += a.x, x[1] += a.y, x[2] += b.x, x[3] += b.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] += unpack_16x2(r[i], type).x;
     }
 }
 
@@ -1022,8 +1045,7 @@ __device__ __forceinline__ void split_rows(const LinearParams &p, uint32_t base,
         if (e.r != nullptr) {
 #pragma unroll
             for (int u = 0; u < R; ++u) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[4 * u + i] += h.r[u][i];
+                add_split_residual<VEC>(e.type, h.r[u], x + 4 * u);
                 // for the next rows, while these are stored
                 const int t = tile_row(u) + R * EPI_WARPS * S;
                 if (t < valid) split_residual<VEC>(p, int64_t(m0) + t, n0, lane, h.r[u]);
