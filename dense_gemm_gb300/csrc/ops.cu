@@ -790,13 +790,14 @@ struct RowShape {
     bool fits;     // the row fits its threads' registers
 };
 
-// One load per thread where 1024 threads hold the row so, else the fewest; short
-// rows share a block of 256 threads.
-RowShape row_shape(int64_t width) {
+// One load per thread where 1024 threads hold the row so, else the fewest; with
+// many rows `least` (four, two of fp32's twice as long ones), so that blocks are small and several on an SM are at different
+// points of load, reduction and store. Short rows share a block of 256 threads.
+RowShape row_shape(int64_t width, int least) {
     RowShape s{1, 32, 1, false};
     for (int nv : {1, 2, 4}) {
         const int64_t t = cdiv(cdiv(width, 8 * nv), 32) * 32;
-        if (t > 1024) continue;
+        if (t > 1024 || nv < least) continue;
         s.nv = nv;
         s.tpr = int(t);
         s.fits = true;
@@ -879,22 +880,22 @@ cudaError_t launch_ring(const RingPlan &r, const P &p, int dev, cudaStream_t str
     return launch_shape(Kernel, dim3(unsigned(r.grid)), dim3(unsigned(r.tpr), unsigned(r.rpb)), r.smem, 1, stream, p, r.ring);
 }
 
-// The persistent form or one block per row(s), both on 16-byte vectors. The ring
-// pays where a thread has two loads or more of a row and a block long enough to
-// work (direct / ring, bf16: 8192 x 4096 without residual 30.3 / 28.2 us, 4096 x 8192
-// 34.7 / 25.8, with a residual and 8 bits 43.1 / 40.7, 2048 x 12288 with a residual
-// 40.6 / 35.1; but 16384 x 2048 27.1 / 47.6, 2048 x 4096 9.7 / 10.0), except for two
-// 16-bit inputs and two 16-bit outputs of rows that 256 threads hold, which either
-// form moves at the memory's rate (4096 x 8192 43.3 / 45.8 us).
-bool ring_pays(const RingPlan &r, const NormParams &p, bool quant) {
-    if (!r.ok || r.nv < 2 || p.rows * p.width < int64_t(48 * 1024) * r.grid) return false;
-    return quant || p.r == nullptr || p.width > 8192;
+// Whether rms_norm_kernel's blocks take four loads per thread: rows of more than
+// 2048 elements, several waves of them (one load or the fewest / four, bf16: 64 x
+// 8192 2.1 / 2.8 us, 3000 x 2047 8.3 / 8.6, 3000 x 8192 25.6 / 19.5, 8000 x 8192 to 8 bits
+// with a residual 78.7 / 68.1), more waves where the residual and its sum move as
+// many bytes again (1000 x 5120 9.0 / 9.7, 3000 x 6144 27.0 / 24.7). The persistent
+// ring of rows that the gradients use was slower here (8000 x 8192 to 8 bits 79.9).
+bool many_rows(const NormParams &p, bool quant, int num_sms) {
+    const int64_t waves = p.r != nullptr && !quant && p.width <= 8192 ? 16 : 4;
+    return p.width > 2048 && p.rows >= waves * num_sms;
 }
 
 template <typename T, bool kQ>
 cudaError_t launch_norm(const NormParams &p, bool vec, bool shift, int dev, int num_sms, cudaStream_t stream) {
+    const int least = !many_rows(p, kQ, num_sms) ? 1 : sizeof(T) == 2 ? 4 : 2;
     if constexpr (sizeof(T) == 2) {
-        const RowShape s = row_shape(p.width + 7);
+        const RowShape s = row_shape(p.width + 7, least);
         if (shift && s.fits) {
             auto *k = s.nv == 1   ? rms_norm_kernel<T, 8, 1, kQ, true>
                       : s.nv == 2 ? rms_norm_kernel<T, 8, 2, kQ, true>
@@ -902,16 +903,11 @@ cudaError_t launch_norm(const NormParams &p, bool vec, bool shift, int dev, int 
             return launch_shape(k, dim3(unsigned(cdiv(p.rows, s.rpb))), dim3(unsigned(s.tpr), unsigned(s.rpb)), 0, 1, stream, p);
         }
     }
-    const RingPlan r = ring_plan(p.rows, p.width, int(sizeof(T)), p.r != nullptr ? 2 : 1, vec, false, false, num_sms);
-    if (r.ok && !vec) return launch_ring<rms_norm_rows_any_kernel<T, kQ>>(r, p, dev, stream);
-    if (ring_pays(r, p, kQ)) {
-        switch (r.nv) {
-            case 2: return launch_ring<rms_norm_rows_kernel<T, 8, 2, kQ>>(r, p, dev, stream);
-            case 3: return launch_ring<rms_norm_rows_kernel<T, 8, 3, kQ>>(r, p, dev, stream);
-            default: return launch_ring<rms_norm_rows_kernel<T, 8, 4, kQ>>(r, p, dev, stream);
-        }
+    if (!vec) {
+        const RingPlan r = ring_plan(p.rows, p.width, int(sizeof(T)), p.r != nullptr ? 2 : 1, false, false, false, num_sms);
+        if (r.ok) return launch_ring<rms_norm_rows_any_kernel<T, kQ>>(r, p, dev, stream);
     }
-    const RowShape s = row_shape(p.width);
+    const RowShape s = row_shape(p.width, least);
     if (!vec || !s.fits)
         return launch_shape(rms_norm_long_kernel<T>, dim3(unsigned(p.rows)), dim3(1024), 0, 1, stream, p, int32_t(kQ));
     auto *k = s.nv == 1   ? rms_norm_kernel<T, 8, 1, kQ, false>

@@ -407,8 +407,8 @@ struct NormParams {
 // t) * VEC + i of the row is value i of load j of thread t.
 // kShift: rows off 16-byte boundaries, their first element `o` into a granule.
 // DRAM bounds it where there are many rows (8192 x 4096 bf16 with residual: 268 MB
-// in 40.7 us, 6.6 TB/s), the chain load - reduction - store where there are few
-// (1 x 4096: 2.0 us).
+// in 41 us, 6.5 TB/s; 4096 x 8192 to 8 bits 235 MB in 36.9 us, 6.4 TB/s), the chain
+// load - reduction - store where there are few (1 x 4096: 2.0 us).
 template <typename T, int VEC, int NV, bool kQ, bool kShift>
 __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
     __shared__ float red[32];
@@ -593,87 +593,6 @@ __device__ __forceinline__ void let_copies_land() {
     }
 }
 
-// 4096 x 8192 bf16 with a residual, 8-bit y: 235 MB in 40.3 us one call after the
-// other (31.6 alone after others: the writes are still in L2), 5.8 TB/s, bound by DRAM.
-template <typename T, int VEC, int NV, bool kQ>
-__global__ void __launch_bounds__(kRingThreads) rms_norm_rows_kernel(const NormParams p, const RingShape ring) {
-    __shared__ float red[2][32];
-    __shared__ uint32_t redq[2][32];
-    __shared__ __align__(8) uint64_t full[kRingSlots];
-    extern __shared__ __align__(16) uint8_t rows[];
-    if (threadIdx.y == 0 && threadIdx.x == 0) {
-        for (int s = 0; s < ring.slots; ++s) mbar_init(smem_addr(&full[s]), 1);
-        fence_mbar_init();
-    }
-    __syncthreads();
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t step = int64_t(gridDim.x) * blockDim.y;
-    const int64_t first = int64_t(blockIdx.x) * blockDim.y;
-    const RowSource<T> src[3] = {{static_cast<const T *>(p.x), p.ldx}, {static_cast<const T *>(p.r), p.ldr}, {nullptr, 0}};
-    const int arrays = p.r != nullptr ? 2 : 1;
-    auto refill = [&](int64_t base, int slot) {
-        if (base < p.rows) fill_slot(src, arrays, int(blockDim.y), ring, rows, slot, smem_addr(&full[slot]), base, p.rows, p.width);
-    };
-    for (int s = 0; s < ring.slots; ++s) refill(first + s * step, s);
-    auto at_of = [&](int j) { return (j * int(blockDim.x) + int(threadIdx.x)) * VEC; };
-    const int width = int(p.width);
-    Raw<T, VEC> w16[NV];  // a weight of T's type; fp32 weights are read again for each row
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-        if (at_of(j) < width && !p.w_f32) w16[j] = load_raw<T, VEC>(static_cast<const T *>(p.w) + at_of(j));
-    const uint32_t ring0 = smem_addr(rows) + uint32_t(int(threadIdx.y) * ring.pitch);
-    const bool has_r = p.r != nullptr, has_h = p.h != nullptr;
-    int slot = 0, flip = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int64_t base = first; base < p.rows; base += step, flip ^= 1) {
-        const int64_t row = base + threadIdx.y;
-        const bool live = row < p.rows;
-        ok = mbar_wait(smem_addr(&full[slot]), phase, p.wait) && ok;
-        const uint32_t mine = ring0 + uint32_t(slot * ring.slot_bytes);
-        const uint32_t x = mine, r = mine + uint32_t(ring.array_bytes);  // rows on 16-byte boundaries
-        T *h = static_cast<T *>(p.h) + row * p.ldh;
-        F32<VEC> t[NV];
-        auto ss2 = splat<VEC>(0.0f);
-        float tmax = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (!live || at_of(j) >= width) continue;
-            t[j] = widen<T, VEC>(load_raw_shared<T, VEC>(x + uint32_t(at_of(j)) * uint32_t(sizeof(T))));
-            if (has_r) {
-                const F32<VEC> f = widen<T, VEC>(load_raw_shared<T, VEC>(r + uint32_t(at_of(j)) * uint32_t(sizeof(T))));
-#pragma unroll
-                for (int i = 0; i < F32<VEC>::PAIRS; ++i) t[j].p[i] = add2(t[j].p[i], f.p[i]);
-                if (has_h) store_f32<T, VEC>(h + at_of(j), t[j]);
-            }
-            square_and_weigh<VEC, kQ>(t[j], p.w_f32 ? load_weight<T, VEC>(p.w, true, at_of(j)) : widen<T, VEC>(w16[j]), ss2, tmax);
-        }
-        float ss = total(ss2);
-        if constexpr (kQ) row_sum_max(ss, tmax, red[flip], redq[flip]);
-        else ss = row_sum<true>(ss, red[flip]);
-        refill(base + int64_t(ring.slots) * step, slot);  // every thread has its values of this slot in registers
-        const float rstd = rsqrtf(fmaf(ss, p.inv_width, p.eps));
-        float mul = rstd;
-        if constexpr (kQ) {
-            float scale;
-            quant_factors(tmax, rstd, mul, scale);
-            if (live && threadIdx.x == 0) p.scale[row] = scale;
-        }
-        if (live && p.rstd != nullptr && threadIdx.x == 0) p.rstd[row] = rstd;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            if (!live || at_of(j) >= width) continue;
-#pragma unroll
-            for (int i = 0; i < F32<VEC>::PAIRS; ++i) t[j].p[i] = mul2(t[j].p[i], splat<VEC>(mul));
-            if constexpr (kQ) store_e4m3<VEC>(static_cast<uint8_t *>(p.y) + row * p.ldy + at_of(j), t[j]);
-            else store_f32<T, VEC>(static_cast<T *>(p.y) + row * p.ldy + at_of(j), t[j]);
-        }
-        if (++slot == ring.slots) { slot = 0; phase ^= 1u; }
-    }
-    if (!ok) let_copies_land();
-}
-
 // Rows that neither lie on 16-byte boundaries nor all start at the same place in
 // a granule, or fp32 ones off them: element by element out of the slots, lane by
 // lane along the row, so that the stores of a warp stay contiguous. A slot is read
@@ -770,10 +689,9 @@ struct NormBackwardParams {
     WaitCtl wait;
 };
 
-// The persistent form, as rms_norm_rows_kernel: rows arrive through a ring of
-// shared-memory slots, and a thread keeps its columns, so that their dweight
-// sums stay in its registers and each block writes one row of partial sums at
-// its end. A slot is read twice (for the row's dot product and for dx) and
+// The persistent form: rows arrive through a ring of shared-memory slots, and a
+// thread keeps its columns, so that their dweight sums stay in its registers and
+// each block writes one row of partial sums at its end. A slot is read twice (for the row's dot product and for dx) and
 // refilled after the next step's barrier. The chain of a row's reduction is long
 // beside its arithmetic, so a thread works on R rows at a time (row base +
 // threadIdx.y * R + r), with one barrier for all of them. 8192 x 4096 bf16 with

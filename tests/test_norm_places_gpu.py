@@ -118,3 +118,24 @@ def test_gaps_of_nothing_but_nan_and_infinity():
     keep = [i for i in range(41) if i not in (7, 23, 30)]
     assert torch.equal(got[keep], want[keep]) and torch.equal(dgot[keep], dwant[keep])
     assert torch.isnan(got[7]).all()
+
+
+@pytest.mark.parametrize("rows,width", [(700, 2056), (2500, 2304), (610, 8192), (615, 12296)])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("with_residual", [False, True])
+def test_many_rows(rows, width, dtype, with_residual):
+    x, w = normal(10, rows, width, dtype=dtype), normal(11, width, dtype=dtype)
+    r = normal(12, rows, width, dtype=dtype) if with_residual else None
+    hd = x.double() + (r.double() if with_residual else 0)
+    rstd = (hd.square().mean(1) + EPS).rsqrt()
+    ref = hd * rstd[:, None] * w.double()
+    n = rms_norm(x, w, residual=r, return_rstd=True)
+    # h is the unrounded sum in fp32: half a unit of 2^-24 of it
+    assert_close(n.y, ref, (bound(width) + 2.0 ** -24) * ref.abs(), "y")
+    if with_residual:
+        assert_close(n.h, hd, 2.0 ** -24 * hd.abs(), "h")
+    n = rms_norm(x, w, residual=r, out_dtype=E4M3)
+    top = ref.abs().amax(1)
+    d = (n.y.float().double() * n.scale.double()[:, None] - ref).abs()
+    assert bool((d <= 1.001 * torch.maximum(2.0 ** -4 * ref.abs(), 2.0 ** -10 * (top / 448)[:, None])
+                 + 3 * (bound(width) + 2.0 ** -24) * ref.abs()).all())
