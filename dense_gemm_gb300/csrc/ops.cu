@@ -945,12 +945,15 @@ cudaError_t launch_norm_backward(NormBackwardParams p, bool vec, bool shift, flo
         else if constexpr (sizeof(T) == 2) e = launch_norm_backward_rows<T, true>(r, p, dev, stream);
         else e = cudaErrorInvalidValue;  // shift is for 16-bit types
     } else {
-        e = launch_shape(rms_norm_backward_long_kernel<T>, dim3(unsigned(p.rows)), dim3(1024), 0, 1, stream, p);
+        // dweight's sums first: they read grad, which dx may be written over
         const int64_t rows_per_block = cdiv(p.rows, kNormParts);
         parts = cdiv(p.rows, rows_per_block);
-        if (e == cudaSuccess && dweight != nullptr)
+        e = cudaSuccess;
+        if (dweight != nullptr)
             e = launch_shape(rms_norm_dweight_long_kernel<T>, dim3(unsigned(cdiv(p.width, 256)), unsigned(parts)), dim3(256),
                              0, 1, stream, p, rows_per_block);
+        if (e == cudaSuccess)
+            e = launch_shape(rms_norm_backward_long_kernel<T>, dim3(unsigned(p.rows)), dim3(1024), 0, 1, stream, p);
     }
     if (e == cudaSuccess && dweight != nullptr)
         e = launch_shape(sum_partials_kernel, dim3(unsigned(cdiv(p.width, 32))), dim3(32, kPartGroups), 0, 1, stream,
