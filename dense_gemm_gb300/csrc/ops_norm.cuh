@@ -360,21 +360,30 @@ __device__ __forceinline__ void row_sum_max(float &v, float &m, float *red, uint
     m = __uint_as_float(mb);
 }
 
-// Rows whose largest |y| is below this (zero rows among them) are stored as
-// zeros with scale 1: their 448 / a would leave fp32's range.
+// Rows whose largest |y| is below this are stored as zeros with scale 1, as zero
+// rows are: their scale would come near the smallest normal number.
 constexpr float kQuantTiny = 7.7e-34f;
 constexpr float kE4m3Max = 448.0f;
+constexpr float kQuantTwoSteps = 1.4e-36f;  // below this, 448 / x may leave fp32's range
 
 // With t = w h, y = t rstd and a = max|y| = rstd max|t|, so y 448 / a = t 448 /
-// max|t|: the row's factor for t and its scale, from max|t|. One pass over the
-// row then gives both its sum and its maximum.
-__device__ __forceinline__ void quant_factors(float tmax, float rstd, float &mul, float &scale) {
+// max|t|: the row's factor `mul` for t and its scale, from max|t|. One pass over the
+// row then gives both its sum and its maximum. Where max|t| is too small for that
+// quotient while a is not, t is first multiplied by rstd (`first`, else 1), then by
+// 448 / a.
+__device__ __forceinline__ void quant_factors(float tmax, float rstd, float &first, float &mul, float &scale) {
     const float a = tmax * rstd;
+    first = 1.0f;
     if (a < kQuantTiny) {
         mul = 0.0f;
         scale = 1.0f;
     } else {  // a NaN (also from an infinity, whose rstd is 0) makes the row NaN
-        mul = a == a ? kE4m3Max / tmax : a;
+        if (tmax < kQuantTwoSteps) {
+            first = rstd;
+            mul = kE4m3Max / a;
+        } else {
+            mul = a == a ? kE4m3Max / tmax : a;
+        }
         scale = a * (1.0f / kE4m3Max);
     }
 }
@@ -469,9 +478,17 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
     if (p.rstd != nullptr && threadIdx.x == 0) p.rstd[row] = rstd;
     float mul = rstd;
     if constexpr (kQ) {
-        float scale;
-        quant_factors(tmax, rstd, mul, scale);
+        float scale, first;
+        quant_factors(tmax, rstd, first, mul, scale);
         if (threadIdx.x == 0) p.scale[row] = scale;
+        if (first != 1.0f) {  // the whole row; rare
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (at_of(j) >= width) continue;
+#pragma unroll
+                for (int i = 0; i < F32<VEC>::PAIRS; ++i) t[j].p[i] = mul2(t[j].p[i], splat<VEC>(first));
+            }
+        }
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -510,15 +527,15 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const NormParams p,
     row_sum_max(ss, tmax, red, redq);
     const float rstd = rsqrtf(fmaf(ss, p.inv_width, p.eps));
     if (p.rstd != nullptr && threadIdx.x == 0) p.rstd[row] = rstd;
-    float mul = rstd, scale = 1.0f;
+    float mul = rstd, first = 1.0f, scale = 1.0f;
     if (quant) {
-        quant_factors(tmax, rstd, mul, scale);
+        quant_factors(tmax, rstd, first, mul, scale);
         if (threadIdx.x == 0) p.scale[row] = scale;
     }
     for (int64_t at = threadIdx.x; at < p.width; at += blockDim.x) {
         const float h = sum(at);
         F32<1> y;
-        y.p[0] = h * load_weight<T, 1>(p.w, p.w_f32 != 0, at).p[0] * mul;
+        y.p[0] = h * load_weight<T, 1>(p.w, p.w_f32 != 0, at).p[0] * first * mul;
         if (p.h != nullptr) static_cast<T *>(p.h)[row * p.ldh + at] = from_f32<T>(h);
         if (quant) store_e4m3<1>(static_cast<uint8_t *>(p.y) + row * p.ldy + at, y);
         else store_f32<T, 1>(static_cast<T *>(p.y) + row * p.ldy + at, y);
@@ -650,10 +667,10 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_rows_any_kernel(const N
         else ss = row_sum<true>(ss, red[flip]);
         if (base >= first + step) refill(base + int64_t(ring.slots - 1) * step, last);  // all have left the step before
         const float rstd = rsqrtf(fmaf(ss, p.inv_width, p.eps));
-        float mul = rstd;
+        float mul = rstd, first = 1.0f;
         if constexpr (kQ) {
             float scale;
-            quant_factors(tmax, rstd, mul, scale);
+            quant_factors(tmax, rstd, first, mul, scale);
             if (live && threadIdx.x == 0) p.scale[row] = scale;
         }
         if (live && p.rstd != nullptr && threadIdx.x == 0) p.rstd[row] = rstd;
@@ -664,7 +681,9 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_rows_any_kernel(const N
                 const float h = sum(c);
                 if (has_h) ho[c] = from_f32<T>(h);
                 F32<1> y;
-                y.p[0] = h * load_weight<T, 1>(p.w, p.w_f32 != 0, c).p[0] * mul;
+                y.p[0] = h * load_weight<T, 1>(p.w, p.w_f32 != 0, c).p[0];
+                if constexpr (kQ) y.p[0] *= first;
+                y.p[0] *= mul;
                 if constexpr (kQ) store_e4m3<1>(static_cast<uint8_t *>(p.y) + row * p.ldy + c, y);
                 else store_f32<T, 1>(static_cast<T *>(p.y) + row * p.ldy + c, y);
             }
