@@ -370,11 +370,12 @@ constexpr float kQuantTwoSteps = 1.4e-36f;  // below this, 448 / x may leave fp3
 // max|t|: the row's factor `mul` for t and its scale, from max|t|. One pass over the
 // row then gives both its sum and its maximum. Where max|t| is too small for that
 // quotient while a is not, t is first multiplied by rstd (`first`, else 1), then by
-// 448 / a.
+// 448 / a. (max|t| = 0 is looked at by itself: without eps, a zero row's rstd is
+// infinite.)
 __device__ __forceinline__ void quant_factors(float tmax, float rstd, float &first, float &mul, float &scale) {
     const float a = tmax * rstd;
     first = 1.0f;
-    if (a < kQuantTiny) {
+    if (tmax == 0.0f || a < kQuantTiny) {
         mul = 0.0f;
         scale = 1.0f;
     } else {  // a NaN (also from an infinity, whose rstd is 0) makes the row NaN

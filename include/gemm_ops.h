@@ -145,7 +145,7 @@ gemm_status_t gemm_linear_backward_workspace_size(const gemm_matrix_t *G, const 
  * once. x, residual and h have one type, fp32, fp16 or bf16; y has that type or
  * e4m3; weight [width] has x's type or is fp32. With an e4m3 y, a = max_j
  * |y[i,j]|, scale[i] = a / 448 and y[i,j] holds nearest-even(y[i,j] * (448 /
- * a)), so that the value is y * scale; a row of zeros and a
+ * a)), so that the value is y * scale; a row of zeros (also with eps = 0) and a
  * row whose a is below 7.7e-34 have scale 1 and zeros; a row with a NaN or an
  * infinity has scale NaN and NaNs. weight * h is a value in fp32 of its own: what
  * of it falls below fp32's smallest numbers counts as 0. scale must be given

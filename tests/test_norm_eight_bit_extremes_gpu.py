@@ -1,5 +1,5 @@
-"""GPU: the 8-bit norm on rows whose values are very small, through each of its
-kernels, against the definition in 64 bits."""
+"""GPU: the 8-bit norm on rows whose values are very small, zero or not finite,
+through each of its kernels, against the definition in 64 bits."""
 import pytest
 import torch
 
@@ -8,7 +8,7 @@ from gpu_util import require_gpu
 from ops_util import assert_close, strided
 
 pytestmark = pytest.mark.gpu
-BF16, F32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+F16, BF16, F32, E4M3 = torch.float16, torch.bfloat16, torch.float32, torch.float8_e4m3fn
 TINY = 7.7e-34  # rows whose largest |y| is below are stored as zeros with scale 1
 
 
@@ -72,6 +72,17 @@ def test_small_weights_without_eps(form, dtype):
     assert torch.equal(q, pattern(3, width).double() * 448)
     # rstd of a sum of `width` squares: half of (terms per thread + tree) 2^-24
     assert_close(scale, a / 448, (max(32, width / 1024) + 48) * 2.0 ** -24 * a / 448, "scale")
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_rows_of_zeros(form, dtype, eps):
+    width, *offsets = form
+    x = torch.ones(3, width, device="cuda", dtype=dtype)
+    x[1] = 0
+    q, scale = quantised(x, torch.ones(width, device="cuda", dtype=dtype), eps, offsets)
+    assert scale[1] == 1 and bool((q[1] == 0).all()) and bool((q[[0, 2]] == 448).all())
 
 
 @pytest.mark.parametrize("form", FORMS)
