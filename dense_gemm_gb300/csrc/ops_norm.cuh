@@ -365,25 +365,28 @@ __device__ __forceinline__ void row_sum_max(float &v, float &m, float *red, uint
 constexpr float kQuantTiny = 7.7e-34f;
 constexpr float kE4m3Max = 448.0f;
 constexpr float kQuantTwoSteps = 1.4e-36f;  // below this, 448 / x may leave fp32's range
+constexpr float kLargest = 3.402823466e38f;
 
 // With t = w h, y = t rstd and a = max|y| = rstd max|t|, so y 448 / a = t 448 /
 // max|t|: the row's factor `mul` for t and its scale, from max|t|. One pass over the
 // row then gives both its sum and its maximum. Where max|t| is too small for that
 // quotient while a is not, t is first multiplied by rstd (`first`, else 1), then by
-// 448 / a. (max|t| = 0 is looked at by itself: without eps, a zero row's rstd is
-// infinite.)
+// 448 / a. An infinity or a NaN among y makes the row and its scale NaN. (max|t| = 0
+// is looked at by itself: without eps, a zero row's rstd is infinite.)
 __device__ __forceinline__ void quant_factors(float tmax, float rstd, float &first, float &mul, float &scale) {
     const float a = tmax * rstd;
     first = 1.0f;
     if (tmax == 0.0f || a < kQuantTiny) {
         mul = 0.0f;
         scale = 1.0f;
-    } else {  // a NaN (also from an infinity, whose rstd is 0) makes the row NaN
+    } else if (!(a <= kLargest)) {
+        mul = scale = __int_as_float(0x7fffffff);  // NaN
+    } else {
         if (tmax < kQuantTwoSteps) {
             first = rstd;
             mul = kE4m3Max / a;
         } else {
-            mul = a == a ? kE4m3Max / tmax : a;
+            mul = kE4m3Max / tmax;
         }
         scale = a * (1.0f / kE4m3Max);
     }

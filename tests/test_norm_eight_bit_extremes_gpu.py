@@ -92,3 +92,17 @@ def test_rows_below_the_smallest_scale_are_zeros(form, dtype):
     x = (pattern(2, width) * 5e-37).to(dtype)  # a = 5e-34 at eps 1e-6
     q, scale = quantised(x, torch.ones(width, device="cuda", dtype=dtype), 1e-6, offsets)
     assert bool((scale == 1).all()) and bool((q == 0).all())
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_an_infinite_weight_makes_rows_nan(form, dtype, bad):
+    """y has an infinity (or a NaN, where h is zero) in that column."""
+    width, *offsets = form
+    x = torch.ones(3, width, device="cuda", dtype=dtype)
+    x[1, width // 2] = 0
+    w = torch.ones(width, device="cuda", dtype=dtype)
+    w[width // 2] = bad
+    q, scale = quantised(x, w, 1e-6, offsets)
+    assert bool(scale.isnan().all()) and bool(q.isnan().all())
