@@ -986,10 +986,13 @@ __global__ void __launch_bounds__(256) rms_norm_dweight_long_kernel(const NormBa
 
 // out[c] = sum of partial[0..parts)[c]: 32 columns per block, blockDim.y threads
 // each add every blockDim.y-th row, then the first adds theirs in order. Bound by
-// latency (304 x 4096: 5.0 MB, 3.4 us of a call).
+// latency (304 x 4096: 5.0 MB, 3.4 us of a call). The partials come from L2: this
+// kernel may be on an SM before they are written, and with `late` reads them before its
+// own wait, so they are neither data that stays the same while it runs (no restricted
+// pointer, which would promise that) nor safe to take from an L1 that an earlier
+// launch has filled.
 constexpr int kPartGroups = 32;
-__global__ void __launch_bounds__(32 * kPartGroups) sum_partials_kernel(const float *__restrict__ partial,
-                                                                        float *__restrict__ out, int64_t parts,
+__global__ void __launch_bounds__(32 * kPartGroups) sum_partials_kernel(const float *partial, float *out, int64_t parts,
                                                                         int64_t width, uint32_t late) {
     __shared__ float s[kPartGroups][33];
     griddep_enter(late);
@@ -997,7 +1000,7 @@ __global__ void __launch_bounds__(32 * kPartGroups) sum_partials_kernel(const fl
     float v = 0.0f;
     if (col < width) {
 #pragma unroll 4
-        for (int64_t r = threadIdx.y; r < parts; r += kPartGroups) v += partial[r * width + col];
+        for (int64_t r = threadIdx.y; r < parts; r += kPartGroups) v += __ldcg(partial + r * width + col);
     }
     s[threadIdx.y][threadIdx.x] = v;
     griddep_leave(late);
