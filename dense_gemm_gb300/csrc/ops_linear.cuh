@@ -1357,18 +1357,20 @@ struct GradParams {
 constexpr int kGradGroups = 8;
 
 // Eight elements of a row from `at` on as they come: the one or, kShift, two
-// granules that hold them.
+// granules that hold them. They come from L2: with `late` the kernel reads before its
+// own wait, what the call's first kernel found complete, and so relies on no L1 line
+// that an earlier launch has left.
 template <typename T, bool kShift>
 struct GradLoad {
     Raw<T, 8> lo, hi;
     __device__ __forceinline__ void fetch(const T *row, int64_t at, int64_t n) {
         if constexpr (kShift) {
             const int s = place_in_granule(row + at);
-            lo = load_raw<T, 8>(row + at - s);
+            lo = load_raw_l2<T>(row + at - s);
             hi.q[0] = make_uint4(0u, 0u, 0u, 0u);
-            if (s != 0 && at + 8 - s < n) hi = load_raw<T, 8>(row + at - s + 8);  // only where the row reaches into it
+            if (s != 0 && at + 8 - s < n) hi = load_raw_l2<T>(row + at - s + 8);  // only where the row reaches into it
         } else {
-            lo = load_raw<T, 8>(row + at);
+            lo = load_raw_l2<T>(row + at);
         }
     }
     // the values, zero from column n on

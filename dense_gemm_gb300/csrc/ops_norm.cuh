@@ -68,6 +68,15 @@ __device__ __forceinline__ Raw<T, VEC> load_raw(const T *p) {
     return r;
 }
 
+// Eight elements from L2, past this SM's L1.
+template <typename T>
+__device__ __forceinline__ Raw<T, 8> load_raw_l2(const T *p) {
+    Raw<T, 8> r;
+#pragma unroll
+    for (int i = 0; i < int(sizeof(r) / 16); ++i) r.q[i] = __ldcg(reinterpret_cast<const uint4 *>(p) + i);
+    return r;
+}
+
 // The same from a shared-memory address (VEC = 8: 16-byte aligned).
 template <typename T, int VEC>
 __device__ __forceinline__ Raw<T, VEC> load_raw_shared(uint32_t addr) {
