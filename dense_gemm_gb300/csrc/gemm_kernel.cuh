@@ -1179,8 +1179,7 @@ __global__ void tile_map_kernel(Sched s, int32_t num_tiles, int32_t *out) {
 // Split-K reduction: C[i][j] = sum over s = 0 .. S-1, in that order, of
 // W[s][i][j] (W dense [S][M][ldw] fp32). Fixed order: the result does not
 // depend on scheduling. Four consecutive columns per thread.
-__global__ void splitk_reduce_kernel(const float *__restrict__ W, void *__restrict__ Cv, int64_t M,
-                                     int64_t N, int64_t ldw, int64_t scm, int32_t S,
+__global__ void splitk_reduce_kernel(const float *W, void *Cv, int64_t M, int64_t N, int64_t ldw, int64_t scm, int32_t S,
                                      uint32_t out_dtype, float alpha) {
     griddep_wait();  // the partial slices are the previous kernel's output
     griddep_launch_dependents();
@@ -1236,7 +1235,7 @@ __global__ void splitk_reduce_kernel(const float *__restrict__ W, void *__restri
 // rounded to C's type. Fixed order: the result does not depend on scheduling.
 // Four consecutive columns per thread.
 template <int TILE>
-__global__ void tail_reduce_kernel(const float *__restrict__ W, void *__restrict__ Cv, int64_t M, int64_t N,
+__global__ void tail_reduce_kernel(const float *W, void *Cv, int64_t M, int64_t N,
                                    int64_t scm, Sched sched, int32_t first, int32_t tiles, int32_t S,
                                    uint32_t out_dtype, float alpha) {
     griddep_wait();  // the partial tiles are the previous kernel's output
@@ -1329,10 +1328,10 @@ __global__ void pack_rows_kernel(PackJob a, PackJob b) {
         const uintptr_t g0 = s & ~uintptr_t(15);
         const uint32_t m = uint32_t(s - g0);  // even: fp16 elements
         uint32_t w[8];
-        const uint4 lo = __ldg(reinterpret_cast<const uint4 *>(g0));
+        const uint4 lo = *reinterpret_cast<const uint4 *>(g0);
         w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
         if (m + 2 * cnt > 16) {  // the last elements lie in the next granule
-            const uint4 hi = __ldg(reinterpret_cast<const uint4 *>(g0 + 16));
+            const uint4 hi = *reinterpret_cast<const uint4 *>(g0 + 16);
             w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
         } else {
             w[4] = w[5] = w[6] = w[7] = 0u;

@@ -19,7 +19,7 @@ def code(name):
     return re.sub(r"//[^\n]*", "", text)
 
 
-@pytest.mark.parametrize("name", ["ops_linear.cuh", "ops_norm.cuh"])
+@pytest.mark.parametrize("name", ["ops_linear.cuh", "ops_norm.cuh", "gemm_kernel.cuh", "gemm_pair.cuh"])
 def test_nothing_is_promised_to_stay_the_same(name):
     """A restricted pointer to const and __ldg say that the data does not change
     while the kernel runs; what the launch in front of it writes does."""
