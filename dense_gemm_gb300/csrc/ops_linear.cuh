@@ -1109,7 +1109,7 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     bool ready = false;  // epilogue warps: the accumulator is complete
     uint32_t tmem_base = 0;
     const int ew = warp - EPI_WARP0;
-    const bool vec = p.e.vec4 && n0 + lin::SPLIT_ROWS <= p.N;
+    const bool vec = p.e.vec4 && int64_t(n0) + lin::SPLIT_ROWS <= p.N;  // n0 may lie within 128 of 2^31
     SplitColumns columns = {};
 
     const uint32_t w_piece = p.b.mn ? lin::KPS * MN_CHUNK_BYTES : lin::SPLIT_ROWS * 128;  // between an operand's copies
