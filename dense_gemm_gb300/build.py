@@ -9,8 +9,11 @@ trapping. The binding loads it when GEMM_LIBRARY=debug.
 One translation unit, one -gencode, static CUDA runtime; no cmake. The same
 command works on x86-64 and aarch64 hosts. Beside it, the CPython extension
 _native.so (ops.py's argument marshalling, on PyTorch's C++ API) is built with
-the host compiler, at the same time.
+the host compiler, at the same time. The library needs none of what that takes:
+where this PyTorch has no CUDA parts, or there is no C++ compiler or no Python.h,
+the library is built without it and ops.py's calls raise.
 """
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -59,15 +62,31 @@ def up_to_date(lib: str = LIB, depends=None) -> bool:
     return all(os.path.getmtime(d) <= t for d in (DEPENDS if depends is None else depends))
 
 
+def torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def cxx() -> str:
+    return os.environ.get("CXX", "g++")
+
+
+def native_unbuildable() -> str:
+    """Why _native.so cannot be built on this machine; empty where it can."""
+    if shutil.which(cxx()) is None:
+        return f"no C++ compiler ({cxx()})"
+    needed = [os.path.join(torch_dir(), "include", "c10", "cuda", "CUDAStream.h"), os.path.join(torch_dir(), "lib", "libc10_cuda.so"),
+              os.path.join(sysconfig.get_paths()["include"], "Python.h")]
+    missing = [p for p in needed if not os.path.exists(p)]
+    return f"{missing[0]} is missing" if missing else ""
+
+
 def native_command(out: str):
     """The host compiler's command for _native.so; found without importing torch
     (a slow import), which the extension's own process has loaded when it is used."""
-    import importlib.util
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
-    lib = os.path.join(torch_dir, "lib")
-    inc = [os.path.join(torch_dir, "include"), os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+    lib = os.path.join(torch_dir(), "lib")
+    inc = [os.path.join(torch_dir(), "include"), os.path.join(torch_dir(), "include", "torch", "csrc", "api", "include"),
            os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), INCLUDE, sysconfig.get_paths()["include"]]
-    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
+    return [cxx(), "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-fvisibility=hidden",
             *(f"-I{d}" for d in inc), "-o", out, NATIVE_DEPENDS[0], f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python", "-ltorch",
             "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
@@ -84,12 +103,16 @@ def build_native(force: bool = False) -> str:
 def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
     lib = DEBUG_LIB if debug else LIB
     with ThreadPoolExecutor(1) as beside:
-        native = beside.submit(build_native, force)
+        why = native_unbuildable()
+        native = None if why else beside.submit(build_native, force)
+        if why:
+            print(f"{os.path.basename(NATIVE)} is not built: {why} (linear, rms_norm and their gradients will raise)", file=sys.stderr)
         if force or not up_to_date(lib):
             tmp = lib + f".tmp{os.getpid()}"
             subprocess.run(command(tmp, verbose_ptxas, debug), check=True)
             os.replace(tmp, lib)
-        native.result()
+        if native is not None:
+            native.result()
     return lib
 
 

@@ -39,7 +39,8 @@ def _native():
         try:
             from . import _native as module
         except ImportError as e:
-            raise GemmError(3, f"dense_gemm_gb300/_native.so ({e}): build it with `python -m dense_gemm_gb300.build`") from e
+            from .build import native_unbuildable
+            raise GemmError(3, f"dense_gemm_gb300/_native.so ({e}): {native_unbuildable() or 'build it with `python -m dense_gemm_gb300.build`'}") from e
         module.setup({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ENTRIES}, GemmError, RmsNormResult)
         _module = module
     return _module
