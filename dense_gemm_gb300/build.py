@@ -8,13 +8,15 @@ trapping. The binding loads it when GEMM_LIBRARY=debug.
 
 One translation unit, one -gencode, static CUDA runtime; no cmake. The same
 command works on x86-64 and aarch64 hosts. Beside it, the CPython extension
-_native.so (ops.py's argument marshalling, on PyTorch's C++ API) is built with
-the host compiler, at the same time. The library needs none of what that takes:
+_native (ops.py's argument marshalling, on PyTorch's C++ API) is built with the
+host compiler, at the same time. Its file's name carries the Python and PyTorch it
+was built for, so that another's is never loaded. The library needs none of what that takes:
 where this PyTorch has no CUDA parts, or there is no C++ compiler or no Python.h,
 the library is built without it and ops.py's calls raise.
 """
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -32,7 +34,6 @@ DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_f16.cu", "ops.cu", "g
                                                      "ops_linear.cuh", "ops_norm.cuh", "ptx.cuh")] + \
     [os.path.join(INCLUDE, f) for f in ("gemm_f16.h", "gemm_ops.h")]
 
-NATIVE = os.path.join(HERE, "_native.so")
 NATIVE_DEPENDS = [os.path.join(CSRC, "native.cpp")] + [os.path.join(INCLUDE, f) for f in ("gemm_f16.h", "gemm_ops.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -66,12 +67,19 @@ def torch_dir() -> str:
     return os.path.dirname(importlib.util.find_spec("torch").origin)
 
 
+def native_path() -> str:
+    """The extension's file for this Python and PyTorch, whose version is read, not imported."""
+    with open(os.path.join(torch_dir(), "version.py")) as f:
+        version = re.search(r"""__version__ = ['"]([^'"]+)['"]""", f.read()).group(1)
+    return os.path.join(HERE, f"_native.{sysconfig.get_config_var('SOABI')}-torch{version}.so")
+
+
 def cxx() -> str:
     return os.environ.get("CXX", "g++")
 
 
 def native_unbuildable() -> str:
-    """Why _native.so cannot be built on this machine; empty where it can."""
+    """Why the extension cannot be built on this machine; empty where it can."""
     if shutil.which(cxx()) is None:
         return f"no C++ compiler ({cxx()})"
     needed = [os.path.join(torch_dir(), "include", "c10", "cuda", "CUDAStream.h"), os.path.join(torch_dir(), "lib", "libc10_cuda.so"),
@@ -81,7 +89,7 @@ def native_unbuildable() -> str:
 
 
 def native_command(out: str):
-    """The host compiler's command for _native.so; found without importing torch
+    """The host compiler's command for the extension; found without importing torch
     (a slow import), which the extension's own process has loaded when it is used."""
     lib = os.path.join(torch_dir(), "lib")
     inc = [os.path.join(torch_dir(), "include"), os.path.join(torch_dir(), "include", "torch", "csrc", "api", "include"),
@@ -92,12 +100,13 @@ def native_command(out: str):
 
 
 def build_native(force: bool = False) -> str:
-    if not force and up_to_date(NATIVE, NATIVE_DEPENDS):
-        return NATIVE
-    tmp = NATIVE + f".tmp{os.getpid()}"
+    native = native_path()
+    if not force and up_to_date(native, NATIVE_DEPENDS):
+        return native
+    tmp = native + f".tmp{os.getpid()}"
     subprocess.run(native_command(tmp), check=True)
-    os.replace(tmp, NATIVE)
-    return NATIVE
+    os.replace(tmp, native)
+    return native
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
@@ -106,7 +115,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False)
         why = native_unbuildable()
         native = None if why else beside.submit(build_native, force)
         if why:
-            print(f"{os.path.basename(NATIVE)} is not built: {why} (linear, rms_norm and their gradients will raise)", file=sys.stderr)
+            print(f"{os.path.basename(native_path())} is not built: {why} (linear, rms_norm and their gradients will raise)", file=sys.stderr)
         if force or not up_to_date(lib):
             tmp = lib + f".tmp{os.getpid()}"
             subprocess.run(command(tmp, verbose_ptxas, debug), check=True)

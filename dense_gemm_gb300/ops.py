@@ -7,6 +7,8 @@ and workspaces that are not given are allocated on the stream the kernels run
 on (``stream``, or the current one).
 """
 import ctypes
+import importlib.util
+import os
 from typing import NamedTuple, Optional
 
 import torch
@@ -36,11 +38,13 @@ def _native():
     global _module
     if _module is None:
         lib = load_library()
-        try:
-            from . import _native as module
-        except ImportError as e:
-            from .build import native_unbuildable
-            raise GemmError(3, f"dense_gemm_gb300/_native.so ({e}): {native_unbuildable() or 'build it with `python -m dense_gemm_gb300.build`'}") from e
+        from .build import native_path, native_unbuildable
+        path = native_path()
+        if not os.path.exists(path):
+            raise GemmError(3, f"{path} is missing: {native_unbuildable() or 'build it with `python -m dense_gemm_gb300.build`'}")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._native", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
         module.setup({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ENTRIES}, GemmError, RmsNormResult)
         _module = module
     return _module

@@ -4,6 +4,7 @@ writes the output file; PyTorch's folder by one made for the test."""
 import importlib.util
 import os
 import subprocess
+import sysconfig
 from types import SimpleNamespace
 
 import pytest
@@ -25,7 +26,7 @@ def machine(tmp_path, monkeypatch):
                         lambda name, *a: SimpleNamespace(origin=str(torch / "__init__.py")) if name == "torch" else find(name, *a))
     monkeypatch.setattr(b, "HERE", str(tmp_path))
     monkeypatch.setattr(b, "LIB", str(tmp_path / "libgemm_f16.so"))
-    monkeypatch.setattr(b, "NATIVE", str(tmp_path / "_native.so"), raising=False)
+    monkeypatch.setattr(b, "NATIVE", str(tmp_path / "_native.so"), raising=False)  # a fixed name, where there is one
     monkeypatch.setattr(b, "nvcc", lambda: "/usr/local/cuda/bin/nvcc")
     monkeypatch.delenv("CXX", raising=False)
     commands = []
@@ -78,3 +79,32 @@ def test_an_error_in_the_extension_is_not_passed_over(machine, monkeypatch):
     with pytest.raises(subprocess.CalledProcessError):
         b.build()
     assert os.path.exists(b.LIB)
+
+
+def test_another_pytorch_gets_an_extension_of_its_own(machine, monkeypatch):
+    """The same sources and file times, another PyTorch or Python: what is there is
+    neither taken for up to date nor found by the operators."""
+    b.build()
+    (machine.torch / "version.py").write_text("__version__ = '9.10.0+cu130'\n")
+    b.build()
+    assert machine.commands.count("g++") == 2
+    config = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: "cpython-399-other" if name == "SOABI" else config(name))
+    b.build()
+    assert machine.commands.count("g++") == 3
+    b.build()
+    assert machine.commands.count("g++") == 3
+    assert len(list(machine.dir.glob("_native*.so"))) == 3
+
+
+def test_the_operators_name_what_is_missing(machine, monkeypatch):
+    import torch
+    from dense_gemm_gb300 import GemmError, ops
+    monkeypatch.setattr(ops, "_module", None)
+    monkeypatch.setattr(ops, "load_library", lambda: None)
+    x = torch.zeros(2, 8)
+    with pytest.raises(GemmError, match="_native.*build it with"):
+        ops.rms_norm(x, x[0])
+    (machine.torch / "lib/libc10_cuda.so").unlink()
+    with pytest.raises(GemmError, match="_native.*libc10_cuda.so is missing"):
+        ops.rms_norm(x, x[0])
