@@ -45,12 +45,18 @@ __device__ __forceinline__ void mma_f8_pair_elect(uint32_t d_tmem, uint64_t a_de
 
 // ------------------------------------------------------------------ activations
 // Exponentials are 2^(x log2 e) by ex2.approx (2 units in the last place, plus the
-// argument's rounding) and reciprocals rcp.approx (1): far inside the 16-bit
-// outputs' rounding and about 1e-6 for fp32 ones. Work is on pairs of values, one
+// argument's rounding) and reciprocals rcp.approx (1): silu and the tanh form of gelu
+// are relatively within (8 + 2 |x|) and (8 + 8 |z|) 2^-24, z the logistic's argument,
+// inside the 16-bit outputs' rounding. Work is on pairs of values, one
 // instruction per pair where there is one (fma2 and its like).
-// The normal distribution's cumulative function is Abramowitz & Stegun 26.2.17: for
+// The normal distribution's cumulative function Phi is Abramowitz & Stegun 26.2.17: for
 // x >= 0, 1 - Z(x) (b1 t + ... + b5 t^5) with t = 1 / (1 + 0.2316419 x) and Z the
-// density, off by less than 7.5e-8; the density is what gelu's slope needs too.
+// density, which gelu's slope needs too. It is off by less than 7.5e-8, absolutely, so
+// gelu by 7.5e-8 |x|. Relatively that grows in the negative tail, where Phi itself is
+// small: 5e-5 at x = -3 (gelu -0.004), 4.7e-4 at -4 (-1.3e-4), 1.6e-3 at -5 (-1.4e-6),
+// 3.6e-3 at -6 (-6e-9): from -5 on about half a unit of a bf16 value, more in fp16 or
+// fp32. (1 + erf(x / sqrt 2) in fp32 cancels there and is 0 from -5.5 on.) A logistic
+// below 2^-126 is 0.
 // D = G gelu'(P) of 4096 x 8192 takes 82 us with CUDA's erff and __expf, 57 with the
 // formula value by value, 36.5 in pairs with four rows loaded ahead.
 constexpr uint32_t kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4;  // GEMM_ACT_*
