@@ -18,9 +18,9 @@ namespace g16 {
 // A kernel of a call that needs nothing of the kernel right before it (late != 0)
 // does not wait for it before its work but before it ends. What it does read was
 // written by kernels that had completed before that one's own wait returned, and
-// so before this one could be scheduled; and whatever follows on the stream still
-// finds both complete. In gradients the second product's tiles so fill the SMs
-// that the first one's last round leaves idle.
+// so before this one could be scheduled; it comes from L2, by TMA or by loads that
+// pass L1. Whatever follows on the stream still finds both complete. In gradients the
+// second product's tiles so fill the SMs that the first one's last round leaves idle.
 __device__ __forceinline__ void griddep_enter(uint32_t late) {
     if (!late) griddep_wait();
     griddep_launch_dependents();
@@ -956,9 +956,11 @@ __global__ void __launch_bounds__(kRingThreads) rms_norm_backward_rows_any_kerne
     }
 }
 
-// Rows longer than the register form holds: dx with one block per row (two
-// passes over it, element by element), dweight's column sums by another kernel
-// (512 x 20000 bf16 with grad_h: 90.6 us for both; 512 x 16384 in the ring form 26.5).
+// Rows of which the ring's shared memory does not hold two slots, or of more than
+// 16384 elements: dx with one block per row (two passes over it, element by element),
+// dweight's column sums by another kernel before it. On 16-byte boundaries these are
+// 16-bit rows past 16384; fp32 rows from 4736 to 8192 elements, where two blocks share
+// an SM, and from 9560 on with grad_h, from 7104 to 8192 and from 14336 on without (512 x 20000 bf16 with grad_h: 90.6 us for both; 512 x 16384 in the ring form 26.5).
 template <typename T>
 __global__ void __launch_bounds__(1024) rms_norm_backward_long_kernel(const NormBackwardParams p) {
     __shared__ float red[32];

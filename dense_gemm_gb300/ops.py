@@ -5,6 +5,13 @@ The arguments are checked and marshalled by the extension ``_native`` (built
 with the library); the arithmetic runs in the library's CUDA kernels. Outputs
 and workspaces that are not given are allocated on the stream the kernels run
 on (``stream``, or the current one).
+
+The calls record no gradient: outputs do not require one whatever the inputs do,
+and ``linear_backward`` and ``rms_norm_backward`` are called by the caller's own
+``torch.autograd.Function`` (``examples/mlp_block.py`` has both). C, ``pre``,
+``residual``, ``grad`` and all matrices of the norms are stored by rows (unit
+column stride, any row stride); A and B by rows or by columns, 8-bit ones with K
+contiguous.
 """
 import ctypes
 import importlib.util
@@ -93,7 +100,9 @@ def linear_backward(grad: torch.Tensor, A: torch.Tensor, B: torch.Tensor, *, pre
     ``pre`` is what ``linear(..., return_pre=True)`` kept (needed with an
     activation). dA [M, K] and dB [K, N] have ``grad_dtype`` (default A's type)
     and the memory order of A and B; dbias [N] is float32. The residual's
-    gradient is ``grad`` itself.
+    gradient is ``grad`` itself. With an activation, D = grad * act'(pre) is
+    rounded to A's type for the two products, whatever ``grad_dtype`` is; dbias is
+    summed from D before that.
     """
     return (_module or _native()).linear_backward(
         grad, A, B, pre, _code(ACTIVATIONS, activation, "activation"), bool(need_a), bool(need_b), bool(need_bias), grad_dtype,
@@ -108,7 +117,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tensor = 
     x [rows, width] is float32, float16 or bfloat16; ``weight`` [width] has x's
     type or is float32. y has x's type, or with ``out_dtype=torch.float8_e4m3fn``
     holds 8-bit floats whose value is y * scale[:, None] (``scale`` fp32
-    [rows]): an A and scale_a for ``linear``. ``h`` (x's type) is made when a
+    [rows]): an A and scale_a for ``linear``; rows of zeros, and rows whose largest
+    |y| is below 7.7e-34, are zeros with scale 1. ``h`` (x's type) is made when a
     residual is given; ``h_out`` may be x or residual itself. ``return_rstd``
     keeps 1 / sqrt(mean(h^2) + eps) for ``rms_norm_backward``.
     """
