@@ -197,7 +197,8 @@ bool passed(int status, const char *what) {
     return false;
 }
 
-// The caller's workspace (any CUDA tensor) or one of `need` bytes.
+// The caller's workspace (any contiguous CUDA tensor: the bytes of one with strides, or
+// expanded, are not all its own) or one of `need` bytes.
 struct Workspace {
     at::Tensor made;
     void *data = nullptr;
@@ -215,6 +216,10 @@ struct Workspace {
         if (!read_tensor(given, &t, "workspace")) return false;
         if (t.device != device) {
             PyErr_SetString(PyExc_ValueError, "the workspace is on another device than the tensors");
+            return false;
+        }
+        if (!THPVariable_Unpack(given).is_contiguous()) {
+            PyErr_SetString(PyExc_ValueError, "the workspace must be a contiguous tensor");
             return false;
         }
         data = t.data;

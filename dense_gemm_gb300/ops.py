@@ -4,7 +4,8 @@ root-mean-square norm, and their gradients.
 The arguments are checked and marshalled by the extension ``_native`` (built
 with the library); the arithmetic runs in the library's CUDA kernels. Outputs
 and workspaces that are not given are allocated on the stream the kernels run
-on (``stream``, or the current one).
+on (``stream``, or the current one); a workspace that is given is a contiguous
+tensor of any type.
 
 The calls record no gradient: outputs do not require one whatever the inputs do,
 and ``linear_backward`` and ``rms_norm_backward`` are called by the caller's own
