@@ -1,6 +1,6 @@
 """GB300-native persistent FP16 GEMM (C[M,N] = A[M,K] @ B[K,N], FP32 accumulate)
-and the operators of a transformer block around it (``linear``, ``rms_norm`` and
-their gradients).
+and the operators of a transformer block around it (``linear``, ``rms_norm``,
+``layer_norm``, their gradients, and ``quantize_rows``).
 
 The compute path is the C-ABI library ``libgemm_f16.so`` built from ``csrc/``
 (hand-written CUDA for sm_103a). This package only marshals arguments to it;
@@ -15,5 +15,6 @@ from .binding import (  # noqa: F401
     gemm_splitk_noalloc, gemm_packed, packed_workspace_size,
 )
 from .ops import (  # noqa: F401
-    RmsNormResult, linear, linear_backward, linear_workspace_size, rms_norm, rms_norm_backward,
+    LayerNormResult, RmsNormResult, layer_norm, layer_norm_backward, linear, linear_backward, linear_workspace_size, quantize_rows,
+    rms_norm, rms_norm_backward,
 )

@@ -6,7 +6,7 @@
 bounds and alignment checks (GEMM_DEBUG) that report GEMM_ERR_CHECK instead of
 trapping. The binding loads it when GEMM_LIBRARY=debug.
 
-One translation unit, one -gencode, static CUDA runtime; no cmake. The same
+Two translation units, compiled side by side, one -gencode, static CUDA runtime; no cmake. The same
 command works on x86-64 and aarch64 hosts. Beside it, the CPython extension
 _native (ops.py's argument marshalling, on PyTorch's C++ API) is built with the
 host compiler, at the same time. Its file's name carries the Python and PyTorch it
@@ -29,9 +29,10 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgemm_f16.so")
 DEBUG_LIB = os.path.join(HERE, "libgemm_f16_debug.so")
-SOURCES = [os.path.join(CSRC, "library.cu")]
-DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_f16.cu", "ops.cu", "gemm_kernel.cuh", "gemm_pair.cuh",
-                                                     "ops_linear.cuh", "ops_norm.cuh", "ptx.cuh")] + \
+SOURCES = [os.path.join(CSRC, "library.cu"), os.path.join(CSRC, "ops_rows.cu")]
+DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_f16.cu", "ops.cu", "ops_block.cu", "gemm_kernel.cuh", "gemm_pair.cuh",
+                                                     "elements.cuh", "ops_eight.cuh", "ops_linear.cuh", "ops_norm.cuh", "ops_rows.h",
+                                                     "ptx.cuh")] + \
     [os.path.join(INCLUDE, f) for f in ("gemm_f16.h", "gemm_ops.h")]
 
 NATIVE_DEPENDS = [os.path.join(CSRC, "native.cpp")] + [os.path.join(INCLUDE, f) for f in ("gemm_f16.h", "gemm_ops.h")]
@@ -47,7 +48,7 @@ def nvcc() -> str:
 
 
 def command(out: str, verbose_ptxas: bool = False, debug: bool = False):
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH, "-t", str(len(SOURCES)), "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
            "-Xcompiler", "-Wall", "-I", INCLUDE, "-I", CSRC, "-o", out, *SOURCES]
     if verbose_ptxas:
         cmd.insert(1, "-Xptxas=-v")
@@ -115,7 +116,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False)
         why = native_unbuildable()
         native = None if why else beside.submit(build_native, force)
         if why:
-            print(f"{os.path.basename(native_path())} is not built: {why} (linear, rms_norm and their gradients will raise)", file=sys.stderr)
+            print(f"{os.path.basename(native_path())} is not built: {why} (the operators of ops.py will raise)", file=sys.stderr)
         if force or not up_to_date(lib):
             tmp = lib + f".tmp{os.getpid()}"
             subprocess.run(command(tmp, verbose_ptxas, debug), check=True)

@@ -28,26 +28,35 @@
 namespace {
 
 // ------------------------------------------------------------------ what setup() stores
-enum Entry { kLinear, kLinearSize, kBackward, kBackwardSize, kNorm, kNormBackward, kNormBackwardSize, kEntries };
+enum Entry {
+    kLinear, kLinearSize, kBackward, kBackwardSize, kNorm, kNormBackward, kNormBackwardSize,
+    kLayerNorm, kLayerNormBackward, kLayerNormBackwardSize, kQuantize, kSaved, kSavedSize, kEntries
+};
 const char *const kEntryNames[kEntries] = {"gemm_linear", "gemm_linear_workspace_size", "gemm_linear_backward",
                                            "gemm_linear_backward_workspace_size", "gemm_rms_norm",
-                                           "gemm_rms_norm_backward", "gemm_rms_norm_backward_workspace_size"};
+                                           "gemm_rms_norm_backward", "gemm_rms_norm_backward_workspace_size",
+                                           "gemm_layer_norm", "gemm_layer_norm_backward",
+                                           "gemm_layer_norm_backward_workspace_size", "gemm_quantize_rows",
+                                           "gemm_saved_backward", "gemm_saved_backward_workspace_size"};
 void *g_entry[kEntries];
 
 template <typename F>
 F *entry(Entry e, F *) { return reinterpret_cast<F *>(g_entry[e]); }
 #define CALL(e, fn) (entry(e, &fn))
 
-PyObject *g_error, *g_norm_result;  // GemmError, RmsNormResult (owned)
+PyObject *g_error, *g_norm_result, *g_layer_norm_result;  // GemmError, RmsNormResult, LayerNormResult (owned)
 
-const char *const kTypeNames[4] = {"float32", "float16", "bfloat16", "float8_e4m3fn"};
-const at::ScalarType kTypes[4] = {at::kFloat, at::kHalf, at::kBFloat16, at::kFloat8_e4m3fn};
+constexpr int kTypeCount = 5;
+const char *const kTypeNames[kTypeCount] = {"float32", "float16", "bfloat16", "float8_e4m3fn", "int8"};
+const at::ScalarType kTypes[kTypeCount] = {at::kFloat, at::kHalf, at::kBFloat16, at::kFloat8_e4m3fn, at::kChar};
 
 int type_code(at::ScalarType t) {
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kTypeCount; ++i)
         if (t == kTypes[i]) return i;
     return -1;
 }
+
+bool is_eight(int type) { return type == GEMM_TYPE_E4M3 || type == GEMM_TYPE_I8; }
 
 // ------------------------------------------------------------------ tensors
 struct Tensor {
@@ -236,7 +245,7 @@ bool arguments(Py_ssize_t got, Py_ssize_t want) {
 
 bool operands(const Tensor &A, const Tensor &B) {
     if (!A || !B || A.type < GEMM_TYPE_F16 || A.type != B.type) {
-        PyErr_SetString(PyExc_TypeError, "A and B must both be float16, bfloat16 or float8_e4m3fn");
+        PyErr_SetString(PyExc_TypeError, "A and B must both be float16, bfloat16, float8_e4m3fn or int8");
         return false;
     }
     if (A.dims != 2 || B.dims != 2 || A.n[1] != B.n[0]) {
@@ -246,7 +255,7 @@ bool operands(const Tensor &A, const Tensor &B) {
     return true;
 }
 
-// The type code of a torch.dtype argument; None: `otherwise`. -1: not one of the four.
+// The type code of a torch.dtype argument; None: `otherwise`. -1: not one of the five.
 int dtype_code(PyObject *o, int otherwise) {
     if (o == Py_None) return otherwise;
     return THPDtype_Check(o) ? type_code(reinterpret_cast<const THPDtype *>(o)->scalar_type) : -1;
@@ -292,9 +301,9 @@ PyObject *py_linear(PyObject *, PyObject *const *a, Py_ssize_t n) {
         !read_tensor(a[7], &out, "out") || !read_tensor(a[9], &pre, "pre"))
         return nullptr;
     const int64_t M = A.n[0], K = A.n[1], N = B.n[1];
-    const bool eight = A.type == GEMM_TYPE_E4M3;
+    const bool eight = is_eight(A.type);
     if (eight != bool(sa) || eight != bool(sb)) {
-        PyErr_SetString(PyExc_ValueError, "scale_a and scale_b go with float8_e4m3fn operands, and only with them");
+        PyErr_SetString(PyExc_ValueError, "scale_a and scale_b go with float8_e4m3fn and int8 operands, and only with them");
         return nullptr;
     }
     const int type = out ? out.type : dtype_code(a[8], res ? res.type : eight ? GEMM_TYPE_BF16 : A.type);
@@ -337,8 +346,8 @@ PyObject *py_linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!read_tensor(a[0], &G, "grad") || !read_tensor(a[1], &A, "A") || !read_tensor(a[2], &B, "B") || !operands(A, B) ||
         !read_tensor(a[3], &pre, "pre"))
         return nullptr;
-    if (A.type == GEMM_TYPE_E4M3 || !G) {
-        PyErr_SetString(PyExc_TypeError, "linear_backward takes a gradient and float16 or bfloat16 operands");
+    if (is_eight(A.type) || !G) {
+        PyErr_SetString(PyExc_TypeError, "linear_backward takes a gradient and float16 or bfloat16 operands (8-bit ones with scale_a)");
         return nullptr;
     }
     const int64_t M = A.n[0], K = A.n[1], N = B.n[1];
@@ -372,6 +381,197 @@ PyObject *py_linear_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
                 kEntryNames[kBackward]))
         return nullptr;
     return tuple_of({da.give(), db.give(), dbias.give()});
+    END_HANDLE_TH_ERRORS
+}
+
+// Values kept in 8 bits, with a scale for each row.
+bool is_kept(const Tensor &t, const Tensor &scale, int64_t rows, const char *what) {
+    if (is_eight(t.type) == bool(scale)) return is_vector(scale, rows, GEMM_TYPE_F32, GEMM_TYPE_F32, what);
+    PyErr_Format(PyExc_ValueError, "%s goes with float8_e4m3fn or int8 values, and only with them", what);
+    return false;
+}
+
+// (grad, A, scale_a, activation_a, B, pre, scale_pre, activation, need_a, need_b, need_bias, grad_dtype, flags, workspace, stream)
+PyObject *py_saved_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 15)) return nullptr;
+    Tensor G, A, sa, B, pre, sp;
+    if (!read_tensor(a[0], &G, "grad") || !read_tensor(a[1], &A, "A") || !read_tensor(a[2], &sa, "scale_a") ||
+        !read_tensor(a[4], &B, "B") || !read_tensor(a[5], &pre, "pre") || !read_tensor(a[6], &sp, "scale_pre"))
+        return nullptr;
+    if (!G || !A || !B || (B.type != GEMM_TYPE_F16 && B.type != GEMM_TYPE_BF16) || (A.type != B.type && !is_eight(A.type))) {
+        PyErr_SetString(PyExc_TypeError,
+                        "linear_backward takes a gradient, a float16 or bfloat16 B, and an A of B's type, float8_e4m3fn or int8");
+        return nullptr;
+    }
+    if (A.dims != 2 || B.dims != 2 || A.n[1] != B.n[0]) {
+        PyErr_SetString(PyExc_ValueError, "A and B must be matrices whose shapes chain ([M, K] and [K, N])");
+        return nullptr;
+    }
+    const int64_t M = A.n[0], K = A.n[1], N = B.n[1];
+    const int32_t act_a = int32_t(PyLong_AsLong(a[3])), act = int32_t(PyLong_AsLong(a[7]));
+    if (act != GEMM_ACT_NONE && !pre) {
+        PyErr_SetString(PyExc_ValueError, "with an activation, linear_backward needs pre (linear(..., return_pre=True), or kept in 8 bits)");
+        return nullptr;
+    }
+    if (act_a != GEMM_ACT_NONE && !sa) {
+        PyErr_SetString(PyExc_ValueError, "activation_a goes with an A kept in 8 bits (scale_a)");
+        return nullptr;
+    }
+    if (!is_kept(A, sa, M, "scale_a") || !is_kept(pre, sp, M, "scale_pre")) return nullptr;
+    if (act == GEMM_ACT_NONE) pre = sp = Tensor();
+    const int type = dtype_code(a[11], B.type);
+    if (!is_c_type(type, "gradients") || !same_device(A, {&B, &G, &pre, &sa, &sp}) || !is_matrix(G, M, N, B.type, "grad") ||
+        !is_matrix(pre, M, N, sp ? pre.type : B.type, "pre"))
+        return nullptr;
+    const bool need_a = a[8] == Py_True, need_b = a[9] == Py_True, need_bias = a[10] == Py_True;
+    const gemm_matrix_t mg = matrix(G), ma = matrix(A), mb = matrix(B), mp = matrix(pre);
+    uint64_t need = 0;
+    if (!passed(CALL(kSavedSize, gemm_saved_backward_workspace_size)(&mg, &ma, &mb, act, need_bias, M, N, K, &need), kEntryNames[kSaved]))
+        return nullptr;
+    Place place;
+    Workspace ws;
+    if (!place.enter(A.device, a[14]) || !ws.set(a[13], need, A.device, place)) return nullptr;
+    Output da, db, dbias;
+    // gradients are stored as their operands are: by columns where those are
+    auto turned = [](const Tensor &t) { return t.s[0] == 1 && t.s[1] != 1 && t.n[0] > 1 && t.n[1] > 1; };
+    if (need_a) da.set(Tensor(), M, K, type, turned(A), place);
+    if (need_b) db.set(Tensor(), K, N, type, turned(B), place);
+    if (need_bias) dbias.set_vector(N, place);
+    if (!passed(CALL(kSaved, gemm_saved_backward)(&mg, &ma, static_cast<const float *>(sa.data), act_a, &mb, &mp,
+                                                  static_cast<const float *>(sp.data), act, &da.m, &db.m, dbias.floats(), M, N, K,
+                                                  uint32_t(PyLong_AsLong(a[12])), ws.data, ws.bytes, place.stream),
+                kEntryNames[kSaved]))
+        return nullptr;
+    return tuple_of({da.give(), db.give(), dbias.give()});
+    END_HANDLE_TH_ERRORS
+}
+
+// A named tuple's type filled from new references (each taken, also on failure), as its _make.
+PyObject *named_tuple(PyObject *type, std::initializer_list<PyObject *> items) {
+    PyObject *t = tuple_of(items);
+    if (t == nullptr) return nullptr;
+    PyObject *args = tuple_of({t});
+    if (args == nullptr) return nullptr;
+    PyObject *result = PyTuple_Type.tp_new(reinterpret_cast<PyTypeObject *>(type), args, nullptr);
+    Py_DECREF(args);
+    return result;
+}
+
+// (x, weight, bias, residual, eps, out_dtype, return_stats, out, h_out, stream) -> LayerNormResult
+PyObject *py_layer_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 10)) return nullptr;
+    Tensor x, w, b, r, out, h;
+    if (!read_tensor(a[0], &x, "x") || !read_tensor(a[1], &w, "weight") || !read_tensor(a[2], &b, "bias") ||
+        !read_tensor(a[3], &r, "residual") || !read_tensor(a[7], &out, "out") || !read_tensor(a[8], &h, "h_out"))
+        return nullptr;
+    if (!x || !w || x.dims != 2 || x.type < GEMM_TYPE_F32 || x.type > GEMM_TYPE_BF16) {
+        PyErr_SetString(PyExc_TypeError, "x must be a float32, float16 or bfloat16 matrix, weight a vector");
+        return nullptr;
+    }
+    const int64_t rows = x.n[0], width = x.n[1];
+    const int type = out ? out.type : dtype_code(a[5], x.type);
+    if (type != x.type && !is_eight(type)) {
+        PyErr_SetString(PyExc_TypeError, "y has x's type, float8_e4m3fn or int8");
+        return nullptr;
+    }
+    const double eps = PyFloat_AsDouble(a[4]);
+    if (eps == -1.0 && PyErr_Occurred()) return nullptr;
+    if (h && !r) {
+        PyErr_SetString(PyExc_ValueError, "h_out goes with a residual: without one h is x");
+        return nullptr;
+    }
+    if (!same_device(x, {&w, &b, &r, &out, &h}) || !is_vector(w, width, GEMM_TYPE_F32, x.type, "weight") ||
+        !is_vector(b, width, w.type, w.type, "bias") || !is_matrix(r, rows, width, x.type, "residual") ||
+        !is_matrix(out, rows, width, type, "out") || !is_matrix(h, rows, width, x.type, "h_out"))
+        return nullptr;
+    Place place;
+    if (!place.enter(x.device, a[9])) return nullptr;
+    Output y, sum, scale, mean, rstd;
+    y.set(out, rows, width, type, false, place);
+    if (r) sum.set(h, rows, width, x.type, false, place);
+    if (is_eight(type)) scale.set_vector(rows, place);
+    if (a[6] == Py_True) {
+        mean.set_vector(rows, place);
+        rstd.set_vector(rows, place);
+    }
+    const gemm_matrix_t mx = matrix(x), mr = matrix(r);
+    if (!passed(CALL(kLayerNorm, gemm_layer_norm)(&mx, &mr, w.data, b.data, w.type, &y.m, &sum.m, scale.floats(), mean.floats(),
+                                                  rstd.floats(), rows, width, float(eps), place.stream),
+                kEntryNames[kLayerNorm]))
+        return nullptr;
+    return named_tuple(g_layer_norm_result, {y.give(), sum.give(), scale.give(), mean.give(), rstd.give()});
+    END_HANDLE_TH_ERRORS
+}
+
+// (grad, h, weight, mean, rstd, grad_h, need_weight, need_bias, out, workspace, stream) -> (dx, dweight, dbias)
+PyObject *py_layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 11)) return nullptr;
+    Tensor g, h, w, mean, rstd, gh, out;
+    if (!read_tensor(a[0], &g, "grad") || !read_tensor(a[1], &h, "h") || !read_tensor(a[2], &w, "weight") ||
+        !read_tensor(a[3], &mean, "mean") || !read_tensor(a[4], &rstd, "rstd") || !read_tensor(a[5], &gh, "grad_h") ||
+        !read_tensor(a[8], &out, "out"))
+        return nullptr;
+    if (!h || !g || !w || !mean || !rstd || h.dims != 2 || h.type < GEMM_TYPE_F32 || h.type > GEMM_TYPE_BF16) {
+        PyErr_SetString(PyExc_TypeError, "h must be a float32, float16 or bfloat16 matrix; grad, weight, mean and rstd are needed");
+        return nullptr;
+    }
+    const int64_t rows = h.n[0], width = h.n[1];
+    if (!same_device(h, {&g, &w, &mean, &rstd, &gh, &out}) || !is_matrix(g, rows, width, h.type, "grad") ||
+        !is_matrix(gh, rows, width, h.type, "grad_h") || !is_matrix(out, rows, width, h.type, "out") ||
+        !is_vector(w, width, GEMM_TYPE_F32, h.type, "weight") || !is_vector(mean, rows, GEMM_TYPE_F32, GEMM_TYPE_F32, "mean") ||
+        !is_vector(rstd, rows, GEMM_TYPE_F32, GEMM_TYPE_F32, "rstd"))
+        return nullptr;
+    const bool need_weight = a[6] == Py_True, need_bias = a[7] == Py_True;
+    uint64_t need = 0;
+    if ((need_weight || need_bias) &&
+        !passed(CALL(kLayerNormBackwardSize, gemm_layer_norm_backward_workspace_size)(rows, width, &need), kEntryNames[kLayerNormBackward]))
+        return nullptr;
+    Place place;
+    Workspace ws;
+    if (!place.enter(h.device, a[10]) || !ws.set(a[9], need, h.device, place)) return nullptr;
+    Output dx, dw, db;
+    dx.set(out, rows, width, h.type, false, place);
+    if (need_weight) dw.set_vector(width, place);
+    if (need_bias) db.set_vector(width, place);
+    const gemm_matrix_t mg = matrix(g), mh = matrix(h), mgh = matrix(gh);
+    if (!passed(CALL(kLayerNormBackward, gemm_layer_norm_backward)(&mg, &mh, w.data, w.type, static_cast<const float *>(mean.data),
+                                                                   static_cast<const float *>(rstd.data), &mgh, &dx.m, dw.floats(),
+                                                                   db.floats(), rows, width, ws.data, ws.bytes, place.stream),
+                kEntryNames[kLayerNormBackward]))
+        return nullptr;
+    return tuple_of({dx.give(), dw.give(), db.give()});
+    END_HANDLE_TH_ERRORS
+}
+
+// (x, dtype, out, stream) -> (values, scale)
+PyObject *py_quantize_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments(n, 4)) return nullptr;
+    Tensor x, out;
+    if (!read_tensor(a[0], &x, "x") || !read_tensor(a[2], &out, "out")) return nullptr;
+    if (!x || x.dims != 2 || x.type < GEMM_TYPE_F32 || x.type > GEMM_TYPE_BF16) {
+        PyErr_SetString(PyExc_TypeError, "x must be a float32, float16 or bfloat16 matrix");
+        return nullptr;
+    }
+    const int64_t rows = x.n[0], width = x.n[1];
+    const int type = out ? out.type : dtype_code(a[1], GEMM_TYPE_E4M3);
+    if (!is_eight(type)) {
+        PyErr_SetString(PyExc_TypeError, "rows are quantized to float8_e4m3fn or int8");
+        return nullptr;
+    }
+    if (!same_device(x, {&out}) || !is_matrix(out, rows, width, type, "out")) return nullptr;
+    Place place;
+    if (!place.enter(x.device, a[3])) return nullptr;
+    Output q, scale;
+    q.set(out, rows, width, type, false, place);
+    scale.set_vector(rows, place);
+    const gemm_matrix_t mx = matrix(x);
+    if (!passed(CALL(kQuantize, gemm_quantize_rows)(&mx, &q.m, scale.floats(), rows, width, place.stream), kEntryNames[kQuantize]))
+        return nullptr;
+    return tuple_of({q.give(), scale.give()});
     END_HANDLE_TH_ERRORS
 }
 
@@ -415,13 +615,7 @@ PyObject *py_rms_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                            float(eps), place.stream),
                 kEntryNames[kNorm]))
         return nullptr;
-    PyObject *t = tuple_of({y.give(), sum.give(), scale.give(), rstd.give()});
-    if (t == nullptr) return nullptr;
-    PyObject *args = tuple_of({t});
-    if (args == nullptr) return nullptr;
-    PyObject *result = PyTuple_Type.tp_new(reinterpret_cast<PyTypeObject *>(g_norm_result), args, nullptr);  // as its _make
-    Py_DECREF(args);
-    return result;
+    return named_tuple(g_norm_result, {y.give(), sum.give(), scale.give(), rstd.give()});
     END_HANDLE_TH_ERRORS
 }
 
@@ -462,10 +656,10 @@ PyObject *py_rms_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// setup({entry name: address}, GemmError, RmsNormResult)
+// setup({entry name: address}, GemmError, RmsNormResult, LayerNormResult)
 PyObject *py_setup(PyObject *, PyObject *args) {
-    PyObject *entries, *error, *norm_result;
-    if (!PyArg_ParseTuple(args, "O!OO", &PyDict_Type, &entries, &error, &norm_result)) return nullptr;
+    PyObject *entries, *error, *norm_result, *layer_norm_result;
+    if (!PyArg_ParseTuple(args, "O!OOO", &PyDict_Type, &entries, &error, &norm_result, &layer_norm_result)) return nullptr;
     for (int i = 0; i < kEntries; ++i) {
         PyObject *p = PyDict_GetItemString(entries, kEntryNames[i]);
         if (p == nullptr) {
@@ -477,6 +671,7 @@ PyObject *py_setup(PyObject *, PyObject *args) {
     }
     Py_XSETREF(g_error, Py_NewRef(error));
     Py_XSETREF(g_norm_result, Py_NewRef(norm_result));
+    Py_XSETREF(g_layer_norm_result, Py_NewRef(layer_norm_result));
     Py_RETURN_NONE;
 }
 
@@ -490,6 +685,10 @@ PyMethodDef kMethods[] = {
     {"linear_backward", as_function(&py_linear_backward), METH_FASTCALL, nullptr},
     {"rms_norm", as_function(&py_rms_norm), METH_FASTCALL, nullptr},
     {"rms_norm_backward", as_function(&py_rms_norm_backward), METH_FASTCALL, nullptr},
+    {"layer_norm", as_function(&py_layer_norm), METH_FASTCALL, nullptr},
+    {"layer_norm_backward", as_function(&py_layer_norm_backward), METH_FASTCALL, nullptr},
+    {"quantize_rows", as_function(&py_quantize_rows), METH_FASTCALL, nullptr},
+    {"saved_backward", as_function(&py_saved_backward), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", "Argument marshalling of ops.py.", -1, kMethods, nullptr, nullptr,

@@ -3,13 +3,15 @@
 // Compiled in one translation unit with gemm_f16.cu (library.cu), whose device
 // set-up, tensor-map, launch and status helpers it uses.
 #include "gemm_ops.h"
+#include "ops_eight.cuh"
 #include "ops_linear.cuh"
 #include "ops_norm.cuh"
 
 namespace {
 
 bool is_c_type(int32_t t) { return t >= GEMM_TYPE_F32 && t <= GEMM_TYPE_BF16; }
-int type_bytes(int32_t t) { return t == GEMM_TYPE_F32 ? 4 : t == GEMM_TYPE_E4M3 ? 1 : 2; }
+bool is_eight(int32_t t) { return t == GEMM_TYPE_E4M3 || t == GEMM_TYPE_I8; }
+int type_bytes(int32_t t) { return t == GEMM_TYPE_F32 ? 4 : is_eight(t) ? 1 : 2; }
 bool present(const gemm_matrix_t *m) { return m != nullptr && m->data != nullptr; }
 bool element_aligned(const void *p, int32_t type) { return (reinterpret_cast<uintptr_t>(p) & uintptr_t(type_bytes(type) - 1)) == 0; }
 uint64_t round128(uint64_t x) { return (x + 127u) / 128u * 128u; }
@@ -88,7 +90,10 @@ const OpsState *ops_init(int dev, int num_sms) {
     if (e == cudaSuccess) e = allow_smem(linear_pair<false, 4>, lin::PAIR_SMEM);
     if (e == cudaSuccess) e = allow_smem(linear_pair<true, 2>, lin::PAIR_SMEM);
     if (e == cudaSuccess) e = allow_smem(linear_pair<true, 4>, lin::PAIR_SMEM);
+    if (e == cudaSuccess) e = allow_smem(linear_pair<false, 2, true>, lin::PAIR_SMEM);
+    if (e == cudaSuccess) e = allow_smem(linear_pair<false, 4, true>, lin::PAIR_SMEM);
     if (e == cudaSuccess) e = allow_smem(linear_split<false>, 232448);
+    if (e == cudaSuccess) e = allow_smem(linear_split<false, true>, 232448);
     if (e == cudaSuccess) e = allow_smem(linear_split<true>, 232448);
     for (int t = 0; e == cudaSuccess && t < kSplitTs; ++t) {
         const int T = 16 << t;
@@ -146,12 +151,12 @@ gemm_status_t classify(const void *data, int32_t type, int64_t outer, int64_t K,
     if (stride_k == 1 || K == 1) {
         *op = Operand{data, outer, K, stride_outer, type, false};
     } else if (stride_outer == 1 || outer == 1) {
-        if (type == GEMM_TYPE_E4M3) return GEMM_ERR_UNSUPPORTED;
+        if (is_eight(type)) return GEMM_ERR_UNSUPPORTED;
         *op = Operand{data, K, outer, stride_k, type, true};
     } else {
         return GEMM_ERR_UNSUPPORTED;
     }
-    if (K == 1 && stride_outer == 1 && type != GEMM_TYPE_E4M3) *op = Operand{data, 1, outer, stride_k, type, true};
+    if (K == 1 && stride_outer == 1 && !is_eight(type)) *op = Operand{data, 1, outer, stride_k, type, true};
     if (op->rows == 1) op->ld = op->copy_ld();
     return GEMM_OK;
 }
@@ -204,6 +209,46 @@ cudaError_t pack_operands(Operand *a, void *dst_a, Operand *b, void *dst_b, int 
     }
     return e;
 }
+
+// A job of expand_rows_kernel: an 8-bit operand's rows to 16-bit ones at dst (nullptr:
+// none). Blocks of 256 granules of rows that long, else of as many rows; enough blocks for
+// each thread to visit some eight rows, up to 16 blocks on an SM.
+ExpandJob expand_job(const Operand &o, void *dst, const float *scale, uint32_t act, int num_sms) {
+    ExpandJob j;
+    std::memset(&j, 0, sizeof(j));
+    if (dst == nullptr || o.rows == 0 || o.inner == 0) return j;
+    j.src = static_cast<const uint8_t *>(o.data);
+    j.dst = dst;
+    j.scale = scale;
+    j.rows = o.rows;
+    j.inner = o.inner;
+    j.ld_src = o.ld;
+    j.ld_dst = (o.inner + 63) / 64 * 64;
+    j.type = uint32_t(o.type);
+    j.act = act;
+    const int64_t granules = cdiv(o.inner, 8);
+    while (j.lg < 8 && (int64_t(1) << j.lg) < granules) ++j.lg;
+    j.bx = int32_t(cdiv(granules, int64_t(1) << j.lg));
+    j.by = int32_t(std::max<int64_t>(1, std::min<int64_t>(cdiv(o.rows, int64_t(256 >> j.lg) * 8), 16 * int64_t(num_sms) / j.bx)));
+    return j;
+}
+
+// Up to two 8-bit operands' rows in 16 bits of `type` at dst_a / dst_b; points them there.
+// Whole numbers of a product (kPlain) go to fp16, kept values to G's type.
+template <typename T, bool kPlain>
+cudaError_t expand_operands(Operand *a, ExpandJob ja, Operand *b, ExpandJob jb, int32_t type, cudaStream_t stream) {
+    for (Operand *o : {a, b}) {
+        const ExpandJob &j = o == a ? ja : jb;
+        if (o == nullptr || j.dst == nullptr) continue;
+        o->data = j.dst;
+        o->ld = j.ld_dst;
+        o->type = type;
+    }
+    const int blocks = ja.bx * ja.by + jb.bx * jb.by;
+    if (blocks == 0) return cudaSuccess;
+    return launch_overlapped(expand_rows_kernel<T, kPlain>, blocks, 256, 0, stream, ja, jb);
+}
+uint64_t expanded_bytes(const Operand &o) { return uint64_t(o.rows) * uint64_t((o.inner + 63) / 64 * 64) * 2u; }
 
 // The tensor map of an operand for stages of `kbs` k-blocks of 128 bytes and `mn`
 // rows (or columns) per CTA, and how a stage is fetched through it (OperandLoad).
@@ -354,7 +399,7 @@ constexpr int kOneBufferKb = 32;
 gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t N, int64_t K, const EpilogueParams &e,
                          uint32_t flags, const DeviceState *ds, const OpsState *ops, cudaStream_t stream,
                          Order order = Order::kAlone) {
-    const bool f8 = A.type == GEMM_TYPE_E4M3;
+    const bool f8 = A.type == GEMM_TYPE_E4M3, scaled = e.sa != nullptr;
     const int es = e.type == 0 ? 4 : 2;
     LinearParams p;
     std::memset(&p, 0, sizeof(p));
@@ -396,8 +441,9 @@ gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t 
         p.bufs = e.pre != nullptr || (e.r != nullptr && p.num_kb < kOneBufferKb) ? 2 : 1;
         p.stages = p.bufs == 2 ? 5 : 6;
         const dim3 grid(unsigned(2 * std::min<int64_t>(p.num_units, ds->max_pairs)));
-        auto *kernel = f8 ? (es == 4 ? linear_pair<true, 4> : linear_pair<true, 2>)
-                          : (es == 4 ? linear_pair<false, 4> : linear_pair<false, 2>);
+        auto *kernel = f8       ? (es == 4 ? linear_pair<true, 4> : linear_pair<true, 2>)
+                       : scaled ? (es == 4 ? linear_pair<false, 4, true> : linear_pair<false, 2, true>)
+                                : (es == 4 ? linear_pair<false, 4> : linear_pair<false, 2>);
         err = launch_shape(kernel, grid, dim3(lin::PAIR_THREADS), lin::PAIR_SMEM, 1, stream, tmA, tmB, tmBhalf, tmC, tmR,
                            tmP, p);
     } else {
@@ -417,7 +463,8 @@ gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t 
         p.e.vec4 = quad_aligned(e.c, e.ldc, es) && (e.pre == nullptr || quad_aligned(e.pre, e.ldp, es)) &&
                    (e.r == nullptr || quad_aligned(e.r, e.ldr, es));
         const dim3 grid(unsigned(int64_t(p.num_units) * pl.split));
-        err = launch_shape(f8 ? linear_split<true> : linear_split<false>, grid, dim3(lin::SPLIT_THREADS),
+        auto *kernel = f8 ? linear_split<true> : scaled ? linear_split<false, true> : linear_split<false>;
+        err = launch_shape(kernel, grid, dim3(lin::SPLIT_THREADS),
                            lin::split_smem(pl.stages, pl.T), pl.split, stream, tmB, tmA, p);
     }
     if (log_enabled())
@@ -427,8 +474,14 @@ gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t 
     return err == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
-// Workspace of two operands' copies: [A's][B's], each from a 256-byte boundary.
+// Workspace of two operands' copies: [A's][B's], each from a 256-byte boundary. Whole
+// numbers are copied to fp16.
 void copies_needed(const Operand &A, const Operand &B, uint64_t *a_bytes, uint64_t *b_bytes) {
+    if (A.type == GEMM_TYPE_I8) {
+        *a_bytes = round256(expanded_bytes(A));
+        *b_bytes = round256(expanded_bytes(B));
+        return;
+    }
     *a_bytes = A.tma() ? 0u : round256(A.copy_bytes());
     *b_bytes = B.tma() ? 0u : round256(B.copy_bytes());
 }
@@ -436,7 +489,7 @@ void copies_needed(const Operand &A, const Operand &B, uint64_t *a_bytes, uint64
 gemm_status_t check_operands(const gemm_matrix_t *A, const gemm_matrix_t *B, int64_t M, int64_t N, int64_t K, Operand *a,
                              Operand *b) {
     if (A == nullptr || B == nullptr) return GEMM_ERR_INVALID_ARG;
-    if (A->type != B->type || A->type < GEMM_TYPE_F16 || A->type > GEMM_TYPE_E4M3) return GEMM_ERR_INVALID_ARG;
+    if (A->type != B->type || A->type < GEMM_TYPE_F16 || A->type > GEMM_TYPE_I8) return GEMM_ERR_INVALID_ARG;
     gemm_status_t st = classify(A->data, A->type, M, K, A->stride_row, A->stride_col, a);
     if (st == GEMM_OK) st = classify(B->data, B->type, N, K, B->stride_col, B->stride_row, b);
     return st;
@@ -480,12 +533,11 @@ gemm_status_t gemm_linear(const gemm_matrix_t *A, const gemm_matrix_t *B, const 
     if (ep->bias != nullptr && ((ep->bias_type != GEMM_TYPE_F32 && ep->bias_type != C->type) ||
                                 !element_aligned(ep->bias, ep->bias_type)))
         return GEMM_ERR_INVALID_ARG;
-    const bool f8 = A->type == GEMM_TYPE_E4M3;
-    if ((ep->scale_a == nullptr) != (ep->scale_b == nullptr)) return GEMM_ERR_INVALID_ARG;
-    if (f8 != (ep->scale_a != nullptr)) return GEMM_ERR_INVALID_ARG;
     if (((reinterpret_cast<uintptr_t>(ep->scale_a) | reinterpret_cast<uintptr_t>(ep->scale_b)) & 3u))
         return GEMM_ERR_INVALID_ARG;
-    if (M == 0 || N == 0) return GEMM_OK;
+    if (M == 0 || N == 0) return GEMM_OK;  // (an empty vector of scales may have no address)
+    if ((ep->scale_a == nullptr) != (ep->scale_b == nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (is_eight(A->type) != (ep->scale_a != nullptr)) return GEMM_ERR_INVALID_ARG;
     if (C->data == nullptr || (K > 0 && (A->data == nullptr || B->data == nullptr))) return GEMM_ERR_INVALID_ARG;
     for (const gemm_matrix_t *m : {C, &ep->residual, &ep->pre}) {
         if (m->data == nullptr) continue;
@@ -530,7 +582,10 @@ gemm_status_t gemm_linear(const gemm_matrix_t *A, const gemm_matrix_t *B, const 
                    : GEMM_ERR_CUDA;
     }
     unsigned char *ws = static_cast<unsigned char *>(workspace);
-    if (na + nb > 0 && pack_operands(&a, na ? ws : nullptr, &b, nb ? ws + na : nullptr, ds->num_sms, stream) != cudaSuccess)
+    if (a.type == GEMM_TYPE_I8) {
+        const ExpandJob ja = expand_job(a, ws, nullptr, 0, ds->num_sms), jb = expand_job(b, ws + na, nullptr, 0, ds->num_sms);
+        if (expand_operands<__half, true>(&a, ja, &b, jb, GEMM_TYPE_F16, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+    } else if (na + nb > 0 && pack_operands(&a, na ? ws : nullptr, &b, nb ? ws + na : nullptr, ds->num_sms, stream) != cudaSuccess)
         return GEMM_ERR_CUDA;
     return run_linear(a, b, M, N, K, e, flags, ds, ops, stream);
 }
@@ -555,6 +610,14 @@ GradPlan plan_grad(int64_t M, int64_t N) {
     return g;
 }
 
+// Values kept in 8 bits for the backward pass: A's rows are act(scale_a A), pre's scale_pre
+// pre, each where its type has 8 bits.
+struct Saved {
+    bool allowed;
+    const float *scale_a, *scale_pre;
+    int32_t act_a;
+};
+
 struct BackwardSpace {
     uint64_t d, partial, a, b, total;
     int64_t ldd;
@@ -574,7 +637,12 @@ gemm_status_t backward_space(const gemm_matrix_t *G, const Operand &a, const Ope
         const GradPlan g = plan_grad(M, N);
         if (g.parts > 1) s->partial = round256(uint64_t(g.parts) * uint64_t(N) * 4u);
     }
-    if (K > 0) copies_needed(a, b, &s->a, &s->b);
+    if (K > 0 && is_eight(a.type)) {
+        s->a = round256(expanded_bytes(a));
+        s->b = b.tma() ? 0u : round256(b.copy_bytes());
+    } else if (K > 0) {
+        copies_needed(a, b, &s->a, &s->b);
+    }
     s->total = s->d + s->partial + s->a + s->b;
     return GEMM_OK;
 }
@@ -584,9 +652,21 @@ gemm_status_t check_backward(const gemm_matrix_t *G, const gemm_matrix_t *A, con
     if (!sizes_ok(M, N, K) || G == nullptr) return GEMM_ERR_INVALID_ARG;
     gemm_status_t st = check_operands(A, B, M, N, K, a, b);
     if (st != GEMM_OK) return st;
-    if (A->type == GEMM_TYPE_E4M3) return GEMM_ERR_UNSUPPORTED;
+    if (is_eight(A->type)) return GEMM_ERR_UNSUPPORTED;
     if (G->type != A->type) return GEMM_ERR_INVALID_ARG;
     return check_rows(G, M, N);
+}
+
+// The same with A kept in 8 bits.
+gemm_status_t check_backward_saved(const gemm_matrix_t *G, const gemm_matrix_t *A, const gemm_matrix_t *B, int64_t M, int64_t N,
+                                   int64_t K, Operand *a, Operand *b) {
+    if (A == nullptr || !is_eight(A->type)) return check_backward(G, A, B, M, N, K, a, b);
+    if (!sizes_ok(M, N, K) || G == nullptr || B == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (G->type != GEMM_TYPE_F16 && G->type != GEMM_TYPE_BF16) return GEMM_ERR_INVALID_ARG;
+    if (B->type != G->type) return GEMM_ERR_INVALID_ARG;
+    gemm_status_t st = classify(A->data, A->type, M, K, A->stride_row, A->stride_col, a);
+    if (st == GEMM_OK) st = classify(B->data, B->type, N, K, B->stride_col, B->stride_row, b);
+    return st == GEMM_OK ? check_rows(G, M, N) : st;
 }
 
 // A gradient is stored row by row or, like a weight kept as its transpose,
@@ -612,6 +692,13 @@ cudaError_t launch_grad(const GradParams &p, bool vec, int64_t parts, cudaStream
     const dim3 grid(unsigned(cdiv(p.N, 256)), unsigned(parts)), block(32, kGradGroups);
     return vec ? launch_shape(linear_grad_kernel<T, false>, grid, block, 0, 1, stream, p)
                : launch_shape(linear_grad_kernel<T, true>, grid, block, 0, 1, stream, p);
+}
+
+template <typename T>
+cudaError_t launch_saved_grad(const SavedGradParams &p, bool vec, int64_t parts, cudaStream_t stream) {
+    const dim3 grid(unsigned(cdiv(p.g.N, 256)), unsigned(parts)), block(32, kGradGroups);
+    return vec ? launch_shape(saved_grad_kernel<T, false>, grid, block, 0, 1, stream, p)
+               : launch_shape(saved_grad_kernel<T, true>, grid, block, 0, 1, stream, p);
 }
 
 // Rows of a second 16-bit (or, `es` = 1, 8-bit) matrix that start at the same place in
@@ -640,19 +727,24 @@ gemm_status_t gemm_linear_backward_workspace_size(const gemm_matrix_t *G, const 
     return st;
 }
 
-gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *A, const gemm_matrix_t *B,
-                                   const gemm_matrix_t *pre, int32_t activation, const gemm_matrix_t *dA,
-                                   const gemm_matrix_t *dB, float *dbias, int64_t M, int64_t N, int64_t K,
-                                   uint32_t flags, void *workspace, uint64_t workspace_bytes, gemm_stream_t stream_) {
+}  // extern "C"
+
+namespace {
+
+// gemm_linear_backward and gemm_saved_backward (any of whose matrices may be 8-bit).
+gemm_status_t backward(const gemm_matrix_t *G, const gemm_matrix_t *A, const gemm_matrix_t *B, const gemm_matrix_t *pre,
+                       int32_t activation, const Saved &saved, const gemm_matrix_t *dA, const gemm_matrix_t *dB, float *dbias,
+                       int64_t M, int64_t N, int64_t K, uint32_t flags, void *workspace, uint64_t workspace_bytes,
+                       gemm_stream_t stream_) {
     // ---- validation (no GPU work before this point)
     Operand a, b;
-    gemm_status_t st = check_backward(G, A, B, M, N, K, &a, &b);
+    gemm_status_t st = saved.allowed ? check_backward_saved(G, A, B, M, N, K, &a, &b) : check_backward(G, A, B, M, N, K, &a, &b);
     if (st != GEMM_OK) return st;
     if ((flags & ~GEMM_LINEAR_ALL_FLAGS) || flags == GEMM_LINEAR_ALL_FLAGS) return GEMM_ERR_INVALID_ARG;
     if (activation < GEMM_ACT_NONE || activation > GEMM_ACT_SILU) return GEMM_ERR_INVALID_ARG;
     const bool has_pre = activation != GEMM_ACT_NONE;
     if (has_pre && M > 0 && N > 0) {
-        if (!present(pre) || pre->type != G->type) return GEMM_ERR_INVALID_ARG;
+        if (!present(pre) || (pre->type != G->type && !(saved.allowed && is_eight(pre->type)))) return GEMM_ERR_INVALID_ARG;
         st = check_rows(pre, M, N);
         if (st != GEMM_OK) return st;
     }
@@ -687,9 +779,17 @@ gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *
     const bool products = K > 0 && (present(dA) || present(dB));
 
     // ---- operand copies; D and its column sums beside them
-    const bool pack_a = products && present(dB) && s.a > 0, pack_b = products && present(dA) && s.b > 0;
-    const bool packs = pack_a || pack_b;
-    if (packs && pack_operands(&a, pack_a ? ws_a : nullptr, &b, pack_b ? ws_b : nullptr, ds->num_sms, stream) != cudaSuccess)
+    const bool eight = is_eight(a.type), expand = eight && products && present(dB);
+    const bool pack_a = !eight && products && present(dB) && s.a > 0, pack_b = products && present(dA) && s.b > 0;
+    const bool packs = pack_a || pack_b || expand;
+    if (eight && !expand) a.type = G->type;  // not read
+    if (expand) {
+        const ExpandJob job = expand_job(a, ws_a, saved.scale_a, uint32_t(saved.act_a), ds->num_sms), none{};
+        const cudaError_t e = G->type == GEMM_TYPE_F16 ? expand_operands<__half, false>(&a, job, nullptr, none, G->type, stream)
+                                                       : expand_operands<__nv_bfloat16, false>(&a, job, nullptr, none, G->type, stream);
+        if (e != cudaSuccess) return GEMM_ERR_CUDA;
+    }
+    if ((pack_a || pack_b) && pack_operands(&a, pack_a ? ws_a : nullptr, &b, pack_b ? ws_b : nullptr, ds->num_sms, stream) != cudaSuccess)
         return GEMM_ERR_CUDA;
     Operand d_rows{G->data, M, N, G->stride_row, G->type, false};
     const GradPlan gp = plan_grad(M, N);
@@ -708,9 +808,18 @@ gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *
         p.rows_per_block = gp.rows_per_block;
         p.act = uint32_t(activation);
         p.late = packs;
-        const bool vec = N % 8 == 0 && vec16(p.g, p.ldg, 2) && (!has_pre || vec16(p.pre, p.ldp, 2));
-        const cudaError_t e = G->type == GEMM_TYPE_F16 ? launch_grad<__half>(p, vec, gp.parts, stream)
-                                                       : launch_grad<__nv_bfloat16>(p, vec, gp.parts, stream);
+        const bool g_vec = N % 8 == 0 && vec16(p.g, p.ldg, 2);
+        cudaError_t e;
+        if (has_pre && is_eight(pre->type)) {
+            const SavedGradParams sp{p, saved.scale_pre, uint32_t(pre->type)};
+            const bool vec = g_vec && (reinterpret_cast<uintptr_t>(p.pre) & 7u) == 0 && p.ldp % 8 == 0;
+            e = G->type == GEMM_TYPE_F16 ? launch_saved_grad<__half>(sp, vec, gp.parts, stream)
+                                         : launch_saved_grad<__nv_bfloat16>(sp, vec, gp.parts, stream);
+        } else {
+            const bool vec = g_vec && (!has_pre || vec16(p.pre, p.ldp, 2));
+            e = G->type == GEMM_TYPE_F16 ? launch_grad<__half>(p, vec, gp.parts, stream)
+                                         : launch_grad<__nv_bfloat16>(p, vec, gp.parts, stream);
+        }
         if (e != cudaSuccess) return GEMM_ERR_CUDA;
         if (p.d != nullptr) {
             d_rows.data = ws_d;
@@ -775,6 +884,46 @@ gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *
         if (st != GEMM_OK) return st;
     }
     return finish_dbias();
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t gemm_linear_backward(const gemm_matrix_t *G, const gemm_matrix_t *A, const gemm_matrix_t *B,
+                                   const gemm_matrix_t *pre, int32_t activation, const gemm_matrix_t *dA,
+                                   const gemm_matrix_t *dB, float *dbias, int64_t M, int64_t N, int64_t K,
+                                   uint32_t flags, void *workspace, uint64_t workspace_bytes, gemm_stream_t stream) {
+    return backward(G, A, B, pre, activation, Saved{}, dA, dB, dbias, M, N, K, flags, workspace, workspace_bytes, stream);
+}
+
+gemm_status_t gemm_saved_backward(const gemm_matrix_t *G, const gemm_matrix_t *A, const float *scale_a, int32_t activation_a,
+                                  const gemm_matrix_t *B, const gemm_matrix_t *pre, const float *scale_pre, int32_t activation,
+                                  const gemm_matrix_t *dA, const gemm_matrix_t *dB, float *dbias, int64_t M, int64_t N,
+                                  int64_t K, uint32_t flags, void *workspace, uint64_t workspace_bytes,
+                                  gemm_stream_t stream) {
+    if (A == nullptr || activation_a < GEMM_ACT_NONE || activation_a > GEMM_ACT_SILU) return GEMM_ERR_INVALID_ARG;
+    if (M > 0) {  // (an empty vector of scales may have no address)
+        if (is_eight(A->type) != (scale_a != nullptr)) return GEMM_ERR_INVALID_ARG;
+        if (present(pre) && is_eight(pre->type) != (scale_pre != nullptr)) return GEMM_ERR_INVALID_ARG;
+    }
+    if (!is_eight(A->type) && activation_a != GEMM_ACT_NONE) return GEMM_ERR_UNSUPPORTED;
+    if ((reinterpret_cast<uintptr_t>(scale_a) | reinterpret_cast<uintptr_t>(scale_pre)) & 3u) return GEMM_ERR_INVALID_ARG;
+    return backward(G, A, B, pre, activation, Saved{true, scale_a, scale_pre, activation_a}, dA, dB, dbias, M, N, K, flags, workspace,
+                    workspace_bytes, stream);
+}
+
+gemm_status_t gemm_saved_backward_workspace_size(const gemm_matrix_t *G, const gemm_matrix_t *A, const gemm_matrix_t *B,
+                                                 int32_t activation, int32_t need_dbias, int64_t M, int64_t N, int64_t K,
+                                                 uint64_t *bytes) {
+    Operand a, b;
+    gemm_status_t st = check_backward_saved(G, A, B, M, N, K, &a, &b);
+    if (st != GEMM_OK) return st;
+    if (activation < GEMM_ACT_NONE || activation > GEMM_ACT_SILU) return GEMM_ERR_INVALID_ARG;
+    BackwardSpace s;
+    st = backward_space(G, a, b, activation, need_dbias != 0, M, N, K, &s);
+    if (st == GEMM_OK && bytes) *bytes = s.total;
+    return st;
 }
 
 }  // extern "C"

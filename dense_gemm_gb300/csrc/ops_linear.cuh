@@ -370,8 +370,8 @@ __device__ __forceinline__ Unit unit_of(const LinearParams &p, int32_t u, uint32
 
 // The epilogue of one warp: 32 rows (TMEM lanes) by half the unit's columns.
 // OB: bytes per element of C. A chunk is 128 bytes of each row; the warp's chunks
-// take its staging buffers in turn.
-template <bool kF8, int OB>
+// take its staging buffers in turn. kScaled: rows and columns have factors.
+template <bool kScaled, int OB>
 struct PairEpilogue {
     static constexpr int CHUNK = 128 / OB;  // columns: 64 or 32
     const LinearParams &p;
@@ -559,7 +559,7 @@ struct PairEpilogue {
             float x[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(v[i0][i]);
-            if constexpr (kF8) {
+            if constexpr (kScaled) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] *= sa * __shfl_sync(0xffffffffu, j0 == 0 ? sb[i0] : sb[i0 + 2], i);
             }
@@ -611,7 +611,8 @@ struct PairEpilogue {
 // stages instead of 6 change nothing). Two staging buffers per warp instead of one
 // only where the residual or pre needs them: the sixth stage is worth more (8192 x
 // 8192 x 4096: 315 us with one buffer, 340 with two and 5 stages).
-template <bool kF8, int OB>
+// kScaled without kF8: whole numbers as fp16, with the scales of 8-bit integers.
+template <bool kF8, int OB, bool kScaled = kF8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1)
     linear_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmBhalf, const __grid_constant__ CUtensorMap tmC,
@@ -815,7 +816,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
         const int q = warp & 3;  // TMEM lane quarter this warp may access
         const int ew = warp - EPI_WARP0;
         const int half = ew / 4;  // columns [128 half, 128 half + 128) of the tile
-        PairEpilogue<kF8, OB> ep{p,    &tmC, &tmR, &tmP,    sE + uint32_t(ew) * uint32_t(p.bufs) * lin::BUF_BYTES,
+        PairEpilogue<kScaled, OB> ep{p,    &tmC, &tmR, &tmP,    sE + uint32_t(ew) * uint32_t(p.bufs) * lin::BUF_BYTES,
                                  res_bar0 + 16u * ew, lane, q, half, rank, pair_id, 0, num_pairs, 0, 0};
         griddep_enter(p.late);
         ep.begin();
@@ -833,10 +834,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(lin::PAIR_THREADS, 1
                 const int64_t col = col0 + 32 * j + lane;
                 if (j < groups && col < p.N) {
                     if (p.e.bias != nullptr) bias[j] = load_elem(p.e.bias, p.e.bias_type, col);
-                    if (kF8) sb[j] = p.e.sb[col];
+                    if (kScaled) sb[j] = p.e.sb[col];
                 }
             }
-            if (kF8 && row0 + lane < p.M) sa = p.e.sa[row0 + lane];
+            if (kScaled && row0 + lane < p.M) sa = p.e.sa[row0 + lane];
             if (!__all_sync(0xffffffffu, mbar_wait(tfull_bar(acc), use & 1u, p.wait))) break;
             tc_fence_after();
             auto release = [&] {
@@ -974,7 +975,7 @@ __device__ __forceinline__ void add_split_residual(uint32_t type, const uint32_t
 
 // Warp `ew` of CTA `rank` has rows k S + rank of the tile, k = ew, ew + 8, ...; this
 // fetches its columns' factors and the residual of the first kSplitRows of them.
-template <bool kF8, bool VEC>
+template <bool kScaled, bool VEC>
 __device__ __forceinline__ void split_columns(const LinearParams &p, int S, uint32_t rank, int ew, int lane, int32_t m0,
                                               int32_t n0, int valid, SplitColumns &h) {
 #pragma unroll
@@ -982,7 +983,7 @@ __device__ __forceinline__ void split_columns(const LinearParams &p, int S, uint
         const int64_t n = int64_t(n0) + split_col<VEC>(lane, i);
         const bool in = VEC || n < p.N;
         h.bias[i] = in && p.e.bias != nullptr ? load_elem(p.e.bias, p.e.bias_type, n) : 0.0f;
-        h.sb[i] = kF8 && in ? p.e.sb[n] : 1.0f;
+        h.sb[i] = kScaled && in ? p.e.sb[n] : 1.0f;
     }
     if (p.e.r == nullptr) return;
 #pragma unroll
@@ -994,7 +995,7 @@ __device__ __forceinline__ void split_columns(const LinearParams &p, int S, uint
 
 // Sums the S partial rows of this warp's rows of C, in rank order, and runs the
 // epilogue on them, R rows at a time.
-template <bool kF8, int S, bool VEC, int R>
+template <bool kScaled, int S, bool VEC, int R>
 __device__ __forceinline__ void split_rows(const LinearParams &p, uint32_t base, uint32_t rank, int ew, int lane, int32_t m0,
                                            int32_t n0, int valid, SplitColumns &h) {
     const EpilogueParams &e = p.e;
@@ -1003,7 +1004,7 @@ __device__ __forceinline__ void split_rows(const LinearParams &p, uint32_t base,
         float x[4 * R], sa[R];
         auto tile_row = [&](int u) { return (k + u * EPI_WARPS) * S + int(rank); };
 #pragma unroll
-        for (int u = 0; u < R; ++u) sa[u] = kF8 && tile_row(u) < valid ? e.sa[int64_t(m0) + tile_row(u)] : 1.0f;
+        for (int u = 0; u < R; ++u) sa[u] = kScaled && tile_row(u) < valid ? e.sa[int64_t(m0) + tile_row(u)] : 1.0f;
 #pragma unroll
         for (int u = 0; u < R; ++u) {
 #pragma unroll
@@ -1024,7 +1025,7 @@ __device__ __forceinline__ void split_rows(const LinearParams &p, uint32_t base,
                 for (int i = 0; i < 4; ++i) x[4 * u + i] += __uint_as_float(w[i]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[4 * u + i] = (kF8 ? x[4 * u + i] * (sa[u] * h.sb[i]) : x[4 * u + i]) + h.bias[i];
+            for (int i = 0; i < 4; ++i) x[4 * u + i] = (kScaled ? x[4 * u + i] * (sa[u] * h.sb[i]) : x[4 * u + i]) + h.bias[i];
         }
         auto put = [&](void *dst, int64_t ld) {
 #pragma unroll
@@ -1078,7 +1079,7 @@ __device__ __forceinline__ void with_split(int S, F f) {
 // MB in 23.3 us, 5.8 TB/s), else by the chain first copy - products - cluster barrier
 // - partial rows - sum, 5 us of which hold no stream (one token 4096 x 4096: 33.6 MB
 // in 7.9 us; 48 x 4096 x 8192: 68 MB in 14.4 us).
-template <bool kF8>
+template <bool kF8, bool kScaled = kF8>
 __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     linear_split(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const LinearParams p) {
     constexpr int BKE = kF8 ? 128 : 64;
@@ -1232,8 +1233,8 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         mma_commit_elect(done_bar);
         __all_sync(0xffffffffu, mbar_wait_slow(done_bar, 0, cleanup_wait(p.wait), false));
     } else if (warp >= EPI_WARP0) {
-        if (vec) split_columns<kF8, true>(p, S, rank, ew, lane, m0, n0, valid, columns);
-        else split_columns<kF8, false>(p, S, rank, ew, lane, m0, n0, valid, columns);
+        if (vec) split_columns<kScaled, true>(p, S, rank, ew, lane, m0, n0, valid, columns);
+        else split_columns<kScaled, false>(p, S, rank, ew, lane, m0, n0, valid, columns);
         ready = __all_sync(0xffffffffu, mbar_wait(done_bar, 0, p.wait));
         tc_fence_after();
     }
@@ -1264,9 +1265,9 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         const bool one = valid <= EPI_WARPS * S;  // a row for each warp at most
         with_split(S, [&](auto s) {
             constexpr int SPLIT = decltype(s)::value;
-            if (vec && one) split_rows<kF8, SPLIT, true, 1>(p, base, rank, ew, lane, m0, n0, valid, columns);
-            else if (vec) split_rows<kF8, SPLIT, true, kSplitRows>(p, base, rank, ew, lane, m0, n0, valid, columns);
-            else split_rows<kF8, SPLIT, false, kSplitRows>(p, base, rank, ew, lane, m0, n0, valid, columns);
+            if (vec && one) split_rows<kScaled, SPLIT, true, 1>(p, base, rank, ew, lane, m0, n0, valid, columns);
+            else if (vec) split_rows<kScaled, SPLIT, true, kSplitRows>(p, base, rank, ew, lane, m0, n0, valid, columns);
+            else split_rows<kScaled, SPLIT, false, kSplitRows>(p, base, rank, ew, lane, m0, n0, valid, columns);
         });
     }
     griddep_leave(p.late);

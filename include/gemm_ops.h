@@ -12,8 +12,14 @@
  *   gemm_rms_norm           h = x + r, y = w h / sqrt(mean(h^2) + eps),
  *                           in 16 or 32 bits, or in 8 with a scale per row
  *   gemm_rms_norm_backward  its gradients
+ *   gemm_layer_norm         h = x + r, y = w (h - mean) / sqrt(var + eps) + b,
+ *                           in 16 or 32 bits, or in 8 with a scale per row
+ *   gemm_layer_norm_backward  its gradients
+ *   gemm_quantize_rows      rows in 8 bits with a scale each
+ *   gemm_saved_backward     gemm_linear_backward from values kept in 8 bits
  *
- * An 8-bit y and its scales are an A and scale_a of gemm_linear.
+ * An 8-bit y and its scales are an A and scale_a of gemm_linear, and an A and
+ * scale_a (or pre and scale_pre) of gemm_saved_backward.
  */
 #ifndef GEMM_OPS_H
 #define GEMM_OPS_H
@@ -29,6 +35,7 @@ extern "C" {
 #define GEMM_TYPE_F16 GEMM_OUT_F16
 #define GEMM_TYPE_BF16 GEMM_OUT_BF16
 #define GEMM_TYPE_E4M3 3 /* 8-bit float: 4 exponent, 3 mantissa bits, +-448, no infinity */
+#define GEMM_TYPE_I8 4   /* whole number of 8 bits, -128 .. 127 */
 
 /* Activations. x is the value in fp32 after scales and bias.
  * RELU: x < 0 ? 0 : x (a NaN stays). GELU: x Phi(x), Phi the normal
@@ -74,18 +81,20 @@ typedef struct {
  *   C[i,j] = act(x[i,j]) + residual[i,j]
  *
  * The sum and everything after it are in fp32; pre and C are each rounded once
- * (nearest-even). A [M,K] and B [K,N] have one type, fp16, bf16 or e4m3; C is
- * fp32, fp16 or bf16. Scales are for e4m3 operands only (both or neither).
+ * (nearest-even). A [M,K] and B [K,N] have one type, fp16, bf16, e4m3 or int8; C is
+ * fp32, fp16 or bf16. Scales are for 8-bit operands only (both or neither). The
+ * products of int8 operands are exact, and so is their sum while it stays below
+ * 2^24; beyond, it is rounded like any fp32 sum.
  * Layouts: A with a unit row or column stride, B likewise (a B with stride_row
- * == 1 is a weight stored [N,K]); e4m3 operands with K contiguous only; C, pre
+ * == 1 is a weight stored [N,K]); 8-bit operands with K contiguous only; C, pre
  * and residual with stride_col == 1 and stride_row >= N (M > 1). Others ->
  * GEMM_ERR_UNSUPPORTED / INVALID_ARG as in gemm_f16. C may be residual itself
  * (same data and strides); otherwise outputs overlap no input and no other
  * output (undefined).
  * workspace: 128-byte aligned, of gemm_linear_workspace_size() bytes, needed
  * only where that is not 0: an operand whose base or row stride is no multiple
- * of 16 bytes is first copied there onto 128-byte lines (one kernel). Its
- * contents mean nothing between calls.
+ * of 16 bytes is first copied there onto 128-byte lines (one kernel), and int8
+ * operands as fp16. Its contents mean nothing between calls.
  * M, N or K < 0 or >= 2^31 -> INVALID_ARG. M == 0 or N == 0: nothing is done.
  * K == 0: the sum is 0 and the epilogue still runs.
  * Two kernels share the work by a rule on M, N and K: 256x256 tiles on CTA
@@ -179,6 +188,91 @@ gemm_status_t gemm_rms_norm_backward(const gemm_matrix_t *grad, const gemm_matri
                                      void *workspace, uint64_t workspace_bytes, gemm_stream_t stream);
 
 gemm_status_t gemm_rms_norm_backward_workspace_size(int64_t rows, int64_t width, uint64_t *bytes);
+
+/*
+ * gemm_layer_norm — for each row i of `rows`:
+ *
+ *   h = x[i,:] + residual[i,:]      (residual absent: h = x)
+ *   mean[i] = sum(h) / width,  rstd[i] = 1 / sqrt(sum((h - mean)^2) / width + eps)
+ *   y[i,:] = weight * (h - mean[i]) * rstd[i] + bias
+ *
+ * everything in fp32 from the unrounded sum h, the variance from the centred
+ * values; h, y, mean and rstd are each rounded once. x, residual and h have one
+ * type, fp32, fp16 or bf16; y has that type or is e4m3 or int8; weight and bias
+ * [width] both have x's type or both are fp32; bias may be NULL. With an 8-bit y,
+ * a = max_j |y[i,j]|, scale[i] = a / t and y[i,j] holds nearest-even(y[i,j] *
+ * (t / a)), t = 448 (e4m3) or 127 (int8), so that the value is y * scale; a row whose
+ * a is below 7.7e-34 has scale 1 and zeros; a row with a NaN or an infinity has
+ * scale NaN (and NaNs in e4m3, zeros in int8). scale must be given with an 8-bit y,
+ * and only then. A row of equal values with eps = 0 is NaN.
+ * h (given only with residual) may be x or residual itself. mean and rstd may be
+ * NULL. All matrices have stride_col == 1 and stride_row >= width (rows > 1).
+ * rows == 0 or width == 0: nothing is done. eps >= 0, finite.
+ */
+gemm_status_t gemm_layer_norm(const gemm_matrix_t *x, const gemm_matrix_t *residual, const void *weight,
+                              const void *bias, int32_t weight_type, const gemm_matrix_t *y, const gemm_matrix_t *h,
+                              float *scale, float *mean, float *rstd, int64_t rows, int64_t width, float eps,
+                              gemm_stream_t stream);
+
+/*
+ * gemm_layer_norm_backward — gradients of gemm_layer_norm (16- or 32-bit y) from
+ * the gradient `grad` of y, h, mean and rstd as the forward call left them, and the
+ * gradient grad_h that arrives at h itself (the residual path; may be absent):
+ *
+ *   u = (h - mean) rstd, g = grad * weight
+ *   dx = rstd (g - mean(g) - u mean(g u)) + grad_h   (x's and residual's gradient)
+ *   dweight[j] = sum_i grad[i,j] u[i,j],  dbias[j] = sum_i grad[i,j]   (fp32 [width])
+ *
+ * in fp32; dx is rounded once. grad, h, grad_h and dx have one type, fp32, fp16
+ * or bf16. dx may be grad or grad_h itself. dweight and dbias may each be NULL.
+ * Sums over rows are in a fixed order. workspace: 16-byte aligned,
+ * gemm_layer_norm_backward_workspace_size() bytes (partial sums over the rows;
+ * needed when dweight or dbias is asked for). rows == 0: both are zero-filled.
+ */
+gemm_status_t gemm_layer_norm_backward(const gemm_matrix_t *grad, const gemm_matrix_t *h, const void *weight,
+                                       int32_t weight_type, const float *mean, const float *rstd,
+                                       const gemm_matrix_t *grad_h, const gemm_matrix_t *dx, float *dweight, float *dbias,
+                                       int64_t rows, int64_t width, void *workspace, uint64_t workspace_bytes,
+                                       gemm_stream_t stream);
+
+gemm_status_t gemm_layer_norm_backward_workspace_size(int64_t rows, int64_t width, uint64_t *bytes);
+
+/*
+ * gemm_quantize_rows — each row of x in 8 bits with a scale: a = max_j |x[i,j]|,
+ * scale[i] = a / t, q[i,j] = nearest-even(x[i,j] * (t / a)), t = 448 (q in e4m3)
+ * or 127 (int8), rows of tiny values and rows with a NaN or an infinity as in
+ * gemm_layer_norm. x is fp32, fp16 or bf16, scale fp32 [rows]. q overlaps no part
+ * of x. Both matrices have stride_col == 1 and stride_row >= width (rows > 1).
+ * rows == 0 or width == 0: nothing is done.
+ */
+gemm_status_t gemm_quantize_rows(const gemm_matrix_t *x, const gemm_matrix_t *q, float *scale, int64_t rows, int64_t width,
+                                 gemm_stream_t stream);
+
+/*
+ * gemm_saved_backward — gemm_linear_backward of C = act(A' @ B + bias) + R from
+ * what was kept of A' [M,K] and of the values before the activation in 8 bits:
+ *
+ *   A'[i,k] = act_a(scale_a[i] A[i,k])     rounded to G's type
+ *   D = G act'(scale_pre[i] pre[i,j])      in fp32, rounded for the products
+ *   dA' = D B^T  [M,K]      dB = A'^T D  [K,N]      dbias[j] = sum_i D[i,j]
+ *
+ * A is e4m3 or int8 with scale_a [M] fp32 (K contiguous), or 16-bit with scale_a NULL
+ * and activation_a NONE; pre likewise with scale_pre, absent with activation NONE.
+ * activation_a is for a product whose operand is itself an activation: what was
+ * kept is the value before it (dA' is still the gradient of act_a's result). G and B
+ * are fp16 or bf16. Everything else as gemm_linear_backward, whose result this is
+ * for the values that the 8 bits hold. workspace: 128-byte aligned,
+ * gemm_saved_backward_workspace_size() bytes; A' is made there where dB is asked for.
+ */
+gemm_status_t gemm_saved_backward(const gemm_matrix_t *G, const gemm_matrix_t *A, const float *scale_a, int32_t activation_a,
+                                  const gemm_matrix_t *B, const gemm_matrix_t *pre, const float *scale_pre, int32_t activation,
+                                  const gemm_matrix_t *dA, const gemm_matrix_t *dB, float *dbias, int64_t M, int64_t N,
+                                  int64_t K, uint32_t flags, void *workspace, uint64_t workspace_bytes,
+                                  gemm_stream_t stream);
+
+gemm_status_t gemm_saved_backward_workspace_size(const gemm_matrix_t *G, const gemm_matrix_t *A, const gemm_matrix_t *B,
+                                                 int32_t activation, int32_t need_dbias, int64_t M, int64_t N, int64_t K,
+                                                 uint64_t *bytes);
 
 #ifdef __cplusplus
 }
