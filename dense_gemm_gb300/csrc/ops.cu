@@ -66,6 +66,14 @@ constexpr int kSplitTs = 5, kSplitSs = 4;
 // other's stream.
 constexpr int split_stages(int T) { return T == 16 || T == 128 ? 3 : 2; }
 
+// linear_int8's shapes: the same T up to 128, whose tokens in fp16 leave room for one CTA
+// on an SM.
+constexpr int kInt8Ts = 4;
+constexpr int int8_stages(int T) { return T == 16 ? 5 : T == 64 ? 3 : 4; }
+constexpr int int8_smem(int T) { return lin::i8_smem(int8_stages(T), T); }
+static_assert(int8_smem(16) <= 115712 && int8_smem(32) <= 115712 && int8_smem(64) <= 115712 && int8_smem(128) <= 232448,
+              "two CTAs on an SM, or one");
+
 // Done once per device: this file's kernels' shared-memory limits, and how many
 // CTAs of each linear_split shape are resident at once (clusters of 8 do not fill
 // every GPC).
@@ -73,12 +81,30 @@ struct OpsState {
     std::mutex mu;
     std::atomic<bool> ready{false};
     int split_slots[kSplitTs][kSplitSs];
+    int int8_slots[kInt8Ts][kSplitSs];
 };
 OpsState g_ops[kMaxDevices];
 
 template <typename K>
 cudaError_t allow_smem(K *kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+// Clusters of `size` CTAs that are resident at once, one CTA per SM at least.
+template <typename K>
+cudaError_t clusters_at_once(int *n, K *kernel, unsigned size, int smem, int num_sms) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(unsigned(2 * num_sms) / size * size);
+    cfg.blockDim = dim3(lin::SPLIT_THREADS);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
 }
 
 const OpsState *ops_init(int dev, int num_sms) {
@@ -99,22 +125,21 @@ const OpsState *ops_init(int dev, int num_sms) {
         const int T = 16 << t;
         o.split_slots[t][0] = (T <= 64 ? 2 : 1) * num_sms;
         for (int s = 1; e == cudaSuccess && s < kSplitSs; ++s) {
-            cudaLaunchConfig_t cfg = {};
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = 1u << s;
-            attr[0].val.clusterDim.y = 1;
-            attr[0].val.clusterDim.z = 1;
-            cfg.gridDim = dim3(unsigned(2 * num_sms) >> s << s);
-            cfg.blockDim = dim3(lin::SPLIT_THREADS);
-            cfg.dynamicSmemBytes = size_t(lin::split_smem(split_stages(T), T));
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
             int n = 0;
-            e = cudaOccupancyMaxActiveClusters(&n, linear_split<false>, &cfg);
+            e = clusters_at_once(&n, linear_split<false>, 1u << s, lin::split_smem(split_stages(T), T), num_sms);
             // the query counts one CTA per SM for these shapes, also where two fit and run
             // (16384 x 4096 weights, 64 tokens, 128 clusters of 2: 25.6 us, in one round)
             o.split_slots[t][s] = (T <= 64 ? 2 : 1) * std::max(n, 1) << s;
+        }
+    }
+    if (e == cudaSuccess) e = allow_smem(linear_int8, 232448);
+    for (int t = 0; e == cudaSuccess && t < kInt8Ts; ++t) {
+        const int T = 16 << t, per_sm = T <= 64 ? 2 : 1;
+        o.int8_slots[t][0] = per_sm * num_sms;
+        for (int s = 1; e == cudaSuccess && s < kSplitSs; ++s) {
+            int n = 0;
+            e = clusters_at_once(&n, linear_int8, 1u << s, int8_smem(T), num_sms);
+            o.int8_slots[t][s] = per_sm * std::max(n, 1) << s;
         }
     }
     if (e != cudaSuccess) {
@@ -168,7 +193,7 @@ cudaError_t pack_operands(Operand *a, void *dst_a, Operand *b, void *dst_b, int 
     int64_t total = 0;
     auto blocks_for = [&](int64_t n) { return int(std::min<int64_t>(cdiv(n, 256), 8 * int64_t(num_sms))); };
     cudaError_t e = cudaSuccess;
-    if (type == GEMM_TYPE_E4M3) {
+    if (is_eight(type)) {
         auto job = [](const Operand &o, void *dst) {
             PackBytesJob j;
             j.src = static_cast<const uint8_t *>(o.data);
@@ -259,7 +284,7 @@ bool encode_operand(CUtensorMap *map, OperandLoad *load, const Operand &o, int k
     EncodeTiledFn enc = encode_fn();
     if (enc == nullptr) return false;
     const int es = type_bytes(o.type), be = 128 / es;
-    const CUtensorMapDataType dt = o.type == GEMM_TYPE_E4M3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+    const CUtensorMapDataType dt = is_eight(o.type)          ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                    : o.type == GEMM_TYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int pieces = o.mn_major ? mn / be : kbs;
@@ -474,10 +499,89 @@ gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t 
     return err == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
-// Workspace of two operands' copies: [A's][B's], each from a 256-byte boundary. Whole
-// numbers are copied to fp16.
-void copies_needed(const Operand &A, const Operand &B, uint64_t *a_bytes, uint64_t *b_bytes) {
-    if (A.type == GEMM_TYPE_I8) {
+// Whole numbers: linear_int8, or both operands copied to fp16 and a 16-bit product. Up to
+// two tiles of 128 rows, and for small products of any shape, converting the weights anew for
+// every 128 rows costs less than a copy of them that is written and read again (direct /
+// copied: 256 x 8192 x 8192 48.8 / 72.3 us, 256 x 4096 x 4096 17.2 / 19.7, 512 x 4096 x 4096
+// 27.5 / 25.3, 512 x 8192 x 8192 96 / 78, 1024 x 1024 x 1024 8.8 / 10.8, 1 x 4096 x 4096 7.4 / 14.1). By the sizes alone, since the workspace goes by it.
+bool int8_direct(int64_t M, int64_t N, int64_t K) {
+    return M <= 256 || double(M) * double(N) * double(K) <= double(int64_t(1) << 30);
+}
+
+// linear_int8's shape, as plan_split: a stage every kInt8Step along one CTA, and on an SM
+// every kInt8Sm whatever it runs (a stage's conversion takes its warps' time).
+// (4096 x 4096, one token: T = 16, S = 4 7.4 us, 8 7.8, 2 10.5, 1 16.4; 64 x 16384 x 4096:
+// T = 64, S = 2 19.6, 1 22.9, T = 32, S = 2 26.7; 128 x 16384 x 4096: T = 128, S = 1 28.7, T = 64 31.8.)
+constexpr double kInt8Step[kInt8Ts] = {0.37, 0.45, 0.53, 0.68}, kInt8Sm[kInt8Ts] = {0.33, 0.38, 0.45, 0.68}, kInt8Cluster = 0.15;
+struct Int8Plan {
+    int T, split;
+};
+Int8Plan plan_int8(int64_t M, int64_t N, int64_t steps, const DeviceState &ds, const OpsState &o) {
+    Int8Plan best{16, 1};
+    double least = 1e300;
+    for (int t = 0; t < kInt8Ts; ++t) {
+        const int T = 16 << t;
+        const int64_t tiles = cdiv(N, lin::SPLIT_ROWS) * cdiv(M, T);
+        for (int s = 0; s < kSplitSs && (int64_t(1) << s) <= steps; ++s) {
+            const int64_t S = int64_t(1) << s, ctas = tiles * S;
+            // clusters of 8: a few more than fit start late but end soon after the others
+            const double load = double(ctas) / o.int8_slots[t][s];
+            const double rounds = load <= 1.0 ? 1.0 : load <= 1.1 && S == 8 ? load : double(cdiv(ctas, o.int8_slots[t][s]));
+            const double one = kSplitFixed + (s > 0 ? kInt8Cluster * double(S) : 0.0) + kSplitSend * T + kSplitRow * T / double(S);
+            const double stream = rounds * (kLatency + double(cdiv(steps, S) - 1) * kInt8Step[t]);
+            const double sms = double(tiles * steps) / ds.num_sms * kInt8Sm[t];
+            const double weights = double(N) * double(steps) * 128.0;
+            const double rate = std::min(kDramBytes, double(ctas) * int8_stages(T) * lin::I8_W_BYTES / kRingTime);
+            const double cost = rounds * one + std::max({stream, sms, weights / rate});
+            if (cost < least) {
+                least = cost;
+                best = Int8Plan{T, int(S)};
+            }
+        }
+        if (T >= M) break;
+    }
+    return best;
+}
+
+// linear_int8 on operands that TMA can describe. K >= 1.
+gemm_status_t run_int8(const Operand &A, const Operand &B, int64_t M, int64_t N, int64_t K, const EpilogueParams &e, const DeviceState *ds,
+                       const OpsState *ops, cudaStream_t stream) {
+    LinearParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.M = M;
+    p.N = N;
+    p.e = e;
+    p.num_kb = int32_t(cdiv(K, 128));
+    p.wait.timeout_ns = g_timeout_ns.load();
+    p.wait.epoch = next_epoch();
+    const Int8Plan pl = plan_int8(M, N, p.num_kb, *ds, *ops);
+    const int64_t nm = cdiv(M, pl.T), nn = cdiv(N, lin::SPLIT_ROWS);
+    if (nm * nn > kMaxDim / lin::MAX_SPLIT) return GEMM_ERR_UNSUPPORTED;
+    CUtensorMap tmW, tmX;
+    if (!encode_operand(&tmW, &p.b, B, 1, lin::SPLIT_ROWS) || !encode_operand(&tmX, &p.a, A, 1, pl.T)) return GEMM_ERR_CUDA;
+    const int es = e.type == 0 ? 4 : 2;
+    p.sched.nm = int32_t(nm);
+    p.sched.nn = int32_t(nn);
+    p.num_units = int32_t(nm * nn);
+    p.T = pl.T;
+    p.tmem_cols = 256;  // accumulator and two stages of weights
+    p.split = pl.split;
+    p.stages = int8_stages(pl.T);
+    p.idesc = linear_idesc(GEMM_TYPE_F16, false, false, lin::SPLIT_ROWS, uint32_t(pl.T));
+    p.e.vec4 = quad_aligned(e.c, e.ldc, es) && (e.pre == nullptr || quad_aligned(e.pre, e.ldp, es)) &&
+               (e.r == nullptr || quad_aligned(e.r, e.ldr, es));
+    const cudaError_t err = launch_shape(linear_int8, dim3(unsigned(int64_t(p.num_units) * pl.split)), dim3(lin::SPLIT_THREADS),
+                                         int8_smem(pl.T), pl.split, stream, tmW, tmX, p);
+    if (log_enabled())
+        std::fprintf(stderr, "[gemm_linear] M=%lld N=%lld K=%lld kernel=int8 T=%d split=%d stages=%d units=%d\n", (long long)M,
+                     (long long)N, (long long)K, p.T, p.split, p.stages, p.num_units);
+    return err == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+// Workspace of two operands' copies: [A's][B's], each from a 256-byte boundary. `expand`:
+// whole numbers, copied to fp16.
+void copies_needed(const Operand &A, const Operand &B, bool expand, uint64_t *a_bytes, uint64_t *b_bytes) {
+    if (expand) {
         *a_bytes = round256(expanded_bytes(A));
         *b_bytes = round256(expanded_bytes(B));
         return;
@@ -512,7 +616,7 @@ gemm_status_t gemm_linear_workspace_size(const gemm_matrix_t *A, const gemm_matr
     const gemm_status_t st = check_operands(A, B, M, N, K, &a, &b);
     if (st != GEMM_OK) return st;
     uint64_t na = 0, nb = 0;
-    if (M > 0 && N > 0 && K > 0) copies_needed(a, b, &na, &nb);
+    if (M > 0 && N > 0 && K > 0) copies_needed(a, b, a.type == GEMM_TYPE_I8 && !int8_direct(M, N, K), &na, &nb);
     if (bytes) *bytes = na + nb;
     return GEMM_OK;
 }
@@ -546,7 +650,8 @@ gemm_status_t gemm_linear(const gemm_matrix_t *A, const gemm_matrix_t *B, const 
         if (st != GEMM_OK) return st;
     }
     uint64_t na = 0, nb = 0;
-    if (K > 0) copies_needed(a, b, &na, &nb);
+    const bool whole = a.type == GEMM_TYPE_I8, expand = whole && !int8_direct(M, N, K);
+    if (K > 0) copies_needed(a, b, expand, &na, &nb);
     st = check_workspace(workspace, workspace_bytes, na + nb, 128);
     if (st != GEMM_OK) return st;
 
@@ -582,11 +687,12 @@ gemm_status_t gemm_linear(const gemm_matrix_t *A, const gemm_matrix_t *B, const 
                    : GEMM_ERR_CUDA;
     }
     unsigned char *ws = static_cast<unsigned char *>(workspace);
-    if (a.type == GEMM_TYPE_I8) {
+    if (expand) {
         const ExpandJob ja = expand_job(a, ws, nullptr, 0, ds->num_sms), jb = expand_job(b, ws + na, nullptr, 0, ds->num_sms);
         if (expand_operands<__half, true>(&a, ja, &b, jb, GEMM_TYPE_F16, stream) != cudaSuccess) return GEMM_ERR_CUDA;
     } else if (na + nb > 0 && pack_operands(&a, na ? ws : nullptr, &b, nb ? ws + na : nullptr, ds->num_sms, stream) != cudaSuccess)
         return GEMM_ERR_CUDA;
+    if (whole && !expand) return run_int8(a, b, M, N, K, e, ds, ops, stream);
     return run_linear(a, b, M, N, K, e, flags, ds, ops, stream);
 }
 
@@ -641,7 +747,7 @@ gemm_status_t backward_space(const gemm_matrix_t *G, const Operand &a, const Ope
         s->a = round256(expanded_bytes(a));
         s->b = b.tma() ? 0u : round256(b.copy_bytes());
     } else if (K > 0) {
-        copies_needed(a, b, &s->a, &s->b);
+        copies_needed(a, b, false, &s->a, &s->b);
     }
     s->total = s->d + s->partial + s->a + s->b;
     return GEMM_OK;

@@ -144,6 +144,276 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(const ExpandJob a, con
     }
 }
 
+// ================================================================== linear_int8
+// Few rows of C, 8-bit integers: linear_split's tiles and sums with the weights' stream in 8
+// bits. A stage is 128 weights' rows and T tokens by 128 bytes of K. It lands by TMA as it
+// is; four of eight warps turn it into fp16, each thread a row: the weights from registers into
+// tensor memory, where the MMA takes its 128-row operand from, the tokens into shared memory.
+// (As fp16 in shared memory the weights would be written once and read once more there: 32
+// KiB each way a stage, beside the 16 in and 16 out of their bytes, on an SM that gets 16 KiB
+// of weights in 0.36 us from DRAM and moves 128 bytes a cycle.)
+namespace lin {
+constexpr int I8_W_BYTES = SPLIT_ROWS * 128;  // weights of a stage
+constexpr int I8_COPIES = 2;                  // stages in fp16, one of each group of warps
+constexpr int I8_MAX_STAGES = 5;
+constexpr int I8_A_COLS = 64;                 // TMEM columns of a stage's weights: 128 of K, two to a column
+// full[S], empty[S], ready[2], used[2], done
+constexpr int I8_BARS = 2 * I8_MAX_STAGES + 2 * I8_COPIES + 1;
+constexpr int i8_ring(int stages, int T) { return stages * (I8_W_BYTES + T * 128) + I8_COPIES * T * 256; }
+constexpr int i8_smem(int stages, int T) { return i8_ring(stages, T) + I8_BARS * 8 + 16 + 1024; }
+}  // namespace lin
+
+// 32 lanes x 32 consecutive 32-bit columns from registers: thread i has lane (base lane + i).
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    if (!__all_sync(0xffffffffu, G16_CHECK((taddr & 0xFFFFu) + 32u <= 512u))) return;
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
+        "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// D[tmem] (+)= A[tmem] * B[smem desc], fp16 x fp16 -> fp32: A's rows are the lanes, two
+// elements of K to a column.
+__device__ __forceinline__ void mma_f16_tmem_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                   uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred pe, pa;\n\t"
+        "elect.sync _|pe, 0xffffffff;\n\t"
+        "setp.ne.b32 pa, %4, 0;\n\t"
+        "@pe tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pa;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Cluster of p.split CTAs along x, all on the same tile of 128 columns by T rows of C; CTA
+// r sums the stages r n / split ... (r + 1) n / split of n.
+__global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
+    linear_int8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const LinearParams p) {
+    constexpr int MMA_WARP = 1, EPI_WARP0 = 2;
+    const int NST = p.stages, T = p.T;
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;  // same offset in every CTA of the cluster
+    uint8_t *smem = smem_raw + (base - raw);
+    const uint32_t x_bytes = uint32_t(T) * 128u;
+    const uint32_t sW = base, sX = base + uint32_t(NST) * lin::I8_W_BYTES;
+    const uint32_t sX16 = sX + uint32_t(NST) * x_bytes;
+    const uint32_t ring = sX16 + lin::I8_COPIES * 2u * x_bytes - base;
+    const uint32_t bar0 = base + ring;
+    auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (lin::I8_MAX_STAGES + s); };
+    auto ready_bar = [&](uint32_t s) { return bar0 + 8u * (2 * lin::I8_MAX_STAGES + s); };
+    auto used_bar = [&](uint32_t s) { return bar0 + 8u * (2 * lin::I8_MAX_STAGES + lin::I8_COPIES + s); };
+    const uint32_t done_bar = bar0 + 8u * (2 * lin::I8_MAX_STAGES + 2 * lin::I8_COPIES);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + ring + lin::I8_BARS * 8);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int S = p.split;
+    const uint32_t rank = S > 1 ? cluster_ctarank() : 0u;
+    // rows of C vary fastest, so that the CTAs sharing weights run together
+    const int32_t tile = int32_t(blockIdx.x) / S;
+    const int32_t tn = tile / p.sched.nm, tm = tile - tn * p.sched.nm;
+    const int32_t m0 = tm * T, n0 = tn * lin::SPLIT_ROWS;
+    const int32_t steps = p.num_kb;  // stages of the whole sum
+    const int32_t st0 = int32_t(int64_t(steps) * rank / S), st1 = int32_t(int64_t(steps) * (rank + 1) / S);
+    const int valid = int(p.M - m0 < T ? p.M - m0 : T);  // rows of C in this tile
+    const int acc_cols = T < 32 ? 32 : T;                // the weights' stages follow the accumulator
+
+    bool ready = false;  // epilogue warps: the accumulator is complete
+    uint32_t tmem_base = 0;
+    const int ew = warp - EPI_WARP0;
+    const bool vec = p.e.vec4 && int64_t(n0) + lin::SPLIT_ROWS <= p.N;  // n0 may lie within 128 of 2^31
+    SplitColumns columns = {};
+
+    auto load = [&](int32_t st, uint32_t stage) {
+        mbar_expect_tx_elect(full_bar(stage), lin::I8_W_BYTES + x_bytes);
+        tma_load_2d_elect<false>(sW + stage * lin::I8_W_BYTES, &tmW, st * 128, n0, full_bar(stage));
+        tma_load_2d_elect<false>(sX + stage * x_bytes, &tmX, st * 128, m0, full_bar(stage));
+    };
+    if (warp == 0) {
+        // ============================================================ producer
+        if (lane == 0) {
+            prefetch_tensormap(&tmW);
+            prefetch_tensormap(&tmX);
+            for (int s = 0; s < NST; ++s) {
+                mbar_init(full_bar(s), 1);
+                mbar_init(empty_bar(s), EPI_WARPS / 2);
+            }
+            for (int s = 0; s < lin::I8_COPIES; ++s) {
+                mbar_init(ready_bar(s), EPI_WARPS / 2);
+                mbar_init(used_bar(s), 1);
+            }
+            mbar_init(done_bar, 1);
+            fence_mbar_init();
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+        const int32_t first = min(st0 + NST, st1);
+        // the first stages' weights are on their way into L2 while the kernel before ends
+        for (int32_t st = st0; st < first; ++st) prefetch_copies<kLoadOne, false>(&tmW, st, 128, n0);
+        griddep_wait();
+        for (int32_t st = st0; st < first; ++st) load(st, uint32_t(st - st0));
+        __syncthreads();  // the others are set up; tensor memory is allocated
+        griddep_launch_dependents();
+        uint32_t stage = 0, phase = 0;
+        for (int32_t st = st0 + NST; st < st1; ++st) {
+            if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase, p.wait))) {
+                let_copies_land();
+                break;
+            }
+            load(st, stage);
+            if (++stage == uint32_t(NST)) { stage = 0; phase ^= 1u; }
+        }
+        __syncwarp();
+    } else {
+        if (warp == MMA_WARP) {
+            tmem_alloc(smem_addr(tmem_slot), uint32_t(p.tmem_cols));
+            tmem_relinquish();
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        griddep_enter(0u);
+        tmem_base = *tmem_slot;
+    }
+
+    if (warp == MMA_WARP) {
+        // ============================================================ MMA issuer
+        const uint64_t dx = smem_desc(sX16, 16, 1024);
+        const uint32_t x_kb = (uint32_t(T) * 128u) >> 4;  // the second 64 of K
+        uint32_t c = 0, turn = 0;
+        for (int32_t st = st0; st < st1; ++st) {
+            if (!__all_sync(0xffffffffu, mbar_wait(ready_bar(c), turn, p.wait))) break;
+            tc_fence_after();
+            const uint32_t a0 = tmem_base + uint32_t(acc_cols) + c * lin::I8_A_COLS;
+            const uint64_t x0 = dx + c * 2u * x_kb;
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)  // 16 of K each
+                mma_f16_tmem_elect(tmem_base, a0 + ks * 8, x0 + (ks / 4) * x_kb + (ks % 4) * 2, p.idesc, st != st0 || ks != 0 ? 1u : 0u);
+            mma_commit_elect(used_bar(c));
+            turn ^= c;  // two copies in turn
+            c ^= 1u;
+        }
+        // also what the epilogue waits for; after a wait that ran out, no MMA may
+        // still be writing TMEM when it is freed
+        mma_commit_elect(done_bar);
+        __all_sync(0xffffffffu, mbar_wait_slow(done_bar, 0, cleanup_wait(p.wait), false));
+    } else if (warp >= EPI_WARP0) {
+        // ============================================================ to fp16, then epilogue
+        // Two groups of four warps take the stages in turn, so that one's loads and stores
+        // pass while the other converts.
+        const int q = warp & 3, group = ew / 4;  // the TMEM lanes this warp may write
+        const uint32_t row = uint32_t(q * 32 + lane), thread = uint32_t(ew & 3) * 32u + uint32_t(lane);
+        const uint32_t a_tmem = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc_cols);
+        const uint32_t tasks = uint32_t(T) * 8u;
+        const uint32_t c = uint32_t(group);  // the group's copy
+        uint32_t stage = uint32_t(group), phase = 0, turn = 0;
+        bool ok = true;
+        for (int32_t st = st0 + group; st < st1; st += 2) {
+            if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, p.wait))) {
+                ok = false;
+                break;
+            }
+            // the copy's place is free
+            if (!__all_sync(0xffffffffu, mbar_wait(used_bar(c), turn ^ 1u, p.wait))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            // tokens: 16 bytes of K of one token at a time, four on their way together
+            const uint32_t x_from = sX + stage * x_bytes, x_to = sX16 + c * 2u * x_bytes;
+#pragma unroll 1
+            for (uint32_t e0 = thread; e0 < tasks; e0 += 4u * 128u) {
+                uint32_t x[4][4];
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k) {
+                    const uint32_t e = e0 + k * 128u;
+                    if (e < tasks) ld_shared_v4(x_from + swz128(e >> 3, e & 7u), x[k][0], x[k][1], x[k][2], x[k][3]);
+                }
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k) {
+                    const uint32_t e = e0 + k * 128u;
+                    if (e >= tasks) break;
+                    const uint32_t r = e >> 3, u = e & 7u, to = x_to + (u >> 2) * x_bytes, v = (u & 3u) * 2u;
+#pragma unroll
+                    for (uint32_t i = 0; i < 2; ++i) {
+                        const uint2 lo = i8x4_to_f16(x[k][2 * i]), hi = i8x4_to_f16(x[k][2 * i + 1]);
+                        st_shared_v4(to + swz128(r, v + i), lo.x, lo.y, hi.x, hi.y);
+                    }
+                }
+            }
+            uint32_t w[8][4];
+            const uint32_t w_row = sW + stage * lin::I8_W_BYTES;
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) ld_shared_v4(w_row + swz128(row, i), w[i][0], w[i][1], w[i][2], w[i][3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            // the stage has been read: its bytes in flight are what the stream's rate goes by
+            if (lane == 0) mbar_arrive(empty_bar(stage));
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t a[32];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const uint2 f = i8x4_to_f16(w[4 * half + i / 4][i % 4]);
+                    a[2 * i] = f.x;
+                    a[2 * i + 1] = f.y;
+                }
+                tmem_st_32x32b_x32(a_tmem + c * lin::I8_A_COLS + 32 * half, a);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ready_bar(c));
+            stage += 2;
+            if (stage >= uint32_t(NST)) { stage -= uint32_t(NST); phase ^= 1u; }
+            turn ^= 1u;
+        }
+        if (vec) split_columns<true, true>(p, S, rank, ew, lane, m0, n0, valid, columns);
+        else split_columns<true, false>(p, S, rank, ew, lane, m0, n0, valid, columns);
+        ready = __all_sync(0xffffffffu, mbar_wait(done_bar, 0, p.wait)) && ok;
+        tc_fence_after();
+    }
+
+    // ---------------------------------------------------------------- the cluster's sum and the epilogue, as in linear_split
+    __syncwarp();
+    if (S > 1) cluster_sync();
+    else __syncthreads();
+    if (ready) {
+        // two warps per TMEM lane quarter: rows [0, T/2) and [T/2, T) of the tile
+        const int q = warp & 3, t0 = (ew / 4) * (T / 2);
+        with_split(S, [&](auto s) {
+            split_send<decltype(s)::value>(tmem_base + (uint32_t(q * 32) << 16), base, rank, q * 32 + lane, t0, min(t0 + T / 2, valid),
+                                           acc_cols);
+        });
+        tc_fence_before();
+    }
+    __syncwarp();
+    if (S > 1) cluster_sync();
+    else __syncthreads();
+    if (ready) {
+        const bool one = valid <= EPI_WARPS * S;  // a row for each warp at most
+        with_split(S, [&](auto s) {
+            constexpr int SPLIT = decltype(s)::value;
+            if (vec && one) split_rows<true, SPLIT, true, 1>(p, base, rank, ew, lane, m0, n0, valid, columns);
+            else if (vec) split_rows<true, SPLIT, true, kSplitRows>(p, base, rank, ew, lane, m0, n0, valid, columns);
+            else split_rows<true, SPLIT, false, kSplitRows>(p, base, rank, ew, lane, m0, n0, valid, columns);
+        });
+    }
+    if (warp == MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, uint32_t(p.tmem_cols));
+    }
+}
+
 // ------------------------------------------------------------------ D from 8-bit values
 // D = G act'(s P8) and the column sums of D over blocks of rows: linear_grad_kernel with
 // the values before the activation in 8 bits and a scale per row.
