@@ -380,71 +380,114 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The persistent form: a block walks over the rows, its threads keep their columns and
-// the sums of dweight and dbias over them, and the rows of the next STAGES - 1 steps are
-// on their way into shared memory. A thread copies what it will itself read, so
-// that a step waits for the thread's own copies only; the one barrier of a step is that
-// of the two row sums, for R rows at a time.
+constexpr int kBackThreads = 512;  // of a block at most: 128 registers each
+
+// rows_sum for rows side by side in a block that do not wait for one another: a barrier
+// of the row's own threads, none for a row of one warp.
+template <int N>
+__device__ __forceinline__ void own_rows_sum(float (&v)[N], float (*red)[32]) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < N; ++r) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
+    const int wpr = blockDim.x >> 5, lane = threadIdx.x & 31, base = int(threadIdx.y) * wpr;
+    if (wpr == 1) return;
+    if (lane == 0) {
+#pragma unroll
+        for (int r = 0; r < N; ++r) red[r][base + (threadIdx.x >> 5)] = v[r];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
+#pragma unroll
+    for (int r = 0; r < N; ++r) v[r] = lane < wpr ? red[r][base + lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int r = 0; r < N; ++r) v[r] += __shfl_xor_sync(0xffffffffu, v[r], o);
+}
+
+// The persistent form: a block of up to 512 threads walks over the rows, several side by side where
+// they are short; its threads keep their columns and the sums of dweight and dbias over
+// them, and the rows of the next STAGES - 1 steps are on their way into shared memory. A
+// thread copies what it will itself read, so that a step waits for the thread's own
+// copies only; the one barrier of a step is that of the two row sums, for R rows at a time.
 // kShift: rows off 16-byte boundaries. A thread's rows are then a multiple of 8 rows apart
 // (the grid is a multiple of 8), so that all of them start at the same place in a granule
 // and the thread keeps its columns.
-template <typename T, int THREADS, int NV, int R, int STAGES, bool kShift>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) layer_norm_backward_rows_kernel(const LayerNormBackwardArgs p) {
-    constexpr int G = int(sizeof(Raw<T, 8>)) / 16;  // granules of a load
+template <typename T, int NV, int R, int STAGES, bool kShift>
+__global__ void __launch_bounds__(kBackThreads) layer_norm_backward_rows_kernel(const LayerNormBackwardArgs p) {
+    constexpr int G = int(sizeof(Raw<T, 8>)) / 16;          // granules of a load
+    constexpr uint32_t LINE = uint32_t(kBackThreads) * 16u;  // one granule of every thread
+    constexpr uint32_t ARRAY = R * NV * G * LINE, STAGE = 3 * ARRAY;
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float red[2][2 * R][32];
     const int tid = int(threadIdx.y * blockDim.x + threadIdx.x);
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t first = int64_t(blockIdx.x) * int(blockDim.y) * (kShift ? 1 : R) + int(threadIdx.y) * (kShift ? 1 : R);
+    const int64_t base0 = int64_t(blockIdx.x) * int(blockDim.y) * (kShift ? 1 : R);  // the block's first row
+    const int64_t first = base0 + int(threadIdx.y) * (kShift ? 1 : R);
     const int64_t step = int64_t(gridDim.x) * int(blockDim.y) * R;
     const int64_t apart = kShift ? int64_t(gridDim.x) * blockDim.y : 1;  // rows between a thread's R rows
     const bool has_d = p.dh != nullptr;
-    const T *g = static_cast<const T *>(p.g) + first * p.ldg, *h = static_cast<const T *>(p.h) + first * p.ldh,
-            *d = static_cast<const T *>(p.dh) + first * p.lddh;
-    const Row<T, NV, kShift> a(g, int(p.width), first < p.rows);
-    constexpr uint32_t LINE = THREADS * 16;  // one granule of every thread
+    const Row<T, NV, kShift> a(static_cast<const T *>(p.g) + first * p.ldg, int(p.width), first < p.rows);
+    bool has[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) has[j] = a.has(j);
+    // this thread's first element of the rows to be fetched and written next; the others by offsets in bytes
+    const char *gp = reinterpret_cast<const char *>(static_cast<const T *>(p.g) + first * p.ldg + a.at(0));
+    const char *hp = reinterpret_cast<const char *>(static_cast<const T *>(p.h) + first * p.ldh + a.at(0));
+    const char *dp = reinterpret_cast<const char *>(static_cast<const T *>(p.dh) + first * p.lddh + a.at(0));
+    char *xp = reinterpret_cast<char *>(static_cast<T *>(p.dx) + first * p.lddx + a.at(0));
+    constexpr int64_t E = int64_t(sizeof(T));
+    const int64_t g_step = step * p.ldg * E, h_step = step * p.ldh * E, d_step = step * p.lddh * E, x_step = step * p.lddx * E;
+    const int64_t g_row = apart * p.ldg * E, h_row = apart * p.ldh * E, d_row = apart * p.lddh * E, x_row = apart * p.lddx * E;
+    const uint32_t jump = blockDim.x * 16u * G;  // bytes between a thread's loads
     const uint32_t mine = smem_addr(ring) + uint32_t(tid) * 16u;
-    auto place = [&](int stage, int array, int r, int j) {
-        return mine + uint32_t((((stage * 3 + array) * R + r) * NV + j) * G) * LINE;
-    };
-    // rows n steps on -> their slot
-    auto fetch = [&](int64_t row, int64_t n, int stage) {
+    // rows row, row + apart, ... -> the slot at `to`; on to the next step's
+    auto fetch = [&](int64_t row, uint32_t to) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             if (row + r * apart >= p.rows) break;
-            const int64_t ahead = n * step + r * apart;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                if (!a.has(j)) continue;
+                if (!has[j]) continue;
 #pragma unroll
                 for (int k = 0; k < G; ++k) {
-                    const int e = a.at(j) + k * 16 / int(sizeof(T));
-                    copy16_async(place(stage, 0, r, j) + k * LINE, g + ahead * p.ldg + e);
-                    copy16_async(place(stage, 1, r, j) + k * LINE, h + ahead * p.ldh + e);
-                    if (has_d) copy16_async(place(stage, 2, r, j) + k * LINE, d + ahead * p.lddh + e);
+                    const uint32_t at = to + uint32_t((r * NV + j) * G + k) * LINE;
+                    copy16_async(at, gp + r * g_row + j * jump + 16 * k);
+                    copy16_async(at + ARRAY, hp + r * h_row + j * jump + 16 * k);
+                    if (has_d) copy16_async(at + 2 * ARRAY, dp + r * d_row + j * jump + 16 * k);
                 }
             }
         }
         copies_commit();
+        gp += g_step;
+        hp += h_step;
+        dp += d_step;
     };
-    auto loaded = [&](uint32_t at) {
+    auto values = [&](uint32_t at, int j) {
         Raw<T, 8> v;
 #pragma unroll
         for (int k = 0; k < G; ++k)
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.q[k].x), "=r"(v.q[k].y), "=r"(v.q[k].z), "=r"(v.q[k].w) : "r"(at + k * LINE) : "memory");
-        return v;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.q[k].x), "=r"(v.q[k].y), "=r"(v.q[k].z), "=r"(v.q[k].w)
+                         : "r"(at + k * LINE)
+                         : "memory");
+        a.keep(v, j);
+        return widen<T, 8>(v);
     };
     F32<8> dw[NV], db[NV];
-    Raw<T, 8> w16[NV];  // a weight of T's type; fp32 weights are read again for each row
+    // a weight of T's type; fp32 weights, and those of four loads per thread, whose registers
+    // the sums need, are read again for each row
+    constexpr bool kKeep = NV < 4;
+    Raw<T, 8> w16[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) dw[j].p[i] = db[j].p[i] = splat<8>(0.0f);
-        if (a.has(j) && !p.w_f32) w16[j] = a.column(p.w, j);
+        if (kKeep && has[j] && !p.w_f32) w16[j] = a.column(p.w, j);
     }
-    auto weight = [&](int j) { return p.w_f32 ? a.column(p.w, true, j) : widen<T, 8>(w16[j]); };
-    for (int s = 0; s < STAGES; ++s) fetch(first + s * step, s, s);
+    auto weight = [&](int j) { return !kKeep || p.w_f32 ? a.column(p.w, p.w_f32 != 0, j) : widen<T, 8>(w16[j]); };
+    for (int s = 0; s < STAGES; ++s) fetch(first + s * step, mine + uint32_t(s) * STAGE);
     float mu_next[R], rs_next[R];
     auto stats = [&](int64_t row) {
 #pragma unroll
@@ -455,66 +498,61 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) layer_norm_ba
         }
     };
     stats(first);
-    const int64_t base0 = int64_t(blockIdx.x) * int(blockDim.y) * (kShift ? 1 : R);  // the block's first row: the loop is the same for all its threads
-    int stage = 0, flip = 0;
-    int64_t n = 0;
-    for (int64_t base = base0, row = first; base < p.rows; base += step, row += step, ++n, flip ^= 1) {
+    uint32_t slot = mine;
+    int flip = 0;
+    for (int64_t base = base0, row = first; base < p.rows; base += step, row += step, flip ^= 1, xp += x_step) {
         float mu[R], rs[R], sum[2 * R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) mu[r] = mu_next[r], rs[r] = rs_next[r];
+        for (int r = 0; r < R; ++r) mu[r] = -mu_next[r], rs[r] = rs_next[r];
         stats(row + step);
         copies_wait<STAGES - 1>();
         int left = 0;  // rows of this thread that exist
 #pragma unroll
         for (int r = 0; r < R; ++r) left += row + r * apart < p.rows;
-        auto values = [&](int array, int r, int j) {
-            Raw<T, 8> v = loaded(place(stage, array, r, j));
-            a.keep(v, j);
-            return widen<T, 8>(v);
-        };
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             float2 s1 = splat<8>(0.0f), s2 = s1;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                if (r >= left || !a.has(j)) continue;
-                const F32<8> fg = values(0, r, j), fh = values(1, r, j), w = weight(j);
+                if (r >= left || !has[j]) continue;
+                const uint32_t at = slot + uint32_t((r * NV + j) * G) * LINE;
+                const F32<8> fg = values(at, j), fh = values(at + ARRAY, j), w = weight(j);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 gw = mul2(fg.p[i], w.p[i]);
                     s1 = add2(s1, gw);
-                    s2 = fma2(gw, add2(fh.p[i], splat<8>(-mu[r])), s2);
+                    s2 = fma2(gw, add2(fh.p[i], splat<8>(mu[r])), s2);
                 }
             }
             sum[2 * r] = total(s1);
             sum[2 * r + 1] = total(s2);
         }
-        rows_sum<2 * R>(sum, red[flip]);
-        // dx = rstd g + (-rstd mean(g u)) u + (-rstd mean(g)) + dh
+        own_rows_sum<2 * R>(sum, red[flip]);
+        // with c = h - mean: dx = (rstd g) w + c (-rstd^2 mean(g u)) + (-rstd mean(g)) + dh, dw = sum (rstd g) c
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float2 rs2 = splat<8>(rs[r]), c1 = splat<8>(-rs[r] * (sum[2 * r] * p.inv_width)),
-                         c2 = splat<8>(-rs[r] * (sum[2 * r + 1] * rs[r] * p.inv_width));
-            T *dx = static_cast<T *>(p.dx) + (row + r * apart) * p.lddx;
+                         c2 = splat<8>(-rs[r] * rs[r] * (sum[2 * r + 1] * rs[r] * p.inv_width));
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                if (r >= left || !a.has(j)) continue;
-                const F32<8> fg = values(0, r, j), fh = values(1, r, j), w = weight(j);
+                if (r >= left || !has[j]) continue;
+                const uint32_t at = slot + uint32_t((r * NV + j) * G) * LINE;
+                const F32<8> fg = values(at, j), fh = values(at + ARRAY, j), w = weight(j);
                 F32<8> v;
-                if (has_d) v = values(2, r, j);
+                if (has_d) v = values(at + 2 * ARRAY, j);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 u = mul2(add2(fh.p[i], splat<8>(-mu[r])), rs2);
-                    dw[j].p[i] = fma2(fg.p[i], u, dw[j].p[i]);
+                    const float2 c = add2(fh.p[i], splat<8>(mu[r])), t = mul2(fg.p[i], rs2);
+                    dw[j].p[i] = fma2(t, c, dw[j].p[i]);
                     db[j].p[i] = add2(fg.p[i], db[j].p[i]);
-                    const float2 through = has_d ? add2(v.p[i], c1) : c1;
-                    v.p[i] = fma2(u, c2, fma2(mul2(fg.p[i], w.p[i]), rs2, through));
+                    v.p[i] = fma2(c, c2, fma2(t, w.p[i], has_d ? add2(v.p[i], c1) : c1));
                 }
-                store_out<T, kOutSame>(dx + a.at(j), v, a.lo(j), a.hi(j));
+                store_out<T, kOutSame>(reinterpret_cast<T *>(xp + r * x_row + j * jump), v, a.lo(j), a.hi(j));
             }
         }
-        fetch(row + STAGES * step, n + STAGES, stage);  // this thread has read the slot
-        if (++stage == STAGES) stage = 0;
+        fetch(row + STAGES * step, slot);  // this thread has read the slot
+        slot += STAGE;
+        if (slot == mine + STAGES * STAGE) slot = mine;
     }
     copies_wait<0>();
     if (p.partial == nullptr) return;
@@ -653,17 +691,23 @@ constexpr int kKeptBytes = 200 * 1024;
 int kept_bytes(int64_t width) { return width * 4 <= kKeptBytes ? int(width * 4) : 0; }
 int any_threads(int64_t width) { return int(std::min<int64_t>(1024, std::max<int64_t>(32, cdiv(cdiv(width, 4), 32) * 32))); }
 
-// Four loads per thread, and so small blocks of which several are on an SM at different
-// points of load, sums and store, for several waves of long rows.
-int least_loads(int64_t rows, int64_t width, int64_t waves, size_t es, int num_sms) {
-    if (width <= 2048 || rows < waves * num_sms) return 1;
-    return es == 2 ? 4 : 2;
+// One load per thread for up to two rows an SM, where the chain load - sums - store is
+// what counts; then more, so that blocks are small and several on an SM are at different
+// points of it: two (1000 x 4096 bf16 with residual, one / two / four loads: 10.3 / 7.8 /
+// 8.1 us, 2000 x 4096 17.9 / 13.0 / 14.4, 8192 x 4096 63.8 / 44.2 / 44.2), four of long rows
+// (4096 x 8192 72.9 / 47.2 / 44.3, to 8 bits 76.7 / 48.2 / 40.9). fp32's are twice as long
+// (4096 x 4096 49.9 / 53.2 / 55.8).
+int norm_loads(int64_t rows, int64_t width, size_t es, int num_sms) {
+    if (es == 4 || rows <= 2 * num_sms) return 1;
+    return width < 8192 ? 2 : 4;
 }
+// Without weights and further sums, four (16384 x 1024 bf16 11.5 / 9.8 / 9.1 us, 4096 x 16384
+// 38.3 / 38.0 / 32.7, 300 x 4096 1.5 / 1.7 / 1.7).
+int quantize_loads(int64_t rows, size_t es, int num_sms) { return es == 4 || rows <= 2 * num_sms ? 1 : 4; }
 
 template <typename T, int OUT>
 cudaError_t norm(const LayerNormArgs &p, int num_sms, cudaStream_t stream) {
-    const int64_t waves = p.r != nullptr && OUT == kOutSame && p.width <= 8192 ? 16 : 4;
-    const int least = least_loads(p.rows, p.width, waves, sizeof(T), num_sms);
+    const int least = norm_loads(p.rows, p.width, sizeof(T), num_sms);
     auto go = [&](auto *k, const RowShape &s) {
         return launch(k, dim3(unsigned(cdiv(p.rows, s.rpb))), dim3(unsigned(s.tpr), unsigned(s.rpb)), 0, stream, p);
     };
@@ -690,7 +734,7 @@ cudaError_t norm(const LayerNormArgs &p, int num_sms, cudaStream_t stream) {
 
 template <typename T, int OUT>
 cudaError_t quantize(const QuantizeArgs &p, int num_sms, cudaStream_t stream) {
-    const int least = least_loads(p.rows, p.width, 4, sizeof(T), num_sms);
+    const int least = quantize_loads(p.rows, sizeof(T), num_sms);
     auto go = [&](auto *k, const RowShape &s) {
         return launch(k, dim3(unsigned(cdiv(p.rows, s.rpb))), dim3(unsigned(s.tpr), unsigned(s.rpb)), 0, stream, p);
     };
@@ -715,13 +759,13 @@ cudaError_t quantize(const QuantizeArgs &p, int num_sms, cudaStream_t stream) {
                   int32_t(kept > 0));
 }
 
-// The persistent backward form. Blocks of 256 threads, two on an SM, hold rows of up to
-// 4096 elements in two loads per thread, blocks of 512 rows of up to 8192; 1024 threads
-// (64 registers each) 16-bit rows of up to 16384. A slot is 16 bytes of each array for every
-// load of a thread.
+// The persistent backward form: one block of up to 512 threads (128 registers each) on an
+// SM, NV loads of 8 elements per thread and as many rows side by side as there are threads
+// for; NV by how many of the threads' loads are used. A step's copies take 16 bytes of each
+// array for every load of a thread (32 of fp32).
 struct BackwardPlan {
     bool ok, shift;
-    int threads, nv, rpt, tpr, rpb, grid, smem;
+    int nv, rpt, tpr, rpb, grid;
 };
 
 template <typename T>
@@ -730,51 +774,47 @@ BackwardPlan plan_backward(const LayerNormBackwardArgs &p, int num_sms) {
     b.shift = sizeof(T) == 2 && p.shift;
     if (!p.vec && !b.shift) return b;
     const int64_t loads = cdiv(p.width + (b.shift ? 7 : 0), 8);
-    b.threads = loads <= 512 ? 256 : loads <= 1024 ? 512 : 1024;
+    // one load per thread for few rows, whose chain is then short, and for short ones (64 x
+    // 4096 6.1 / 8.2 us with two, 300 x 4096 8.6 / 10.3, 4096 x 768 12.3 / 13.2); else two (8192 x
+    // 4096 56.2 / 50.7, with three 56.4), more where the row needs them
+    b.nv = loads <= 512 && (p.rows <= 2 * num_sms || loads <= 128) ? 1 : loads <= 1024 ? 2 : loads <= 1536 ? 3 : 4;
     if (loads > (sizeof(T) == 2 ? 2048 : 1024)) return b;
-    b.nv = loads <= 256 ? 1 : 2;
     b.tpr = int(cdiv(cdiv(loads, b.nv), 32) * 32);
-    while (b.threads % b.tpr) b.tpr += 32;
-    b.rpb = b.threads / b.tpr;
-    const int most = (b.threads == 256 ? 2 : 1) * num_sms;
+    if (b.tpr > kBackThreads) return b;
+    b.rpb = std::min(kBackThreads / b.tpr, 15);  // a barrier each, besides the block's
     // shifted: a thread's rows are 8 k apart, or it has one row only
-    const bool one_row = b.shift && cdiv(p.rows, b.rpb) <= most;
-    b.rpt = b.threads == 1024 || sizeof(T) == 4 || one_row ? 1 : 2;
-    b.grid = int(std::min<int64_t>(cdiv(p.rows, b.rpb * b.rpt), most));
+    const bool one_row = b.shift && cdiv(p.rows, b.rpb) <= num_sms;
+    b.rpt = sizeof(T) == 4 || b.nv > 2 || one_row ? 1 : 2;
+    b.grid = int(std::min<int64_t>(cdiv(p.rows, b.rpb * b.rpt), num_sms));
     if (b.shift && !one_row) {
-        if (most < 8) return b;
-        b.grid = int(std::min<int64_t>(cdiv(b.grid, 8) * 8, most / 8 * 8));
+        if (num_sms < 8) return b;
+        b.grid = int(std::min<int64_t>(cdiv(b.grid, 8) * 8, num_sms / 8 * 8));
     }
     b.ok = true;
     return b;
 }
 
-template <typename T, int THREADS, int NV, int R, int STAGES, bool kShift>
+template <typename T, int NV, int R, int STAGES, bool kShift>
 cudaError_t backward_rows(const LayerNormBackwardArgs &p, const BackwardPlan &b, int dev, cudaStream_t stream) {
-    constexpr int ring = THREADS * 16 * (int(sizeof(Raw<T, 8>)) / 16) * 3 * NV * R * STAGES, sums = THREADS * NV * 8 * 4 + 64;
-    constexpr int smem = ring > sums ? ring : sums;
-    static_assert(smem + 4 * R * 32 * 4 <= (THREADS == 256 ? 113 : 226) * 1024, "shared memory of an SM, or of half of one");
-    const cudaError_t e = allow_smem<layer_norm_backward_rows_kernel<T, THREADS, NV, R, STAGES, kShift>>(dev, smem);
+    constexpr int per_thread = 16 * (int(sizeof(Raw<T, 8>)) / 16) * 3 * NV * R * STAGES, sums = NV * 8 * 4;
+    static_assert(per_thread >= sums, "the sums' way out fits the ring");
+    static_assert(kBackThreads * per_thread + 4 * R * 32 * 4 <= 226 * 1024, "shared memory of an SM");
+    const cudaError_t e = allow_smem<layer_norm_backward_rows_kernel<T, NV, R, STAGES, kShift>>(dev, kBackThreads * per_thread);
     if (e != cudaSuccess) return e;
-    return launch(layer_norm_backward_rows_kernel<T, THREADS, NV, R, STAGES, kShift>, dim3(unsigned(b.grid)),
-                  dim3(unsigned(b.tpr), unsigned(b.rpb)), smem, stream, p);
+    return launch(layer_norm_backward_rows_kernel<T, NV, R, STAGES, kShift>, dim3(unsigned(b.grid)),
+                  dim3(unsigned(b.tpr), unsigned(b.rpb)), kBackThreads * per_thread, stream, p);
 }
 
 template <typename T, bool kShift>
 cudaError_t backward_rows(const LayerNormBackwardArgs &p, const BackwardPlan &b, int dev, cudaStream_t stream) {
     if constexpr (sizeof(T) == 4) {
-        if (b.threads == 256)
-            return b.nv == 1 ? backward_rows<T, 256, 1, 1, 4, kShift>(p, b, dev, stream) : backward_rows<T, 256, 2, 1, 2, kShift>(p, b, dev, stream);
-        return backward_rows<T, 512, 2, 1, 2, kShift>(p, b, dev, stream);
+        return b.nv == 1 ? backward_rows<T, 1, 1, 4, kShift>(p, b, dev, stream) : backward_rows<T, 2, 1, 2, kShift>(p, b, dev, stream);
     } else {
-        if (b.threads == 256) {
-            if (b.nv == 1)
-                return b.rpt == 1 ? backward_rows<T, 256, 1, 1, 4, kShift>(p, b, dev, stream) : backward_rows<T, 256, 1, 2, 4, kShift>(p, b, dev, stream);
-            return b.rpt == 1 ? backward_rows<T, 256, 2, 1, 4, kShift>(p, b, dev, stream) : backward_rows<T, 256, 2, 2, 2, kShift>(p, b, dev, stream);
-        }
-        if (b.threads == 512)
-            return b.rpt == 1 ? backward_rows<T, 512, 2, 1, 4, kShift>(p, b, dev, stream) : backward_rows<T, 512, 2, 2, 2, kShift>(p, b, dev, stream);
-        return backward_rows<T, 1024, 2, 1, 2, kShift>(p, b, dev, stream);
+        if (b.nv == 1)
+            return b.rpt == 1 ? backward_rows<T, 1, 1, 4, kShift>(p, b, dev, stream) : backward_rows<T, 1, 2, 4, kShift>(p, b, dev, stream);
+        if (b.nv == 2)
+            return b.rpt == 1 ? backward_rows<T, 2, 1, 4, kShift>(p, b, dev, stream) : backward_rows<T, 2, 2, 2, kShift>(p, b, dev, stream);
+        return b.nv == 3 ? backward_rows<T, 3, 1, 3, kShift>(p, b, dev, stream) : backward_rows<T, 4, 1, 2, kShift>(p, b, dev, stream);
     }
 }
 
