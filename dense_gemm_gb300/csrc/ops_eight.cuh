@@ -66,8 +66,9 @@ __device__ __forceinline__ uint2 load_eight(const uint8_t *p, int64_t n) {
 // Rows of `inner` 8-bit elements, any base and pitch -> rows of 16-bit ones on 128-byte
 // lines (dst 128-byte aligned, ld_dst a multiple of 64), zero in the rest of a row's last
 // granule. kPlain: whole numbers as they are, in fp16. Else act(scale x), rounded to T.
-// A thread has one granule of the copy in every row it visits, four rows at a time. Bound by
-// DRAM, one byte read and two written.
+// A thread has one granule of the copy in every row it visits, eight rows at a time. Bound by
+// DRAM, one byte read and two written, and with an activation by its arithmetic. (Two
+// granules per thread: stores 32 bytes apart, 27 million whole numbers 17.9 us instead of 12.0.)
 struct ExpandJob {
     const uint8_t *src;
     void *dst;
@@ -77,6 +78,7 @@ struct ExpandJob {
     int32_t lg;          // 2^lg granules of a row, 256 >> lg rows per block and step
     int32_t bx, by;      // blocks along a row, along the rows; 0: no job
 };
+constexpr int kExpandAhead = 8;
 
 template <typename T, bool kPlain, bool kAligned, uint32_t ACT>
 __device__ __forceinline__ void expand_rows(const ExpandJob &J, int block) {
@@ -84,7 +86,7 @@ __device__ __forceinline__ void expand_rows(const ExpandJob &J, int block) {
     const int64_t i0 = 8 * ((int64_t(block % J.bx) << J.lg) + tx);
     if (i0 >= J.inner) return;
     const int64_t left = J.inner - i0, step = int64_t(J.by) * per;
-    constexpr int AHEAD = 4;
+    constexpr int AHEAD = kAligned ? kExpandAhead : kExpandAhead / 2;
 #pragma unroll 1
     for (int64_t r = int64_t(block / J.bx) * per + ty; r < J.rows; r += AHEAD * step) {
         uint2 w[AHEAD];

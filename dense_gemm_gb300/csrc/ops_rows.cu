@@ -701,24 +701,32 @@ int norm_loads(int64_t rows, int64_t width, size_t es, int num_sms) {
     if (es == 4 || rows <= 2 * num_sms) return 1;
     return width < 8192 ? 2 : 4;
 }
+// Of two and four loads the one whose blocks leave fewer of an SM's threads idle (64
+// registers each), where that counts: 8191 elements take 544 threads with two loads, one
+// block on an SM, 288 with four, three (4096 x 8191 87 us with two).
+RowShape norm_shape(int64_t rows, int64_t width, size_t es, int num_sms) {
+    const int least = norm_loads(rows, width, es, num_sms);
+    const RowShape s = row_shape(width, least), t = row_shape(width, 4);
+    auto busy = [](const RowShape &r) { return r.tpr > 0 ? 1024 / (r.tpr * r.rpb) * (r.tpr * r.rpb) : 0; };
+    return least == 2 && s.fits && t.fits && busy(s) * 100 < busy(t) * 85 ? t : s;
+}
 // Without weights and further sums, four (16384 x 1024 bf16 11.5 / 9.8 / 9.1 us, 4096 x 16384
 // 38.3 / 38.0 / 32.7, 300 x 4096 1.5 / 1.7 / 1.7).
 int quantize_loads(int64_t rows, size_t es, int num_sms) { return es == 4 || rows <= 2 * num_sms ? 1 : 4; }
 
 template <typename T, int OUT>
 cudaError_t norm(const LayerNormArgs &p, int num_sms, cudaStream_t stream) {
-    const int least = norm_loads(p.rows, p.width, sizeof(T), num_sms);
     auto go = [&](auto *k, const RowShape &s) {
         return launch(k, dim3(unsigned(cdiv(p.rows, s.rpb))), dim3(unsigned(s.tpr), unsigned(s.rpb)), 0, stream, p);
     };
     if constexpr (sizeof(T) == 2) {
-        const RowShape s = row_shape(p.width + 7, least);
+        const RowShape s = norm_shape(p.rows, p.width + 7, sizeof(T), num_sms);
         if (p.shift && s.fits)
             return go(s.nv == 1   ? layer_norm_kernel<T, 1, OUT, true>
                       : s.nv == 2 ? layer_norm_kernel<T, 2, OUT, true>
                                   : layer_norm_kernel<T, 4, OUT, true>, s);
     }
-    const RowShape s = row_shape(p.width, least);
+    const RowShape s = norm_shape(p.rows, p.width, sizeof(T), num_sms);
     if (p.vec && s.fits)
         return go(s.nv == 1   ? layer_norm_kernel<T, 1, OUT, false>
                   : s.nv == 2 ? layer_norm_kernel<T, 2, OUT, false>
