@@ -267,7 +267,7 @@ template <typename T, bool kPlain>
 cudaError_t expand_operands(Operand *a, ExpandJob ja, Operand *b, ExpandJob jb, int32_t type, cudaStream_t stream) {
     for (Operand *o : {a, b}) {
         const ExpandJob &j = o == a ? ja : jb;
-        if (o == nullptr || j.dst == nullptr) continue;
+        if (j.dst == nullptr) continue;
         o->data = j.dst;
         o->ld = j.ld_dst;
         o->type = type;
@@ -892,13 +892,14 @@ gemm_status_t backward(const gemm_matrix_t *G, const gemm_matrix_t *A, const gem
     const bool pack_a = !eight && products && present(dB) && s.a > 0, pack_b = products && present(dA) && s.b > 0;
     const bool packs = pack_a || pack_b || expand;
     if (eight && !expand) a.type = G->type;  // not read
-    if (expand) {
-        const ExpandJob job = expand_job(a, ws_a, saved.scale_a, uint32_t(saved.act_a), ds->num_sms), none{};
-        const cudaError_t e = G->type == GEMM_TYPE_F16 ? expand_operands<__half, false>(&a, job, nullptr, none, G->type, stream)
-                                                       : expand_operands<__nv_bfloat16, false>(&a, job, nullptr, none, G->type, stream);
+    if (expand) {  // and B's copy in the same launch
+        const ExpandJob ja = expand_job(a, ws_a, saved.scale_a, uint32_t(saved.act_a), ds->num_sms),
+                        jb = pack_b ? expand_job(b, ws_b, nullptr, 0, ds->num_sms) : ExpandJob{};
+        const cudaError_t e = G->type == GEMM_TYPE_F16 ? expand_operands<__half, false>(&a, ja, &b, jb, G->type, stream)
+                                                       : expand_operands<__nv_bfloat16, false>(&a, ja, &b, jb, G->type, stream);
         if (e != cudaSuccess) return GEMM_ERR_CUDA;
     }
-    if ((pack_a || pack_b) && pack_operands(&a, pack_a ? ws_a : nullptr, &b, pack_b ? ws_b : nullptr, ds->num_sms, stream) != cudaSuccess)
+    if (!expand && (pack_a || pack_b) && pack_operands(&a, pack_a ? ws_a : nullptr, &b, pack_b ? ws_b : nullptr, ds->num_sms, stream) != cudaSuccess)
         return GEMM_ERR_CUDA;
     Operand d_rows{G->data, M, N, G->stride_row, G->type, false};
     const GradPlan gp = plan_grad(M, N);
