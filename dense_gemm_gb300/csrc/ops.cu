@@ -506,7 +506,8 @@ gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t 
 // two tiles of 128 rows, and for small products of any shape, converting the weights anew for
 // every 128 rows costs less than a copy of them that is written and read again (direct /
 // copied: 256 x 8192 x 8192 48.8 / 72.3 us, 256 x 4096 x 4096 17.2 / 19.7, 512 x 4096 x 4096
-// 27.5 / 25.3, 512 x 8192 x 8192 96 / 78, 1024 x 1024 x 1024 8.8 / 10.8, 1 x 4096 x 4096 7.4 / 14.1). By the sizes alone, since the workspace goes by it.
+// 27.5 / 25.3, 512 x 8192 x 8192 96 / 78, 1024 x 1024 x 1024 8.8 / 10.8, 1 x 4096 x 4096
+// 7.4 / 14.1). By the sizes alone, since the workspace goes by it.
 bool int8_direct(int64_t M, int64_t N, int64_t K) {
     return M <= 256 || double(M) * double(N) * double(K) <= double(int64_t(1) << 30);
 }
@@ -899,7 +900,8 @@ gemm_status_t backward(const gemm_matrix_t *G, const gemm_matrix_t *A, const gem
                                                        : expand_operands<__nv_bfloat16, false>(&a, ja, &b, jb, G->type, stream);
         if (e != cudaSuccess) return GEMM_ERR_CUDA;
     }
-    if (!expand && (pack_a || pack_b) && pack_operands(&a, pack_a ? ws_a : nullptr, &b, pack_b ? ws_b : nullptr, ds->num_sms, stream) != cudaSuccess)
+    if (!expand && packs &&
+        pack_operands(&a, pack_a ? ws_a : nullptr, &b, pack_b ? ws_b : nullptr, ds->num_sms, stream) != cudaSuccess)
         return GEMM_ERR_CUDA;
     Operand d_rows{G->data, M, N, G->stride_row, G->type, false};
     const GradPlan gp = plan_grad(M, N);

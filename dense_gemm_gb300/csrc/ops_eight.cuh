@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         const int q = warp & 3, group = ew / 4;  // the TMEM lanes this warp may write
         const uint32_t row = uint32_t(q * 32 + lane), thread = uint32_t(ew & 3) * 32u + uint32_t(lane);
         const uint32_t a_tmem = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc_cols);
-        const uint32_t tasks = uint32_t(T) * 8u;
+        const uint32_t tasks = uint32_t(valid) * 8u;  // what lies in the copies of further tokens reaches no row of C
         const uint32_t c = uint32_t(group);  // the group's copy
         uint32_t stage = uint32_t(group), phase = 0, turn = 0;
         bool ok = true;

@@ -809,7 +809,9 @@ BackwardPlan plan_backward(const LayerNormBackwardArgs &p, int num_sms) {
     // shifted: a thread's rows are 8 k apart, or it has one row only
     const bool one_row = b.shift && cdiv(p.rows, b.rpb) <= num_sms;
     b.rpt = sizeof(T) == 4 || b.nv > 2 || one_row ? 1 : 2;
-    b.grid = int(std::min<int64_t>(cdiv(p.rows, b.rpb * b.rpt), num_sms));
+    // as few blocks, and parts of the column sums, as take the same number of steps
+    const int64_t units = cdiv(p.rows, b.rpb * b.rpt);
+    b.grid = int(cdiv(units, cdiv(units, num_sms)));
     if (b.shift && !one_row) {
         if (num_sms < 8) return b;
         b.grid = int(std::min<int64_t>(cdiv(b.grid, 8) * 8, num_sms / 8 * 8));

@@ -101,7 +101,9 @@ typedef struct {
  * pairs where they keep the GPU's pairs busy; below that (few tokens: decoding,
  * short prompts; few output tiles) tiles of 128 columns by 16..256 rows with K
  * split over a cluster of up to 8 CTAs, whose partial sums are added in rank
- * order through distributed shared memory. Every result is deterministic.
+ * order through distributed shared memory. int8 operands of up to 256 rows, and
+ * small products of them, have a kernel of their own, whatever the flags.
+ * Every result is deterministic.
  * The second kernel may ask for lines of B in L2 before the kernels before it on
  * the stream have ended; it uses no data of theirs before they have.
  */
