@@ -66,12 +66,15 @@ constexpr int kSplitTs = 5, kSplitSs = 4;
 // other's stream.
 constexpr int split_stages(int T) { return T == 16 || T == 128 ? 3 : 2; }
 
-// linear_int8's shapes: the same T up to 128, whose tokens in fp16 leave room for one CTA
-// on an SM.
-constexpr int kInt8Ts = 4;
-constexpr int int8_stages(int T) { return T == 16 ? 5 : T == 64 ? 3 : 4; }
-constexpr int int8_smem(int T) { return lin::i8_smem(int8_stages(T), T); }
-static_assert(int8_smem(16) <= 115712 && int8_smem(32) <= 115712 && int8_smem(64) <= 115712 && int8_smem(128) <= 232448,
+// linear_int8's shapes: T = 16 << t rows of C, from 128 on with the tokens in fp16 (wide); two
+// CTAs on an SM up to T = 64.
+constexpr int kInt8Ts = 5;
+constexpr bool int8_wide(int T) { return T >= 128; }
+constexpr int int8_stages(int T) { return T <= 32 ? 4 : T == 64 ? 3 : 6; }
+constexpr int int8_x(int T) { return T == 128 ? 4 : 2; }
+constexpr int int8_smem(int T) { return lin::i8_smem(int8_wide(T), int8_stages(T), int8_x(T), T); }
+static_assert(int8_smem(16) <= 115712 && int8_smem(32) <= 115712 && int8_smem(64) <= 115712 && int8_smem(128) <= 232448 &&
+                  int8_smem(256) <= 232448,
               "two CTAs on an SM, or one");
 
 // Done once per device: this file's kernels' shared-memory limits, and how many
@@ -132,13 +135,14 @@ const OpsState *ops_init(int dev, int num_sms) {
             o.split_slots[t][s] = (T <= 64 ? 2 : 1) * std::max(n, 1) << s;
         }
     }
-    if (e == cudaSuccess) e = allow_smem(linear_int8, 232448);
+    if (e == cudaSuccess) e = allow_smem(linear_int8<false>, 232448);
+    if (e == cudaSuccess) e = allow_smem(linear_int8<true>, 232448);
     for (int t = 0; e == cudaSuccess && t < kInt8Ts; ++t) {
         const int T = 16 << t, per_sm = T <= 64 ? 2 : 1;
         o.int8_slots[t][0] = per_sm * num_sms;
         for (int s = 1; e == cudaSuccess && s < kSplitSs; ++s) {
             int n = 0;
-            e = clusters_at_once(&n, linear_int8, 1u << s, int8_smem(T), num_sms);
+            e = clusters_at_once(&n, int8_wide(T) ? linear_int8<true> : linear_int8<false>, 1u << s, int8_smem(T), num_sms);
             o.int8_slots[t][s] = per_sm * std::max(n, 1) << s;
         }
     }
@@ -503,28 +507,35 @@ gemm_status_t run_linear(const Operand &A, const Operand &B, int64_t M, int64_t 
 }
 
 // Whole numbers: linear_int8, or both operands copied to fp16 and a 16-bit product. Up to
-// two tiles of 128 rows, and for small products of any shape, converting the weights anew for
-// every 128 rows costs less than a copy of them that is written and read again (direct /
-// copied: 256 x 8192 x 8192 48.8 / 72.3 us, 256 x 4096 x 4096 17.2 / 19.7, 512 x 4096 x 4096
-// 27.5 / 25.3, 512 x 8192 x 8192 96 / 78, 1024 x 1024 x 1024 8.8 / 10.8, 1 x 4096 x 4096
-// 7.4 / 14.1). By the sizes alone, since the workspace goes by it.
+// three tiles of 256 rows, and for small products of any shape, converting the weights anew for
+// every tile costs less than a copy of them that is written and read again (linear_int8 / both
+// copied: 256 x 8192 x 8192 33.7 / 72.9 us, 512 x 8192 x 8192 57.8 / 78.4, 1024 x 8192 x 8192 110 / 113, 1024 x
+// 16384 x 4096 121 / 107, 512 x 4096 x 4096 21.8 / 25.8, 2048 x 4096 x 4096 64 / 54, 1 x 4096 x
+// 4096 7.4 / 14.1). By the sizes alone, since the workspace goes by it.
 bool int8_direct(int64_t M, int64_t N, int64_t K) {
-    return M <= 256 || double(M) * double(N) * double(K) <= double(int64_t(1) << 30);
+    return M <= 768 || double(M) * double(N) * double(K) <= double(int64_t(1) << 30);
+}
+// Whether linear_int8 takes the tokens as fp16 (wide): more than 64 of them, and not in small
+// products, where the copy's launch counts (128 x 1024 x 1024 5.5 us without, 7.7 with; 128 x
+// 8192 x 8192 28.4 / 24.0; 48 x 4096 x 8192 13.0 / 14.1).
+bool int8_tokens_copied(int64_t M, int64_t N, int64_t K) {
+    return M > 64 && double(M) * double(N) * double(K) > 0.75 * double(int64_t(1) << 30);
 }
 
 // linear_int8's shape, as plan_split: a stage every kInt8Step along one CTA, and on an SM
 // every kInt8Sm whatever it runs (a stage's conversion takes its warps' time).
 // (4096 x 4096, one token: T = 16, S = 4 7.4 us, 8 7.8, 2 10.5, 1 16.4; 64 x 16384 x 4096:
-// T = 64, S = 2 19.6, 1 22.9, T = 32, S = 2 26.7; 128 x 16384 x 4096: T = 128, S = 1 28.7, T = 64 31.8.)
-constexpr double kInt8Step[kInt8Ts] = {0.37, 0.45, 0.53, 0.68}, kInt8Sm[kInt8Ts] = {0.33, 0.38, 0.45, 0.68}, kInt8Cluster = 0.15;
+// T = 64, S = 2 19.6, 1 22.9, T = 32, S = 2 26.7; 256 x 8192 x 8192: T = 256, S = 2 33.8, T = 128, S = 1 37.2.)
+constexpr double kInt8Step[kInt8Ts] = {0.37, 0.45, 0.53, 0.54, 0.82}, kInt8Sm[kInt8Ts] = {0.33, 0.38, 0.45, 0.58, 0.86}, kInt8Cluster = 0.15;
 struct Int8Plan {
     int T, split;
 };
-Int8Plan plan_int8(int64_t M, int64_t N, int64_t steps, const DeviceState &ds, const OpsState &o) {
-    Int8Plan best{16, 1};
+Int8Plan plan_int8(int64_t M, int64_t N, int64_t steps, bool wide, const DeviceState &ds, const OpsState &o) {
+    Int8Plan best{wide ? 128 : 16, 1};
     double least = 1e300;
     for (int t = 0; t < kInt8Ts; ++t) {
         const int T = 16 << t;
+        if (int8_wide(T) != wide) continue;
         const int64_t tiles = cdiv(N, lin::SPLIT_ROWS) * cdiv(M, T);
         for (int s = 0; s < kSplitSs && (int64_t(1) << s) <= steps; ++s) {
             const int64_t S = int64_t(1) << s, ctas = tiles * S;
@@ -547,7 +558,7 @@ Int8Plan plan_int8(int64_t M, int64_t N, int64_t steps, const DeviceState &ds, c
     return best;
 }
 
-// linear_int8 on operands that TMA can describe. K >= 1.
+// linear_int8 on operands that TMA can describe; with many tokens A is their copy in fp16. K >= 1.
 gemm_status_t run_int8(const Operand &A, const Operand &B, int64_t M, int64_t N, int64_t K, const EpilogueParams &e, const DeviceState *ds,
                        const OpsState *ops, cudaStream_t stream) {
     LinearParams p;
@@ -558,23 +569,25 @@ gemm_status_t run_int8(const Operand &A, const Operand &B, int64_t M, int64_t N,
     p.num_kb = int32_t(cdiv(K, 128));
     p.wait.timeout_ns = g_timeout_ns.load();
     p.wait.epoch = next_epoch();
-    const Int8Plan pl = plan_int8(M, N, p.num_kb, *ds, *ops);
+    const bool wide = A.type == GEMM_TYPE_F16;
+    const Int8Plan pl = plan_int8(M, N, p.num_kb, wide, *ds, *ops);
     const int64_t nm = cdiv(M, pl.T), nn = cdiv(N, lin::SPLIT_ROWS);
     if (nm * nn > kMaxDim / lin::MAX_SPLIT) return GEMM_ERR_UNSUPPORTED;
     CUtensorMap tmW, tmX;
-    if (!encode_operand(&tmW, &p.b, B, 1, lin::SPLIT_ROWS) || !encode_operand(&tmX, &p.a, A, 1, pl.T)) return GEMM_ERR_CUDA;
+    if (!encode_operand(&tmW, &p.b, B, 1, lin::SPLIT_ROWS) || !encode_operand(&tmX, &p.a, A, wide ? 2 : 1, pl.T)) return GEMM_ERR_CUDA;
     const int es = e.type == 0 ? 4 : 2;
     p.sched.nm = int32_t(nm);
     p.sched.nn = int32_t(nn);
     p.num_units = int32_t(nm * nn);
     p.T = pl.T;
-    p.tmem_cols = 256;  // accumulator and two stages of weights
+    p.tmem_cols = pl.T <= 128 ? 256 : 512;  // accumulator and two stages of weights
     p.split = pl.split;
     p.stages = int8_stages(pl.T);
+    p.bufs = int8_x(pl.T);
     p.idesc = linear_idesc(GEMM_TYPE_F16, false, false, lin::SPLIT_ROWS, uint32_t(pl.T));
     p.e.vec4 = quad_aligned(e.c, e.ldc, es) && (e.pre == nullptr || quad_aligned(e.pre, e.ldp, es)) &&
                (e.r == nullptr || quad_aligned(e.r, e.ldr, es));
-    const cudaError_t err = launch_shape(linear_int8, dim3(unsigned(int64_t(p.num_units) * pl.split)), dim3(lin::SPLIT_THREADS),
+    const cudaError_t err = launch_shape(wide ? linear_int8<true> : linear_int8<false>, dim3(unsigned(int64_t(p.num_units) * pl.split)), dim3(lin::SPLIT_THREADS),
                                          int8_smem(pl.T), pl.split, stream, tmW, tmX, p);
     if (log_enabled())
         std::fprintf(stderr, "[gemm_linear] M=%lld N=%lld K=%lld kernel=int8 T=%d split=%d stages=%d units=%d\n", (long long)M,
@@ -582,16 +595,17 @@ gemm_status_t run_int8(const Operand &A, const Operand &B, int64_t M, int64_t N,
     return err == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
-// Workspace of two operands' copies: [A's][B's], each from a 256-byte boundary. `expand`:
-// whole numbers, copied to fp16.
-void copies_needed(const Operand &A, const Operand &B, bool expand, uint64_t *a_bytes, uint64_t *b_bytes) {
-    if (expand) {
-        *a_bytes = round256(expanded_bytes(A));
-        *b_bytes = round256(expanded_bytes(B));
-        return;
-    }
-    *a_bytes = A.tma() ? 0u : round256(A.copy_bytes());
-    *b_bytes = B.tma() ? 0u : round256(B.copy_bytes());
+// What becomes of whole numbers before their product.
+enum class Whole { kNone, kTokens, kBoth };  // not such operands or as they are; A copied to fp16; both
+Whole whole_copies(int32_t type, int64_t M, int64_t N, int64_t K) {
+    if (type != GEMM_TYPE_I8) return Whole::kNone;
+    return !int8_direct(M, N, K) ? Whole::kBoth : int8_tokens_copied(M, N, K) ? Whole::kTokens : Whole::kNone;
+}
+
+// Workspace of two operands' copies: [A's][B's], each from a 256-byte boundary.
+void copies_needed(const Operand &A, const Operand &B, Whole whole, uint64_t *a_bytes, uint64_t *b_bytes) {
+    *a_bytes = whole != Whole::kNone ? round256(expanded_bytes(A)) : A.tma() ? 0u : round256(A.copy_bytes());
+    *b_bytes = whole == Whole::kBoth ? round256(expanded_bytes(B)) : B.tma() ? 0u : round256(B.copy_bytes());
 }
 
 gemm_status_t check_operands(const gemm_matrix_t *A, const gemm_matrix_t *B, int64_t M, int64_t N, int64_t K, Operand *a,
@@ -620,7 +634,7 @@ gemm_status_t gemm_linear_workspace_size(const gemm_matrix_t *A, const gemm_matr
     const gemm_status_t st = check_operands(A, B, M, N, K, &a, &b);
     if (st != GEMM_OK) return st;
     uint64_t na = 0, nb = 0;
-    if (M > 0 && N > 0 && K > 0) copies_needed(a, b, a.type == GEMM_TYPE_I8 && !int8_direct(M, N, K), &na, &nb);
+    if (M > 0 && N > 0 && K > 0) copies_needed(a, b, whole_copies(a.type, M, N, K), &na, &nb);
     if (bytes) *bytes = na + nb;
     return GEMM_OK;
 }
@@ -654,8 +668,9 @@ gemm_status_t gemm_linear(const gemm_matrix_t *A, const gemm_matrix_t *B, const 
         if (st != GEMM_OK) return st;
     }
     uint64_t na = 0, nb = 0;
-    const bool whole = a.type == GEMM_TYPE_I8, expand = whole && !int8_direct(M, N, K);
-    if (K > 0) copies_needed(a, b, expand, &na, &nb);
+    const bool integers = a.type == GEMM_TYPE_I8;
+    const Whole whole = whole_copies(a.type, M, N, K);
+    if (K > 0) copies_needed(a, b, whole, &na, &nb);
     st = check_workspace(workspace, workspace_bytes, na + nb, 128);
     if (st != GEMM_OK) return st;
 
@@ -691,12 +706,16 @@ gemm_status_t gemm_linear(const gemm_matrix_t *A, const gemm_matrix_t *B, const 
                    : GEMM_ERR_CUDA;
     }
     unsigned char *ws = static_cast<unsigned char *>(workspace);
-    if (expand) {
-        const ExpandJob ja = expand_job(a, ws, nullptr, 0, ds->num_sms), jb = expand_job(b, ws + na, nullptr, 0, ds->num_sms);
+    if (whole != Whole::kBoth && nb > 0 || whole == Whole::kNone && na > 0) {
+        const bool pa = whole == Whole::kNone && na > 0;
+        if (pack_operands(&a, pa ? ws : nullptr, &b, nb ? ws + na : nullptr, ds->num_sms, stream) != cudaSuccess) return GEMM_ERR_CUDA;
+    }
+    if (whole != Whole::kNone) {
+        const ExpandJob ja = expand_job(a, ws, nullptr, 0, ds->num_sms),
+                        jb = whole == Whole::kBoth ? expand_job(b, ws + na, nullptr, 0, ds->num_sms) : ExpandJob{};
         if (expand_operands<__half, true>(&a, ja, &b, jb, GEMM_TYPE_F16, stream) != cudaSuccess) return GEMM_ERR_CUDA;
-    } else if (na + nb > 0 && pack_operands(&a, na ? ws : nullptr, &b, nb ? ws + na : nullptr, ds->num_sms, stream) != cudaSuccess)
-        return GEMM_ERR_CUDA;
-    if (whole && !expand) return run_int8(a, b, M, N, K, e, ds, ops, stream);
+    }
+    if (integers && whole != Whole::kBoth) return run_int8(a, b, M, N, K, e, ds, ops, stream);
     return run_linear(a, b, M, N, K, e, flags, ds, ops, stream);
 }
 
@@ -751,7 +770,7 @@ gemm_status_t backward_space(const gemm_matrix_t *G, const Operand &a, const Ope
         s->a = round256(expanded_bytes(a));
         s->b = b.tma() ? 0u : round256(b.copy_bytes());
     } else if (K > 0) {
-        copies_needed(a, b, false, &s->a, &s->b);
+        copies_needed(a, b, Whole::kNone, &s->a, &s->b);
     }
     s->total = s->d + s->partial + s->a + s->b;
     return GEMM_OK;

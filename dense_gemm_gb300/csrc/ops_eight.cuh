@@ -185,18 +185,23 @@ __global__ void __launch_bounds__(256) expand_rows_kernel(const ExpandJob a, con
 // bits. A stage is 128 weights' rows and T tokens by 128 bytes of K. It lands by TMA as it
 // is; four of eight warps turn it into fp16, each thread a row: the weights from registers into
 // tensor memory, where the MMA takes its 128-row operand from, the tokens into shared memory.
+// kWide, more than 64 tokens: converting them in every CTA would take longer than the weights,
+// so they come as fp16 (a kernel before this one made a copy of them) in a ring of their own.
 // (As fp16 in shared memory the weights would be written once and read once more there: 32
 // KiB each way a stage, beside the 16 in and 16 out of their bytes, on an SM that gets 16 KiB
 // of weights in 0.36 us from DRAM and moves 128 bytes a cycle.)
 namespace lin {
 constexpr int I8_W_BYTES = SPLIT_ROWS * 128;  // weights of a stage
 constexpr int I8_COPIES = 2;                  // stages in fp16, one of each group of warps
-constexpr int I8_MAX_STAGES = 5;
+constexpr int I8_MAX_STAGES = 6, I8_MAX_X = 4;
 constexpr int I8_A_COLS = 64;                 // TMEM columns of a stage's weights: 128 of K, two to a column
-// full[S], empty[S], ready[2], used[2], done
-constexpr int I8_BARS = 2 * I8_MAX_STAGES + 2 * I8_COPIES + 1;
-constexpr int i8_ring(int stages, int T) { return stages * (I8_W_BYTES + T * 128) + I8_COPIES * T * 256; }
-constexpr int i8_smem(int stages, int T) { return i8_ring(stages, T) + I8_BARS * 8 + 16 + 1024; }
+// full[S], empty[S], ready[2], used[2], done, kWide's tokens: full[4], empty[4]
+constexpr int I8_BARS = 2 * I8_MAX_STAGES + 2 * I8_COPIES + 1 + 2 * I8_MAX_X;
+// stages of weights, and of tokens: in 8 bits beside the weights with two copies in fp16, or (wide) x stages in fp16
+constexpr int i8_ring(bool wide, int stages, int x, int T) {
+    return stages * I8_W_BYTES + (wide ? x * T * 256 : stages * T * 128 + I8_COPIES * T * 256);
+}
+constexpr int i8_smem(bool wide, int stages, int x, int T) { return i8_ring(wide, stages, x, T) + I8_BARS * 8 + 16 + 1024; }
 }  // namespace lin
 
 // 32 lanes x 32 consecutive 32-bit columns from registers: thread i has lane (base lane + i).
@@ -233,6 +238,7 @@ __device__ __forceinline__ void mma_f16_tmem_elect(uint32_t d_tmem, uint32_t a_t
 // 15.8 us, floor 9.9), else by the chain set-up - first weights - conversion - exchange - rows (1 x
 // 4096 x 4096 7.4 us of which the stream is 2.5) and from 32 rows on by the conversion: a stage takes a
 // group some 1400 cycles with 16 tokens, 2700 with 64 (64 x 16384 x 4096 19.6 us, 256 x 4096 x 4096 18.7).
+template <bool kWide>
 __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     linear_int8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const LinearParams p) {
     constexpr int MMA_WARP = 1, EPI_WARP0 = 2;
@@ -244,14 +250,17 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     uint8_t *smem = smem_raw + (base - raw);
     const uint32_t x_bytes = uint32_t(T) * 128u;
     const uint32_t sW = base, sX = base + uint32_t(NST) * lin::I8_W_BYTES;
-    const uint32_t sX16 = sX + uint32_t(NST) * x_bytes;
-    const uint32_t ring = sX16 + lin::I8_COPIES * 2u * x_bytes - base;
+    const uint32_t sX16 = kWide ? sX : sX + uint32_t(NST) * x_bytes;
+    const int XST = kWide ? p.bufs : lin::I8_COPIES;  // stages of tokens in fp16
+    const uint32_t ring = sX16 + uint32_t(XST) * 2u * x_bytes - base;
     const uint32_t bar0 = base + ring;
     auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
     auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (lin::I8_MAX_STAGES + s); };
     auto ready_bar = [&](uint32_t s) { return bar0 + 8u * (2 * lin::I8_MAX_STAGES + s); };
     auto used_bar = [&](uint32_t s) { return bar0 + 8u * (2 * lin::I8_MAX_STAGES + lin::I8_COPIES + s); };
     const uint32_t done_bar = bar0 + 8u * (2 * lin::I8_MAX_STAGES + 2 * lin::I8_COPIES);
+    auto x_full = [&](uint32_t s) { return done_bar + 8u * (1u + s); };
+    auto x_empty = [&](uint32_t s) { return done_bar + 8u * (1u + lin::I8_MAX_X + s); };
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + ring + lin::I8_BARS * 8);
 
     const int warp = threadIdx.x >> 5;
@@ -274,9 +283,15 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     SplitColumns columns = {};
 
     auto load = [&](int32_t st, uint32_t stage) {
-        mbar_expect_tx_elect(full_bar(stage), lin::I8_W_BYTES + x_bytes);
+        mbar_expect_tx_elect(full_bar(stage), kWide ? lin::I8_W_BYTES : lin::I8_W_BYTES + x_bytes);
         tma_load_2d_elect<false>(sW + stage * lin::I8_W_BYTES, &tmW, st * 128, n0, full_bar(stage));
-        tma_load_2d_elect<false>(sX + stage * x_bytes, &tmX, st * 128, m0, full_bar(stage));
+        if constexpr (!kWide) tma_load_2d_elect<false>(sX + stage * x_bytes, &tmX, st * 128, m0, full_bar(stage));
+    };
+    // kWide: both k-blocks of 64 of the tokens
+    auto load_x = [&](auto mode, int32_t st, uint32_t stage) {
+        mbar_expect_tx_elect(x_full(stage), 2u * x_bytes);
+        issue_copies<decltype(mode)::value, false, false>(&tmX, sX16 + stage * 2u * x_bytes, x_bytes, p.a.copies, 2 * st, 64, m0,
+                                                          x_full(stage), lane);
     };
     if (warp == 0) {
         // ============================================================ producer
@@ -292,6 +307,10 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
                 mbar_init(used_bar(s), 1);
             }
             mbar_init(done_bar, 1);
+            for (int s = 0; kWide && s < XST; ++s) {
+                mbar_init(x_full(s), 1);
+                mbar_init(x_empty(s), 1);
+            }
             fence_mbar_init();
             fence_proxy_async_smem();
         }
@@ -299,20 +318,43 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         const int32_t first = min(st0 + NST, st1);
         // the first stages' weights are on their way into L2 while the kernel before ends
         for (int32_t st = st0; st < first; ++st) prefetch_copies<kLoadOne, false>(&tmW, st, 128, n0);
-        griddep_wait();
+        // kWide: the kernel before is the tokens' copy, which the weights need nothing of: what they
+        // hold was complete before that kernel's own wait returned, and so before this one could start
+        if constexpr (!kWide) griddep_wait();
         for (int32_t st = st0; st < first; ++st) load(st, uint32_t(st - st0));
-        __syncthreads();  // the others are set up; tensor memory is allocated
-        griddep_launch_dependents();
-        uint32_t stage = 0, phase = 0;
-        for (int32_t st = st0 + NST; st < st1; ++st) {
-            if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase, p.wait))) {
-                let_copies_land();
-                break;
+        auto later_stages = [&](auto mode) {
+            __syncthreads();  // the others are set up; tensor memory is allocated
+            if constexpr (kWide) {
+                griddep_wait();
+                for (int32_t st = st0; st < min(st0 + XST, st1); ++st) load_x(mode, st, uint32_t(st - st0));
             }
-            load(st, stage);
-            if (++stage == uint32_t(NST)) { stage = 0; phase ^= 1u; }
-        }
-        __syncwarp();
+            griddep_launch_dependents();
+            // kWide: the tokens' ring may be shorter than the weights', which then are as many stages ahead
+            uint32_t stage = 0, phase = 0;
+            [[maybe_unused]] uint32_t x_stage = 0, x_phase = 0;
+            for (int32_t st = st0 + (kWide ? XST : NST); st < st1; ++st) {
+                const int32_t ws = kWide ? st + NST - XST : st;
+                if (ws < st1) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase, p.wait))) {
+                        let_copies_land();
+                        break;
+                    }
+                    load(ws, stage);
+                    if (++stage == uint32_t(NST)) { stage = 0; phase ^= 1u; }
+                }
+                if constexpr (kWide) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(x_empty(x_stage), x_phase, p.wait))) {
+                        let_copies_land();
+                        break;
+                    }
+                    load_x(mode, st, x_stage);
+                    if (++x_stage == uint32_t(XST)) { x_stage = 0; x_phase ^= 1u; }
+                }
+            }
+            __syncwarp();
+        };
+        if constexpr (kWide) with_load(p.a, [&](auto mode, auto) { later_stages(mode); });
+        else later_stages(std::integral_constant<uint32_t, kLoadOne>());
     } else {
         if (warp == MMA_WARP) {
             tmem_alloc(smem_addr(tmem_slot), uint32_t(p.tmem_cols));
@@ -321,7 +363,7 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        griddep_enter(0u);
+        if constexpr (!kWide) griddep_enter(0u);  // kWide: all that these warps read was complete, as the weights
         tmem_base = *tmem_slot;
     }
 
@@ -330,17 +372,25 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         const uint64_t dx = smem_desc(sX16, 16, 1024);
         const uint32_t x_kb = (uint32_t(T) * 128u) >> 4;  // the second 64 of K
         uint32_t c = 0, turn = 0;
+        [[maybe_unused]] uint32_t x = 0, x_phase = 0;
         for (int32_t st = st0; st < st1; ++st) {
             if (!__all_sync(0xffffffffu, mbar_wait(ready_bar(c), turn, p.wait))) break;
+            if constexpr (kWide) {
+                if (!__all_sync(0xffffffffu, mbar_wait(x_full(x), x_phase, p.wait))) break;
+            }
             tc_fence_after();
             const uint32_t a0 = tmem_base + uint32_t(acc_cols) + c * lin::I8_A_COLS;
-            const uint64_t x0 = dx + c * 2u * x_kb;
+            const uint64_t x0 = dx + (kWide ? x : c) * 2u * x_kb;
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)  // 16 of K each
                 mma_f16_tmem_elect(tmem_base, a0 + ks * 8, x0 + (ks / 4) * x_kb + (ks % 4) * 2, p.idesc, st != st0 || ks != 0 ? 1u : 0u);
             mma_commit_elect(used_bar(c));
             turn ^= c;  // two copies in turn
             c ^= 1u;
+            if constexpr (kWide) {
+                mma_commit_elect(x_empty(x));
+                if (++x == uint32_t(XST)) { x = 0; x_phase ^= 1u; }
+            }
         }
         // also what the epilogue waits for; after a wait that ran out, no MMA may
         // still be writing TMEM when it is freed
@@ -349,7 +399,11 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     } else if (warp >= EPI_WARP0) {
         // ============================================================ to fp16, then epilogue
         // Two groups of four warps take the stages in turn, so that one's loads and stores
-        // pass while the other converts.
+        // pass while the other converts. With an odd number of stages a place in the ring is one
+        // group's and then the other's. A wait for a phase tells it from the phase before only, and
+        // copies land in any order: a group may come to a place whose earlier copy, the other
+        // group's, has not landed, and the phase before that one has the parity it asks for. So it
+        // first waits until the other group has released the place.
         const int q = warp & 3, group = ew / 4;  // the TMEM lanes this warp may write
         const uint32_t row = uint32_t(q * 32 + lane), thread = uint32_t(ew & 3) * 32u + uint32_t(lane);
         const uint32_t a_tmem = tmem_base + (uint32_t(q * 32) << 16) + uint32_t(acc_cols);
@@ -358,6 +412,10 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         uint32_t stage = uint32_t(group), phase = 0, turn = 0;
         bool ok = true;
         for (int32_t st = st0 + group; st < st1; st += 2) {
+            if ((NST & 1) != 0 && st >= st0 + NST && !__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, p.wait))) {
+                ok = false;
+                break;
+            }
             if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, p.wait))) {
                 ok = false;
                 break;
@@ -371,7 +429,7 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
             // tokens: 16 bytes of K of one token at a time, four on their way together
             const uint32_t x_from = sX + stage * x_bytes, x_to = sX16 + c * 2u * x_bytes;
 #pragma unroll 1
-            for (uint32_t e0 = thread; e0 < tasks; e0 += 4u * 128u) {
+            for (uint32_t e0 = thread; !kWide && e0 < tasks; e0 += 4u * 128u) {
                 uint32_t x[4][4];
 #pragma unroll
                 for (uint32_t k = 0; k < 4; ++k) {
@@ -394,7 +452,7 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
             const uint32_t w_row = sW + stage * lin::I8_W_BYTES;
 #pragma unroll
             for (uint32_t i = 0; i < 8; ++i) ld_shared_v4(w_row + swz128(row, i), w[i][0], w[i][1], w[i][2], w[i][3]);
-            fence_proxy_async_smem();
+            if constexpr (!kWide) fence_proxy_async_smem();
             __syncwarp();
             // the stage has been read: its bytes in flight are what the stream's rate goes by
             if (lane == 0) mbar_arrive(empty_bar(stage));

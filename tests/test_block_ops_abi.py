@@ -128,6 +128,7 @@ def test_integer_product_workspace(lib):
     n = C.c_uint64()
     size = lambda a, b, *s: (lib.gemm_linear_workspace_size(a, b, *s, n), n.value)  # noqa: E731
     a, b = mat(t=I8, r=4096), mat(t=I8, r=1, c=4096)
-    assert size(a, b, 256, 4096, 4096) == (0, 0)                               # few rows: none
-    assert size(a, b, 257, 4096, 4096) == (0, (257 + 4096) * 4096 * 2)         # copies in fp16
+    assert size(a, b, 64, 4096, 4096) == (0, 0)                                # few rows: none
+    assert size(a, b, 65, 4096, 4096) == (0, 65 * 4096 * 2)                    # A's copy in fp16
+    assert size(a, b, 2048, 4096, 4096) == (0, (2048 + 4096) * 4096 * 2)       # both
     assert size(mat(t=I8, r=33), mat(t=I8, r=1, c=48), 3, 8, 33) == (0, 512)   # a copy on 128-byte lines
