@@ -237,7 +237,9 @@ __device__ __forceinline__ void mma_f16_tmem_elect(uint32_t d_tmem, uint32_t a_t
 // Bound by the weights' stream where N K is large and rows are few (1 x 16384 x 4096 67 MB in
 // 15.8 us, floor 9.9), else by the chain set-up - first weights - conversion - exchange - rows (1 x
 // 4096 x 4096 7.4 us of which the stream is 2.5) and from 32 rows on by the conversion: a stage takes a
-// group some 1400 cycles with 16 tokens, 2700 with 64 (64 x 16384 x 4096 19.6 us, 256 x 4096 x 4096 18.7).
+// group some 1400 cycles with 16 tokens, 2700 with 64 (64 x 16384 x 4096 19.8 us). kWide with T = 256 by
+// shared memory's bandwidth: 0.86 us a stage, 16 KiB of weights in and out and 64 of tokens, for
+// 0.54 of products (256 x 8192 x 8192 33.1 us, 512 57, 256 x 4096 x 4096 17.0).
 template <bool kWide>
 __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
     linear_int8(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const LinearParams p) {

@@ -80,7 +80,7 @@ def _code(table: dict, key, what: str) -> int:
 
 def linear_workspace_size(A: torch.Tensor, B: torch.Tensor) -> int:
     """Workspace bytes of ``linear`` for these operands: 0 where their bases and
-    row strides are multiples of 16 bytes and they are not int8."""
+    row strides are multiples of 16 bytes and they are not int8 (of many rows)."""
     return _native().linear_workspace_size(A, B)
 
 

@@ -94,14 +94,15 @@ typedef struct {
  * workspace: 128-byte aligned, of gemm_linear_workspace_size() bytes, needed
  * only where that is not 0: an operand whose base or row stride is no multiple
  * of 16 bytes is first copied there onto 128-byte lines (one kernel), and int8
- * operands as fp16. Its contents mean nothing between calls.
+ * operands as fp16 (A of more than 64 rows; B too where the product's own kernel
+ * takes 16 bits). Its contents mean nothing between calls.
  * M, N or K < 0 or >= 2^31 -> INVALID_ARG. M == 0 or N == 0: nothing is done.
  * K == 0: the sum is 0 and the epilogue still runs.
  * Two kernels share the work by a rule on M, N and K: 256x256 tiles on CTA
  * pairs where they keep the GPU's pairs busy; below that (few tokens: decoding,
  * short prompts; few output tiles) tiles of 128 columns by 16..256 rows with K
  * split over a cluster of up to 8 CTAs, whose partial sums are added in rank
- * order through distributed shared memory. int8 operands of up to 256 rows, and
+ * order through distributed shared memory. int8 operands of up to 768 rows, and
  * small products of them, have a kernel of their own, whatever the flags.
  * Every result is deterministic.
  * The second kernel may ask for lines of B in L2 before the kernels before it on
