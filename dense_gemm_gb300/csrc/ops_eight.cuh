@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
         tc_fence_before();
         __syncthreads();
         tc_fence_after();
-        if constexpr (!kWide) griddep_enter(0u);  // kWide: all that these warps read was complete, as the weights
+        if constexpr (!kWide) griddep_enter(0u);  // kWide: these warps read global memory at their end only
         tmem_base = *tmem_slot;
     }
 
@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
             if (stage >= uint32_t(NST)) { stage -= uint32_t(NST); phase ^= 1u; }
             turn ^= 1u;
         }
+        if constexpr (kWide) griddep_wait();  // long over; the loads from here on go through L1
         if (vec) split_columns<true, true>(p, S, rank, ew, lane, m0, n0, valid, columns);
         else split_columns<true, false>(p, S, rank, ew, lane, m0, n0, valid, columns);
         ready = __all_sync(0xffffffffu, mbar_wait(done_bar, 0, p.wait)) && ok;

@@ -26,3 +26,14 @@ def test_every_kernel_along_rows_waits_for_the_one_before():
     rows = code("ops_rows.cu")
     kernels = re.findall(r"__global__ void[^{]*\{", rows)
     assert len(kernels) == rows.count("griddep_wait();") == rows.count("griddep_launch_dependents();") == 8
+
+
+def test_integer_products_read_nothing_but_weights_before_their_wait():
+    """With the tokens copied by the kernel before it, linear_int8 starts on the weights (by TMA, from
+    L2) at once; tokens, factors and the residual come after a wait of the warp that reads them."""
+    eight = code("ops_eight.cuh")
+    body = eight[eight.index("linear_int8(const __grid_constant__"):]
+    wait = body.index("if constexpr (kWide) {\n                griddep_wait();")
+    assert body.index("load_x(mode, st, uint32_t(st - st0))") > wait
+    assert body.index("griddep_launch_dependents();") > wait
+    assert body.index("split_columns<true, true>") > body.index("if constexpr (kWide) griddep_wait();") > wait

@@ -44,7 +44,8 @@ def place(x, ld=None, offset=0):
 
 # K up to 1024 with |values| up to 128: below 2^24
 SIZES = [(1, 1, 1), (1, 128, 128), (1, 257, 33), (3, 65, 7), (5, 1000, 1000), (16, 128, 1024), (17, 300, 513), (33, 4096, 256), (64, 129, 1000),
-         (65, 130, 255), (128, 384, 640), (200, 520, 1000), (257, 1000, 513), (700, 72, 300), (600, 1000, 1000), (1000, 1024, 1024), (1030, 1100, 1024), (48, 16384, 512)]
+         (65, 130, 255), (128, 384, 640), (200, 520, 1000), (257, 1000, 513), (700, 72, 300), (600, 1000, 1000), (1000, 1024, 1024), (1030, 1100, 1024), (48, 16384, 512), (300, 3000, 1001),
+         (65, 16000, 1000), (129, 8200, 840), (900, 1100, 1023)]
 
 
 @pytest.mark.parametrize("size", SIZES)
