@@ -458,6 +458,7 @@ __global__ void __launch_bounds__(lin::SPLIT_THREADS, 2)
             __syncwarp();
             // the stage has been read: its bytes in flight are what the stream's rate goes by
             if (lane == 0) mbar_arrive(empty_bar(stage));
+            __syncwarp();  // the stores to tensor memory are the whole warp's
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 uint32_t a[32];
