@@ -76,7 +76,8 @@ __device__ __forceinline__ void row_factor(float a, float &mul, float &scale) {
 // What t / a has beyond its fp32 value `mul`: x mul + x rest is x t / a within 2^-47 of it, so
 // that a value of 16 bits that lies on a rounding's edge is found there and goes to the even
 // side. (mul alone is up to 2^-24 off, and of 4096 x 16384 bf16 values 3 in 10,000 went to the
-// other side.) A row whose mul is 0 or NaN has no rest.
+// other side; it took 31.6 us to e4m3 and 32.0 to int8, this 32.0 and 33.1. With the rest from a
+// division 37.8 and 39.2.) A row whose mul is 0 or NaN has no rest.
 template <int OUT>
 __device__ __forceinline__ float factor_rest(float a, float mul) {
     return mul > 0.0f ? fmaf(-mul, a, kTop<OUT>) * (mul * (1.0f / kTop<OUT>)) : 0.0f;  // mul / t: near enough to 1 / a
@@ -348,7 +349,8 @@ __global__ void __launch_bounds__(1024) layer_norm_any_kernel(const LayerNormArg
 
 // ------------------------------------------------------------------ rows in 8 bits
 // One pass: the row stays in registers between its maximum and its store. DRAM bounds it
-// (4096 x 16384 bf16 201 MB in 32.7 us, 6.2 TB/s; 999 x 5001 fp16 5.0 us).
+// (4096 x 16384 bf16 201 MB in 32.0 us, 6.3 TB/s; 999 x 5001 fp16 5.1 us). 40 registers: three
+// blocks of 512 threads on an SM (4096 x 16384 to int8 38.9 us with 42).
 template <typename T, int NV, int OUT, bool kShift>
 __global__ void __maxnreg__(sizeof(T) == 2 ? 40 : 64) quantize_rows_kernel(const QuantizeArgs p) {
     __shared__ uint32_t redq[32];

@@ -242,9 +242,10 @@ gemm_status_t gemm_layer_norm_backward_workspace_size(int64_t rows, int64_t widt
 
 /*
  * gemm_quantize_rows — each row of x in 8 bits with a scale: a = max_j |x[i,j]|,
- * scale[i] = a / t, q[i,j] = nearest-even(x[i,j] * (t / a)), t = 448 (q in e4m3)
+ * scale[i] = a / t, q[i,j] the value nearest to x[i,j] t / a, t = 448 (q in e4m3)
  * or 127 (int8), rows of tiny values and rows with a NaN or an infinity as in
- * gemm_layer_norm. x is fp32, fp16 or bf16, scale fp32 [rows]. q overlaps no part
+ * gemm_layer_norm. Of two values as near the even one is taken: exactly so for x of
+ * 16 bits; an fp32 x t / a is first rounded to fp32. x is fp32, fp16 or bf16, scale fp32 [rows]. q overlaps no part
  * of x. Both matrices have stride_col == 1 and stride_row >= width (rows > 1).
  * rows == 0 or width == 0: nothing is done.
  */
