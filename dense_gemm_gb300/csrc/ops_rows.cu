@@ -8,8 +8,8 @@
 // A dozen operations per element at most, so DRAM bounds all of them: every row is
 // read once into registers or shared memory and written from there. The variance is
 // summed from the centred values: the difference of the mean square and the squared
-// mean loses what a row's mean has more digits than its deviation. All sums are fp32, in
-// an order that the sizes fix.
+// mean loses what a row's mean has more digits than its deviation. The mean is corrected by
+// the centred values' own sum (RowMean). All sums are fp32, in an order that the sizes fix.
 #include "ops_rows.h"
 
 #include <algorithm>
@@ -136,6 +136,26 @@ __device__ __forceinline__ void store_one(void *p, int64_t at, float v, float mu
     else static_cast<T *>(p)[at] = from_f32<T>(v);
 }
 
+// row_sum<false> of two values: after the first exchange half a warp's lanes have one sum, half the
+// other, so that both take little more than the shuffles of one.
+__device__ __forceinline__ void row_sums(float (&v)[2], float (*red)[32]) {
+    const int lane = threadIdx.x & 31, side = lane >> 4;
+    float s = (side ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, side ? v[0] : v[1], 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int wpr = blockDim.x >> 5, base = int(threadIdx.y) * wpr;
+    if (wpr > 1) {
+        if ((lane & 15) == 0) red[side][base + (threadIdx.x >> 5)] = s;
+        __syncthreads();
+        const int l = lane & 15;
+        s = (l < wpr ? red[side][base + l] : 0.0f) + (l + 16 < wpr ? red[side][base + l + 16] : 0.0f);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    }
+    v[0] = __shfl_sync(0xffffffffu, s, 0);
+    v[1] = __shfl_sync(0xffffffffu, s, 16);
+}
+
 // Every thread of a row gets the row's largest m (>= 0 or NaN: their bits are in their
 // order, a NaN's above infinity's); one barrier.
 __device__ __forceinline__ float row_max(float m, uint32_t *red) {
@@ -193,13 +213,32 @@ __device__ __forceinline__ void clear_outside(F32<8> &v, int lo, int hi) {
     }
 }
 
+// A row's mean and variance from a first mean m1, which is as many roundings off as the row's sum
+// has, and the sums s1 of c = h - m1 and s2 of c^2. c is exact where h and m1 are near one another,
+// so m1 + s1 / width is the mean, rounded once, and the variance that of the values less it.
+// Without the correction a row of equal values keeps for c some units of its mean's last place,
+// which 1 / sqrt(eps) multiplies (eps = 1e-12: y = b +- w). What the correction leaves of the
+// variance below the sums' own rounding is 0. (Without it 8192 x 4096 43.4 us, so 44.5, 4096 x 8192 to 8
+// bits 39.0 and 40.6; corrected only where the mean is larger than the deviation 44.5 and 39.7, and
+// 39.5 for such rows without a residual, which so take 35.3.)
+struct RowMean {
+    float mean, less, var;  // c - less is h - mean
+    __device__ __forceinline__ RowMean(float m1, float s1, float s2, float inv_width) {
+        const float more = s1 * inv_width, square = s2 * inv_width;
+        mean = more == more ? m1 + more : m1;  // an infinite row's
+        less = mean - m1;
+        var = fmaf(less, less - 2.0f * more, square);
+        if (var < square * 0x1p-16f) var = 0.0f;
+    }
+};
+
 // Bound by DRAM and the issue slots where there are many rows (4096 x 8192 bf16 with residual
-// to 8 bits 235 MB in 41.0 us, 5.7 TB/s, 8192 x 4096 268 MB in 44.2, 6.1), by the chain load - sums -
+// to 8 bits 235 MB in 40.6 us, 5.8 TB/s, 8192 x 4096 268 MB in 44.5, 6.0), by the chain load - sums -
 // store where there are few (1 x 4096 2.1 us). Loads that pass L1 for x and r, to leave it to the
 // weights, were 2 to 4 % slower.
 template <typename T, int NV, int OUT, bool kShift>
 __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs p) {
-    __shared__ float red[2][32];
+    __shared__ float red[3][32];
     __shared__ uint32_t redq[32];
     const int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
     griddep_wait();
@@ -247,18 +286,27 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum = add2(sum, t[j].p[i]);
     }
-    const float mean = row_sum<false>(total(sum), red[0]) * p.inv_width;
-    float2 ss = splat<8>(0.0f);
+    const float m1 = row_sum<false>(total(sum), red[0]) * p.inv_width;
+    float2 s1 = splat<8>(0.0f), s2 = s1;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         if (!a.has(j)) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) t[j].p[i] = add2(t[j].p[i], splat<8>(-mean));
+        for (int i = 0; i < 4; ++i) t[j].p[i] = add2(t[j].p[i], splat<8>(-m1));
         if (a.cut(j)) clear_outside(t[j], a.lo(j), a.hi(j));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ss = fma2(t[j].p[i], t[j].p[i], ss);
+        for (int i = 0; i < 4; ++i) {
+            s1 = add2(s1, t[j].p[i]);
+            s2 = fma2(t[j].p[i], t[j].p[i], s2);
+        }
     }
-    const float rstd = rsqrtf(fmaf(row_sum<false>(total(ss), red[1]), p.inv_width, p.eps));
+    float sums[2] = {total(s1), total(s2)};
+    row_sums(sums, red + 1);
+    const RowMean m(m1, sums[0], sums[1], p.inv_width);
+    const float mean = m.mean, rstd = rsqrtf(m.var + p.eps);
+    // h - mean times rstd in one multiply-add; a row of equal values takes no rounding's rest with it
+    const float zero = 0.0f * rstd;  // NaN with eps = 0
+    const float2 by = splat<8>(m.var == 0.0f ? zero : rstd), off = splat<8>(m.var == 0.0f ? zero : -m.less * rstd);
     float top = 0.0f;
     Stored<OUT, T> *y = static_cast<Stored<OUT, T> *>(p.y) + row * p.ldy;
 #pragma unroll
@@ -269,7 +317,7 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs p)
         if (p.b != nullptr) fb = early ? widen<T, 8>(b[j]) : a.column(p.b, p.w_f32 != 0, j);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 u = mul2(t[j].p[i], splat<8>(rstd));
+            const float2 u = fma2(t[j].p[i], by, off);
             t[j].p[i] = p.b != nullptr ? fma2(u, fw.p[i], fb.p[i]) : mul2(u, fw.p[i]);
         }
         if constexpr (OUT == kOutSame) store_same<T>(y + a.at(j), t[j], a.lo(j), a.hi(j));
@@ -298,7 +346,7 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs p)
 template <typename T, int OUT>
 __global__ void __launch_bounds__(1024) layer_norm_any_kernel(const LayerNormArgs p, int32_t cached) {
     extern __shared__ float kept[];
-    __shared__ float red[2][32];
+    __shared__ float red[3][32];
     __shared__ uint32_t redq[32];
     griddep_wait();
     griddep_launch_dependents();
@@ -314,14 +362,17 @@ __global__ void __launch_bounds__(1024) layer_norm_any_kernel(const LayerNormArg
         if (cached) kept[at] = h;
         s += h;
     }
-    const float mean = row_sum<false>(s, red[0]) * p.inv_width;
-    s = 0.0f;
+    const float m1 = row_sum<false>(s, red[0]) * p.inv_width;
+    float sums[2] = {0.0f, 0.0f};
 #pragma unroll 4
     for (int64_t at = threadIdx.x; at < p.width; at += blockDim.x) {
-        const float c = value(at) - mean;
-        s = fmaf(c, c, s);
+        const float c = value(at) - m1;
+        sums[0] += c;
+        sums[1] = fmaf(c, c, sums[1]);
     }
-    const float rstd = rsqrtf(fmaf(row_sum<false>(s, red[1]), p.inv_width, p.eps));
+    row_sums(sums, red + 1);
+    const RowMean m(m1, sums[0], sums[1], p.inv_width);
+    const float mean = m.mean, rstd = rsqrtf(m.var + p.eps);
     auto result = [&](float h, int64_t at) {
         const float w = load_weight<T, 1>(p.w, p.w_f32 != 0, at).p[0], u = (h - mean) * rstd;
         return p.b != nullptr ? fmaf(u, w, load_weight<T, 1>(p.b, p.w_f32 != 0, at).p[0]) : u * w;

@@ -199,15 +199,16 @@ gemm_status_t gemm_rms_norm_backward_workspace_size(int64_t rows, int64_t width,
  *   mean[i] = sum(h) / width,  rstd[i] = 1 / sqrt(sum((h - mean)^2) / width + eps)
  *   y[i,:] = weight * (h - mean[i]) * rstd[i] + bias
  *
- * everything in fp32 from the unrounded sum h, the variance from the centred
- * values; h, y, mean and rstd are each rounded once. x, residual and h have one
+ * everything in fp32 from the unrounded sum h, the mean corrected by the centred
+ * values' own sum, the variance from them; h, y, mean and rstd are each rounded once. x, residual and h have one
  * type, fp32, fp16 or bf16; y has that type or is e4m3 or int8; weight and bias
  * [width] both have x's type or both are fp32; bias may be NULL. With an 8-bit y,
  * a = max_j |y[i,j]|, scale[i] = a / t and y[i,j] holds nearest-even(y[i,j] *
  * (t / a)), t = 448 (e4m3) or 127 (int8), so that the value is y * scale; a row whose
  * a is below 7.7e-34 has scale 1 and zeros; a row with a NaN or an infinity has
  * scale NaN (and NaNs in e4m3, zeros in int8). scale must be given with an 8-bit y,
- * and only then. A row of equal values with eps = 0 is NaN.
+ * and only then. A row of equal values has that value as its mean and is the bias;
+ * with eps = 0 it is NaN.
  * h (given only with residual) may be x or residual itself. mean and rstd may be
  * NULL. All matrices have stride_col == 1 and stride_row >= width (rows > 1).
  * rows == 0 or width == 0: nothing is done. eps >= 0, finite.
