@@ -1059,6 +1059,27 @@ gemm_status_t gemm_saved_backward_workspace_size(const gemm_matrix_t *G, const g
 
 }  // extern "C"
 
+// ------------------------------------------------------------------ rows of no values
+namespace {
+
+bool words_aligned(std::initializer_list<const float *> ps) {
+    for (const float *p : ps)
+        if (reinterpret_cast<uintptr_t>(p) & 3u) return false;
+    return true;
+}
+
+// What a norm or a conversion to 8 bits leaves beside rows of width 0, as beside rows of zeros; each may be absent.
+gemm_status_t empty_rows(float *scale, float *mean, float *rstd, int64_t rows, float eps, cudaStream_t stream) {
+    if (scale == nullptr && mean == nullptr && rstd == nullptr) return GEMM_OK;
+    DeviceState *ds = nullptr;
+    if (device_state(&ds) < 0) return GEMM_ERR_CUDA;
+    return launch_shape(empty_rows_kernel, dim3(unsigned(cdiv(rows, 256))), dim3(256), 0, 1, stream, scale, mean, rstd, rows, eps) == cudaSuccess
+               ? GEMM_OK
+               : GEMM_ERR_CUDA;
+}
+
+}  // namespace
+
 // ------------------------------------------------------------------ RMS norm
 namespace {
 
@@ -1254,7 +1275,11 @@ gemm_status_t gemm_rms_norm(const gemm_matrix_t *x, const gemm_matrix_t *residua
     if (weight_type != GEMM_TYPE_F32 && weight_type != x->type) return GEMM_ERR_INVALID_ARG;
     if (!(eps >= 0.0f) || !(eps <= 3.0e38f)) return GEMM_ERR_INVALID_ARG;
     const bool quant = y->type == GEMM_TYPE_E4M3;
-    if (rows == 0 || width == 0) return GEMM_OK;
+    if (rows == 0) return GEMM_OK;
+    if (width == 0) {  // rows of no values (whose matrices may have no address): what stands beside them
+        if (!words_aligned({scale, rstd})) return GEMM_ERR_INVALID_ARG;
+        return empty_rows(scale, nullptr, rstd, rows, eps, reinterpret_cast<cudaStream_t>(stream_));
+    }
     if (x->data == nullptr || y->data == nullptr || weight == nullptr || quant != (scale != nullptr)) return GEMM_ERR_INVALID_ARG;
     if (present(h) && !present(residual)) return GEMM_ERR_INVALID_ARG;
     if (!element_aligned(weight, weight_type) ||

@@ -31,12 +31,6 @@ struct Places {
 
 int32_t out_code(int32_t type, int32_t x) { return type == x ? g16::kOutSame : type == GEMM_TYPE_I8 ? g16::kOutI8 : g16::kOutE4m3; }
 
-bool words_aligned(std::initializer_list<const float *> ps) {
-    for (const float *p : ps)
-        if (reinterpret_cast<uintptr_t>(p) & 3u) return false;
-    return true;
-}
-
 }  // namespace
 
 extern "C" {
@@ -50,7 +44,11 @@ gemm_status_t gemm_layer_norm(const gemm_matrix_t *x, const gemm_matrix_t *resid
     if (!is_c_type(x->type) || (y->type != x->type && !is_eight(y->type))) return GEMM_ERR_INVALID_ARG;
     if (weight_type != GEMM_TYPE_F32 && weight_type != x->type) return GEMM_ERR_INVALID_ARG;
     if (!(eps >= 0.0f) || !(eps <= 3.0e38f)) return GEMM_ERR_INVALID_ARG;
-    if (rows == 0 || width == 0) return GEMM_OK;
+    if (rows == 0) return GEMM_OK;
+    if (width == 0) {  // rows of no values (whose matrices may have no address): what stands beside them
+        if (!words_aligned({scale, mean, rstd})) return GEMM_ERR_INVALID_ARG;
+        return empty_rows(scale, mean, rstd, rows, eps, reinterpret_cast<cudaStream_t>(stream));
+    }
     if (x->data == nullptr || y->data == nullptr || weight == nullptr || is_eight(y->type) != (scale != nullptr))
         return GEMM_ERR_INVALID_ARG;
     if (present(h) && !present(residual)) return GEMM_ERR_INVALID_ARG;
@@ -172,7 +170,11 @@ gemm_status_t gemm_quantize_rows(const gemm_matrix_t *x, const gemm_matrix_t *q,
     // ---- validation (no GPU work before this point)
     if (!sizes_ok(rows, width, 0) || x == nullptr || q == nullptr) return GEMM_ERR_INVALID_ARG;
     if (!is_c_type(x->type) || !is_eight(q->type)) return GEMM_ERR_INVALID_ARG;
-    if (rows == 0 || width == 0) return GEMM_OK;
+    if (rows == 0) return GEMM_OK;
+    if (width == 0) {
+        if (!words_aligned({scale})) return GEMM_ERR_INVALID_ARG;
+        return empty_rows(scale, nullptr, nullptr, rows, 0.0f, reinterpret_cast<cudaStream_t>(stream));
+    }
     if (x->data == nullptr || q->data == nullptr || scale == nullptr || !words_aligned({scale})) return GEMM_ERR_INVALID_ARG;
     for (const gemm_matrix_t *m : {x, q}) {
         const gemm_status_t st = check_rows(m, rows, width);

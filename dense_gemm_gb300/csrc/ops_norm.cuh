@@ -703,4 +703,15 @@ __global__ void __launch_bounds__(32 * kPartGroups) sum_partials_kernel(const fl
     out[col] = v;
 }
 
+// Rows of no values: scale 1, mean 0 and rstd 1 / sqrt(eps), as rows of zeros have them. Each may be absent.
+__global__ void __launch_bounds__(256) empty_rows_kernel(float *scale, float *mean, float *rstd, int64_t rows, float eps) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t row = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (row >= rows) return;
+    if (scale != nullptr) scale[row] = 1.0f;
+    if (mean != nullptr) mean[row] = 0.0f;
+    if (rstd != nullptr) rstd[row] = rsqrtf(eps);
+}
+
 }  // namespace g16

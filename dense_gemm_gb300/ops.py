@@ -202,7 +202,7 @@ def quantize_rows(x: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, *, 
 
     What a backward pass needs later is kept so in half the memory (``linear_backward``
     takes it as A or ``pre``), and it is an A and scale_a for ``linear``. The largest |x|
-    of a row becomes 448 or 127; rows of zeros have scale 1, rows with a NaN or an
-    infinity scale NaN. ``out`` (contiguous columns) gives the type where it is given.
+    of a row becomes 448 or 127; rows of zeros, and of no values, have scale 1, rows with
+    a NaN or an infinity scale NaN. ``out`` (contiguous columns) gives the type where it is given.
     """
     return (_module or _native()).quantize_rows(x, dtype, out, stream)

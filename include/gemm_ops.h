@@ -164,7 +164,8 @@ gemm_status_t gemm_linear_backward_workspace_size(const gemm_matrix_t *G, const 
  * with an e4m3 y, and only then.
  * h (given only with residual) may be x or residual itself. rstd may be NULL.
  * All matrices have stride_col == 1 and stride_row >= width (rows > 1).
- * rows == 0 or width == 0: nothing is done. eps >= 0, finite.
+ * rows == 0: nothing is done. width == 0: scale 1 and rstd 1 / sqrt(eps), where
+ * given, are all that is written. eps >= 0, finite.
  */
 gemm_status_t gemm_rms_norm(const gemm_matrix_t *x, const gemm_matrix_t *residual, const void *weight,
                             int32_t weight_type, const gemm_matrix_t *y, const gemm_matrix_t *h, float *scale,
@@ -211,7 +212,8 @@ gemm_status_t gemm_rms_norm_backward_workspace_size(int64_t rows, int64_t width,
  * with eps = 0 it is NaN.
  * h (given only with residual) may be x or residual itself. mean and rstd may be
  * NULL. All matrices have stride_col == 1 and stride_row >= width (rows > 1).
- * rows == 0 or width == 0: nothing is done. eps >= 0, finite.
+ * rows == 0: nothing is done. width == 0: scale 1, mean 0 and rstd 1 / sqrt(eps),
+ * where given, are all that is written. eps >= 0, finite.
  */
 gemm_status_t gemm_layer_norm(const gemm_matrix_t *x, const gemm_matrix_t *residual, const void *weight,
                               const void *bias, int32_t weight_type, const gemm_matrix_t *y, const gemm_matrix_t *h,
@@ -248,7 +250,7 @@ gemm_status_t gemm_layer_norm_backward_workspace_size(int64_t rows, int64_t widt
  * gemm_layer_norm. Of two values as near the even one is taken: exactly so for x of
  * 16 bits; an fp32 x t / a is first rounded to fp32. x is fp32, fp16 or bf16, scale fp32 [rows]. q overlaps no part
  * of x. Both matrices have stride_col == 1 and stride_row >= width (rows > 1).
- * rows == 0 or width == 0: nothing is done.
+ * rows == 0: nothing is done. width == 0: a scale of 1 is all that is written.
  */
 gemm_status_t gemm_quantize_rows(const gemm_matrix_t *x, const gemm_matrix_t *q, float *scale, int64_t rows, int64_t width,
                                  gemm_stream_t stream);
