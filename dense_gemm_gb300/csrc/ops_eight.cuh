@@ -2,8 +2,8 @@
 // 16 bits, and the elementwise part of a product's backward pass from 8-bit values.
 //
 // A whole number of 8 bits is exact in fp16, and so is the product of two in the fp32
-// sums of the 16-bit tensor cores (11-bit factors); a sum is exact to 2^24 and from
-// there on rounded like any other fp32 sum. sm_103a's tensor cores have no integer kind at
+// sums of the 16-bit tensor cores (11-bit factors); a sum is exact while that of the
+// magnitudes is below 2^24, and from there on an addition may lose 2^-23 of them. sm_103a's tensor cores have no integer kind at
 // a rate worth using, and 8-bit floats hold no whole numbers past 16.
 #pragma once
 #include "ops_linear.cuh"

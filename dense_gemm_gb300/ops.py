@@ -92,7 +92,9 @@ def linear(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor = None, *, activ
 
     A [M, K] and B [K, N] are float16, bfloat16, or float8_e4m3fn or int8 with fp32
     ``scale_a`` [M] and ``scale_b`` [N]; a weight kept as [N, K] goes in as its
-    transpose. Sums of int8 products are exact to 2^24. ``activation``: "none", "relu", "gelu", "gelu_tanh" or "silu".
+    transpose. Sums of int8 products are exact while their magnitudes add up to less than
+    2^24 (K up to 1024 whatever the values); beyond, they are fp32 sums of the tensor cores, off by up to
+    (K + 16) 2^-23 of those magnitudes. ``activation``: "none", "relu", "gelu", "gelu_tanh" or "silu".
     C has ``out``'s type or ``out_dtype``, else the residual's, else A's
     (bfloat16 for 8-bit operands); ``residual`` [M, N] has C's type and may be
     ``out`` itself; ``bias`` [N] has C's type or is float32. With ``return_pre``

@@ -83,8 +83,11 @@ typedef struct {
  * The sum and everything after it are in fp32; pre and C are each rounded once
  * (nearest-even). A [M,K] and B [K,N] have one type, fp16, bf16, e4m3 or int8; C is
  * fp32, fp16 or bf16. Scales are for 8-bit operands only (both or neither). The
- * products of int8 operands are exact, and so is their sum while it stays below
- * 2^24; beyond, it is rounded like any fp32 sum.
+ * products of int8 operands are exact, and so is their sum while the sum of their
+ * magnitudes stays below 2^24 (K up to 1024 whatever the values). Beyond, it is a sum
+ * in fp32 on the tensor cores, not a 32-bit integer one: each addition may lose
+ * 2^-23 of the magnitudes added up so far (twice what rounding to nearest loses), in
+ * all (K + 16) 2^-23 sum_k |A[i,k] B[k,j]| at most, also where the sum is small.
  * Layouts: A with a unit row or column stride, B likewise (a B with stride_row
  * == 1 is a weight stored [N,K]); 8-bit operands with K contiguous only; C, pre
  * and residual with stride_col == 1 and stride_row >= N (M > 1). Others ->
