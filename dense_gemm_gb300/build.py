@@ -31,7 +31,7 @@ LIB = os.path.join(HERE, "libgemm_f16.so")
 DEBUG_LIB = os.path.join(HERE, "libgemm_f16_debug.so")
 SOURCES = [os.path.join(CSRC, "library.cu"), os.path.join(CSRC, "ops_rows.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("gemm_f16.cu", "ops.cu", "ops_block.cu", "gemm_kernel.cuh", "gemm_pair.cuh",
-                                                     "elements.cuh", "ops_eight.cuh", "ops_linear.cuh", "ops_norm.cuh", "ops_rows.h",
+                                                     "elements.cuh", "ops_eight.cuh", "ops_linear.cuh", "ops_norm.cuh", "ops_rows.h", "rows_check.cuh",
                                                      "ptx.cuh")] + \
     [os.path.join(INCLUDE, f) for f in ("gemm_f16.h", "gemm_ops.h")]
 

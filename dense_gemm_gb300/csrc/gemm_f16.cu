@@ -15,6 +15,7 @@
 #include "gemm_f16.h"
 #include "gemm_kernel.cuh"
 #include "gemm_pair.cuh"
+#include "ops_rows.h"
 
 namespace {
 
@@ -956,7 +957,8 @@ gemm_status_t gemm_f16_selftest_pair_abort(const void *A, const void *B, float *
 gemm_status_t gemm_f16_selftest_check(gemm_stream_t stream_) {
 #ifdef GEMM_DEBUG
     check_selftest_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream_)>>>();
-    return cudaGetLastError() == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+    if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_CUDA;
+    return g16::rows_check_selftest(reinterpret_cast<cudaStream_t>(stream_)) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
 #else
     (void)stream_;
     return GEMM_ERR_UNSUPPORTED;  // the product build has no device-side checks
@@ -975,6 +977,9 @@ gemm_status_t gemm_f16_sync_status(gemm_stream_t stream_) {
         if (cudaMemcpyFromSymbol(&line, g_check_line, sizeof(line)) == cudaSuccess)
             std::fprintf(stderr, "[gemm_f16] device check failed at source line %u\n", line);
     }
+    unsigned int rows_line = 0;
+    if (g16::take_rows_check_line(&rows_line) != cudaSuccess) return GEMM_ERR_CUDA;
+    if (rows_line != 0) std::fprintf(stderr, "[gemm_f16] device check failed at source line %u of ops_rows.cu\n", rows_line);
 #endif
     if (st != 0) {
         // clear the status, and the aborted launch's epoch: a CUDA graph replays a
@@ -983,6 +988,9 @@ gemm_status_t gemm_f16_sync_status(gemm_stream_t stream_) {
             cudaMemcpyToSymbol(g_abort_epoch, &zero, sizeof(zero)) != cudaSuccess)
             return GEMM_ERR_CUDA;
     }
+#ifdef GEMM_DEBUG
+    if (st == 0 && rows_line != 0) st = kStatusCheck;
+#endif
     return st == 0 ? GEMM_OK : static_cast<gemm_status_t>(st);
 }
 

@@ -17,7 +17,7 @@
 #include <utility>
 
 #include "elements.cuh"
-#include "ptx.cuh"
+#include "rows_check.cuh"
 
 namespace g16 {
 namespace {
@@ -189,6 +189,12 @@ struct Row {
     __device__ __forceinline__ bool cut(int j) const { return kShift && (at(j) < 0 || at(j) + 8 > width); }
     __device__ __forceinline__ int lo(int j) const { return kShift ? -at(j) : 0; }
     __device__ __forceinline__ int hi(int j) const { return kShift ? width - at(j) : 8; }
+    // (checks) load j's granule has an element of the row, is all the row's unless shifted, and lies at `p` on
+    // the boundary that its elements' size asks for
+    __device__ __forceinline__ bool ok(int j, const void *p, int es) const {
+        return live && at(j) > -8 && at(j) < width && (kShift || (at(j) >= 0 && at(j) + 8 <= width)) &&
+               (reinterpret_cast<uintptr_t>(p) & uintptr_t(es == 1 ? 7 : 15)) == 0;
+    }
     __device__ __forceinline__ void keep(Raw<T, 8> &r, int j) const {
         if constexpr (kShift) {
             if (cut(j)) keep_elems<T>(r, lo(j), hi(j));
@@ -254,9 +260,9 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs p)
         const T *r = static_cast<const T *>(p.r) + row * p.ldr;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if (!a.has(j)) continue;
+            if (!a.has(j) || !G16_CHECK(row < p.rows && a.ok(j, x + a.at(j), sizeof(T)))) continue;
             rx[j] = load_raw<T, 8>(x + a.at(j));
-            if (p.r != nullptr) rr[j] = load_raw<T, 8>(r + a.at(j));
+            if (p.r != nullptr && G16_CHECK(a.ok(j, r + a.at(j), sizeof(T)))) rr[j] = load_raw<T, 8>(r + a.at(j));
         }
         if constexpr (kEarly) {
 #pragma unroll
@@ -282,7 +288,8 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs p)
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         if (!a.has(j)) continue;
-        if (p.h != nullptr) store_same<T>(static_cast<T *>(p.h) + row * p.ldh + a.at(j), t[j], a.lo(j), a.hi(j));
+        T *h = static_cast<T *>(p.h) + row * p.ldh + a.at(j);
+        if (p.h != nullptr && G16_CHECK(a.ok(j, h, sizeof(T)))) store_same<T>(h, t[j], a.lo(j), a.hi(j));
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum = add2(sum, t[j].p[i]);
     }
@@ -320,8 +327,8 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs p)
             const float2 u = fma2(t[j].p[i], by, off);
             t[j].p[i] = p.b != nullptr ? fma2(u, fw.p[i], fb.p[i]) : mul2(u, fw.p[i]);
         }
-        if constexpr (OUT == kOutSame) store_same<T>(y + a.at(j), t[j], a.lo(j), a.hi(j));
-        else top = largest(t[j], top);
+        if constexpr (OUT != kOutSame) top = largest(t[j], top);
+        else if (G16_CHECK(a.ok(j, y + a.at(j), sizeof(*y)))) store_same<T>(y + a.at(j), t[j], a.lo(j), a.hi(j));
     }
     if (a.live && threadIdx.x == 0) {
         if (p.mean != nullptr) p.mean[row] = mean;
@@ -333,7 +340,8 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs p)
         if (a.live && threadIdx.x == 0) p.scale[row] = scale;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if (a.has(j)) store_out<T, OUT>(y + a.at(j), t[j], mul, scale != scale, a.lo(j), a.hi(j));
+            if (a.has(j) && G16_CHECK(a.ok(j, y + a.at(j), sizeof(*y))))
+                store_out<T, OUT>(y + a.at(j), t[j], mul, scale != scale, a.lo(j), a.hi(j));
         }
     }
 }
@@ -359,7 +367,7 @@ __global__ void __launch_bounds__(1024) layer_norm_any_kernel(const LayerNormArg
 #pragma unroll 4
     for (int64_t at = threadIdx.x; at < p.width; at += blockDim.x) {
         const float h = made(at);
-        if (cached) kept[at] = h;
+        if (cached && G16_CHECK(smem_window_ok(smem_addr(kept + at), 4))) kept[at] = h;
         s += h;
     }
     const float m1 = row_sum<false>(s, red[0]) * p.inv_width;
@@ -413,7 +421,7 @@ __global__ void __maxnreg__(sizeof(T) == 2 ? 40 : 64) quantize_rows_kernel(const
     Raw<T, 8> rx[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-        if (a.has(j)) rx[j] = load_raw<T, 8>(x + a.at(j));
+        if (a.has(j) && G16_CHECK(row < p.rows && a.ok(j, x + a.at(j), sizeof(T)))) rx[j] = load_raw<T, 8>(x + a.at(j));
     float top = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -429,7 +437,7 @@ __global__ void __maxnreg__(sizeof(T) == 2 ? 40 : 64) quantize_rows_kernel(const
     uint8_t *q = static_cast<uint8_t *>(p.q) + row * p.ldq;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        if (!a.has(j)) continue;
+        if (!a.has(j) || !G16_CHECK(a.ok(j, q + a.at(j), 1))) continue;
         store_out<T, OUT, true>(q + a.at(j), widen<T, 8>(rx[j]), mul, scale != scale, a.lo(j), a.hi(j), rest);
     }
 }
@@ -446,7 +454,7 @@ __global__ void __launch_bounds__(1024) quantize_any_kernel(const QuantizeArgs p
 #pragma unroll 4
     for (int64_t at = threadIdx.x; at < p.width; at += blockDim.x) {
         const float v = to_f32<T>(x[at]);
-        if (cached) kept[at] = v;
+        if (cached && G16_CHECK(smem_window_ok(smem_addr(kept + at), 4))) kept[at] = v;
         top = max_nan(top, fabsf(v));
     }
     top = row_max(top, redq);
@@ -462,6 +470,7 @@ __global__ void __launch_bounds__(1024) quantize_any_kernel(const QuantizeArgs p
 
 // ------------------------------------------------------------------ gradients
 __device__ __forceinline__ void copy16_async(uint32_t dst, const void *src) {
+    if (!G16_CHECK(((dst | uint32_t(reinterpret_cast<uintptr_t>(src))) & 15u) == 0 && smem_window_ok(dst, 16))) return;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -469,6 +478,11 @@ template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 constexpr int kBackThreads = 512;  // of a block at most: 128 registers each
+
+// (checks) column `col` of part `part` lies in the workspace
+[[maybe_unused]] __device__ __forceinline__ bool part_ok(const LayerNormBackwardArgs &p, int64_t part, int64_t col) {
+    return p.partial != nullptr && part < p.rows && part < kLayerNormParts && col >= 0 && col < p.width;
+}
 
 // rows_sum for rows side by side in a block that do not wait for one another: a barrier
 // of the row's own threads, none for a row of one warp.
@@ -532,6 +546,11 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_rows_kernel(
     const int64_t g_row = apart * p.ldg * E, h_row = apart * p.ldh * E, d_row = apart * p.lddh * E, x_row = apart * p.lddx * E;
     const uint32_t jump = blockDim.x * 16u * G;  // bytes between a thread's loads
     const uint32_t mine = smem_addr(ring) + uint32_t(tid) * 16u;
+    // (checks) a stepped address is that of load j of `row`, which exists
+    [[maybe_unused]] auto at_row = [&](const char *stepped, const void *base, int64_t ld, int64_t row, int j) {
+        const T *direct = static_cast<const T *>(base) + row * ld + a.at(j);
+        return row >= 0 && row < p.rows && stepped == reinterpret_cast<const char *>(direct) && a.ok(j, direct, sizeof(T));
+    };
     // rows row, row + apart, ... -> the slot at `to`; on to the next step's
     auto fetch = [&](int64_t row, uint32_t to) {
 #pragma unroll
@@ -539,7 +558,10 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_rows_kernel(
             if (row + r * apart >= p.rows) break;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                if (!has[j]) continue;
+                if (!has[j] || !G16_CHECK(at_row(gp + r * g_row + j * jump, p.g, p.ldg, row + r * apart, j) &&
+                                          at_row(hp + r * h_row + j * jump, p.h, p.ldh, row + r * apart, j) &&
+                                          (!has_d || at_row(dp + r * d_row + j * jump, p.dh, p.lddh, row + r * apart, j))))
+                    continue;
 #pragma unroll
                 for (int k = 0; k < G; ++k) {
                     const uint32_t at = to + uint32_t((r * NV + j) * G + k) * LINE;
@@ -555,10 +577,10 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_rows_kernel(
         dp += d_step;
     };
     auto values = [&](uint32_t at, int j) {
-        Raw<T, 8> v;
+        Raw<T, 8> v = {};
 #pragma unroll
         for (int k = 0; k < G; ++k)
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+            if (G16_CHECK(smem_window_ok(at + k * LINE, 16))) asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v.q[k].x), "=r"(v.q[k].y), "=r"(v.q[k].z), "=r"(v.q[k].w)
                          : "r"(at + k * LINE)
                          : "memory");
@@ -637,7 +659,8 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_rows_kernel(
                     db[j].p[i] = add2(fg.p[i], db[j].p[i]);
                     v.p[i] = fma2(c, c2, fma2(t, w.p[i], has_d ? add2(v.p[i], c1) : c1));
                 }
-                store_same<T>(reinterpret_cast<T *>(xp + r * x_row + j * jump), v, a.lo(j), a.hi(j));
+                if (G16_CHECK(at_row(xp + r * x_row + j * jump, p.dx, p.lddx, row + r * apart, j)))
+                    store_same<T>(reinterpret_cast<T *>(xp + r * x_row + j * jump), v, a.lo(j), a.hi(j));
             }
         }
         fetch(row + STAGES * step, slot);  // this thread has read the slot
@@ -659,14 +682,15 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_rows_kernel(
             for (int j = 0; j < NV; ++j) {
                 if (kShift || a.at(j) < a.width) {
                     float *to = sums + int(threadIdx.y) * span + a.at(j);
-                    store_elems(to, k == 0 ? dw[j] : db[j], a.lo(j), a.hi(j));
+                    if (G16_CHECK(a.at(j) > -8 && a.at(j) + a.o + 8 <= span && smem_window_ok(smem_addr(sums + (int(threadIdx.y) + 1) * span - 1), 4)))
+                        store_elems(to, k == 0 ? dw[j] : db[j], a.lo(j), a.hi(j));
                 }
             }
             __syncthreads();
             for (int c = tid; c < span && c < a.width; c += int(blockDim.x * blockDim.y)) {
                 float s = sums[c];
                 for (int y = 1; y < int(blockDim.y); ++y) s += sums[y * span + c];
-                out[k * p.width + c] = s;
+                if (G16_CHECK(part_ok(p, blockIdx.x, c))) out[k * p.width + c] = s;
             }
         }
         return;
@@ -674,7 +698,7 @@ __global__ void __launch_bounds__(kBackThreads) layer_norm_backward_rows_kernel(
     if constexpr (!kShift) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            if (a.at(j) >= a.width) continue;
+            if (a.at(j) >= a.width || !G16_CHECK(part_ok(p, blockIdx.x, a.at(j) + 7))) continue;
             store_f32<float, 8>(out + a.at(j), dw[j]);  // width is a multiple of 8, the workspace aligned
             store_f32<float, 8>(out + p.width + a.at(j), db[j]);
         }
@@ -726,6 +750,7 @@ __global__ void __launch_bounds__(256) layer_norm_columns_kernel(const LayerNorm
         db += g;
     }
     float *out = p.partial + int64_t(blockIdx.y) * 2 * p.width + col;
+    if (!G16_CHECK(part_ok(p, blockIdx.y, col))) return;
     out[0] = dw;
     out[p.width] = db;
 }

@@ -54,4 +54,11 @@ G16_HIDDEN cudaError_t launch_layer_norm_backward(const LayerNormBackwardArgs &p
                                                   cudaStream_t stream);
 G16_HIDDEN cudaError_t launch_quantize_rows(const QuantizeArgs &p, int num_sms, cudaStream_t stream);
 
+#ifdef GEMM_DEBUG
+// The checked build's: the source line in ops_rows.cu of the first check that failed (0: none), which is
+// then forgotten; and a kernel of one failing check that guards nothing.
+G16_HIDDEN cudaError_t take_rows_check_line(unsigned int *line);
+G16_HIDDEN cudaError_t rows_check_selftest(cudaStream_t stream);
+#endif
+
 }  // namespace g16

@@ -16,8 +16,11 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p) {
 // access it guards is skipped. In the product build it is the constant true and
 // compiles to nothing.
 #ifdef GEMM_DEBUG
-__device__ bool check_failed(int line);  // defined beside the status words
-#define G16_CHECK(cond) ((cond) || ::g16::check_failed(__LINE__))
+#ifndef G16_CHECK_FAILED
+#define G16_CHECK_FAILED check_failed  // another name in a translation unit with a status of its own
+#endif
+__device__ bool G16_CHECK_FAILED(int line);  // defined beside the status words
+#define G16_CHECK(cond) ((cond) || ::g16::G16_CHECK_FAILED(__LINE__))
 #else
 #define G16_CHECK(cond) true
 #endif
