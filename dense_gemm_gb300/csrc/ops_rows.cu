@@ -136,24 +136,15 @@ __device__ __forceinline__ void store_one(void *p, int64_t at, float v, float mu
     else static_cast<T *>(p)[at] = from_f32<T>(v);
 }
 
-// row_sum<false> of two values: after the first exchange half a warp's lanes have one sum, half the
-// other, so that both take little more than the shuffles of one.
-__device__ __forceinline__ void row_sums(float (&v)[2], float (*red)[32]) {
-    const int lane = threadIdx.x & 31, side = lane >> 4;
-    float s = (side ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, side ? v[0] : v[1], 16);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const int wpr = blockDim.x >> 5, base = int(threadIdx.y) * wpr;
-    if (wpr > 1) {
-        if ((lane & 15) == 0) red[side][base + (threadIdx.x >> 5)] = s;
-        __syncthreads();
-        const int l = lane & 15;
-        s = (l < wpr ? red[side][base + l] : 0.0f) + (l + 16 < wpr ? red[side][base + l + 16] : 0.0f);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    }
-    v[0] = __shfl_sync(0xffffffffu, s, 0);
-    v[1] = __shfl_sync(0xffffffffu, s, 16);
+// row_sum<false> with a barrier of the row's own threads: rows side by side in a block need not all take it.
+__device__ __forceinline__ float own_row_sum(float v, float *red) {
+    v = warp_sum(v);
+    const int wpr = blockDim.x >> 5;
+    if (wpr == 1) return v;
+    const int lane = threadIdx.x & 31, base = int(threadIdx.y) * wpr;
+    if (lane == 0) red[base + (threadIdx.x >> 5)] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + threadIdx.y), "r"(blockDim.x) : "memory");
+    return warp_sum(lane < wpr ? red[base + lane] : 0.0f);
 }
 
 // Every thread of a row gets the row's largest m (>= 0 or NaN: their bits are in their
@@ -219,19 +210,26 @@ __device__ __forceinline__ void clear_outside(F32<8> &v, int lo, int hi) {
     }
 }
 
-// A row's mean and variance from a first mean m1, which is as many roundings off as the row's sum
-// has, and the sums s1 of c = h - m1 and s2 of c^2. c is exact where h and m1 are near one another,
-// so m1 + s1 / width is the mean, rounded once, and the variance that of the values less it.
-// Without the correction a row of equal values keeps for c some units of its mean's last place,
-// which 1 / sqrt(eps) multiplies (eps = 1e-12: y = b +- w). What the correction leaves of the
-// variance below the sums' own rounding is 0. (Without it 8192 x 4096 43.4 us, so 44.5, 4096 x 8192 to 8
-// bits 39.0 and 40.6; corrected only where the mean is larger than the deviation 44.5 and 39.7, and
-// 39.5 for such rows without a residual, which so take 35.3.)
+// A row's mean and variance. m1 = sum / width is as many roundings off as the sum has: none or few for
+// values of 16 bits, units of m1's last place where the mean is large beside the deviation. Past four
+// deviations c = h - m1 is exact or nearly so, the mean of c is what m1 lacks, and the variance is that
+// of the values less the two. Without it a row of equal values keeps some units of its mean's last
+// place for c, which 1 / sqrt(eps) multiplies (eps = 1e-12: y = b +- w). What the correction leaves of
+// the variance below the sums' own rounding is 0. (Without it 8192 x 4096 43.4 us, so 44.5, 4096 x 8192 to
+// 8 bits 39.0 and 39.8; rows that take it, 8192 x 4096 without a residual, 33.5 and 39.6. For every row,
+// with one barrier for both sums, 44.7, 40.6 and 35.7.)
+__device__ __forceinline__ float first_mean(float sum, float width, float inv_width) {
+    const float m = sum * inv_width;
+    const float r = fmaf(fmaf(-m, width, sum), inv_width, m);  // sum / width, rounded once
+    return r - r == 0.0f ? r : m;
+}
 struct RowMean {
-    float mean, less, var;  // c - less is h - mean
-    __device__ __forceinline__ RowMean(float m1, float s1, float s2, float inv_width) {
-        const float more = s1 * inv_width, square = s2 * inv_width;
-        mean = more == more ? m1 + more : m1;  // an infinite row's
+    float mean, var, less;  // c - less is h - mean
+    __device__ __forceinline__ RowMean(float m1, float square) : mean(m1), var(square), less(0.0f) {}
+    __device__ __forceinline__ bool rough() const { return __builtin_expect(var < 0.0625f * mean * mean, 0); }
+    __device__ __forceinline__ void correct(float more) {  // by the mean of c
+        const float m1 = mean, square = var;
+        mean = m1 + more;
         less = mean - m1;
         var = fmaf(less, less - 2.0f * more, square);
         if (var < square * 0x1p-16f) var = 0.0f;
@@ -239,7 +237,7 @@ struct RowMean {
 };
 
 // Bound by DRAM and the issue slots where there are many rows (4096 x 8192 bf16 with residual
-// to 8 bits 235 MB in 40.6 us, 5.8 TB/s, 8192 x 4096 268 MB in 44.5, 6.0), by the chain load - sums -
+// to 8 bits 235 MB in 39.8 us, 5.9 TB/s, 8192 x 4096 268 MB in 44.5, 6.0), by the chain load - sums -
 // store where there are few (1 x 4096 2.1 us). Loads that pass L1 for x and r, to leave it to the
 // weights, were 2 to 4 % slower.
 template <typename T, int NV, int OUT, bool kShift>
@@ -293,8 +291,8 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum = add2(sum, t[j].p[i]);
     }
-    const float m1 = row_sum<false>(total(sum), red[0]) * p.inv_width;
-    float2 s1 = splat<8>(0.0f), s2 = s1;
+    const float m1 = first_mean(row_sum<false>(total(sum), red[0]), float(a.width), p.inv_width);
+    float2 ss = splat<8>(0.0f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         if (!a.has(j)) continue;
@@ -302,18 +300,26 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs p)
         for (int i = 0; i < 4; ++i) t[j].p[i] = add2(t[j].p[i], splat<8>(-m1));
         if (a.cut(j)) clear_outside(t[j], a.lo(j), a.hi(j));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s1 = add2(s1, t[j].p[i]);
-            s2 = fma2(t[j].p[i], t[j].p[i], s2);
+        for (int i = 0; i < 4; ++i) ss = fma2(t[j].p[i], t[j].p[i], ss);
+    }
+    RowMean m(m1, row_sum<false>(total(ss), red[1]) * p.inv_width);
+    if (m.rough()) {
+        sum = splat<8>(0.0f);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (!a.has(j)) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum = add2(sum, t[j].p[i]);
+        }
+        m.correct(own_row_sum(total(sum), red[2]) * p.inv_width);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (!a.has(j)) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t[j].p[i] = add2(t[j].p[i], splat<8>(-m.less));
         }
     }
-    float sums[2] = {total(s1), total(s2)};
-    row_sums(sums, red + 1);
-    const RowMean m(m1, sums[0], sums[1], p.inv_width);
     const float mean = m.mean, rstd = rsqrtf(m.var + p.eps);
-    // h - mean times rstd in one multiply-add; a row of equal values takes no rounding's rest with it
-    const float zero = 0.0f * rstd;  // NaN with eps = 0
-    const float2 by = splat<8>(m.var == 0.0f ? zero : rstd), off = splat<8>(m.var == 0.0f ? zero : -m.less * rstd);
     float top = 0.0f;
     Stored<OUT, T> *y = static_cast<Stored<OUT, T> *>(p.y) + row * p.ldy;
 #pragma unroll
@@ -324,7 +330,7 @@ __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs p)
         if (p.b != nullptr) fb = early ? widen<T, 8>(b[j]) : a.column(p.b, p.w_f32 != 0, j);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 u = fma2(t[j].p[i], by, off);
+            const float2 u = mul2(t[j].p[i], splat<8>(rstd));
             t[j].p[i] = p.b != nullptr ? fma2(u, fw.p[i], fb.p[i]) : mul2(u, fw.p[i]);
         }
         if constexpr (OUT != kOutSame) top = largest(t[j], top);
@@ -370,16 +376,16 @@ __global__ void __launch_bounds__(1024) layer_norm_any_kernel(const LayerNormArg
         if (cached && G16_CHECK(smem_window_ok(smem_addr(kept + at), 4))) kept[at] = h;
         s += h;
     }
-    const float m1 = row_sum<false>(s, red[0]) * p.inv_width;
-    float sums[2] = {0.0f, 0.0f};
+    const float m1 = first_mean(row_sum<false>(s, red[0]), float(p.width), p.inv_width);
+    float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll 4
     for (int64_t at = threadIdx.x; at < p.width; at += blockDim.x) {
         const float c = value(at) - m1;
-        sums[0] += c;
-        sums[1] = fmaf(c, c, sums[1]);
+        s1 += c;
+        s2 = fmaf(c, c, s2);
     }
-    row_sums(sums, red + 1);
-    const RowMean m(m1, sums[0], sums[1], p.inv_width);
+    RowMean m(m1, row_sum<false>(s2, red[1]) * p.inv_width);
+    if (m.rough()) m.correct(own_row_sum(s1, red[2]) * p.inv_width);
     const float mean = m.mean, rstd = rsqrtf(m.var + p.eps);
     auto result = [&](float h, int64_t at) {
         const float w = load_weight<T, 1>(p.w, p.w_f32 != 0, at).p[0], u = (h - mean) * rstd;

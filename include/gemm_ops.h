@@ -203,9 +203,10 @@ gemm_status_t gemm_rms_norm_backward_workspace_size(int64_t rows, int64_t width,
  *   mean[i] = sum(h) / width,  rstd[i] = 1 / sqrt(sum((h - mean)^2) / width + eps)
  *   y[i,:] = weight * (h - mean[i]) * rstd[i] + bias
  *
- * everything in fp32 from the unrounded sum h, the mean corrected by the centred
- * values' own sum, the variance from them; h, y, mean and rstd are each rounded once. x, residual and h have one
- * type, fp32, fp16 or bf16; y has that type or is e4m3 or int8; weight and bias
+ * everything in fp32 from the unrounded sum h, the variance from the centred values,
+ * whose own sum corrects a mean that is large beside it; h, y, mean and rstd are each
+ * rounded once. The squares are numbers of fp32: deviations from 1e-18 to 1e18. x,
+ * residual and h have one type, fp32, fp16 or bf16; y has that type or is e4m3 or int8; weight and bias
  * [width] both have x's type or both are fp32; bias may be NULL. With an 8-bit y,
  * a = max_j |y[i,j]|, scale[i] = a / t and y[i,j] holds nearest-even(y[i,j] *
  * (t / a)), t = 448 (e4m3) or 127 (int8), so that the value is y * scale; a row whose
@@ -232,7 +233,8 @@ gemm_status_t gemm_layer_norm(const gemm_matrix_t *x, const gemm_matrix_t *resid
  *   dx = rstd (g - mean(g) - u mean(g u)) + grad_h   (x's and residual's gradient)
  *   dweight[j] = sum_i grad[i,j] u[i,j],  dbias[j] = sum_i grad[i,j]   (fp32 [width])
  *
- * in fp32; dx is rounded once. grad, h, grad_h and dx have one type, fp32, fp16
+ * in fp32, where rstd^2 mean(g u) has to be a number too (rstd up to 1e18); dx is
+ * rounded once. grad, h, grad_h and dx have one type, fp32, fp16
  * or bf16. dx may be grad or grad_h itself. dweight and dbias may each be NULL.
  * Sums over rows are in a fixed order. workspace: 16-byte aligned,
  * gemm_layer_norm_backward_workspace_size() bytes (partial sums over the rows;
