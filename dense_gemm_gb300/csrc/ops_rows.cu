@@ -5,11 +5,13 @@
 //                                   dw = sum_rows dy u,  db = sum_rows dy
 //   q = round(x TOP / a), scale = a / TOP,  a = max|x| of the row, TOP 448 (e4m3) or 127 (int8)
 //
-// A dozen operations per element at most, so DRAM bounds all of them: every row is
-// read once into registers or shared memory and written from there. The variance is
-// summed from the centred values: the difference of the mean square and the squared
-// mean loses what a row's mean has more digits than its deviation. The mean is corrected by
-// the centred values' own sum (RowMean). All sums are fp32, in an order that the sizes fix.
+// A dozen operations per element at most: the floor of all of them is DRAM's, so every row is
+// read once into registers or shared memory and written from there. They come near it where rows are
+// many and some thousand elements wide; elsewhere what a row does in series (loads, sums over its
+// threads, store) counts, with too few loads in flight meanwhile: neither DRAM nor the issue slots are
+// full. The variance is summed from the centred values: the difference of the mean square and the squared
+// mean loses what a row's mean has more digits than its deviation; a mean that is large beside
+// it is corrected by their own sum (RowMean). All sums are fp32, in an order that the sizes fix.
 #include "ops_rows.h"
 
 #include <algorithm>
@@ -236,9 +238,10 @@ struct RowMean {
     }
 };
 
-// Bound by DRAM and the issue slots where there are many rows (4096 x 8192 bf16 with residual
-// to 8 bits 235 MB in 39.8 us, 5.9 TB/s, 8192 x 4096 268 MB in 44.5, 6.0), by the chain load - sums -
-// store where there are few (1 x 4096 2.1 us). Loads that pass L1 for x and r, to leave it to the
+// Many rows: 4096 x 8192 bf16 with residual to 8 bits 235 MB in 39.8 us (5.9 TB/s), 8192 x 4096 268 MB
+// in 44.5 (6.0), DRAM and the issue slots each three fifths busy: the blocks on an SM (64 registers a
+// thread) have too few loads in flight while others sum. Few: the chain load - sums - store
+// (1 x 4096 2.1 us, 1000 x 5000 10.2 for 5.9 of DRAM). Loads that pass L1 for x and r, to leave it to the
 // weights, were 2 to 4 % slower.
 template <typename T, int NV, int OUT, bool kShift>
 __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs p) {
@@ -518,8 +521,10 @@ __device__ __forceinline__ void own_rows_sum(float (&v)[N], float (*red)[32]) {
 // them, and the rows of the next STAGES - 1 steps are on their way into shared memory. A
 // thread copies what it will itself read, so that a step waits for the thread's own
 // copies only; the one barrier of a step is that of the two row sums, for R rows at a time.
-// Bound by issue slots and DRAM: 8192 x 4096 bf16 with grad_h 268 MB in 46 us (5.8 TB/s), 50.5
-// with the partial sums' launch; 4096 x 8192 53.4, 2048 x 16384 79, 8192 x 1024 20.4.
+// 8192 x 4096 bf16 with grad_h 268 MB in 46 us (5.8 TB/s), 50.5 with the partial sums' launch: DRAM two
+// thirds, issue slots 56 % busy, one block of 16 warps on an SM. 4096 x 8192 53.4. Twice DRAM's time at
+// 8192 x 1024 (20.4 us for 9.9: one load per thread, a barrier for 128 of them) and 2048 x 16384 (79 for
+// 39.6: one row and one step ahead), more where rows are few (513 x 4095 fp16 13.4 for 1.9).
 // kShift: rows off 16-byte boundaries. A thread's rows are then a multiple of 8 rows apart
 // (the grid is a multiple of 8), so that all of them start at the same place in a granule
 // and the thread keeps its columns.

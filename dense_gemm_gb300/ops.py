@@ -100,7 +100,8 @@ def linear(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor = None, *, activ
     ``out`` itself; ``bias`` [N] has C's type or is float32. With ``return_pre``
     (or a ``pre`` [M, N] to write) the value before the activation is kept, and
     (C, pre) is returned. ``kernel`` chooses between "pair" and "split" by hand
-    (gemm_linear in include/gemm_ops.h).
+    (gemm_linear in include/gemm_ops.h); int8 operands of up to 768 rows, and small products of
+    them, have a kernel of their own whatever it says.
     """
     return (_module or _native()).linear(
         A, B, bias, _code(ACTIVATIONS, activation, "activation"), residual, scale_a, scale_b, out, out_dtype, pre,
