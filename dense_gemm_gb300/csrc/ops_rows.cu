@@ -238,10 +238,10 @@ struct RowMean {
     }
 };
 
-// Many rows: 4096 x 8192 bf16 with residual to 8 bits 235 MB in 39.8 us (5.9 TB/s), 8192 x 4096 268 MB
-// in 44.5 (6.0), DRAM and the issue slots each three fifths busy: the blocks on an SM (64 registers a
+// Many rows: 4096 x 8192 bf16 with residual to 8 bits 235 MB in 42.0 us (5.6 TB/s), 8192 x 4096 268 MB
+// in 46.1 (5.8), DRAM and the issue slots each three fifths busy: the blocks on an SM (64 registers a
 // thread) have too few loads in flight while others sum. Few: the chain load - sums - store
-// (1 x 4096 2.1 us, 1000 x 5000 10.2 for 5.9 of DRAM). Loads that pass L1 for x and r, to leave it to the
+// (1 x 4096 2.1 us, 1000 x 5000 10.4 for 5.9 of DRAM). Loads that pass L1 for x and r, to leave it to the
 // weights, were 2 to 4 % slower.
 template <typename T, int NV, int OUT, bool kShift>
 __global__ void __launch_bounds__(1024) layer_norm_kernel(const LayerNormArgs p) {
@@ -416,9 +416,9 @@ __global__ void __launch_bounds__(1024) layer_norm_any_kernel(const LayerNormArg
 }
 
 // ------------------------------------------------------------------ rows in 8 bits
-// One pass: the row stays in registers between its maximum and its store. DRAM bounds it
-// (4096 x 16384 bf16 201 MB in 32.0 us, 6.3 TB/s; 999 x 5001 fp16 5.1 us). 40 registers: three
-// blocks of 512 threads on an SM (4096 x 16384 to int8 38.9 us with 42).
+// One pass: the row stays in registers between its maximum and its store. 4096 x 16384 bf16 takes
+// 33.4 us (201 MB, 6.0 TB/s, nine tenths of a copy's rate), to int8 34.7; 999 x 5001 fp16 5.4 us. 40
+// registers: three blocks of 512 threads on an SM (4096 x 16384 to int8 38.9 us with 42).
 template <typename T, int NV, int OUT, bool kShift>
 __global__ void __maxnreg__(sizeof(T) == 2 ? 40 : 64) quantize_rows_kernel(const QuantizeArgs p) {
     __shared__ uint32_t redq[32];
