@@ -93,3 +93,26 @@ def test_gradients_of_equal_rows(width):
     assert_close(dx, r * (p - p.mean(1, keepdim=True)), r * U * (8 * p.abs() + (T + 10) * p.abs().mean(1, keepdim=True)), "dx")
     assert (dw == 0).all()
     assert_close(db, dy.double().sum(0), 12 * U * dy.double().abs().sum(0), "dbias")
+
+
+@pytest.mark.parametrize("rows,width", [(9, 64), (700, 520), (2000, 1024), (1000, 1001), (700, 2047), (2000, 4096), (40, 9000)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("out", [None, I8])
+def test_rows_with_and_without_a_correction_side_by_side(rows, width, dtype, out):
+    """A block's rows do not wait for one another's correction, and none reaches another: a row has the same
+    bits whatever stands beside it. (Rows change places with rows 8 k away: at an odd width a row starts
+    width * row elements into a granule of 8, mod 8, and its threads' columns, and so the order of its
+    sum, go by that.)"""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.randn(rows, width, generator=g, device="cuda")
+    x[::2] += 50
+    x[::5] = 7
+    x = x.to(dtype)
+    w, b = (torch.randn(width, generator=g, device="cuda").to(dtype) for _ in range(2))
+    order = torch.arange(rows, device="cuda")
+    for k in range(8):
+        mine = order[k::8]
+        order[k::8] = mine[torch.randperm(mine.numel(), generator=g, device="cuda")]
+    one, other = (layer_norm(v.contiguous(), w, b, out_dtype=out, return_stats=True) for v in (x, x[order]))
+    for p, q in zip(one, other):
+        assert p is None or torch.equal(p[order], q)
