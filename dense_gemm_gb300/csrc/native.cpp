@@ -189,8 +189,14 @@ struct Output {
         m.data = made.data_ptr();
     }
     float *floats() const { return static_cast<float *>(m.data); }
-    PyObject *give() {  // new reference
-        if (given != nullptr) return Py_NewRef(given);
+    // New reference. A tensor that was given has been written: autograd is told, so that a graph that saved
+    // its old values refuses them instead of using the new ones.
+    PyObject *give() {
+        if (given != nullptr) {
+            const at::Tensor &t = THPVariable_Unpack(given);
+            if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+            return Py_NewRef(given);
+        }
         return made.defined() ? THPVariable_Wrap(std::move(made)) : Py_NewRef(Py_None);
     }
 };

@@ -10,7 +10,8 @@ tensor of any type.
 The calls record no gradient: outputs do not require one whatever the inputs do,
 and ``linear_backward``, ``rms_norm_backward`` and ``layer_norm_backward`` are called
 by the caller's own ``torch.autograd.Function`` (``examples/mlp_block.py`` and
-``examples/eight_bit_block.py`` have them). C, ``pre``,
+``examples/eight_bit_block.py`` have them). A tensor that is given for an output counts as
+changed in place: a graph that saved its old values refuses its backward pass. C, ``pre``,
 ``residual``, ``grad`` and all matrices of the norms are stored by rows (unit
 column stride, any row stride); A and B by rows or by columns, 8-bit ones with K
 contiguous.
